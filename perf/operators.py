@@ -167,26 +167,30 @@ def prepare(case, seed):
     s = _inputs(c, seed)
     s["case"] = c
     if own:
-        # what a serving program holds for the life of its model: the workspace of a call (and the
-        # descriptor with the weights' addresses); neither weights nor inputs are touched here
+        # what a serving program does once per model and holds for its life: 4-bit weights in the
+        # kernels' order, the workspace of a call, a layer's descriptor with its weights' addresses
         import combine_moe_route_softmax_gb300 as moe
         if c["op"] == "linear":
+            s["packed"] = moe.moe_pack_w4(s["q"], s["scales"], s["zeros"])
             s["ws"] = moe.moe_linear_w4_workspace(c["T"], c["N"], c["K"])
         elif c["op"] == "route":
-            s["ws"] = moe.moe_route_hidden_workspace(c["T"], c["E"])
+            s["ws"] = moe.moe_route_hidden_workspace()
         else:
-            sh = c["shared"]
+            def form(w, one):
+                if w is None:
+                    return None, None
+                if c["dtype"] == "w4":
+                    return moe.moe_pack_w4(w["w"], w["scales"], w["zeros"]), None
+                pick = (lambda t: None if t is None else t[0]) if one else (lambda t: t)
+                return pick(w["w"]), pick(w["scales"])
+
+            (w13, c13), (w2, c2) = form(s["w13"], False), form(s["w2"], False)
+            (s13, d13), (s2, d2) = form(s["s13"], True), form(s["s2"], True)
             s["layer"] = moe.MoeLayerFew(
                 c["T"], c["H"], c["I"], c["E"], c["K"],
                 {"bf16": moe.MOE_BF16, "e4m3": moe.MOE_E4M3, "w4": moe.MOE_W4}[c["dtype"]],
-                w13=s["w13"]["w"], w2=s["w2"]["w"], w13_scales=s["w13"]["scales"], w2_scales=s["w2"]["scales"],
-                w13_zeros=s["w13"]["zeros"], w2_zeros=s["w2"]["zeros"],
-                shared_w13=s["s13"]["w"][0] if sh else None, shared_w2=s["s2"]["w"][0] if sh else None,
-                shared_w13_scales=s["s13"]["scales"][0] if sh and s["s13"]["scales"] is not None else None,
-                shared_w2_scales=s["s2"]["scales"][0] if sh and s["s2"]["scales"] is not None else None,
-                shared_w13_zeros=s["s13"]["zeros"][0] if sh and s["s13"]["zeros"] is not None else None,
-                shared_w2_zeros=s["s2"]["zeros"][0] if sh and s["s2"]["zeros"] is not None else None,
-                w_router=s.get("w_router"))
+                w13=w13, w2=w2, shared_w13=s13, shared_w2=s2, w13_scales=c13, w2_scales=c2,
+                shared_w13_scales=d13, shared_w2_scales=d2, w_router=s.get("w_router"))
     return s
 
 
@@ -268,7 +272,7 @@ def run(state):
     if own:
         import combine_moe_route_softmax_gb300 as moe
         if c["op"] == "linear":
-            return moe.moe_linear_w4(s["x"], s["q"], s["scales"], zeros=s["zeros"], bias=s["bias"],
+            return moe.moe_linear_w4(s["x"], s["packed"], bias=s["bias"],
                                      out_dtype=torch.float32 if c["f32"] else torch.bfloat16, ws=s["ws"])
         if c["op"] == "route":
             return moe.moe_route_hidden(s["x"], s["w_router"], c["K"], bias=s["bias"], ws=s["ws"])
