@@ -13,13 +13,14 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmoe.so")
 
-MOE_BF16, MOE_E4M3 = 0, 1
+MOE_BF16, MOE_E4M3, MOE_W4 = 0, 1, 2
+MOE_FEW_MAX_TOKENS = 32   # tokens of one few-token call (moe_route_hidden, moe_layer_few)
 MOE_W_TILED = 0x100   # ORed into a grouped GEMM dtype: weights in the tile layout of moe_pack_weights
 MOE_EPI_NONE, MOE_EPI_SWIGLU = 0, 1
 MOE_DEV_BAD_EXPERT, MOE_DEV_VERIFY_MISMATCH, MOE_DEV_PIPELINE_TIMEOUT, MOE_DEV_OVERFLOW = 1, 2, 4, 8
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_ARG", 2: "MOE_ERR_WORKSPACE", 3: "MOE_ERR_UNSUPPORTED", 4: "MOE_ERR_CUDA"}
 
-_P, _I, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_P, _I, _Z, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong
 
 
 class MoeError(RuntimeError):
@@ -37,6 +38,17 @@ class LayerDesc(ctypes.Structure):
 class LayerWeights(ctypes.Structure):
     _fields_ = [(n, _P) for n in ("w13", "w13_scales", "w2", "w2_scales", "shared_w13", "shared_w13_scales",
                                   "shared_w2", "shared_w2_scales")]
+
+
+class FewDesc(ctypes.Structure):
+    _fields_ = [("T", _I), ("H", _I), ("I", _I), ("E", _I), ("K", _I), ("dtype", _I), ("has_shared", _I),
+                ("weight_tiles", _I), ("group", _I)]
+
+
+class FewWeights(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("w13", "w13_scales", "w13_zeros", "w2", "w2_scales", "w2_zeros", "shared_w13",
+                                  "shared_w13_scales", "shared_w13_zeros", "shared_w2", "shared_w2_scales",
+                                  "shared_w2_zeros", "w_router", "router_bias")]
 
 
 class LayerViews(ctypes.Structure):
@@ -79,6 +91,16 @@ _SIGS = {
     "moe_layer_views": ([ctypes.POINTER(LayerDesc), _P, ctypes.POINTER(LayerViews)], _I),
     "moe_layer_forward": ([ctypes.POINTER(LayerDesc), ctypes.POINTER(LayerWeights), _P, _P, _P, _P, _P, _P, _P,
                            _P, _P, _Z, _P, _P], _I),
+    "moe_quantize_weight_w4": ([_P, _I, _I, _I, _I, _P, _P, _P, _P], _I),
+    "moe_w4_packed_bytes": ([_I, _I], _Z),
+    "moe_pack_w4": ([_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P], _I),
+    "moe_linear_w4_workspace_bytes": ([_I, _I, _I], _Z),
+    "moe_linear_w4": ([_P, _I, _I, _L, _P, _P, _P, _I, _I, _P, _P, _I, _L, _P, _Z, _P], _I),
+    "moe_route_hidden_workspace_bytes": ([], _Z),
+    "moe_route_hidden": ([_P, _I, _I, _P, _P, _I, _I, _P, _P, _P, _P, _P, _Z, _P], _I),
+    "moe_layer_few_workspace_bytes": ([ctypes.POINTER(FewDesc)], _Z),
+    "moe_layer_few": ([ctypes.POINTER(FewDesc), ctypes.POINTER(FewWeights), _P, _P, _P, _P, _P, _P, _P, _Z, _P, _P],
+                      _I),
 }
 
 _lib = None
@@ -446,3 +468,174 @@ class MoeLayer:
             _ptr(topk_w), _ptr(x), _ptr(fq_scale), _ptr(dispatch_scale), _ptr(out), _ptr(self.ws), self.ws.numel(),
             _ptr(dev_status), _stream(stream)))
         return out
+
+
+# ------------------------------------------------------------------------ a few tokens
+class W4Packed:
+    """4-bit weights in the kernels' order (moe_pack_w4): `mats` matrices of N rows, K columns,
+    scales per `group` columns, zero points or not.  [i] is one matrix of a stack."""
+
+    def __init__(self, q, scales, zeros, mats, N, K, group):
+        self.q, self.scales, self.zeros = q, scales, zeros
+        self.mats, self.N, self.K, self.group = mats, N, K, group
+
+    def __getitem__(self, i):
+        if not -self.mats <= i < self.mats:
+            raise IndexError(i)
+        return W4Packed(self.q[i:i + 1] if i != -1 else self.q[i:], self.scales[i:i + 1] if i != -1 else self.scales[i:],
+                        None if self.zeros is None else self.zeros[i:i + 1] if i != -1 else self.zeros[i:], 1, self.N,
+                        self.K, self.group)
+
+
+def moe_quantize_weight_w4(w, group, zeros=False, stream=None):
+    """w BF16 [..., rows, cols] -> (codes uint8 [..., rows, cols/2], scales BF16 [..., cols/group,
+    rows], zero points uint8 like scales, or None)."""
+    _dev(w)
+    rows, cols = w.shape[-2:]
+    lead = w.shape[:-2]
+    mats = w.numel() // (rows * cols)
+    q = torch.empty(*lead, rows, cols // 2, dtype=torch.uint8, device=w.device)
+    s = torch.empty(*lead, cols // group, rows, dtype=torch.bfloat16, device=w.device)
+    z = torch.empty(*lead, cols // group, rows, dtype=torch.uint8, device=w.device) if zeros else None
+    _check("moe_quantize_weight_w4", lib().moe_quantize_weight_w4(_ptr(w), mats, rows, cols, group, _ptr(q), _ptr(s),
+                                                                  _ptr(z), _stream(stream)))
+    return q, s, z
+
+
+def moe_pack_w4(q, scales, zeros=None, stream=None):
+    """Codes [..., N, K/2], scales BF16 [..., K/group, N] and zero points (uint8, like scales, or
+    None) -> W4Packed."""
+    _dev(q)
+    _dev(scales)
+    N, K = q.shape[-2], 2 * q.shape[-1]
+    mats = q.numel() // (N * q.shape[-1])
+    if scales.dtype != torch.bfloat16 or scales.shape[-1] != N or scales.numel() % (mats * N):
+        raise ValueError("scales are BF16 [..., K / group, N]")
+    kg = scales.numel() // (mats * N)
+    group = K // kg
+    if zeros is not None and (_dev(zeros).dtype != torch.uint8 or zeros.numel() != scales.numel()):
+        raise ValueError("zeros are uint8 with the shape of scales")
+    if group * kg != K:
+        raise ValueError("the scales' rows do not divide K")
+    nbytes = lib().moe_w4_packed_bytes(N, K)
+    n = nbytes * 2 // group
+    qp = torch.empty(mats, nbytes, dtype=torch.uint8, device=q.device)
+    sp = torch.empty(mats, n, dtype=torch.bfloat16, device=q.device)
+    zp = torch.empty(mats, n, dtype=torch.uint8, device=q.device) if zeros is not None else None
+    _check("moe_pack_w4", lib().moe_pack_w4(_ptr(q), _ptr(scales), _ptr(zeros), mats, N, K, group, _ptr(qp), _ptr(sp),
+                                            _ptr(zp), _stream(stream)))
+    return W4Packed(qp, sp, zp, mats, N, K, group)
+
+
+def _zeroed(nbytes, device):
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+
+
+def moe_linear_w4_workspace(T, N, K, device="cuda"):
+    """A workspace for moe_linear_w4 (zeroed once here; each call leaves its counters zero)."""
+    nbytes = lib().moe_linear_w4_workspace_bytes(T, N, K)
+    if nbytes == 0:
+        raise MoeError("moe_linear_w4_workspace_bytes", 1)
+    return _zeroed(nbytes, device)
+
+
+def moe_linear_w4(x, w, bias=None, out=None, out_dtype=torch.bfloat16, ws=None, stream=None):
+    """x BF16 [T, K] (rows may be strided), w a W4Packed matrix -> out [T, N] = x w^T (+ bias float32
+    [N]) in BF16 or float32.  ws: a workspace kept from moe_linear_w4_workspace (made here
+    otherwise); calls that may overlap need one each."""
+    assert x.is_cuda and x.dim() == 2 and x.stride(1) == 1 and x.dtype == torch.bfloat16, "x is BF16 [T, K] on the GPU"
+    T, K = x.shape
+    assert w.mats == 1 and w.K == K, "w is one matrix with x's K"
+    if out is None:
+        out = torch.empty(T, w.N, dtype=out_dtype, device=x.device)
+    assert out.shape == (T, w.N) and out.stride(1) == 1 and out.dtype in (torch.bfloat16, torch.float32)
+    if ws is None:
+        ws = moe_linear_w4_workspace(T, w.N, K, x.device)
+    _check("moe_linear_w4", lib().moe_linear_w4(
+        x.data_ptr(), T, K, x.stride(0) if T > 1 else K, w.q.data_ptr(), w.scales.data_ptr(), _ptr(w.zeros), w.N,
+        w.group, _ptr(bias), out.data_ptr(), int(out.dtype == torch.float32), out.stride(0) if T > 1 else w.N,
+        ws.data_ptr(), ws.numel(), _stream(stream)))
+    return out
+
+
+def moe_route_hidden_workspace(T=None, E=None, device="cuda"):
+    """A workspace for moe_route_hidden (zeroed once here)."""
+    return _zeroed(lib().moe_route_hidden_workspace_bytes(), device)
+
+
+def moe_route_hidden(x, w_router, K, bias=None, num_tokens=None, logits=None, topk_idx=None, topk_w=None, ws=None,
+                     stream=None):
+    """The router from hidden states: x BF16 [T, H], w_router BF16 [E, H] -> (topk_idx int32 [T, K],
+    topk_w float32 [T, K], logits float32 [T, E])."""
+    _dev(x)
+    _dev(w_router)
+    assert x.dtype == torch.bfloat16 and w_router.dtype == torch.bfloat16
+    T, H = x.shape
+    E = w_router.shape[0]
+    if logits is None:
+        logits = torch.empty(T, E, dtype=torch.float32, device=x.device)
+    if topk_idx is None:
+        topk_idx = torch.empty(T, K, dtype=torch.int32, device=x.device)
+    if topk_w is None:
+        topk_w = torch.empty(T, K, dtype=torch.float32, device=x.device)
+    if ws is None:
+        ws = moe_route_hidden_workspace(device=x.device)
+    _check("moe_route_hidden", lib().moe_route_hidden(
+        x.data_ptr(), T, H, w_router.data_ptr(), _ptr(bias), E, K, _ptr(num_tokens), logits.data_ptr(),
+        topk_idx.data_ptr(), topk_w.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
+    return topk_idx, topk_w, logits
+
+
+class MoeLayerFew:
+    """The layer for up to T tokens (T <= MOE_FEW_MAX_TOKENS) in one launch: moe_layer_few with the
+    weight pointers, descriptor and workspace of one model layer.  Weights as MoeLayer's: BF16
+    or E4M3 tensors (weight_tiles=True: already in the layout of moe_pack_weights, as
+    MoeLayer.tensors holds them), or W4Packed for MOE_W4 (scales and zeros inside, or
+    given apart).  w_router [E, H] (+ router_bias [E]): forward routes by itself."""
+
+    def __init__(self, T, H, I, E, K, dtype=MOE_BF16, w13=None, w2=None, shared_w13=None, shared_w2=None,
+                 w13_scales=None, w2_scales=None, shared_w13_scales=None, shared_w2_scales=None, w_router=None,
+                 router_bias=None, weight_tiles=False, device="cuda"):
+        group = w13.group if dtype == MOE_W4 else 0
+        if dtype == MOE_W4:
+            for m, n, k in ((w13, 2 * I, H), (w2, H, I), (shared_w13, 2 * I, H), (shared_w2, H, I)):
+                if m is not None and (m.N, m.K, m.group) != (n, k, group):
+                    raise ValueError("a packed matrix has another shape or group than the layer")
+        self.desc = FewDesc(T, H, I, E, K, dtype, int(shared_w13 is not None), int(weight_tiles), group)
+        parts = []
+        for m, s in ((w13, w13_scales), (w2, w2_scales), (shared_w13, shared_w13_scales),
+                     (shared_w2, shared_w2_scales)):
+            parts += [m.q, m.scales, m.zeros] if isinstance(m, W4Packed) else [m, s, None]
+        self.tensors = parts + [w_router, router_bias]
+        self.weights = FewWeights(*(_ptr(t) for t in self.tensors))
+        nbytes = lib().moe_layer_few_workspace_bytes(ctypes.byref(self.desc))
+        if nbytes == 0:
+            raise MoeError("moe_layer_few_workspace_bytes", 1)
+        self.ws = _zeroed(nbytes, device)
+        self.max_tokens = T
+        self._descs = {T: self.desc}
+
+    def forward(self, x, out=None, topk_idx=None, topk_w=None, logits=None, num_tokens=None, dev_status=None,
+                stream=None):
+        """x BF16 [t, H], t <= T -> (out [t, H], topk_idx, topk_w).  topk_idx / topk_w are inputs
+        unless the layer routes (w_router, or logits [t, E])."""
+        _dev(x)
+        t, H = x.shape
+        d = self._descs.get(t)
+        if d is None:
+            if t > self.max_tokens:
+                raise ValueError("more tokens than the layer was made for")
+            d = self._descs[t] = FewDesc(t, *(getattr(self.desc, f) for f, _ in FewDesc._fields_[1:]))
+        assert x.dtype == torch.bfloat16 and H == d.H
+        if out is None:
+            out = torch.empty_like(x)
+        if topk_idx is None:
+            if self.weights.w_router is None and logits is None:
+                raise ValueError("topk_idx and topk_w are needed: the layer has no router and no logits")
+            topk_idx = torch.empty(t, d.K, dtype=torch.int32, device=x.device)
+            topk_w = torch.empty(t, d.K, dtype=torch.float32, device=x.device)
+        _check("moe_layer_few", lib().moe_layer_few(
+            ctypes.byref(d), ctypes.byref(self.weights), x.data_ptr(), _ptr(logits), _ptr(num_tokens),
+            topk_idx.data_ptr(), topk_w.data_ptr(), out.data_ptr(), self.ws.data_ptr(), self.ws.numel(),
+            _ptr(dev_status), _stream(stream)))
+        return out, topk_idx, topk_w

@@ -1,0 +1,114 @@
+// Host side of moe_layer_few: workspace, argument checks, choice of the weight format's kernel.
+#include "few_layer.cuh"
+
+namespace moe {
+namespace few {
+
+struct FewPlan {
+  size_t off_part_count, off_tile_count, off_logits, off_hhi, off_hlo, off_y, off_part, total, zeroed;
+};
+
+inline bool plan_few(const moe_few_desc_t* d, FewPlan* p) {
+  if (!d) return false;
+  if (d->T < 0 || d->T > kMaxTokens || d->H <= 0 || d->I <= 0 || d->H % 128 || d->I % 128 || d->E < 1 ||
+      d->E > kMaxExperts || d->K < 1 || d->K > d->E || d->K > kMaxTopK || (d->has_shared != 0 && d->has_shared != 1) ||
+      (d->weight_tiles != 0 && d->weight_tiles != 1))
+    return false;
+  if (d->dtype != MOE_BF16 && d->dtype != MOE_E4M3 && d->dtype != MOE_W4) return false;
+  if (d->dtype == MOE_W4 ? (d->group != 32 && d->group != 64 && d->group != 128) || d->weight_tiles : d->group != 0)
+    return false;
+  const size_t slots = (size_t)d->T * d->K + d->T;
+  const size_t workers = (size_t)num_sms() * WARPS;
+  size_t o = 256;                                                       // barrier words
+  p->off_part_count = o; o = align256(o + 4 * workers);
+  p->off_tile_count = o; o = align256(o + 4 * (size_t)(d->H / 32));
+  p->zeroed = o;
+  p->off_logits = o;     o = align256(o + 4 * (size_t)d->T * d->E);
+  p->off_hhi = o;        o = align256(o + 2 * slots * d->I);
+  p->off_hlo = o;        o = align256(o + 2 * slots * d->I);
+  p->off_y = o;          o = align256(o + 4 * slots * d->H);
+  p->off_part = o;       o = align256(o + workers * 2 * PART_FLOATS * 4);
+  p->total = o;
+  return true;
+}
+
+}  // namespace few
+}  // namespace moe
+
+extern "C" size_t moe_layer_few_workspace_bytes(const moe_few_desc_t* d) {
+  moe::few::FewPlan p;
+  return moe::few::plan_few(d, &p) ? p.total : 0;
+}
+
+extern "C" moe_status_t moe_layer_few(const moe_few_desc_t* d, const moe_few_weights_t* w, const uint16_t* x,
+                                      const float* logits, const int32_t* num_tokens, int32_t* topk_idx,
+                                      float* topk_w, uint16_t* out, void* ws, size_t ws_bytes, int32_t* dev_status,
+                                      void* stream) {
+  using namespace moe;
+  using namespace moe::few;
+  FewPlan p;
+  if (!plan_few(d, &p) || !w) return MOE_ERR_ARG;
+  if (!ws || ws_bytes < p.total) return MOE_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(ws) & 255) return MOE_ERR_ARG;
+  if (d->T == 0) return MOE_OK;
+  if (!x || !topk_idx || !topk_w || !out || !w->w13 || !w->w2) return MOE_ERR_ARG;
+  if (w->w_router && logits) return MOE_ERR_ARG;          // one source of the routing
+  if (d->dtype != MOE_BF16 && (!w->w13_scales || !w->w2_scales)) return MOE_ERR_ARG;
+  const bool zeros = w->w13_zeros != nullptr;
+  if (zeros != (w->w2_zeros != nullptr) || (zeros && d->dtype != MOE_W4)) return MOE_ERR_ARG;
+  if (d->has_shared) {
+    if (!w->shared_w13 || !w->shared_w2) return MOE_ERR_ARG;
+    if (d->dtype != MOE_BF16 && (!w->shared_w13_scales || !w->shared_w2_scales)) return MOE_ERR_ARG;
+    if (zeros != (w->shared_w13_zeros != nullptr) || zeros != (w->shared_w2_zeros != nullptr)) return MOE_ERR_ARG;
+  }
+  const void* al16[] = {x, w->w_router};
+  for (const void* q : al16)
+    if (reinterpret_cast<uintptr_t>(q) & 15) return MOE_ERR_ARG;
+  const void* al32[] = {w->w13, w->w2, d->has_shared ? w->shared_w13 : nullptr, d->has_shared ? w->shared_w2 : nullptr};
+  for (const void* q : al32)
+    if (reinterpret_cast<uintptr_t>(q) & 31) return MOE_ERR_ARG;
+  if (d->dtype == MOE_W4) {
+    const void* al[] = {w->w13_scales, w->w2_scales, w->w13_zeros, w->w2_zeros,
+                        d->has_shared ? w->shared_w13_scales : nullptr, d->has_shared ? w->shared_w2_scales : nullptr,
+                        d->has_shared ? w->shared_w13_zeros : nullptr, d->has_shared ? w->shared_w2_zeros : nullptr};
+    for (const void* q : al)
+      if (reinterpret_cast<uintptr_t>(q) & 15) return MOE_ERR_ARG;
+  }
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  LayerArgs a;
+  a.T = d->T; a.H = d->H; a.I = d->I; a.E = d->E; a.K = d->K;
+  a.shared = d->has_shared;
+  a.tiled = d->weight_tiles;
+  a.w13 = static_cast<const uint8_t*>(w->w13);
+  a.w2 = static_cast<const uint8_t*>(w->w2);
+  a.sw13 = static_cast<const uint8_t*>(w->shared_w13);
+  a.sw2 = static_cast<const uint8_t*>(w->shared_w2);
+  a.w13_s = w->w13_scales; a.w2_s = w->w2_scales; a.sw13_s = w->shared_w13_scales; a.sw2_s = w->shared_w2_scales;
+  a.w13_z = w->w13_zeros; a.w2_z = w->w2_zeros; a.sw13_z = w->shared_w13_zeros; a.sw2_z = w->shared_w2_zeros;
+  a.w_router = w->w_router;
+  a.router_bias = w->router_bias;
+  a.logits_in = logits;
+  a.num_tokens = num_tokens;
+  a.logits = reinterpret_cast<float*>(b + p.off_logits);
+  a.topk_idx = topk_idx;
+  a.topk_w = topk_w;
+  a.x = x;
+  a.out = out;
+  a.dev_status = dev_status;
+  a.bar = reinterpret_cast<uint32_t*>(b);
+  a.part_count = reinterpret_cast<int32_t*>(b + p.off_part_count);
+  a.tile_count = reinterpret_cast<int32_t*>(b + p.off_tile_count);
+  a.h_hi = reinterpret_cast<uint16_t*>(b + p.off_hhi);
+  a.h_lo = reinterpret_cast<uint16_t*>(b + p.off_hlo);
+  a.y = reinterpret_cast<float*>(b + p.off_y);
+  a.part = reinterpret_cast<float*>(b + p.off_part);
+  cudaStream_t st = as_stream(stream);
+  const cudaError_t e = d->dtype == MOE_BF16   ? launch_layer_bf16(a, st)
+                        : d->dtype == MOE_E4M3 ? launch_layer_e4m3(a, st)
+                                               : launch_layer_w4(a, d->group, st);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
+}

@@ -1,0 +1,320 @@
+// moe_linear_w4: y = x W^T (+ bias) for a few rows of BF16 x and 4-bit weights with a BF16
+// scale (and optionally a zero point) per group of 32, 64 or 128 columns.  The weight
+// stream, the work division and the arithmetic are those of few.cuh, with one matrix and the
+// rows of x as columns, 32 at a time (each pass over the weights serves 32 rows of x).
+//
+// Also the one-time preparation of such weights: moe_quantize_weight_w4 and moe_pack_w4.
+#include "few.cuh"
+
+namespace moe {
+namespace few {
+
+constexpr int LIN_COLS = 32;
+
+struct LinearArgs {
+  const uint16_t* x;
+  long long x_stride, out_stride;
+  int T, N;
+  const uint8_t* q;
+  const void *scales, *zeros;
+  const float* bias;
+  void* out;
+  int out_f32;
+  int32_t* part_count;
+  float* part;
+  Strides st;
+  int tiles;
+  long long F;
+  int W;
+};
+
+template <int GROUP>
+__device__ __forceinline__ Tile linear_tile(const LinearArgs& a, int tile, int s0, int n, int lane) {
+  Tile r;
+  r.s0 = s0;
+  r.n = n;
+  const long long blk = (long long)tile * 2 * a.st.nsl + s0;
+  constexpr int NG = Item<F_W4, GROUP>::NG;
+  r.w = a.q + blk * 2048 + lane * 32;
+  r.sc = static_cast<const uint32_t*>(a.scales) + (blk * 8 + (lane >> 2)) * NG;
+  r.zp = a.zeros ? static_cast<const uint16_t*>(a.zeros) + (blk * 8 + (lane >> 2)) * NG : nullptr;
+  return r;
+}
+
+template <int GROUP, int NT>
+__device__ __forceinline__ void linear_do_tile(const LinearArgs& a, Item<F_W4, GROUP>& it, const Tile& cur,
+                                               const Tile& next, int t0, int tile, long long f, int me, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  const uint16_t* x[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) x[n] = t0 + n * 8 + g < a.T ? a.x + (t0 + n * 8 + g) * a.x_stride : nullptr;
+  Sums<NT> sums;
+  run_tile<F_W4, GROUP, NT>(sums, it, cur, next, a.st, x, t);
+  if (cur.n < a.st.nsl) {
+    const long long a0 = f - cur.s0;
+    const int w0 = worker_of(a0, a.F, a.W), w1 = worker_of(a0 + a.st.nsl - 1, a.F, a.W);
+    if (!join_parts<NT>(sums, a.part, a.part_count, me, cur.s0 == 0 ? 1 : 0, w0, w1, lane)) return;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = tile * 32 + h * 16 + (i >> 1) * 8 + g;
+      if (row >= a.N) continue;
+      const float b = a.bias ? __ldg(a.bias + row) : 0.0f;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int c = t0 + n * 8 + 2 * t + (i & 1);
+        if (c >= a.T) continue;
+        const float v = a.bias ? sums.v[n][h][i] + b : sums.v[n][h][i];
+        const long long o = c * a.out_stride + row;
+        if (a.out_f32)
+          static_cast<float*>(a.out)[o] = v;
+        else
+          static_cast<uint16_t*>(a.out)[o] = f32_to_bf16(v);
+      }
+    }
+}
+
+template <int GROUP>
+__global__ void __launch_bounds__(THREADS, 1) linear_w4_kernel(const LinearArgs a) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int me = my_worker(a.W, blockIdx.x, gridDim.x, warp);
+  if (me < 0) return;
+  long long f = run_start(a.F, me, a.W);
+  const long long f1 = run_start(a.F, me + 1, a.W);
+  const long long q = f / a.st.nsl;
+  int s0 = (int)(f - q * a.st.nsl);
+  int blk = (int)(q / a.tiles), tile = (int)(q - (long long)blk * a.tiles);
+  Tile cur = linear_tile<GROUP>(a, tile, s0, (int)min((long long)(a.st.nsl - s0), f1 - f), lane);
+  Item<F_W4, GROUP> it;
+  it.load(cur.w, cur.sc, cur.zp, a.st);
+  while (true) {
+    const long long fn = f + cur.n;
+    Tile next;
+    next.n = 0;
+    int tile_n = tile, blk_n = blk;
+    if (fn < f1) {
+      if (++tile_n == a.tiles) { tile_n = 0; ++blk_n; }
+      next = linear_tile<GROUP>(a, tile_n, 0, (int)min((long long)a.st.nsl, f1 - fn), lane);
+    }
+    const int t0 = blk * LIN_COLS, nc = a.T - t0;
+    if (nc <= 8) linear_do_tile<GROUP, 1>(a, it, cur, next, t0, tile, f, me, lane);
+    else if (nc <= 16) linear_do_tile<GROUP, 2>(a, it, cur, next, t0, tile, f, me, lane);
+    else linear_do_tile<GROUP, 4>(a, it, cur, next, t0, tile, f, me, lane);
+    if (next.n == 0) return;
+    f = fn;
+    cur = next;
+    tile = tile_n;
+    blk = blk_n;
+  }
+}
+
+// ------------------------------------------------------------------- weight preparation
+// One thread per group of one row: scale (and zero point), then the codes, two per byte.
+//   symmetric   s = bf16(amax / 7), code = clamp(rn(w / s), -8, 7) + 8
+//   zero points lo = min(0, min w), hi = max(0, max w), s = bf16((hi - lo) / 15),
+//               z = clamp(rn(-lo / s), 0, 15), code = clamp(rn(w / s) + z, 0, 15)
+// s = 1 where that is not positive; IEEE float32 divisions, halves to even.
+__global__ void __launch_bounds__(256) quant_w4_kernel(const uint16_t* __restrict__ w, long long groups, int rows,
+                                                       int cols, int group, uint8_t* __restrict__ q,
+                                                       uint16_t* __restrict__ scales, uint8_t* __restrict__ zeros) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= groups) return;
+  const int per_row = cols / group;
+  const long long mr = i / per_row;            // matrix * rows + row
+  const int gi = (int)(i - mr * per_row);
+  const long long m = mr / rows;
+  const int r = (int)(mr - m * rows);
+  const uint16_t* src = w + mr * cols + (long long)gi * group;
+  float lo = 0.0f, hi = 0.0f;
+  for (int c = 0; c < group; ++c) {
+    const float v = bf16_to_f32(src[c]);
+    lo = fminf(lo, v);
+    hi = fmaxf(hi, v);
+  }
+  const float raw = zeros ? __fdiv_rn(__fsub_rn(hi, lo), 15.0f) : __fdiv_rn(fmaxf(hi, -lo), 7.0f);
+  uint16_t sb = f32_to_bf16(raw);
+  if (!(bf16_to_f32(sb) > 0.0f)) sb = 0x3f80;
+  const float s = bf16_to_f32(sb);
+  const float z = zeros ? fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.0f), 15.0f) : 8.0f;
+  uint8_t* dst = q + (mr * cols + (long long)gi * group) / 2;
+  for (int c = 0; c < group; c += 2) {
+    uint32_t b = 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float v = rintf(__fdiv_rn(bf16_to_f32(src[c + j]), s)) + z;
+      b |= (uint32_t)fminf(fmaxf(v, 0.0f), 15.0f) << (4 * j);
+    }
+    dst[c / 2] = (uint8_t)b;
+  }
+  const long long o = (m * per_row + gi) * rows + r;
+  scales[o] = sb;
+  if (zeros) zeros[o] = (uint8_t)z;
+}
+
+// One warp per (matrix, 16-row block, 256-column slice): lane (g, t) writes the 32 bytes it will
+// load for row g and for row g + 8; rows past N and columns past K are code 0 with scale 0.
+__global__ void __launch_bounds__(256) pack_w4_kernel(const uint8_t* __restrict__ q, const uint16_t* __restrict__ sc,
+                                                      const uint8_t* __restrict__ zp, long long blocks, int N, int K,
+                                                      int group, uint8_t* __restrict__ oq, uint32_t* __restrict__ osc,
+                                                      uint16_t* __restrict__ ozp) {
+  const long long blk = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (blk >= blocks) return;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int nsl = (int)w4_slices(K), nrb = (int)ceil_div(N, 32) * 2;
+  const int s = (int)(blk % nsl);
+  const long long mrb = blk / nsl;
+  const int rb = (int)(mrb % nrb);
+  const long long m = mrb / nrb;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int row = rb * 16 + h * 8 + g;
+    uint32_t out[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int k = s * 256 + j * 32 + t * 8;
+      uint32_t v = 0;
+      if (row < N && k < K) {
+        const uint32_t u = *reinterpret_cast<const uint32_t*>(q + ((m * N + row) * K + k) / 2);
+        // even columns to nibbles 0-3, odd ones to nibbles 4-7
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v |= ((u >> (8 * i)) & 15u) << (4 * i) | ((u >> (8 * i + 4)) & 15u) << (4 * i + 16);
+      }
+      out[j] = v;
+    }
+    uint4* d = reinterpret_cast<uint4*>(oq + blk * 2048 + h * 1024 + lane * 32);
+    d[0] = make_uint4(out[0], out[1], out[2], out[3]);
+    d[1] = make_uint4(out[4], out[5], out[6], out[7]);
+  }
+  const int ng = 256 / group, kg = K / group;
+  for (int i = lane; i < 8 * ng; i += 32) {
+    const int gg = i / ng, gi = i % ng, kgi = s * ng + gi;
+    uint32_t sv = 0, zv = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = rb * 16 + h * 8 + gg;
+      if (row < N && kgi < kg) {
+        const long long o = (m * kg + kgi) * N + row;
+        sv |= (uint32_t)sc[o] << (16 * h);
+        if (zp) zv |= (uint32_t)(zp[o] & 15) << (8 * h);
+      }
+    }
+    osc[(blk * 8 + gg) * ng + gi] = sv;
+    if (zp) ozp[(blk * 8 + gg) * ng + gi] = (uint16_t)zv;
+  }
+}
+
+inline bool w4_shape_ok(int mats, int N, int K, int group) {
+  return mats >= 0 && N > 0 && K > 0 && (group == 32 || group == 64 || group == 128) && K % 128 == 0 &&
+         N <= (1 << 24) && K <= (1 << 24);
+}
+inline uintptr_t bits_of(const void* p) { return reinterpret_cast<uintptr_t>(p); }
+
+}  // namespace few
+}  // namespace moe
+
+extern "C" moe_status_t moe_quantize_weight_w4(const uint16_t* w, int mats, int rows, int cols, int group, uint8_t* q,
+                                               uint16_t* scales, uint8_t* zeros, void* stream) {
+  using namespace moe;
+  using namespace moe::few;
+  if (!w4_shape_ok(mats, rows, cols, group)) return MOE_ERR_ARG;
+  if (mats == 0) return MOE_OK;
+  if (!w || !q || !scales) return MOE_ERR_ARG;
+  const long long groups = (long long)mats * rows * (cols / group);
+  if (ceil_div(groups, 256) > 0x7fffffffll) return MOE_ERR_ARG;
+  quant_w4_kernel<<<(unsigned)ceil_div(groups, 256), 256, 0, as_stream(stream)>>>(w, groups, rows, cols, group, q,
+                                                                                  scales, zeros);
+  MOE_CHECK_LAUNCH();
+  return MOE_OK;
+}
+
+extern "C" size_t moe_w4_packed_bytes(int N, int K) {
+  using namespace moe::few;
+  if (!w4_shape_ok(0, N, K, 32)) return 0;
+  // whole 32-row tiles, so that the last tile's second half is there to be read
+  return (size_t)(ceil_div(N, 32) * 2 * w4_slices(K) * 2048);
+}
+
+extern "C" moe_status_t moe_pack_w4(const uint8_t* q, const uint16_t* scales, const uint8_t* zeros, int mats, int N,
+                                    int K, int group, uint8_t* q_packed, uint16_t* scales_packed,
+                                    uint8_t* zeros_packed, void* stream) {
+  using namespace moe;
+  using namespace moe::few;
+  if (!w4_shape_ok(mats, N, K, group)) return MOE_ERR_ARG;
+  if (mats == 0) return MOE_OK;
+  if (!q || !scales || !q_packed || !scales_packed || (zeros != nullptr) != (zeros_packed != nullptr))
+    return MOE_ERR_ARG;
+  if ((bits_of(q) & 3) || (bits_of(q_packed) & 31) || (bits_of(scales_packed) & 15) || (bits_of(zeros_packed) & 15))
+    return MOE_ERR_ARG;
+  const size_t in = (size_t)mats * N * K / 2, outb = (size_t)mats * moe_w4_packed_bytes(N, K);
+  if (bits_of(q) < bits_of(q_packed) + outb && bits_of(q_packed) < bits_of(q) + in) return MOE_ERR_ARG;   // overlap
+  if (mats > 1 && N % 32) return MOE_ERR_ARG;     // a stack of matrices is addressed by whole tiles
+  const long long blocks = (long long)(outb / 2048);
+  if (ceil_div(blocks, 8) > 0x7fffffffll) return MOE_ERR_ARG;
+  pack_w4_kernel<<<(unsigned)ceil_div(blocks, 8), 256, 0, as_stream(stream)>>>(
+      q, scales, zeros, blocks, N, K, group, q_packed, reinterpret_cast<uint32_t*>(scales_packed),
+      reinterpret_cast<uint16_t*>(zeros_packed));
+  MOE_CHECK_LAUNCH();
+  return MOE_OK;
+}
+
+extern "C" size_t moe_linear_w4_workspace_bytes(int T, int N, int K) {
+  using namespace moe;
+  using namespace moe::few;
+  if (T < 0 || !w4_shape_ok(0, N, K, 32)) return 0;
+  const size_t workers = (size_t)num_sms() * WARPS;
+  return align256(4 * workers) + workers * 2 * PART_FLOATS * 4;
+}
+
+extern "C" moe_status_t moe_linear_w4(const uint16_t* x, int T, int K, long long x_stride, const uint8_t* q_packed,
+                                      const uint16_t* scales_packed, const uint8_t* zeros_packed, int N, int group,
+                                      const float* bias, void* out, int out_f32, long long out_stride, void* ws,
+                                      size_t ws_bytes, void* stream) {
+  using namespace moe;
+  using namespace moe::few;
+  if (T < 0 || !w4_shape_ok(0, N, K, group) || x_stride < K || x_stride % 8 || out_stride < N ||
+      (out_f32 != 0 && out_f32 != 1))
+    return MOE_ERR_ARG;
+  if (!ws || ws_bytes < moe_linear_w4_workspace_bytes(T, N, K)) return MOE_ERR_WORKSPACE;
+  if (bits_of(ws) & 255) return MOE_ERR_ARG;
+  if (T == 0) return MOE_OK;
+  if (!x || !q_packed || !scales_packed || !out) return MOE_ERR_ARG;
+  if ((bits_of(x) & 15) || (bits_of(q_packed) & 31) || (bits_of(scales_packed) & 15) || (bits_of(zeros_packed) & 15) ||
+      (bits_of(out) & (out_f32 ? 3 : 1)) || (bits_of(bias) & 3))
+    return MOE_ERR_ARG;
+  LinearArgs a;
+  a.x = x;
+  a.x_stride = x_stride;
+  a.out_stride = out_stride;
+  a.T = T;
+  a.N = N;
+  a.q = q_packed;
+  a.scales = scales_packed;
+  a.zeros = zeros_packed;
+  a.bias = bias;
+  a.out = out;
+  a.out_f32 = out_f32;
+  a.part_count = static_cast<int32_t*>(ws);
+  const int ctas = num_sms();
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align256(4 * (size_t)ctas * WARPS));
+  a.st.k = K;
+  a.st.nsl = (int)w4_slices(K);
+  a.st.step = 2048;
+  a.st.row8 = 1024;
+  a.st.half = (long long)a.st.nsl * 2048;
+  a.st.sc_half = (long long)a.st.nsl * 8 * (256 / group);
+  a.tiles = (int)ceil_div(N, 32);
+  a.F = ceil_div(T, LIN_COLS) * a.tiles * a.st.nsl;
+  a.W = workers_for(a.F, ctas * WARPS, 1);
+  cudaStream_t st = as_stream(stream);
+  if (group == 32)
+    linear_w4_kernel<32><<<ctas, THREADS, 0, st>>>(a);
+  else if (group == 64)
+    linear_w4_kernel<64><<<ctas, THREADS, 0, st>>>(a);
+  else
+    linear_w4_kernel<128><<<ctas, THREADS, 0, st>>>(a);
+  MOE_CHECK_LAUNCH();
+  return MOE_OK;
+}

@@ -46,7 +46,8 @@ typedef enum {
   MOE_ERR_CUDA = 4          /* a CUDA runtime call or launch failed */
 } moe_status_t;
 
-typedef enum { MOE_BF16 = 0, MOE_E4M3 = 1 } moe_dtype_t;
+/* MOE_W4: 4-bit codes with group scales, only for the few-token calls (moe_layer_few). */
+typedef enum { MOE_BF16 = 0, MOE_E4M3 = 1, MOE_W4 = 2 } moe_dtype_t;
 /* ORed into the dtype argument of moe_grouped_gemm, _ex, _batched and _combine: w and
  * w_extra are in the tile layout of moe_pack_weights (ABI 6). */
 #define MOE_W_TILED 0x100
@@ -487,6 +488,123 @@ moe_status_t moe_layer_forward(const moe_layer_desc_t* d, const moe_layer_weight
                                float* topk_w, const uint16_t* x, const float* fq_scale,
                                const float* dispatch_scale, uint16_t* out, void* ws, size_t ws_bytes,
                                int32_t* dev_status, void* stream);
+
+/* ======================================================================================
+ * A few tokens: decode steps of 1 to 32 tokens.  (The pages have no counterpart: these are
+ * additions of this library.)  The calls above move rows between eight kernels made for
+ * many rows per expert; with a handful of tokens an expert meets one or two rows and the
+ * time is reading its weights once, plus launches.  The calls below are one launch each.
+ * Their workspaces hold counters that have to be zero when a workspace is first used; every
+ * call leaves them zero (after a MOE_DEV_PIPELINE_TIMEOUT the caller zeroes them again).
+ * Two calls that may overlap on the GPU need workspaces of their own. */
+#define MOE_FEW_MAX_TOKENS 32
+
+/* ------------------------------------------------------------------- 4-bit weights (W4)
+ * value(n, k) = (code(n, k) - zero(k / group, n)) * scale(k / group, n), codes 0..15,
+ * group 32, 64 or 128; zero is 8 everywhere when there is no zero tensor.
+ *
+ * moe_quantize_weight_w4: BF16 w [mats, rows, cols] -> codes q [mats, rows, cols/2] (column 2i
+ * in the low nibble of byte i), scales BF16 [mats, cols/group, rows], zeros (nullable) uint8
+ * [mats, cols/group, rows].
+ *   symmetric (zeros NULL): s = bf16_rn(amax / 7), code = clamp(rn(w / s), -8, 7) + 8;
+ *   zero points: lo = min(0, min w), hi = max(0, max w), s = bf16_rn((hi - lo) / 15),
+ *                z = clamp(rn(-lo / s), 0, 15), code = clamp(rn(w / s) + z, 0, 15);
+ *   s is 1 where that is not positive; IEEE float32 steps, ties to even; w finite.
+ * moe_pack_w4: the same values in the order the kernels read them, once per model:
+ *   q_packed      mats * moe_w4_packed_bytes(N, K) bytes, 32-byte aligned;
+ *   scales_packed mats * moe_w4_packed_bytes(N, K) * 2 / group elements (two bytes each), and
+ *   zeros_packed  as many single bytes, both 16-byte aligned.
+ *   Blocks of 16 rows x 256 columns, row block major, whole pairs of row blocks and whole
+ *   slices of 256 columns (the padding has scale 0).  zeros and zeros_packed: both or neither.
+ * K (cols) % 128 == 0, N and K at most 2^24; N % 32 == 0 when mats > 1.
+ * Errors: MOE_ERR_ARG for sizes, null pointers, alignment, overlapping q and q_packed. */
+moe_status_t moe_quantize_weight_w4(const uint16_t* w, int mats, int rows, int cols, int group, uint8_t* q,
+                                    uint16_t* scales, uint8_t* zeros, void* stream);
+size_t moe_w4_packed_bytes(int N, int K);
+moe_status_t moe_pack_w4(const uint8_t* q, const uint16_t* scales, const uint8_t* zeros, int mats, int N, int K,
+                         int group, uint8_t* q_packed, uint16_t* scales_packed, uint8_t* zeros_packed, void* stream);
+
+/* out[t, n] = sum_k x[t, k] * value(n, k) (+ bias[n]), BF16 products, float32 sums, one
+ * rounding.  Made for few rows: every 32 rows of x read the weights again.
+ *   x          BF16 [T, K], row t at x + t * x_stride (elements, a multiple of 8, >= K),
+ *              16-byte aligned.
+ *   q_packed, scales_packed, zeros_packed (nullable)  one matrix from moe_pack_w4.
+ *   bias       nullable float32 [N].
+ *   out        BF16 (out_f32 = 0) or float32 (1) [T, N], row t at out + t * out_stride (>= N).
+ *   ws         moe_linear_w4_workspace_bytes(T, N, K) bytes, 256-byte aligned, zero at first use.
+ * Any N >= 1 (mats = 1), K % 128 == 0.  The result does not depend on timing.
+ * Errors: MOE_ERR_ARG, MOE_ERR_WORKSPACE. */
+size_t moe_linear_w4_workspace_bytes(int T, int N, int K);
+moe_status_t moe_linear_w4(const uint16_t* x, int T, int K, long long x_stride, const uint8_t* q_packed,
+                           const uint16_t* scales_packed, const uint8_t* zeros_packed, int N, int group,
+                           const float* bias, void* out, int out_f32, long long out_stride, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/* The router from hidden states, T <= MOE_FEW_MAX_TOKENS:
+ *   logits[t, e] = float32(sum_h x[t, h] * w_router[e, h] + bias[e]), the sum carried to about
+ *   48 bits before its one rounding, so which expert wins a near tie does not hang on the
+ *   order of the sum; then the selection and weights of moe_route_topk.
+ *   x BF16 [T, H], w_router BF16 [E, H] (both 16-byte aligned), bias nullable float32 [E],
+ *   logits out float32 [T, E]; num_tokens, topk_idx, topk_w as moe_route_topk (the logits of
+ *   rows past num_tokens are written too).
+ *   ws         moe_route_hidden_workspace_bytes() bytes, 256-byte aligned, zero at first use.
+ * H % 128 == 0; E, K as moe_route_topk.  Errors: MOE_ERR_ARG, MOE_ERR_WORKSPACE. */
+size_t moe_route_hidden_workspace_bytes(void);
+moe_status_t moe_route_hidden(const uint16_t* x, int T, int H, const uint16_t* w_router, const float* bias, int E,
+                              int K, const int32_t* num_tokens, float* logits, int32_t* topk_idx, float* topk_w,
+                              void* ws, size_t ws_bytes, void* stream);
+
+/* The whole layer for T <= MOE_FEW_MAX_TOKENS tokens in one cooperative launch: (router ->)
+ * gate/up + SwiGLU -> down -> combine.  It computes moe_layer_forward's layer with fewer
+ * roundings: activations stay BF16 with every weight format (no FP8 activations), h is kept
+ * to 16 bits of mantissa and the expert rows in float32, so
+ *     out[t] = bf16_rn( sum over ascending k of w_tk * (W2_e silu(g) u), float32 from +0,
+ *                       the shared expert's row last )
+ * and a token with no valid slot gets +0 and no shared row.  The result does not depend on
+ * timing.  Not offered here: fake-quantisation, router weights in the down projection. */
+typedef struct {
+  int T;              /* tokens of the call, 0..MOE_FEW_MAX_TOKENS */
+  int H, I, E, K;     /* as moe_layer_desc_t */
+  moe_dtype_t dtype;  /* MOE_BF16; MOE_E4M3 (weights with 128x128 scales); MOE_W4 (packed) */
+  int has_shared;     /* 1: one shared expert of the same I and format */
+  int weight_tiles;   /* 1: BF16 / E4M3 weights in the tile layout of moe_pack_weights */
+  int group;          /* MOE_W4: 32, 64 or 128; else 0 */
+} moe_few_desc_t;
+
+typedef struct {
+  const void* w13;         /* [E, 2I, H] gate rows then up rows, 32-byte aligned; W4: packed */
+  const void* w13_scales;  /* E4M3: float32 [E, 2I/128, H/128]; W4: packed scales */
+  const void* w13_zeros;   /* W4: packed zeros or NULL (for all four matrices or for none) */
+  const void* w2;          /* [E, H, I] */
+  const void* w2_scales;
+  const void* w2_zeros;
+  const void* shared_w13;  /* has_shared: [2I, H] */
+  const void* shared_w13_scales;
+  const void* shared_w13_zeros;
+  const void* shared_w2;   /* has_shared: [H, I] */
+  const void* shared_w2_scales;
+  const void* shared_w2_zeros;
+  const uint16_t* w_router;   /* nullable BF16 [E, H]: route inside the layer (moe_route_hidden) */
+  const float* router_bias;   /* nullable float32 [E] */
+} moe_few_weights_t;
+
+/* Workspace bytes for a layer of this shape (0 for an invalid descriptor). */
+size_t moe_layer_few_workspace_bytes(const moe_few_desc_t* d);
+/*   d, w       host structs (read during the call only).
+ *   x          BF16 [T, H], 16-byte aligned.
+ *   logits     nullable float32 [T, E]: select from these (not with w->w_router).
+ *   num_tokens as moe_route_topk, with w_router or logits.
+ *   topk_idx, topk_w  [T, K]: written when routed here, else inputs (slots -1 are padding; an
+ *              id outside [-1, E) sets MOE_DEV_BAD_EXPERT and counts as padding; a repeated
+ *              id is one more slot).
+ *   out        BF16 [T, H], every row written.
+ *   ws         moe_layer_few_workspace_bytes(d) bytes, 256-byte aligned, zero at first use.
+ *   dev_status nullable; MOE_DEV_BAD_EXPERT, MOE_DEV_PIPELINE_TIMEOUT (a grid barrier gave up).
+ * Errors: MOE_ERR_ARG, MOE_ERR_WORKSPACE; MOE_ERR_CUDA if the launch fails (it needs every SM
+ * of the GPU to itself: one block per SM). */
+moe_status_t moe_layer_few(const moe_few_desc_t* d, const moe_few_weights_t* w, const uint16_t* x,
+                           const float* logits, const int32_t* num_tokens, int32_t* topk_idx, float* topk_w,
+                           uint16_t* out, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
 
 #ifdef __cplusplus
 }
