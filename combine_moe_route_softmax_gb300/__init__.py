@@ -95,7 +95,7 @@ _SIGS = {
     "moe_w4_packed_bytes": ([_I, _I], _Z),
     "moe_pack_w4": ([_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P], _I),
     "moe_linear_w4_workspace_bytes": ([_I, _I, _I], _Z),
-    "moe_linear_w4": ([_P, _I, _I, _L, _P, _P, _P, _I, _I, _P, _P, _I, _L, _P, _Z, _P], _I),
+    "moe_linear_w4": ([_P, _I, _I, _L, _P, _P, _P, _I, _I, _P, _P, _I, _L, _P, _Z, _P, _P], _I),
     "moe_route_hidden_workspace_bytes": ([], _Z),
     "moe_route_hidden": ([_P, _I, _I, _P, _P, _I, _I, _P, _P, _P, _P, _P, _Z, _P], _I),
     "moe_layer_few_workspace_bytes": ([ctypes.POINTER(FewDesc)], _Z),
@@ -539,7 +539,7 @@ def moe_linear_w4_workspace(T, N, K, device="cuda"):
     return _zeroed(nbytes, device)
 
 
-def moe_linear_w4(x, w, bias=None, out=None, out_dtype=torch.bfloat16, ws=None, stream=None):
+def moe_linear_w4(x, w, bias=None, out=None, out_dtype=torch.bfloat16, ws=None, dev_status=None, stream=None):
     """x BF16 [T, K] (rows may be strided), w a W4Packed matrix -> out [T, N] = x w^T (+ bias float32
     [N]) in BF16 or float32.  ws: a workspace kept from moe_linear_w4_workspace (made here
     otherwise); calls that may overlap need one each."""
@@ -554,7 +554,7 @@ def moe_linear_w4(x, w, bias=None, out=None, out_dtype=torch.bfloat16, ws=None, 
     _check("moe_linear_w4", lib().moe_linear_w4(
         x.data_ptr(), T, K, x.stride(0) if T > 1 else K, w.q.data_ptr(), w.scales.data_ptr(), _ptr(w.zeros), w.N,
         w.group, _ptr(bias), out.data_ptr(), int(out.dtype == torch.float32), out.stride(0) if T > 1 else w.N,
-        ws.data_ptr(), ws.numel(), _stream(stream)))
+        ws.data_ptr(), ws.numel(), _ptr(dev_status), _stream(stream)))
     return out
 
 

@@ -1,175 +1,189 @@
-// Weight streaming for products with a few columns (1 to 16 activation rows per weight
+// Weight streaming for products with a few columns (1 to 32 activation rows per weight
 // matrix), shared by the few-token layer (few_layer.cuh) and the 4-bit product
 // (few_linear.cu).  Internal header.
 //
 // The mathematics: y[n, c] = sum_k W[n, k] x[c, k] for a handful of columns c.  Every weight is
 // used a few times only, so the bound is reading W once; the arithmetic rides along on
-// mma.sync.m16n8k16 (BF16 in, float32 sums), weights as the 16-row operand and activation
-// rows as the 8 columns -- 2 to 4 tensor instructions per KB of weights, far below any
+// mma.sync.m16n8k16 (16-bit operands, float32 sums), weights as the 16-row operand and activation
+// rows as the 8 columns -- 2 to 8 tensor instructions per KB of weights, far below any
 // tensor-core limit, which is why these kernels do not use the 128-row tcgen05 tiles.
 //
-// Work is cut into items: 32 weight rows x 128 bytes of K, 4 KB.  The items of a launch
-// phase, in the order (matrix, row tile, K slice) or (row tile, matrix, K slice), are
-// divided evenly over the workers (16 warps per SM), each taking one contiguous run, so every
-// SM reads the same number of bytes whatever the shapes (to one item).  A warp reads an
-// item as four 256-bit loads per lane, each 8 rows x one whole 128-byte line, straight into
-// the registers the tensor instruction takes them from: the K order inside a line is
-// whatever the lanes hold, since a dot product does not care and the activations are read
-// in the same order.  Measured with loads alone, 1.6 GB row-major: 7.0 TB/s so; 5.5 with
-// 128-bit loads (8 rows x 64 bytes); 6.5 without the 256-byte L2 prefetch hint; 5.5 through
-// 16-byte cp.async into shared memory by four warps; 2.1 through 512-byte bulk copies.
-//
-// A row tile whose slices fall to several workers is joined by the one that finishes last:
-// each writes its partial sums, fences and counts; the last adds all parts in worker
-// order, so the result does not depend on who was last.  Nobody waits.
+// Work is cut into items: 32 weight rows (a row tile) x 128 bytes of K, 4 KB; a few neighbouring
+// items of a tile are a unit.  A CTA (one per SM) takes whole tiles, one after the other,
+// and its worker warps take the units of that sequence in turn, each running ahead on its own:
+// a warp copies its items with cp.async into a ring of its own in shared memory, whole
+// 128-byte lines, ahead of their use, across units and tiles.  The K order inside a line is
+// whatever the lanes hold, since a dot product does not care and the activations are read in
+// the same order.  The sums of a tile's units are joined in shared memory by the warp that
+// finishes last, in unit order, so the result does not depend on who was last.
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include "common.cuh"
 
 namespace moe {
 namespace few {
 
-constexpr int WARPS = 16;
-constexpr int THREADS = WARPS * 32;
 constexpr int kMaxTokens = MOE_FEW_MAX_TOKENS;
-constexpr int COLS = 16;             // columns of one matrix handled in one pass over it
-constexpr int PART_FLOATS = 1024;    // one worker's partial sums: 32 rows x 32 columns
+constexpr int COLS = 16;             // columns of one matrix handled in one pass over it (layer)
 constexpr unsigned long long TIMEOUT_NS = 2000000000ull;
 
 enum { F_BF16 = 0, F_E4M3 = 1, F_W4 = 2 };
 
-struct V8 {
-  uint32_t x[8];
+__device__ __forceinline__ unsigned long long clock_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+// Bounded wait for done(): false (and the status bit) after TIMEOUT_NS.
+template <class Done>
+__device__ __forceinline__ bool wait_for(Done done, int32_t* dev_status) {
+  if (done()) return true;
+  const unsigned long long t0 = clock_ns();
+  while (!done()) {
+    if (clock_ns() - t0 > TIMEOUT_NS) {
+      if (dev_status) atomicOr(dev_status, MOE_DEV_PIPELINE_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
+// HALF: operands are FP16, else BF16.
+template <bool HALF>
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+  if (HALF)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Four E4M3 codes -> two FP16 pairs, exactly (FP16 holds every E4M3 value).
+__device__ __forceinline__ void e4m3x4_to_half(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(v));
+}
+
+// Eight 4-bit codes of one word minus their zero point -> four pairs (columns 0 1, 2 3, 4 5, 6 7).
+// Column 2i sits at nibble i and 2i + 1 at nibble i + 4, so a mask leaves a pair of codes in
+// the low mantissa bits of two 16-bit halves.  BF16: 0x4300 | c is exactly 128 + c, and minus
+// (128 + z) is exact.  FP16: 0x6400 | c is 1024 + c, and 0x6400 | 16 c is 1024 + 16 c, a
+// sixteenth of which minus (64 + z) is exact in one multiply-add: two shifts fewer.
+template <bool HALF>
+struct W4Zero {
+  uint32_t a, b;               // 128 + z; or 1024 + z and -(64 + z)
+  // z in byte `sel` of the word
+  __device__ __forceinline__ W4Zero(uint32_t z, int sel) {
+    if (HALF) {
+      const uint32_t p = __byte_perm(z, 0, 0x4040 | sel * 0x0101);
+      a = p | 0x64006400u;
+      b = (p << 4) | 0xd400d400u;
+    } else {
+      a = __byte_perm(z, 0x43u, 0x4040 | sel * 0x0101);
+      b = 0;
+    }
+  }
 };
-// Read-once weights: not kept in L1, the neighbouring 128 bytes fetched into L2 with them.
-__device__ __forceinline__ V8 ld_weights(const uint8_t* p) {
-  V8 v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(v.x[0]), "=r"(v.x[1]), "=r"(v.x[2]), "=r"(v.x[3]), "=r"(v.x[4]), "=r"(v.x[5]), "=r"(v.x[6]),
-                 "=r"(v.x[7])
-               : "l"(p));
-  return v;
-}
-// Activations: kept in L1 (the warps of an SM read the same rows); not .nc, since the layer
-// writes some of them in the same launch.
-__device__ __forceinline__ uint4 ld_act(const uint16_t* p) {
-  uint4 v;
-  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
-
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+template <bool HALF>
+__device__ __forceinline__ void w4_pairs(uint32_t v, const W4Zero<HALF>& z, uint32_t (&p)[4]) {
+  if (HALF) {
+    const uint32_t w = v >> 8;
+    const uint32_t c0 = (v & 0x000f000fu) | 0x64006400u, c1 = (v & 0x00f000f0u) | 0x64006400u;
+    const uint32_t c2 = (w & 0x000f000fu) | 0x64006400u, c3 = (w & 0x00f000f0u) | 0x64006400u;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p[0]) : "r"(c0), "r"(z.a));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p[1]) : "r"(c1), "r"(0x2c002c00u), "r"(z.b));   // 0x2c00 = 1/16
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p[2]) : "r"(c2), "r"(z.a));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p[3]) : "r"(c3), "r"(0x2c002c00u), "r"(z.b));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t c = ((v >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+      asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(p[i]) : "r"(c), "r"(z.a));
+    }
+  }
 }
 
-// Two E4M3 codes in the low byte of each half of h -> two BF16, exactly: the sign to bit 15,
-// the other 7 bits behind a zeroed upper exponent give the value times 2^-120 (a subnormal
-// BF16 for a subnormal code), and the product with 2^120 is exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t h) {
-  const uint32_t m = ((h >> 4) & 0x07f007f0u) | (h & 0x80008000u);
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(0x7b807b80u));   // 0x7b80 = 2^120
-  return r;
-}
-
-// ------------------------------------------------------------------------- work division
-// Worker w of W takes items [F*w/W, F*(w+1)/W).
-__host__ __device__ __forceinline__ long long run_start(long long F, long long w, long long W) { return F * w / W; }
-__host__ __device__ __forceinline__ int worker_of(long long f, long long F, long long W) {
-  return (int)(((f + 1) * W - 1) / F);
-}
-// Workers used for F items: all, unless that leaves them less than `least` items each.
-__host__ __device__ __forceinline__ int workers_for(long long F, int all, int least) {
-  const long long n = (F + least - 1) / least;
-  return n < all ? (int)n : all;
-}
-// The worker this warp is: neighbouring warps of an SM take neighbouring runs when all
-// workers are used; fewer are spread over the SMs first.
-__device__ __forceinline__ int my_worker(int W, int cta, int ctas, int warp) {
-  if (W >= ctas * WARPS) return cta * WARPS + warp;
-  const int w = warp * ctas + cta;
-  return w < W ? w : -1;
-}
-
-// Where a lane finds one row tile's items.
+// --------------------------------------------------------------------------------- items
+// Where one row tile's items begin in memory.
 struct Tile {
-  const uint8_t* w;    // this lane's 32 bytes of row g of the first half tile, at slice s0
-  const void* sc;      // scales at slice s0 (E4M3: first half tile's block; W4: this lane's)
-  const void* zp;      // W4 zero points at slice s0, or null
-  int s0, n;           // slices [s0, s0 + n) of the tile
+  const uint8_t* w;    // first row of the first half tile, at the unit's first slice
+  const void* sc;      // E4M3: scale of the first half tile's block; W4: scales of its row block
+  const void* zp;      // W4 zero points, or null
 };
-// Constant strides of a phase's matrices.
+// One phase's matrices: constant strides, and how its tiles are cut into units.
 struct Strides {
   long long step;      // bytes from one slice to the next
-  long long row8;      // bytes from row r to row r + 8
+  long long pitch;     // bytes from one row of a half tile to the next
   long long half;      // bytes from the first half tile (16 rows) to the second
-  long long sc_half;   // scale elements from the first half tile to the second
+  long long sc_half;   // scale elements (E4M3 floats; W4 two-row words) to the second half tile
   int k;               // columns
-  int nsl;             // slices per row
+  int nsl;             // slices (items) per tile
+  int len, parts;      // items per unit (fewer in the last), units per tile
+  // at most `most` units, of at least two items unless there is little work
+  __host__ __device__ __forceinline__ void cut(int most, bool little) {
+    len = (nsl + most - 1) / most;
+    if (len < 2 && !little && nsl > 1) len = 2;
+    parts = (nsl + len - 1) / len;
+  }
 };
 
-// One item's weights with their scales.
 template <int FMT, int GROUP>
-struct Item {
-  static constexpr int NG = FMT == F_W4 ? 256 / GROUP : 1;   // scale groups per slice
-  V8 q[4];                 // rows g, g + 8 of the first half tile, then of the second
-  uint32_t sc[2][NG];      // E4M3: float bits; W4: BF16 pair (row g, row g + 8)
-  uint32_t zp[2][(NG + 1) / 2];   // W4: byte pairs (row g, row g + 8), two groups per word
-
-  __device__ __forceinline__ void load(const uint8_t* w, const void* scales, const void* zeros, const Strides& st) {
-    q[0] = ld_weights(w);
-    q[1] = ld_weights(w + st.row8);
-    q[2] = ld_weights(w + st.half);
-    q[3] = ld_weights(w + st.half + st.row8);
-    if constexpr (FMT == F_E4M3) {
-      const uint32_t* s = static_cast<const uint32_t*>(scales);
-      sc[0][0] = __ldg(s);
-      sc[1][0] = __ldg(s + st.sc_half);
-    }
-    if constexpr (FMT == F_W4) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t* s = static_cast<const uint32_t*>(scales) + h * st.sc_half;
-        if constexpr (NG == 2) {
-          const uint2 v = __ldg(reinterpret_cast<const uint2*>(s));
-          sc[h][0] = v.x; sc[h][1] = v.y;
-        } else {
-#pragma unroll
-          for (int i = 0; i < NG / 4; ++i) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(s) + i);
-            sc[h][4 * i] = v.x; sc[h][4 * i + 1] = v.y; sc[h][4 * i + 2] = v.z; sc[h][4 * i + 3] = v.w;
-          }
-        }
-        if (zeros) {
-          const uint16_t* z = static_cast<const uint16_t*>(zeros) + h * st.sc_half;
-          if constexpr (NG == 2) {
-            zp[h][0] = __ldg(reinterpret_cast<const uint32_t*>(z));
-          } else if constexpr (NG == 4) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(z));
-            zp[h][0] = v.x; zp[h][1] = v.y;
-          } else {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(z));
-            zp[h][0] = v.x; zp[h][1] = v.y; zp[h][2] = v.z; zp[h][3] = v.w;
-          }
-        }
-      }
-    }
-  }
-  // bytes / elements from one slice's scales to the next, per lane pointer
-  static __device__ __forceinline__ const void* next_scales(const void* p) {
-    if constexpr (FMT == F_E4M3) return static_cast<const uint32_t*>(p) + 1;
-    if constexpr (FMT == F_W4) return static_cast<const uint32_t*>(p) + 8 * NG;
-    return p;
-  }
-  static __device__ __forceinline__ const void* next_zeros(const void* p) {
-    if constexpr (FMT == F_W4) return p ? static_cast<const uint16_t*>(p) + 8 * NG : p;
-    return p;
-  }
+struct Format {
+  static constexpr int KI = FMT == F_BF16 ? 64 : FMT == F_E4M3 ? 128 : 256;   // columns per item
+  static constexpr int NG = FMT == F_W4 ? 256 / GROUP : 1;                    // W4 scale groups per slice
+  static constexpr int SC = FMT == F_W4 ? 8 * NG * 4 : 16;                    // scale bytes of a half tile
+  static constexpr int ZP = FMT == F_W4 ? 8 * NG * 2 : 0;                     // zero-point bytes of a half tile
+  static constexpr int HALF_CHUNKS = FMT == F_BF16 ? 1 : FMT == F_E4M3 ? 2 : 4;
+  static constexpr int STAGE = FMT == F_BF16 ? 4096 : 4096 + 2 * (SC + ZP);
 };
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// One warp copies one item into its stage: 32 rows x 128 bytes, each instruction four whole
+// lines.  16-byte chunk c of row r goes to chunk c ^ (r & 1), so that the reads below (two rows x
+// every other chunk per 8 lanes) touch every bank once.
+template <int FMT, int GROUP>
+__device__ __forceinline__ void copy_item(uint32_t stage, const Tile& c, long long pitch, long long half,
+                                          long long sc_half, int lane) {
+  using F = Format<FMT, GROUP>;
+  const int r = lane >> 3, ch = lane & 7;
+  const uint8_t* p = c.w + r * pitch + ch * 16;
+  const uint32_t d = stage + r * 128 + ((ch ^ (r & 1)) << 4);
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) cp16(d + h * 2048 + q * 512, p + h * half + q * 4 * pitch);
+  if constexpr (FMT == F_E4M3) {
+    if (lane < 2) cp4(stage + 4096 + lane * 16, static_cast<const float*>(c.sc) + lane * sc_half);
+  }
+  if constexpr (FMT == F_W4) {
+    constexpr int N = F::SC / 16;   // chunks per half tile
+    if (lane < 2 * N)
+      cp16(stage + 4096 + lane * 16, reinterpret_cast<const uint8_t*>(static_cast<const uint32_t*>(c.sc) +
+                                                                      (lane / N) * sc_half) + (lane % N) * 16);
+    if (c.zp && lane < N)
+      cp16(stage + 4096 + 2 * F::SC + lane * 16,
+           reinterpret_cast<const uint8_t*>(static_cast<const uint16_t*>(c.zp) + (lane / (N / 2)) * sc_half) +
+               (lane % (N / 2)) * 16);
+  }
+}
 
 // Sums of one row tile: [8-column group][half tile][fragment: rows g, g (+1 column), g + 8, g + 8].
 template <int NT>
@@ -188,184 +202,310 @@ struct Sums {
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-// sums += (weights of one item) x (activations); x[n] is this lane's column of group n at
-// column k0 of the item (null: no such column, zeros); kleft: columns from k0 to the end of
-// the row (W4 rows are padded to whole items, activations are not).
-template <int FMT, int GROUP, int NT>
-__device__ __forceinline__ void item_mma(Sums<NT>& sums, const Item<FMT, GROUP>& it, const uint16_t* const (&x)[NT],
-                                         int t, int kleft, bool zeros) {
-  const uint4 zero4 = make_uint4(0, 0, 0, 0);
-  if constexpr (FMT == F_BF16) {
+// This lane's activations: 16-byte chunk I of half J of an item (an item's half is J's 16 of the
+// lane's 32 bytes per weight row, HALF_CHUNKS chunks of activations); x[n] is the lane's column of
+// group n at the item's first column (null: no such column, zeros).  kleft: columns to the
+// row's end (W4 rows are padded to whole items, activations are not).  Activations are kept
+// in L1, which the weights pass by; plain loads, since the layer writes some of them in the
+// same launch.
+template <int FMT, int NT>
+__device__ __forceinline__ void load_acts(uint4 (&b)[NT], const uint16_t* const (&x)[NT], int J, int I, int t,
+                                          int kleft) {
+  const int k = FMT == F_BF16 ? t * 16 + 8 * J : FMT == F_E4M3 ? t * 32 + 16 * J + 8 * I : (4 * J + I) * 32 + t * 8;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {   // 8 of this lane's 16 columns: two k-steps
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const uint4 b = x[n] ? ld_act(x[n] + t * 16 + 8 * j) : zero4;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const V8 &lo = it.q[2 * h], &hi = it.q[2 * h + 1];
-          mma_bf16(sums.v[n][h], lo.x[4 * j], hi.x[4 * j], lo.x[4 * j + 1], hi.x[4 * j + 1], b.x, b.y);
-          mma_bf16(sums.v[n][h], lo.x[4 * j + 2], hi.x[4 * j + 2], lo.x[4 * j + 3], hi.x[4 * j + 3], b.z, b.w);
-        }
-      }
-    }
-  } else if constexpr (FMT == F_E4M3) {
-    // an item is one 128-column scale block: unscaled sums first, then one multiply-add each
-    Sums<NT> acc;
-    acc.clear();
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {   // 8 of this lane's 32 columns: two k-steps
-      uint32_t a[4][4];             // [row][pair of columns]
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t q = it.q[r].x[2 * j + i];
-          a[r][2 * i] = e4m3x2_to_bf16x2(__byte_perm(q, 0, 0x1404));       // bytes 0, 1 to the top of each half
-          a[r][2 * i + 1] = e4m3x2_to_bf16x2(__byte_perm(q, 0, 0x3424));   // bytes 2, 3
-        }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const uint4 b = x[n] ? ld_act(x[n] + t * 32 + 8 * j) : zero4;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          mma_bf16(acc.v[n][h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b.x, b.y);
-          mma_bf16(acc.v[n][h], a[2 * h][2], a[2 * h + 1][2], a[2 * h][3], a[2 * h + 1][3], b.z, b.w);
-        }
-      }
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float s = __uint_as_float(it.sc[h][0]);
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sums.v[n][h][i] = fmaf(s, acc.v[n][h][i], sums.v[n][h][i]);
-    }
-  } else {
-    // Word j of the lane's 8 holds columns j*32 + t*8 .. + 8, column 2i at nibble i and 2i + 1
-    // at nibble i + 4: a mask leaves a pair of codes in the low mantissa bits of two BF16
-    // halves, 0x4300 | c is exactly 128 + c, and minus (128 + zero point) is exact.
-    constexpr int WPG = GROUP / 32;   // words per scale group
-#pragma unroll
-    for (int gi = 0; gi < Item<FMT, GROUP>::NG; ++gi) {
-      Sums<NT> acc;
-      acc.clear();
-      uint32_t off[4];               // 128 + zero point, per row, as a BF16 pair
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        if (zeros) {
-          const uint32_t z = it.zp[r >> 1][gi >> 1];
-          off[r] = __byte_perm(z, 0x43u, ((gi & 1) * 2 + (r & 1)) * 0x0101 | 0x4040);
-        } else {
-          off[r] = 0x43084308u;
-        }
-      }
-#pragma unroll
-      for (int jj = 0; jj < WPG; ++jj) {
-        const int j = gi * WPG + jj;
-        uint32_t a[4][4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t c = ((it.q[r].x[j] >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-            asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(a[r][i]) : "r"(c), "r"(off[r]));
-          }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const uint4 b = x[n] && j * 32 + t * 8 < kleft ? ld_act(x[n] + j * 32 + t * 8) : zero4;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            mma_bf16(acc.v[n][h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b.x, b.y);
-            mma_bf16(acc.v[n][h], a[2 * h][2], a[2 * h + 1][2], a[2 * h][3], a[2 * h + 1][3], b.z, b.w);
-          }
-        }
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float s0 = bf_lo(it.sc[h][gi]), s1 = bf_hi(it.sc[h][gi]);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          sums.v[n][h][0] = fmaf(s0, acc.v[n][h][0], sums.v[n][h][0]);
-          sums.v[n][h][1] = fmaf(s0, acc.v[n][h][1], sums.v[n][h][1]);
-          sums.v[n][h][2] = fmaf(s1, acc.v[n][h][2], sums.v[n][h][2]);
-          sums.v[n][h][3] = fmaf(s1, acc.v[n][h][3], sums.v[n][h][3]);
-        }
-      }
-    }
-  }
+  for (int n = 0; n < NT; ++n)
+    b[n] = x[n] && (FMT != F_W4 || k < kleft) ? *reinterpret_cast<const uint4*>(x[n] + k) : make_uint4(0, 0, 0, 0);
 }
 
-// Items [cur.s0, cur.s0 + cur.n) of one tile.  `it` holds the first item's weights on entry
-// and the first of the next tile's (next, if it has any) on return: the next item's loads are
-// in flight while this one's are used.
-template <int FMT, int GROUP, int NT>
-__device__ __forceinline__ void run_tile(Sums<NT>& sums, Item<FMT, GROUP>& it, const Tile& cur, const Tile& next,
-                                         const Strides& st, const uint16_t* const (&x0)[NT], int t) {
-  constexpr int KI = FMT == F_BF16 ? 64 : FMT == F_E4M3 ? 128 : 256;   // columns per item
-  const uint8_t* w = cur.w;
-  const void* sc = cur.sc;
-  const void* zp = cur.zp;
-  const uint16_t* x[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) x[n] = x0[n] ? x0[n] + (long long)cur.s0 * KI : nullptr;
-  int kleft = st.k - cur.s0 * KI;
-  const bool zeros = cur.zp != nullptr;
-  sums.clear();
-  for (int i = 0; i < cur.n; ++i) {
-    const Item<FMT, GROUP> use = it;
-    if (i + 1 < cur.n) {
-      w += st.step;
-      sc = Item<FMT, GROUP>::next_scales(sc);
-      zp = Item<FMT, GROUP>::next_zeros(zp);
-      it.load(w, sc, zp, st);
-    } else if (next.n > 0) {
-      it.load(next.w, next.sc, next.zp, st);
-    }
-    item_mma<FMT, GROUP, NT>(sums, use, x, t, kleft, zeros);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-      if (x[n]) x[n] += KI;
-    kleft -= KI;
-  }
-}
-
-// This worker's part of a tile whose items belong to workers w0..w1: true on the warp that
-// completes it, with the whole sums.  slot: 1 if the part starts the tile, else 0 (a worker has
-// at most one of each in flight).  count: one word per worker, zero between launches.
-template <int NT>
-__device__ __forceinline__ bool join_parts(Sums<NT>& sums, float* part, int32_t* count, int worker, int slot, int w0,
-                                           int w1, int lane) {
-  float4* mine = reinterpret_cast<float4*>(part + ((size_t)worker * 2 + slot) * PART_FLOATS);
+template <bool HALF, int NT>
+__device__ __forceinline__ void mma_step(Sums<NT>& acc, const uint32_t (&a)[4][4], const uint4 (&b)[NT]) {
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      __stcg(&mine[(n * 2 + h) * 32 + lane],
-             make_float4(sums.v[n][h][0], sums.v[n][h][1], sums.v[n][h][2], sums.v[n][h][3]));
-  __threadfence();
-  __syncwarp();
-  int old = 0;
-  if (lane == 0) old = atomicAdd(&count[w0], 1);
-  old = __shfl_sync(0xffffffffu, old, 0);
-  if (old != w1 - w0) return false;
-  __threadfence();
-  if (lane == 0) count[w0] = 0;
-  sums.clear();
-  for (int w = w0; w <= w1; ++w) {
-    const float4* p = reinterpret_cast<const float4*>(part + ((size_t)w * 2 + (w == w0 ? 1 : 0)) * PART_FLOATS);
+    for (int h = 0; h < 2; ++h) {
+      mma16<HALF>(acc.v[n][h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b[n].x, b[n].y);
+      mma16<HALF>(acc.v[n][h], a[2 * h][2], a[2 * h + 1][2], a[2 * h][3], a[2 * h + 1][3], b[n].z, b[n].w);
+    }
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// Half an item: sums += weights x activations.  acc: E4M3 sums of the item so far, unscaled.
+template <int FMT, int GROUP, bool HALF, int NT, int PASSES, int J, class Acts>
+__device__ __forceinline__ void half_item(Sums<NT>& sums, Sums<NT>& acc, const uint8_t* stage, Acts acts, int g, int t,
+                                          bool zeros) {
+  using F = Format<FMT, GROUP>;
+  uint4 q[4];                      // rows g, g + 8 of the first half tile, then of the second
+  const uint8_t* base = stage + g * 128 + (((2 * t + J) ^ (g & 1)) << 4);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+  for (int r = 0; r < 4; ++r) q[r] = *reinterpret_cast<const uint4*>(base + r * 1024);
+  if constexpr (FMT == F_BF16) {
+    uint32_t a[4][4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) { a[r][0] = q[r].x; a[r][1] = q[r].y; a[r][2] = q[r].z; a[r][3] = q[r].w; }
+    uint4 b[PASSES][NT];
+    acts(b, J, 0);
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) mma_step<HALF, NT>(sums, a, b[p]);
+  } else if constexpr (FMT == F_E4M3) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint4 b[PASSES][NT];
+      acts(b, J, i);
+      uint32_t a[4][4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) e4m3x4_to_half(word(q[r], 2 * i + w), a[r][2 * w], a[r][2 * w + 1]);
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) mma_step<HALF, NT>(acc, a, b[p]);
+    }
+  } else {
+    // word j of the lane's 8 holds columns j*32 + t*8 .. + 8
+    constexpr int WPG = GROUP / 32;   // words per scale group
+    const uint32_t* scales = reinterpret_cast<const uint32_t*>(stage + 4096) + g * F::NG;
+    const uint16_t* zps = reinterpret_cast<const uint16_t*>(stage + 4096 + 2 * F::SC) + g * F::NG;
+#pragma unroll
+    for (int i0 = 0; i0 < 4; i0 += WPG) {
+      const int gi = (4 * J + i0) / WPG;
+      const uint32_t za = zeros ? zps[gi] : 0x0808u, zb = zeros ? zps[F::ZP / 2 + gi] : 0x0808u;
+      const W4Zero<HALF> z[4] = {{za, 0}, {za, 1}, {zb, 0}, {zb, 1}};
+      Sums<NT> part;
+      part.clear();
+#pragma unroll
+      for (int i = i0; i < i0 + WPG; ++i) {
+        uint4 b[PASSES][NT];
+        acts(b, J, i);
+        uint32_t a[4][4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) w4_pairs<HALF>(word(q[r], i), z[r], a[r]);
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) mma_step<HALF, NT>(part, a, b[p]);
+      }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float4 v = __ldcg(&p[(n * 2 + h) * 32 + lane]);
-        sums.v[n][h][0] += v.x;
-        sums.v[n][h][1] += v.y;
-        sums.v[n][h][2] += v.z;
-        sums.v[n][h][3] += v.w;
+        const uint32_t sc = scales[h * (F::SC / 4) + gi];
+        const float s0 = bf_lo(sc), s1 = bf_hi(sc);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          sums.v[n][h][0] = fmaf(s0, part.v[n][h][0], sums.v[n][h][0]);
+          sums.v[n][h][1] = fmaf(s0, part.v[n][h][1], sums.v[n][h][1]);
+          sums.v[n][h][2] = fmaf(s1, part.v[n][h][2], sums.v[n][h][2]);
+          sums.v[n][h][3] = fmaf(s1, part.v[n][h][3], sums.v[n][h][3]);
+        }
       }
+    }
   }
+}
+
+// -------------------------------------------------------------------------------- stream
+// A CTA's sequence of tiles, as one worker warp sees it.  Src says what the sequence is:
+//   tile(q)            number of the CTA's q-th tile, negative past the end (may wait);
+//   strides(tile)      the strides and the cut of its phase;
+//   where(tile, s0)    where its items begin at slice s0;  zeros().
+// Units are counted over the sequence; worker w of WORKERS takes units w, w + WORKERS, ...  Its ring
+// of STAGES stages is filled STAGES - 1 items ahead of their use.
+template <int FMT, int GROUP, bool HALF, int STAGES, int WORKERS, class Src>
+struct Stream {
+  using F = Format<FMT, GROUP>;
+  const Src& src;
+  uint8_t* ring;
+  uint32_t ring_addr;
+  int lane;
+  int in, out;                 // stage to fill next, stage to use next
+  struct Cursor {
+    int u, q, part, tile;      // unit, its place in the sequence, its part of the tile (number < 0: the end)
+  } fillc, usec;
+  int left;                    // items left of the unit being filled
+  Tile c;
+  long long step, pitch, half, sc_half;
+
+  __device__ __forceinline__ Stream(const Src& s, uint8_t* r, int worker, int lane_)
+      : src(s), ring(r), lane(lane_), in(0), out(0) {
+    ring_addr = static_cast<uint32_t>(__cvta_generic_to_shared(r));
+    fillc.u = worker;
+    fillc.q = 0;
+    fillc.part = worker;
+    settle(fillc);
+    usec = fillc;
+    open();
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) fill();
+  }
+  // from a part that may be past its tile to the tile it falls to
+  __device__ __forceinline__ void settle(Cursor& k) const {
+    while (true) {
+      k.tile = src.tile(k.q);
+      if (k.tile < 0) return;
+      const int n = src.strides(k.tile).parts;
+      if (k.part < n) return;
+      k.part -= n;
+      ++k.q;
+    }
+  }
+  __device__ __forceinline__ void hop(Cursor& k) const {
+    k.u += WORKERS;
+    k.part += WORKERS;
+    settle(k);
+  }
+  __device__ __forceinline__ void open() {
+    if (fillc.tile < 0) return;
+    const Strides& st = src.strides(fillc.tile);
+    const int s0 = fillc.part * st.len;
+    left = min(st.len, st.nsl - s0);
+    step = st.step;
+    pitch = st.pitch;
+    half = st.half;
+    sc_half = st.sc_half;
+    c = src.where(fillc.tile, s0);
+  }
+  __device__ __forceinline__ void fill() {
+    if (fillc.tile >= 0) {
+      copy_item<FMT, GROUP>(ring_addr + in * F::STAGE, c, pitch, half, sc_half, lane);
+      if (--left > 0) {
+        c.w += step;
+        if constexpr (FMT == F_E4M3) c.sc = static_cast<const float*>(c.sc) + 1;
+        if constexpr (FMT == F_W4) {
+          c.sc = static_cast<const uint32_t*>(c.sc) + 8 * F::NG;
+          if (c.zp) c.zp = static_cast<const uint16_t*>(c.zp) + 8 * F::NG;
+        }
+      } else {
+        hop(fillc);
+        open();
+      }
+    }
+    cp_commit();
+    in = in + 1 == STAGES ? 0 : in + 1;
+  }
+  // The items of the unit at usec: sums = weights x activations.  x0[p][n] is this lane's column
+  // of group n, or null; PASSES sets of columns are added into the same sums.
+  template <int NT, int PASSES>
+  __device__ __forceinline__ void run(Sums<NT>& sums, const Strides& st, const uint16_t* const (&x0)[PASSES][NT]) {
+    const int g = lane >> 2, t = lane & 3;
+    const int s0 = usec.part * st.len, n = min(st.len, st.nsl - s0);
+    const uint16_t* x[PASSES][NT];
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) x[p][i] = x0[p][i] ? x0[p][i] + (long long)s0 * F::KI : nullptr;
+    int kleft = st.k - s0 * F::KI;
+    const bool zeros = src.zeros();
+    sums.clear();
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      fill();
+      // few columns: the item's activations are on their way before its weights are waited for
+      constexpr bool EARLY = F::HALF_CHUNKS * NT * PASSES <= 4;
+      uint4 early[EARLY ? 2 * F::HALF_CHUNKS : 1][PASSES][NT];
+      if constexpr (EARLY) {
+#pragma unroll
+        for (int q = 0; q < 2 * F::HALF_CHUNKS; ++q)
+#pragma unroll
+          for (int p = 0; p < PASSES; ++p)
+            load_acts<FMT, NT>(early[q][p], x[p], q / F::HALF_CHUNKS, q % F::HALF_CHUNKS, t, kleft);
+      }
+      auto acts = [&](uint4(&b)[PASSES][NT], int J, int I) {
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) {
+          if constexpr (EARLY) {
+#pragma unroll
+            for (int q = 0; q < NT; ++q) b[p][q] = early[J * F::HALF_CHUNKS + I][p][q];
+          } else {
+            load_acts<FMT, NT>(b[p], x[p], J, I, t, kleft);
+          }
+        }
+      };
+      cp_wait<STAGES - 1>();
+      __syncwarp();
+      const uint8_t* stage = ring + out * F::STAGE;
+      Sums<NT> acc;
+      if constexpr (FMT == F_E4M3) acc.clear();
+      half_item<FMT, GROUP, HALF, NT, PASSES, 0>(sums, acc, stage, acts, g, t, zeros);
+      half_item<FMT, GROUP, HALF, NT, PASSES, 1>(sums, acc, stage, acts, g, t, zeros);
+      if constexpr (FMT == F_E4M3) {
+        // an item is one 128-column scale block
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float s = *reinterpret_cast<const float*>(stage + 4096 + h * 16);
+#pragma unroll
+          for (int q = 0; q < NT; ++q)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sums.v[q][h][j] = fmaf(s, acc.v[q][h][j], sums.v[q][h][j]);
+        }
+      }
+      __syncwarp();     // the stage may be filled again
+      out = out + 1 == STAGES ? 0 : out + 1;
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p)
+#pragma unroll
+        for (int q = 0; q < NT; ++q)
+          if (x[p][q]) x[p][q] += F::KI;
+      kleft -= F::KI;
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------------- join
+constexpr int MAX_SLOTS = 48;
+struct JoinShared {
+  int turn[MAX_SLOTS];         // unit that may use the slot next
+  int count[MAX_SLOTS];        // units done of the tile whose first unit has this slot
+};
+
+__device__ __forceinline__ void join_init(JoinShared& j) {
+  if (threadIdx.x < MAX_SLOTS) {
+    j.turn[threadIdx.x] = threadIdx.x;
+    j.count[threadIdx.x] = 0;
+  }
+}
+
+// Joins the units [u0, u0 + n) of one tile; unit u is this warp's.  Slot i % slots of `parts`
+// (`stride` float4 each) belongs to unit i until its tile is summed; a warp that is `slots` units
+// ahead waits for it (units are taken in order and a tile has at most `slots` of them, so the wait
+// ends; it is bounded all the same).  True on the warp that has the tile's sums; false also
+// after a timeout, which sets the status bit.
+template <int NT>
+__device__ __forceinline__ bool join(Sums<NT>& sums, JoinShared& j, float4* parts, int slots, int stride, int u, int u0,
+                                     int n, int lane, int32_t* dev_status) {
+  const int mine = u % slots;
+  volatile int* turn = j.turn;
+  if (!__all_sync(0xffffffffu, wait_for([&] { return turn[mine] == u; }, dev_status))) return false;
+  if (n > 1) {
+    float4* p = parts + mine * stride;
+#pragma unroll
+    for (int q = 0; q < NT; ++q)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        p[(q * 2 + h) * 32 + lane] = make_float4(sums.v[q][h][0], sums.v[q][h][1], sums.v[q][h][2], sums.v[q][h][3]);
+    __threadfence_block();
+    __syncwarp();
+    int old = 0;
+    if (lane == 0) old = atomicAdd(&j.count[u0 % slots], 1);
+    old = __shfl_sync(0xffffffffu, old, 0);
+    if (old != n - 1) return false;
+    __threadfence_block();
+    if (lane == 0) j.count[u0 % slots] = 0;
+    sums.clear();
+    int at = u0 % slots;
+#pragma unroll 2
+    for (int i = 0; i < n; ++i) {
+      const float4* v = parts + at * stride;
+#pragma unroll
+      for (int q = 0; q < NT; ++q)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4 f = v[(q * 2 + h) * 32 + lane];
+          sums.v[q][h][0] += f.x;
+          sums.v[q][h][1] += f.y;
+          sums.v[q][h][2] += f.z;
+          sums.v[q][h][3] += f.w;
+        }
+      at = at + 1 == slots ? 0 : at + 1;
+    }
+    __threadfence_block();
+    __syncwarp();
+  }
+  // the slots may be used again
+  for (int i = u0 + lane; i < u0 + n; i += 32) turn[i % slots] = i + slots;
   return true;
 }
 

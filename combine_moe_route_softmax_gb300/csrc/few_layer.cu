@@ -5,29 +5,35 @@ namespace moe {
 namespace few {
 
 struct FewPlan {
-  size_t off_part_count, off_tile_count, off_logits, off_hhi, off_hlo, off_y, off_part, total, zeroed;
+  size_t off_tile, off_entry, off_hmax, off_logits, off_x16, off_xunit, off_h32, off_hunit, off_hhi, off_hlo, off_y,
+      total;
 };
 
 inline bool plan_few(const moe_few_desc_t* d, FewPlan* p) {
   if (!d) return false;
-  if (d->T < 0 || d->T > kMaxTokens || d->H <= 0 || d->I <= 0 || d->H % 128 || d->I % 128 || d->E < 1 ||
-      d->E > kMaxExperts || d->K < 1 || d->K > d->E || d->K > kMaxTopK || (d->has_shared != 0 && d->has_shared != 1) ||
-      (d->weight_tiles != 0 && d->weight_tiles != 1))
+  if (d->T < 0 || d->T > kMaxTokens || d->H <= 0 || d->I <= 0 || d->H % 128 || d->I % 128 || d->H > kMaxWidth ||
+      d->I > kMaxWidth || d->E < 1 || d->E > kMaxExperts || d->K < 1 || d->K > d->E || d->K > kMaxTopK ||
+      (d->has_shared != 0 && d->has_shared != 1) || (d->weight_tiles != 0 && d->weight_tiles != 1))
     return false;
   if (d->dtype != MOE_BF16 && d->dtype != MOE_E4M3 && d->dtype != MOE_W4) return false;
   if (d->dtype == MOE_W4 ? (d->group != 32 && d->group != 64 && d->group != 128) || d->weight_tiles : d->group != 0)
     return false;
   const size_t slots = (size_t)d->T * d->K + d->T;
-  const size_t workers = (size_t)num_sms() * WARPS;
-  size_t o = 256;                                                       // barrier words
-  p->off_part_count = o; o = align256(o + 4 * workers);
-  p->off_tile_count = o; o = align256(o + 4 * (size_t)(d->H / 32));
-  p->zeroed = o;
-  p->off_logits = o;     o = align256(o + 4 * (size_t)d->T * d->E);
-  p->off_hhi = o;        o = align256(o + 2 * slots * d->I);
-  p->off_hlo = o;        o = align256(o + 2 * slots * d->I);
-  p->off_y = o;          o = align256(o + 4 * slots * d->H);
-  p->off_part = o;       o = align256(o + workers * 2 * PART_FLOATS * 4);
+  const bool half = d->dtype != MOE_BF16;
+  size_t o = 256;                                                       // barrier, queue
+  // zero between calls; at the same places for every T
+  p->off_tile = o;   o = align256(o + 4 * (size_t)(d->H / 32));
+  p->off_entry = o;  o = align256(o + 4 * (size_t)kMaxEntries);
+  p->off_hmax = o;   o = align256(o + 4 * (size_t)kMaxTokens * (d->K + 1));
+  // not kept
+  p->off_logits = o; o = align256(o + 4 * (size_t)d->T * d->E);
+  p->off_x16 = o;    o = align256(o + (half ? 2 * (size_t)d->T * d->H : 0));
+  p->off_xunit = o;  o = align256(o + 4 * (size_t)d->T);
+  p->off_h32 = o;    o = align256(o + (half ? 4 * slots * d->I : 0));
+  p->off_hunit = o;  o = align256(o + 4 * slots);
+  p->off_hhi = o;    o = align256(o + 2 * slots * d->I);
+  p->off_hlo = o;    o = align256(o + 2 * slots * d->I);
+  p->off_y = o;      o = align256(o + 4 * slots * d->H);
   p->total = o;
   return true;
 }
@@ -95,13 +101,17 @@ extern "C" moe_status_t moe_layer_few(const moe_few_desc_t* d, const moe_few_wei
   a.x = x;
   a.out = out;
   a.dev_status = dev_status;
-  a.bar = reinterpret_cast<uint32_t*>(b);
-  a.part_count = reinterpret_cast<int32_t*>(b + p.off_part_count);
-  a.tile_count = reinterpret_cast<int32_t*>(b + p.off_tile_count);
+  a.ctl = reinterpret_cast<uint32_t*>(b);
+  a.tile_count = reinterpret_cast<int32_t*>(b + p.off_tile);
+  a.entry_done = reinterpret_cast<int32_t*>(b + p.off_entry);
+  a.h_max = reinterpret_cast<uint32_t*>(b + p.off_hmax);
+  a.x16 = reinterpret_cast<uint16_t*>(b + p.off_x16);
+  a.x_unit = reinterpret_cast<float*>(b + p.off_xunit);
+  a.h32 = reinterpret_cast<float*>(b + p.off_h32);
+  a.h_unit = reinterpret_cast<float*>(b + p.off_hunit);
   a.h_hi = reinterpret_cast<uint16_t*>(b + p.off_hhi);
   a.h_lo = reinterpret_cast<uint16_t*>(b + p.off_hlo);
   a.y = reinterpret_cast<float*>(b + p.off_y);
-  a.part = reinterpret_cast<float*>(b + p.off_part);
   cudaStream_t st = as_stream(stream);
   const cudaError_t e = d->dtype == MOE_BF16   ? launch_layer_bf16(a, st)
                         : d->dtype == MOE_E4M3 ? launch_layer_e4m3(a, st)

@@ -10,6 +10,9 @@ namespace moe {
 namespace few {
 
 constexpr int LIN_COLS = 32;
+constexpr int LIN_WARPS = 16;
+constexpr int LIN_STAGES = 2;
+constexpr int LIN_PARTS = 64 * 1024;
 
 struct LinearArgs {
   const uint16_t* x;
@@ -20,54 +23,61 @@ struct LinearArgs {
   const float* bias;
   void* out;
   int out_f32;
-  int32_t* part_count;
-  float* part;
+  int32_t* dev_status;
   Strides st;
-  int tiles;
-  long long F;
-  int W;
+  int tiles;                   // row tiles x blocks of x
+  int blocks;                  // blocks of LIN_COLS rows of x
 };
 
+// CTA c takes tiles c, c + CTAs, ...; tile = (row tile, block of x rows), blocks inner, so that the
+// second block of a row tile finds its weights in L2.
 template <int GROUP>
-__device__ __forceinline__ Tile linear_tile(const LinearArgs& a, int tile, int s0, int n, int lane) {
-  Tile r;
-  r.s0 = s0;
-  r.n = n;
-  const long long blk = (long long)tile * 2 * a.st.nsl + s0;
-  constexpr int NG = Item<F_W4, GROUP>::NG;
-  r.w = a.q + blk * 2048 + lane * 32;
-  r.sc = static_cast<const uint32_t*>(a.scales) + (blk * 8 + (lane >> 2)) * NG;
-  r.zp = a.zeros ? static_cast<const uint16_t*>(a.zeros) + (blk * 8 + (lane >> 2)) * NG : nullptr;
-  return r;
-}
+struct LinearSrc {
+  const LinearArgs& a;
+  __device__ __forceinline__ int tile(int q) const {
+    const long long n = blockIdx.x + (long long)q * gridDim.x;
+    return n < a.tiles ? (int)n : -1;
+  }
+  __device__ __forceinline__ const Strides& strides(int) const { return a.st; }
+  __device__ __forceinline__ bool zeros() const { return a.zeros != nullptr; }
+  __device__ __forceinline__ Tile where(int tile_, int s0) const {
+    constexpr int NG = Format<F_W4, GROUP>::NG;
+    const long long b = (long long)(tile_ / a.blocks) * 2 * a.st.nsl + s0;
+    Tile r;
+    r.w = a.q + b * 2048;
+    r.sc = static_cast<const uint32_t*>(a.scales) + b * 8 * NG;
+    r.zp = a.zeros ? static_cast<const uint16_t*>(a.zeros) + b * 8 * NG : nullptr;
+    return r;
+  }
+};
+template <int GROUP>
+using LinearStream = Stream<F_W4, GROUP, false, LIN_STAGES, LIN_WARPS, LinearSrc<GROUP>>;
 
 template <int GROUP, int NT>
-__device__ __forceinline__ void linear_do_tile(const LinearArgs& a, Item<F_W4, GROUP>& it, const Tile& cur,
-                                               const Tile& next, int t0, int tile, long long f, int me, int lane) {
+__device__ __forceinline__ void linear_unit(const LinearArgs& a, LinearStream<GROUP>& in, JoinShared& j, float4* parts,
+                                            int slots, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  const uint16_t* x[NT];
+  const int row = in.usec.tile / a.blocks, t0 = (in.usec.tile - row * a.blocks) * LIN_COLS;
+  const uint16_t* x[1][NT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) x[n] = t0 + n * 8 + g < a.T ? a.x + (t0 + n * 8 + g) * a.x_stride : nullptr;
+  for (int n = 0; n < NT; ++n) x[0][n] = t0 + n * 8 + g < a.T ? a.x + (t0 + n * 8 + g) * a.x_stride : nullptr;
   Sums<NT> sums;
-  run_tile<F_W4, GROUP, NT>(sums, it, cur, next, a.st, x, t);
-  if (cur.n < a.st.nsl) {
-    const long long a0 = f - cur.s0;
-    const int w0 = worker_of(a0, a.F, a.W), w1 = worker_of(a0 + a.st.nsl - 1, a.F, a.W);
-    if (!join_parts<NT>(sums, a.part, a.part_count, me, cur.s0 == 0 ? 1 : 0, w0, w1, lane)) return;
-  }
+  in.template run<NT, 1>(sums, a.st, x);
+  if (!join<NT>(sums, j, parts, slots, NT * 64, in.usec.u, in.usec.u - in.usec.part, a.st.parts, lane, a.dev_status))
+    return;
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int row = tile * 32 + h * 16 + (i >> 1) * 8 + g;
-      if (row >= a.N) continue;
-      const float b = a.bias ? __ldg(a.bias + row) : 0.0f;
+      const int r = row * 32 + h * 16 + (i >> 1) * 8 + g;
+      if (r >= a.N) continue;
+      const float b = a.bias ? __ldg(a.bias + r) : 0.0f;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int c = t0 + n * 8 + 2 * t + (i & 1);
         if (c >= a.T) continue;
         const float v = a.bias ? sums.v[n][h][i] + b : sums.v[n][h][i];
-        const long long o = c * a.out_stride + row;
+        const long long o = c * a.out_stride + r;
         if (a.out_f32)
           static_cast<float*>(a.out)[o] = v;
         else
@@ -76,37 +86,21 @@ __device__ __forceinline__ void linear_do_tile(const LinearArgs& a, Item<F_W4, G
     }
 }
 
-template <int GROUP>
-__global__ void __launch_bounds__(THREADS, 1) linear_w4_kernel(const LinearArgs a) {
+template <int GROUP, int NT>
+__global__ void __launch_bounds__(LIN_WARPS * 32, 1) linear_w4_kernel(const LinearArgs a) {
+  extern __shared__ __align__(128) uint8_t rings[];
+  __shared__ JoinShared j;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int me = my_worker(a.W, blockIdx.x, gridDim.x, warp);
-  if (me < 0) return;
-  long long f = run_start(a.F, me, a.W);
-  const long long f1 = run_start(a.F, me + 1, a.W);
-  const long long q = f / a.st.nsl;
-  int s0 = (int)(f - q * a.st.nsl);
-  int blk = (int)(q / a.tiles), tile = (int)(q - (long long)blk * a.tiles);
-  Tile cur = linear_tile<GROUP>(a, tile, s0, (int)min((long long)(a.st.nsl - s0), f1 - f), lane);
-  Item<F_W4, GROUP> it;
-  it.load(cur.w, cur.sc, cur.zp, a.st);
-  while (true) {
-    const long long fn = f + cur.n;
-    Tile next;
-    next.n = 0;
-    int tile_n = tile, blk_n = blk;
-    if (fn < f1) {
-      if (++tile_n == a.tiles) { tile_n = 0; ++blk_n; }
-      next = linear_tile<GROUP>(a, tile_n, 0, (int)min((long long)a.st.nsl, f1 - fn), lane);
-    }
-    const int t0 = blk * LIN_COLS, nc = a.T - t0;
-    if (nc <= 8) linear_do_tile<GROUP, 1>(a, it, cur, next, t0, tile, f, me, lane);
-    else if (nc <= 16) linear_do_tile<GROUP, 2>(a, it, cur, next, t0, tile, f, me, lane);
-    else linear_do_tile<GROUP, 4>(a, it, cur, next, t0, tile, f, me, lane);
-    if (next.n == 0) return;
-    f = fn;
-    cur = next;
-    tile = tile_n;
-    blk = blk_n;
+  constexpr int RING = LIN_STAGES * Format<F_W4, GROUP>::STAGE;
+  constexpr int SLOTS = LIN_PARTS / 1024 / NT < MAX_SLOTS ? LIN_PARTS / 1024 / NT : MAX_SLOTS;
+  float4* parts = reinterpret_cast<float4*>(rings + LIN_WARPS * RING);
+  join_init(j);
+  const LinearSrc<GROUP> src{a};
+  LinearStream<GROUP> in(src, rings + warp * RING, warp, lane);
+  __syncthreads();
+  while (in.usec.tile >= 0) {
+    linear_unit<GROUP, NT>(a, in, j, parts, SLOTS, lane);
+    in.hop(in.usec);
   }
 }
 
@@ -206,6 +200,28 @@ __global__ void __launch_bounds__(256) pack_w4_kernel(const uint8_t* __restrict_
   }
 }
 
+template <int GROUP, int NT>
+moe_status_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
+  constexpr int smem = LIN_WARPS * LIN_STAGES * Format<F_W4, GROUP>::STAGE + LIN_PARTS;
+  static std::atomic<unsigned long long> done{0};
+  if (!once_per_device(done, [] {
+        return cudaFuncSetAttribute(linear_w4_kernel<GROUP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ==
+               cudaSuccess;
+      }))
+    return MOE_ERR_CUDA;
+  const int ctas = a.tiles < num_sms() ? a.tiles : num_sms();
+  linear_w4_kernel<GROUP, NT><<<ctas, LIN_WARPS * 32, smem, stream>>>(a);
+  MOE_CHECK_LAUNCH();
+  return MOE_OK;
+}
+template <int GROUP>
+moe_status_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
+  const int cols = a.T < LIN_COLS ? a.T : LIN_COLS;
+  return cols <= 8    ? launch_linear<GROUP, 1>(a, stream)
+         : cols <= 16 ? launch_linear<GROUP, 2>(a, stream)
+                      : launch_linear<GROUP, 4>(a, stream);
+}
+
 inline bool w4_shape_ok(int mats, int N, int K, int group) {
   return mats >= 0 && N > 0 && K > 0 && (group == 32 || group == 64 || group == 128) && K % 128 == 0 &&
          N <= (1 << 24) && K <= (1 << 24);
@@ -261,17 +277,15 @@ extern "C" moe_status_t moe_pack_w4(const uint8_t* q, const uint16_t* scales, co
 }
 
 extern "C" size_t moe_linear_w4_workspace_bytes(int T, int N, int K) {
-  using namespace moe;
   using namespace moe::few;
   if (T < 0 || !w4_shape_ok(0, N, K, 32)) return 0;
-  const size_t workers = (size_t)num_sms() * WARPS;
-  return align256(4 * workers) + workers * 2 * PART_FLOATS * 4;
+  return 256;
 }
 
 extern "C" moe_status_t moe_linear_w4(const uint16_t* x, int T, int K, long long x_stride, const uint8_t* q_packed,
                                       const uint16_t* scales_packed, const uint8_t* zeros_packed, int N, int group,
                                       const float* bias, void* out, int out_f32, long long out_stride, void* ws,
-                                      size_t ws_bytes, void* stream) {
+                                      size_t ws_bytes, int32_t* dev_status, void* stream) {
   using namespace moe;
   using namespace moe::few;
   if (T < 0 || !w4_shape_ok(0, N, K, group) || x_stride < K || x_stride % 8 || out_stride < N ||
@@ -296,25 +310,18 @@ extern "C" moe_status_t moe_linear_w4(const uint16_t* x, int T, int K, long long
   a.bias = bias;
   a.out = out;
   a.out_f32 = out_f32;
-  a.part_count = static_cast<int32_t*>(ws);
-  const int ctas = num_sms();
-  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align256(4 * (size_t)ctas * WARPS));
   a.st.k = K;
   a.st.nsl = (int)w4_slices(K);
   a.st.step = 2048;
-  a.st.row8 = 1024;
+  a.st.pitch = 128;
   a.st.half = (long long)a.st.nsl * 2048;
   a.st.sc_half = (long long)a.st.nsl * 8 * (256 / group);
-  a.tiles = (int)ceil_div(N, 32);
-  a.F = ceil_div(T, LIN_COLS) * a.tiles * a.st.nsl;
-  a.W = workers_for(a.F, ctas * WARPS, 1);
+  a.blocks = (int)ceil_div(T, LIN_COLS);
+  const long long tiles = ceil_div(N, 32) * a.blocks;
+  if (tiles > 0x7fffffffll) return MOE_ERR_ARG;
+  a.tiles = (int)tiles;
+  a.st.cut(LIN_WARPS, a.tiles <= num_sms());
+  a.dev_status = dev_status;
   cudaStream_t st = as_stream(stream);
-  if (group == 32)
-    linear_w4_kernel<32><<<ctas, THREADS, 0, st>>>(a);
-  else if (group == 64)
-    linear_w4_kernel<64><<<ctas, THREADS, 0, st>>>(a);
-  else
-    linear_w4_kernel<128><<<ctas, THREADS, 0, st>>>(a);
-  MOE_CHECK_LAUNCH();
-  return MOE_OK;
+  return group == 32 ? launch_linear<32>(a, st) : group == 64 ? launch_linear<64>(a, st) : launch_linear<128>(a, st);
 }

@@ -1,5 +1,5 @@
 // moe_route_hidden: router logits from hidden states, top-k and weights in one launch.
-// The warps share out (expert, up to 4 tokens); the CTA that finishes last selects.  Bound:
+// The warps share out the tasks of route_few.cuh; the CTA that finishes last selects.  Bound:
 // reading the router matrix (2 * E * H bytes) once; at these sizes it is in L2 and the
 // time is latency.
 #include <algorithm>
@@ -15,8 +15,9 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_hidden_kernel(
     const uint16_t* x, const uint16_t* wr, const float* bias, int T, int H, int E, int K, const int32_t* num_tokens,
     float* logits, int32_t* topk_idx, float* topk_w, uint32_t* count) {
   __shared__ bool last;
+  __shared__ float2 scratch[ROUTE_WARPS][ROUTE_TOKENS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  router_logits(x, wr, bias, T, H, E, logits, warp * gridDim.x + blockIdx.x, gridDim.x * ROUTE_WARPS, lane);
+  router_logits<ROUTE_WARPS>(x, wr, bias, T, H, E, logits, scratch, blockIdx.x, gridDim.x, warp, lane);
   __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) last = atomicAdd(count, 1u) == gridDim.x - 1;
@@ -54,7 +55,7 @@ extern "C" moe_status_t moe_route_hidden(const uint16_t* x, int T, int H, const 
   if (T == 0) return MOE_OK;
   if (!x || !w_router || !logits || !topk_idx || !topk_w) return MOE_ERR_ARG;
   if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w_router)) & 15) return MOE_ERR_ARG;
-  const int tasks = E * (T == 1 ? 1 : (T + 3) / 4);
+  const int tasks = E * ((T + ROUTE_TOKENS - 1) / ROUTE_TOKENS);
   const int ctas = std::min(tasks, num_sms() * 2);
   route_hidden_kernel<<<ctas, ROUTE_WARPS * 32, 0, as_stream(stream)>>>(
       x, w_router, bias, T, H, E, K, num_tokens, logits, topk_idx, topk_w, static_cast<uint32_t*>(ws));

@@ -532,13 +532,14 @@ moe_status_t moe_pack_w4(const uint8_t* q, const uint16_t* scales, const uint8_t
  *   bias       nullable float32 [N].
  *   out        BF16 (out_f32 = 0) or float32 (1) [T, N], row t at out + t * out_stride (>= N).
  *   ws         moe_linear_w4_workspace_bytes(T, N, K) bytes, 256-byte aligned, zero at first use.
+ *   dev_status nullable; MOE_DEV_PIPELINE_TIMEOUT if a wait within the kernel gave up.
  * Any N >= 1 (mats = 1), K % 128 == 0.  The result does not depend on timing.
  * Errors: MOE_ERR_ARG, MOE_ERR_WORKSPACE. */
 size_t moe_linear_w4_workspace_bytes(int T, int N, int K);
 moe_status_t moe_linear_w4(const uint16_t* x, int T, int K, long long x_stride, const uint8_t* q_packed,
                            const uint16_t* scales_packed, const uint8_t* zeros_packed, int N, int group,
                            const float* bias, void* out, int out_f32, long long out_stride, void* ws,
-                           size_t ws_bytes, void* stream);
+                           size_t ws_bytes, int32_t* dev_status, void* stream);
 
 /* The router from hidden states, T <= MOE_FEW_MAX_TOKENS:
  *   logits[t, e] = float32(sum_h x[t, h] * w_router[e, h] + bias[e]), the sum carried to about
@@ -564,7 +565,7 @@ moe_status_t moe_route_hidden(const uint16_t* x, int T, int H, const uint16_t* w
  * timing.  Not offered here: fake-quantisation, router weights in the down projection. */
 typedef struct {
   int T;              /* tokens of the call, 0..MOE_FEW_MAX_TOKENS */
-  int H, I, E, K;     /* as moe_layer_desc_t */
+  int H, I, E, K;     /* as moe_layer_desc_t; H and I at most 131072 */
   moe_dtype_t dtype;  /* MOE_BF16; MOE_E4M3 (weights with 128x128 scales); MOE_W4 (packed) */
   int has_shared;     /* 1: one shared expert of the same I and format */
   int weight_tiles;   /* 1: BF16 / E4M3 weights in the tile layout of moe_pack_weights */

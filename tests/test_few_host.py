@@ -52,7 +52,7 @@ def test_linear_refusals(lib):
     assert ws > 0 and lib.moe_linear_w4_workspace_bytes(-1, 64, 256) == 0
     names = ("x", "T", "K", "xs", "q", "s", "z", "N", "group", "b", "out", "f32", "os", "ws", "nws")
     d = dict(x=A, T=4, K=256, xs=256, q=A, s=A, z=None, N=64, group=64, b=None, out=A, f32=0, os=64, ws=A, nws=ws)
-    f = lambda **k: lib.moe_linear_w4(*[{**d, **k}[n] for n in names], None)
+    f = lambda **k: lib.moe_linear_w4(*[{**d, **k}[n] for n in names], None, None)
     for bad in (dict(T=-1), dict(K=100), dict(xs=248), dict(xs=260), dict(os=63), dict(group=48), dict(N=0), dict(f32=2),
                 dict(x=None), dict(q=None), dict(s=None), dict(out=None), dict(x=A + 8), dict(q=A + 16), dict(s=A + 8),
                 dict(z=A + 4), dict(out=A + 1), dict(b=A + 2), dict(ws=A + 64)):

@@ -91,7 +91,7 @@ def test_linear_w4(T, N, K, group, zeros, bias, f32):
     assert y.dtype == dt and ref.close(y, want, err) <= 1
     again = moe.moe_linear_w4(x, p, bias=b, out_dtype=dt, ws=ws)
     assert torch.equal(again, y)
-    assert not ws[:4 * 152 * 16].any()          # the counters are zero again
+    assert not ws.any()          # the counters are zero again
 
 
 def test_linear_w4_strides_and_out():
