@@ -42,13 +42,12 @@ class LayerWeights(ctypes.Structure):
 
 class FewDesc(ctypes.Structure):
     _fields_ = [("T", _I), ("H", _I), ("I", _I), ("E", _I), ("K", _I), ("dtype", _I), ("has_shared", _I),
-                ("weight_tiles", _I), ("group", _I)]
+                ("weight_tiles", _I), ("group", _I), ("zeros", _I)]
 
 
 class FewWeights(ctypes.Structure):
-    _fields_ = [(n, _P) for n in ("w13", "w13_scales", "w13_zeros", "w2", "w2_scales", "w2_zeros", "shared_w13",
-                                  "shared_w13_scales", "shared_w13_zeros", "shared_w2", "shared_w2_scales",
-                                  "shared_w2_zeros", "w_router", "router_bias")]
+    _fields_ = [(n, _P) for n in ("w13", "w13_scales", "w2", "w2_scales", "shared_w13", "shared_w13_scales", "shared_w2",
+                                  "shared_w2_scales", "w_router", "router_bias")]
 
 
 class LayerViews(ctypes.Structure):
@@ -92,10 +91,10 @@ _SIGS = {
     "moe_layer_forward": ([ctypes.POINTER(LayerDesc), ctypes.POINTER(LayerWeights), _P, _P, _P, _P, _P, _P, _P,
                            _P, _P, _Z, _P, _P], _I),
     "moe_quantize_weight_w4": ([_P, _I, _I, _I, _I, _P, _P, _P, _P], _I),
-    "moe_w4_packed_bytes": ([_I, _I], _Z),
-    "moe_pack_w4": ([_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P], _I),
+    "moe_w4_packed_bytes": ([_I, _I, _I, _I], _Z),
+    "moe_pack_w4": ([_P, _P, _P, _I, _I, _I, _I, _P, _P], _I),
     "moe_linear_w4_workspace_bytes": ([_I, _I, _I], _Z),
-    "moe_linear_w4": ([_P, _I, _I, _L, _P, _P, _P, _I, _I, _P, _P, _I, _L, _P, _Z, _P, _P], _I),
+    "moe_linear_w4": ([_P, _I, _I, _L, _P, _I, _I, _I, _P, _P, _I, _L, _P, _Z, _P, _P], _I),
     "moe_route_hidden_workspace_bytes": ([], _Z),
     "moe_route_hidden": ([_P, _I, _I, _P, _P, _I, _I, _P, _P, _P, _P, _P, _Z, _P], _I),
     "moe_layer_few_workspace_bytes": ([ctypes.POINTER(FewDesc)], _Z),
@@ -473,18 +472,16 @@ class MoeLayer:
 # ------------------------------------------------------------------------ a few tokens
 class W4Packed:
     """4-bit weights in the kernels' order (moe_pack_w4): `mats` matrices of N rows, K columns,
-    scales per `group` columns, zero points or not.  [i] is one matrix of a stack."""
+    scales per `group` columns, zero points or not; data uint8 [mats, bytes].  [i] is one
+    matrix of a stack."""
 
-    def __init__(self, q, scales, zeros, mats, N, K, group):
-        self.q, self.scales, self.zeros = q, scales, zeros
-        self.mats, self.N, self.K, self.group = mats, N, K, group
+    def __init__(self, data, mats, N, K, group, zeros):
+        self.data, self.mats, self.N, self.K, self.group, self.zeros = data, mats, N, K, group, zeros
 
     def __getitem__(self, i):
-        if not -self.mats <= i < self.mats:
+        if not 0 <= i < self.mats:
             raise IndexError(i)
-        return W4Packed(self.q[i:i + 1] if i != -1 else self.q[i:], self.scales[i:i + 1] if i != -1 else self.scales[i:],
-                        None if self.zeros is None else self.zeros[i:i + 1] if i != -1 else self.zeros[i:], 1, self.N,
-                        self.K, self.group)
+        return W4Packed(self.data[i:i + 1], 1, self.N, self.K, self.group, self.zeros)
 
 
 def moe_quantize_weight_w4(w, group, zeros=False, stream=None):
@@ -517,14 +514,11 @@ def moe_pack_w4(q, scales, zeros=None, stream=None):
         raise ValueError("zeros are uint8 with the shape of scales")
     if group * kg != K:
         raise ValueError("the scales' rows do not divide K")
-    nbytes = lib().moe_w4_packed_bytes(N, K)
-    n = nbytes * 2 // group
-    qp = torch.empty(mats, nbytes, dtype=torch.uint8, device=q.device)
-    sp = torch.empty(mats, n, dtype=torch.bfloat16, device=q.device)
-    zp = torch.empty(mats, n, dtype=torch.uint8, device=q.device) if zeros is not None else None
-    _check("moe_pack_w4", lib().moe_pack_w4(_ptr(q), _ptr(scales), _ptr(zeros), mats, N, K, group, _ptr(qp), _ptr(sp),
-                                            _ptr(zp), _stream(stream)))
-    return W4Packed(qp, sp, zp, mats, N, K, group)
+    nbytes = lib().moe_w4_packed_bytes(N, K, group, int(zeros is not None))
+    data = torch.empty(mats, nbytes, dtype=torch.uint8, device=q.device)
+    _check("moe_pack_w4", lib().moe_pack_w4(_ptr(q), _ptr(scales), _ptr(zeros), mats, N, K, group, _ptr(data),
+                                            _stream(stream)))
+    return W4Packed(data, mats, N, K, group, zeros is not None)
 
 
 def _zeroed(nbytes, device):
@@ -552,8 +546,7 @@ def moe_linear_w4(x, w, bias=None, out=None, out_dtype=torch.bfloat16, ws=None, 
     if ws is None:
         ws = moe_linear_w4_workspace(T, w.N, K, x.device)
     _check("moe_linear_w4", lib().moe_linear_w4(
-        x.data_ptr(), T, K, x.stride(0) if T > 1 else K, w.q.data_ptr(), w.scales.data_ptr(), _ptr(w.zeros), w.N,
-        w.group, _ptr(bias), out.data_ptr(), int(out.dtype == torch.float32), out.stride(0) if T > 1 else w.N,
+        x.data_ptr(), T, K, x.stride(0) if T > 1 else K, w.data.data_ptr(), w.N, w.group, w.zeros, _ptr(bias), out.data_ptr(), int(out.dtype == torch.float32), out.stride(0) if T > 1 else w.N,
         ws.data_ptr(), ws.numel(), _ptr(dev_status), _stream(stream)))
     return out
 
@@ -590,22 +583,22 @@ class MoeLayerFew:
     """The layer for up to T tokens (T <= MOE_FEW_MAX_TOKENS) in one launch: moe_layer_few with the
     weight pointers, descriptor and workspace of one model layer.  Weights as MoeLayer's: BF16
     or E4M3 tensors (weight_tiles=True: already in the layout of moe_pack_weights, as
-    MoeLayer.tensors holds them), or W4Packed for MOE_W4 (scales and zeros inside, or
-    given apart).  w_router [E, H] (+ router_bias [E]): forward routes by itself."""
+    MoeLayer.tensors holds them), or W4Packed for MOE_W4.  w_router [E, H] (+ router_bias [E]): forward routes by itself."""
 
     def __init__(self, T, H, I, E, K, dtype=MOE_BF16, w13=None, w2=None, shared_w13=None, shared_w2=None,
                  w13_scales=None, w2_scales=None, shared_w13_scales=None, shared_w2_scales=None, w_router=None,
                  router_bias=None, weight_tiles=False, device="cuda"):
-        group = w13.group if dtype == MOE_W4 else 0
-        if dtype == MOE_W4:
-            for m, n, k in ((w13, 2 * I, H), (w2, H, I), (shared_w13, 2 * I, H), (shared_w2, H, I)):
-                if m is not None and (m.N, m.K, m.group) != (n, k, group):
-                    raise ValueError("a packed matrix has another shape or group than the layer")
-        self.desc = FewDesc(T, H, I, E, K, dtype, int(shared_w13 is not None), int(weight_tiles), group)
+        w4 = dtype == MOE_W4
+        if w4:
+            for m, e, n, k in ((w13, E, 2 * I, H), (w2, E, H, I), (shared_w13, 1, 2 * I, H), (shared_w2, 1, H, I)):
+                if m is not None and (m.mats, m.N, m.K, m.group, m.zeros) != (e, n, k, w13.group, w13.zeros):
+                    raise ValueError("a packed matrix has another shape, group or zero points than the layer")
+        self.desc = FewDesc(T, H, I, E, K, dtype, int(shared_w13 is not None), int(weight_tiles),
+                            w13.group if w4 else 0, int(w13.zeros) if w4 else 0)
         parts = []
         for m, s in ((w13, w13_scales), (w2, w2_scales), (shared_w13, shared_w13_scales),
                      (shared_w2, shared_w2_scales)):
-            parts += [m.q, m.scales, m.zeros] if isinstance(m, W4Packed) else [m, s, None]
+            parts += [m.data if isinstance(m, W4Packed) else m, s]
         self.tensors = parts + [w_router, router_bias]
         self.weights = FewWeights(*(_ptr(t) for t in self.tensors))
         nbytes = lib().moe_layer_few_workspace_bytes(ctypes.byref(self.desc))

@@ -9,18 +9,24 @@
 // tensor-core limit, which is why these kernels do not use the 128-row tcgen05 tiles.
 //
 // Work is cut into items: 32 weight rows (a row tile) x 128 bytes of K, 4 KB; a few neighbouring
-// items of a tile are a unit.  A CTA (one per SM) takes whole tiles, one after the other,
-// and its worker warps take the units of that sequence in turn, each running ahead on its own:
-// a warp copies its items with cp.async into a ring of its own in shared memory, whole
-// 128-byte lines, ahead of their use, across units and tiles.  The K order inside a line is
-// whatever the lanes hold, since a dot product does not care and the activations are read in
-// the same order.  The sums of a tile's units are joined in shared memory by the warp that
-// finishes last, in unit order, so the result does not depend on who was last.
+// items of a tile are a unit.  A CTA (one per SM) takes whole tiles, one after the other.  Its
+// scheduler warp writes down each unit (where it lies, whose it is) as its workers come near it,
+// and the worker warps take units as they get free.  A worker's items arrive by TMA in a ring
+// of its own in shared memory, one ahead of the one in use, across units and tiles.  The K
+// order inside a 128-byte line is whatever the lanes hold, since a dot product does not care and
+// the activations are read in the same order.  The sums of a tile's units are joined in shared
+// memory by the warp that finishes last, in unit order, so the result does not depend on who
+// was last.
+//
+// Measured with the copies alone (15 warps, two 4 KB stages each, two boxes of 16 rows an item):
+// 7.1 TB/s over 1.6 GB and 6.8 over 0.4 GB, row-major or tiled; three stages no faster; per-warp
+// cp.async of the same items 5.2 to 6.5 with three times the instructions; one warp feeding
+// the SM with 512-byte bulk copies 2.1.
 #pragma once
 
 #include <cuda_fp16.h>
 
-#include "common.cuh"
+#include "gemm_common.cuh"
 
 namespace moe {
 namespace few {
@@ -42,6 +48,7 @@ __device__ __forceinline__ bool wait_for(Done done, int32_t* dev_status) {
   if (done()) return true;
   const unsigned long long t0 = clock_ns();
   while (!done()) {
+    __nanosleep(40);     // a waiting warp leaves the issue slots to the others
     if (clock_ns() - t0 > TIMEOUT_NS) {
       if (dev_status) atomicOr(dev_status, MOE_DEV_PIPELINE_TIMEOUT);
       return false;
@@ -111,78 +118,51 @@ __device__ __forceinline__ void w4_pairs(uint32_t v, const W4Zero<HALF>& z, uint
 }
 
 // --------------------------------------------------------------------------------- items
-// Where one row tile's items begin in memory.
-struct Tile {
-  const uint8_t* w;    // first row of the first half tile, at the unit's first slice
-  const void* sc;      // E4M3: scale of the first half tile's block; W4: scales of its row block
-  const void* zp;      // W4 zero points, or null
-};
-// One phase's matrices: constant strides, and how its tiles are cut into units.
-struct Strides {
-  long long step;      // bytes from one slice to the next
-  long long pitch;     // bytes from one row of a half tile to the next
-  long long half;      // bytes from the first half tile (16 rows) to the second
-  long long sc_half;   // scale elements (E4M3 floats; W4 two-row words) to the second half tile
-  int k;               // columns
-  int nsl;             // slices (items) per tile
-  int len, parts;      // items per unit (fewer in the last), units per tile
-  // at most `most` units, of at least two items unless there is little work
-  __host__ __device__ __forceinline__ void cut(int most, bool little) {
+// How the tiles of a phase are cut: units of `len` items, `parts` to a tile (at most `most`), of
+// at least four items unless there is little work.
+struct Cut {
+  int nsl, len, parts;
+  __host__ __device__ __forceinline__ void set(int items, int most, bool little) {
+    nsl = items;
     len = (nsl + most - 1) / most;
-    if (len < 2 && !little && nsl > 1) len = 2;
+    if (len < 4 && !little) len = nsl < 4 ? nsl : 4;
     parts = (nsl + len - 1) / len;
   }
+};
+
+// One unit, as the scheduler writes it down.  BF16 and E4M3 items are boxes of a tensor map (128
+// bytes of column, rows y0.. and y1.. for the two half tiles; per item x or the rows go on by dx,
+// dy); W4 items are two blocks at p0 and p1.  E4M3: p0, p1 are the half tiles' scales.
+struct __align__(16) Unit {
+  const uint8_t *p0, *p1;
+  const CUtensorMap* map;
+  int x, y0, y1;
+  int entry, row;
+  short s0, n, part, parts;
+  int down;            // layer: phase 2
 };
 
 template <int FMT, int GROUP>
 struct Format {
   static constexpr int KI = FMT == F_BF16 ? 64 : FMT == F_E4M3 ? 128 : 256;   // columns per item
   static constexpr int NG = FMT == F_W4 ? 256 / GROUP : 1;                    // W4 scale groups per slice
-  static constexpr int SC = FMT == F_W4 ? 8 * NG * 4 : 16;                    // scale bytes of a half tile
-  static constexpr int ZP = FMT == F_W4 ? 8 * NG * 2 : 0;                     // zero-point bytes of a half tile
+  static constexpr int SC = 8 * NG * 4;                                       // W4 scale bytes of a block
+  static constexpr int ZP = 8 * NG * 2;                                       // W4 zero-point bytes of a block
   static constexpr int HALF_CHUNKS = FMT == F_BF16 ? 1 : FMT == F_E4M3 ? 2 : 4;
-  static constexpr int STAGE = FMT == F_BF16 ? 4096 : 4096 + 2 * (SC + ZP);
+  static constexpr int HALF = FMT == F_W4 ? 2048 + SC + ZP : 2048;            // bytes of a half tile in a stage
+  static constexpr int STAGE = 2 * HALF;
 };
-
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// The packed 4-bit layout (moe_pack_w4): blocks of 16 rows x 256 columns -- 2 KB of codes, the
+// scales, the zero points if there are any -- row block major.
+__host__ __device__ __forceinline__ int w4_slices(int k) { return (k + 255) / 256; }
+__host__ __device__ __forceinline__ int w4_block(int group, bool zeros) {
+  return 2048 + 8 * (256 / group) * (zeros ? 6 : 4);
 }
 
-// One warp copies one item into its stage: 32 rows x 128 bytes, each instruction four whole
-// lines.  16-byte chunk c of row r goes to chunk c ^ (r & 1), so that the reads below (two rows x
-// every other chunk per 8 lanes) touch every bank once.
-template <int FMT, int GROUP>
-__device__ __forceinline__ void copy_item(uint32_t stage, const Tile& c, long long pitch, long long half,
-                                          long long sc_half, int lane) {
-  using F = Format<FMT, GROUP>;
-  const int r = lane >> 3, ch = lane & 7;
-  const uint8_t* p = c.w + r * pitch + ch * 16;
-  const uint32_t d = stage + r * 128 + ((ch ^ (r & 1)) << 4);
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) cp16(d + h * 2048 + q * 512, p + h * half + q * 4 * pitch);
-  if constexpr (FMT == F_E4M3) {
-    if (lane < 2) cp4(stage + 4096 + lane * 16, static_cast<const float*>(c.sc) + lane * sc_half);
-  }
-  if constexpr (FMT == F_W4) {
-    constexpr int N = F::SC / 16;   // chunks per half tile
-    if (lane < 2 * N)
-      cp16(stage + 4096 + lane * 16, reinterpret_cast<const uint8_t*>(static_cast<const uint32_t*>(c.sc) +
-                                                                      (lane / N) * sc_half) + (lane % N) * 16);
-    if (c.zp && lane < N)
-      cp16(stage + 4096 + 2 * F::SC + lane * 16,
-           reinterpret_cast<const uint8_t*>(static_cast<const uint16_t*>(c.zp) + (lane / (N / 2)) * sc_half) +
-               (lane % (N / 2)) * 16);
-  }
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
 }
 
 // Sums of one row tile: [8-column group][half tile][fragment: rows g, g (+1 column), g + 8, g + 8].
@@ -231,13 +211,17 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 
 
 // Half an item: sums += weights x activations.  acc: E4M3 sums of the item so far, unscaled.
 template <int FMT, int GROUP, bool HALF, int NT, int PASSES, int J, class Acts>
-__device__ __forceinline__ void half_item(Sums<NT>& sums, Sums<NT>& acc, const uint8_t* stage, Acts acts, int g, int t,
+__device__ __forceinline__ void half_item(Sums<NT>& sums, Sums<NT>& acc, const uint8_t* stage, Acts acts, int lane,
                                           bool zeros) {
   using F = Format<FMT, GROUP>;
+  const int g = lane >> 2, t = lane & 3;
   uint4 q[4];                      // rows g, g + 8 of the first half tile, then of the second
-  const uint8_t* base = stage + g * 128 + (((2 * t + J) ^ (g & 1)) << 4);
+  // boxes come with TMA's 128-byte swizzle (16-byte chunk c of row r at c ^ (r & 7)), packed
+  // blocks in lane order: 8 lanes touch every bank once either way
+  const uint8_t* base = stage + (FMT == F_W4 ? J * 512 + lane * 16 : g * 128 + (((2 * t + J) ^ g) << 4));
 #pragma unroll
-  for (int r = 0; r < 4; ++r) q[r] = *reinterpret_cast<const uint4*>(base + r * 1024);
+  for (int r = 0; r < 4; ++r)
+    q[r] = *reinterpret_cast<const uint4*>(base + (r >> 1) * F::HALF + (r & 1) * 1024);
   if constexpr (FMT == F_BF16) {
     uint32_t a[4][4];
 #pragma unroll
@@ -262,12 +246,12 @@ __device__ __forceinline__ void half_item(Sums<NT>& sums, Sums<NT>& acc, const u
   } else {
     // word j of the lane's 8 holds columns j*32 + t*8 .. + 8
     constexpr int WPG = GROUP / 32;   // words per scale group
-    const uint32_t* scales = reinterpret_cast<const uint32_t*>(stage + 4096) + g * F::NG;
-    const uint16_t* zps = reinterpret_cast<const uint16_t*>(stage + 4096 + 2 * F::SC) + g * F::NG;
+    const uint32_t* scales = reinterpret_cast<const uint32_t*>(stage + 2048) + g * F::NG;
+    const uint16_t* zps = reinterpret_cast<const uint16_t*>(stage + 2048 + F::SC) + g * F::NG;
 #pragma unroll
     for (int i0 = 0; i0 < 4; i0 += WPG) {
       const int gi = (4 * J + i0) / WPG;
-      const uint32_t za = zeros ? zps[gi] : 0x0808u, zb = zeros ? zps[F::ZP / 2 + gi] : 0x0808u;
+      const uint32_t za = zeros ? zps[gi] : 0x0808u, zb = zeros ? zps[F::HALF / 2 + gi] : 0x0808u;
       const W4Zero<HALF> z[4] = {{za, 0}, {za, 1}, {zb, 0}, {zb, 1}};
       Sums<NT> part;
       part.clear();
@@ -283,7 +267,7 @@ __device__ __forceinline__ void half_item(Sums<NT>& sums, Sums<NT>& acc, const u
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t sc = scales[h * (F::SC / 4) + gi];
+        const uint32_t sc = scales[h * (F::HALF / 4) + gi];
         const float s0 = bf_lo(sc), s1 = bf_hi(sc);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -297,102 +281,144 @@ __device__ __forceinline__ void half_item(Sums<NT>& sums, Sums<NT>& acc, const u
   }
 }
 
-// -------------------------------------------------------------------------------- stream
-// A CTA's sequence of tiles, as one worker warp sees it.  Src says what the sequence is:
-//   tile(q)            number of the CTA's q-th tile, negative past the end (may wait);
-//   strides(tile)      the strides and the cut of its phase;
-//   where(tile, s0)    where its items begin at slice s0;  zeros().
-// Units are counted over the sequence; worker w of WORKERS takes units w, w + WORKERS, ...  Its ring
-// of STAGES stages is filled STAGES - 1 items ahead of their use.
-template <int FMT, int GROUP, bool HALF, int STAGES, int WORKERS, class Src>
+// -------------------------------------------------------------------------------- feed
+constexpr int FEED = 64;             // units written down at a time
+constexpr int AHEAD = 40;            // ... past the slowest worker's
+template <int WORKERS>
+struct Feed {
+  Unit unit[FEED];
+  int published;                     // units written down so far
+  int total;                         // units of the CTA, once known
+  int next;                          // unit to take next
+  int use[WORKERS];                  // unit each worker is at
+  unsigned long long full[WORKERS][2];
+};
+template <int WORKERS>
+__device__ __forceinline__ void feed_init(Feed<WORKERS>& f) {
+  if (threadIdx.x == 0) {
+    f.published = 0;
+    f.total = 0x7fffffff;
+    f.next = 0;
+    for (int i = 0; i < WORKERS; ++i)
+      for (int j = 0; j < 2; ++j) gg::mbar_init(gg::smem_u32(&f.full[i][j]), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (threadIdx.x < WORKERS) f.use[threadIdx.x] = 0;
+}
+
+// A worker warp's stream of units: take() moves to the next one (false at the end), run() multiplies
+// it.  The item after the one in use is always on its way.
+template <int FMT, int GROUP, bool HALF, int WORKERS>
 struct Stream {
   using F = Format<FMT, GROUP>;
-  const Src& src;
-  uint8_t* ring;
-  uint32_t ring_addr;
-  int lane;
-  int in, out;                 // stage to fill next, stage to use next
-  struct Cursor {
-    int u, q, part, tile;      // unit, its place in the sequence, its part of the tile (number < 0: the end)
-  } fillc, usec;
-  int left;                    // items left of the unit being filled
-  Tile c;
-  long long step, pitch, half, sc_half;
+  Feed<WORKERS>& feed;
+  uint8_t* ring;               // two stages
+  uint32_t ring_addr, bars;    // shared addresses of the ring and of its two barriers
+  int lane, worker;
+  int32_t* dev_status;
+  int dx, dy;                  // tensor maps: from one item to the next
+  int block;                   // W4: bytes of a block
+  bool zeros;
+  int stage;                   // of the item in use: bit 0, and its barriers' phase above
+  int filled;                  // unit of the item on its way, or past the end
+  int left, x, y0, y1;         // its items still to be asked for, and where they are
+  const uint8_t *p0, *p1;
+  const CUtensorMap* map;
+  int cur;                     // unit in use
+  bool dead;                   // a wait gave up
 
-  __device__ __forceinline__ Stream(const Src& s, uint8_t* r, int worker, int lane_)
-      : src(s), ring(r), lane(lane_), in(0), out(0) {
-    ring_addr = static_cast<uint32_t>(__cvta_generic_to_shared(r));
-    fillc.u = worker;
-    fillc.q = 0;
-    fillc.part = worker;
-    settle(fillc);
-    usec = fillc;
-    open();
-#pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) fill();
-  }
-  // from a part that may be past its tile to the tile it falls to
-  __device__ __forceinline__ void settle(Cursor& k) const {
-    while (true) {
-      k.tile = src.tile(k.q);
-      if (k.tile < 0) return;
-      const int n = src.strides(k.tile).parts;
-      if (k.part < n) return;
-      k.part -= n;
-      ++k.q;
+  // the next unit off the feed, for filling
+  __device__ __forceinline__ void grab() {
+    int u = 0;
+    if (lane == 0) u = atomicAdd(&feed.next, 1);
+    u = __shfl_sync(0xffffffffu, u, 0);
+    volatile int *published = &feed.published, *total = &feed.total;
+    if (!wait_for([&] { return *published > u || *total <= u; }, dev_status)) dead = true;
+    __threadfence_block();
+    filled = u;
+    if (dead || *total <= u) {
+      filled = 0x7fffffff;
+      return;
+    }
+    const Unit& k = feed.unit[u & (FEED - 1)];
+    left = k.n;
+    p0 = k.p0;
+    p1 = k.p1;
+    if constexpr (FMT != F_W4) {
+      x = k.x;
+      y0 = k.y0;
+      y1 = k.y1;
+      map = k.map;
     }
   }
-  __device__ __forceinline__ void hop(Cursor& k) const {
-    k.u += WORKERS;
-    k.part += WORKERS;
-    settle(k);
-  }
-  __device__ __forceinline__ void open() {
-    if (fillc.tile < 0) return;
-    const Strides& st = src.strides(fillc.tile);
-    const int s0 = fillc.part * st.len;
-    left = min(st.len, st.nsl - s0);
-    step = st.step;
-    pitch = st.pitch;
-    half = st.half;
-    sc_half = st.sc_half;
-    c = src.where(fillc.tile, s0);
-  }
-  __device__ __forceinline__ void fill() {
-    if (fillc.tile >= 0) {
-      copy_item<FMT, GROUP>(ring_addr + in * F::STAGE, c, pitch, half, sc_half, lane);
-      if (--left > 0) {
-        c.w += step;
-        if constexpr (FMT == F_E4M3) c.sc = static_cast<const float*>(c.sc) + 1;
-        if constexpr (FMT == F_W4) {
-          c.sc = static_cast<const uint32_t*>(c.sc) + 8 * F::NG;
-          if (c.zp) c.zp = static_cast<const uint16_t*>(c.zp) + 8 * F::NG;
-        }
+  __device__ __forceinline__ void fill(int st) {
+    if (left == 0) {
+      if (filled == 0x7fffffff) return;
+      grab();
+      if (filled == 0x7fffffff) return;
+    }
+    if (lane == 0) {
+      const uint32_t d = ring_addr + st * F::STAGE, bar = bars + st * 8;
+      if constexpr (FMT == F_W4) {
+        gg::mbar_expect_tx(bar, 2 * block);
+        bulk_load(d, p0, block, bar);
+        bulk_load(d + F::HALF, p1, block, bar);
       } else {
-        hop(fillc);
-        open();
+        gg::mbar_expect_tx(bar, 4096);
+        gg::tma_load_2d(d, map, x, y0, bar);
+        gg::tma_load_2d(d + 2048, map, x, y1, bar);
       }
     }
-    cp_commit();
-    in = in + 1 == STAGES ? 0 : in + 1;
+    if constexpr (FMT == F_W4) {
+      p0 += block;
+      p1 += block;
+    } else {
+      x += dx;
+      y0 += dy;
+      y1 += dy;
+    }
+    --left;
   }
-  // The items of the unit at usec: sums = weights x activations.  x0[p][n] is this lane's column
-  // of group n, or null; PASSES sets of columns are added into the same sums.
+  __device__ __forceinline__ void start() {
+    stage = 0;
+    left = 0;
+    filled = 0;
+    dead = false;
+    fill(0);
+  }
+  __device__ __forceinline__ bool take() {
+    cur = filled;
+    if (dead || cur == 0x7fffffff) return false;
+    if (lane == 0) *static_cast<volatile int*>(&feed.use[worker]) = cur;
+    return true;
+  }
+  __device__ __forceinline__ const Unit& unit() const { return feed.unit[cur & (FEED - 1)]; }
+  __device__ __forceinline__ void finish() {
+    if (lane == 0) *static_cast<volatile int*>(&feed.use[worker]) = 0x7fffff00;
+  }
+
+  // sums = weights x activations over the unit in use.  x0[p][n] is this lane's column of group n,
+  // or null; PASSES sets of columns are added into the same sums.  k: columns of the matrix.
   template <int NT, int PASSES>
-  __device__ __forceinline__ void run(Sums<NT>& sums, const Strides& st, const uint16_t* const (&x0)[PASSES][NT]) {
-    const int g = lane >> 2, t = lane & 3;
-    const int s0 = usec.part * st.len, n = min(st.len, st.nsl - s0);
-    const uint16_t* x[PASSES][NT];
+  __device__ __forceinline__ void run(Sums<NT>& sums, int k, const uint16_t* const (&x0)[PASSES][NT]) {
+    const int t = lane & 3;
+    const Unit& un = unit();
+    const int s0 = un.s0, n = un.n;
+    const uint16_t* xp[PASSES][NT];
 #pragma unroll
     for (int p = 0; p < PASSES; ++p)
 #pragma unroll
-      for (int i = 0; i < NT; ++i) x[p][i] = x0[p][i] ? x0[p][i] + (long long)s0 * F::KI : nullptr;
-    int kleft = st.k - s0 * F::KI;
-    const bool zeros = src.zeros();
+      for (int i = 0; i < NT; ++i) xp[p][i] = x0[p][i] ? x0[p][i] + (long long)s0 * F::KI : nullptr;
+    int kleft = k - s0 * F::KI;
+    const float *sc0 = nullptr, *sc1 = nullptr;
+    if constexpr (FMT == F_E4M3) {
+      sc0 = reinterpret_cast<const float*>(un.p0);
+      sc1 = reinterpret_cast<const float*>(un.p1);
+    }
     sums.clear();
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
-      fill();
+      fill((stage ^ 1) & 1);
       // few columns: the item's activations are on their way before its weights are waited for
       constexpr bool EARLY = F::HALF_CHUNKS * NT * PASSES <= 4;
       uint4 early[EARLY ? 2 * F::HALF_CHUNKS : 1][PASSES][NT];
@@ -401,7 +427,12 @@ struct Stream {
         for (int q = 0; q < 2 * F::HALF_CHUNKS; ++q)
 #pragma unroll
           for (int p = 0; p < PASSES; ++p)
-            load_acts<FMT, NT>(early[q][p], x[p], q / F::HALF_CHUNKS, q % F::HALF_CHUNKS, t, kleft);
+            load_acts<FMT, NT>(early[q][p], xp[p], q / F::HALF_CHUNKS, q % F::HALF_CHUNKS, t, kleft);
+      }
+      float f0 = 1.0f, f1 = 1.0f;
+      if constexpr (FMT == F_E4M3) {
+        f0 = __ldg(sc0 + i);
+        f1 = __ldg(sc1 + i);
       }
       auto acts = [&](uint4(&b)[PASSES][NT], int J, int I) {
 #pragma unroll
@@ -410,39 +441,82 @@ struct Stream {
 #pragma unroll
             for (int q = 0; q < NT; ++q) b[p][q] = early[J * F::HALF_CHUNKS + I][p][q];
           } else {
-            load_acts<FMT, NT>(b[p], x[p], J, I, t, kleft);
+            load_acts<FMT, NT>(b[p], xp[p], J, I, t, kleft);
           }
         }
       };
-      cp_wait<STAGES - 1>();
-      __syncwarp();
-      const uint8_t* stage = ring + out * F::STAGE;
+      const uint32_t bar = bars + (stage & 1) * 8, phase = (stage >> 1) & 1;
+      if (!gg::mbar_try_wait(bar, phase) &&
+          !wait_for([&] { return gg::mbar_try_wait(bar, phase); }, dev_status))
+        dead = true;
+      const uint8_t* st = ring + (stage & 1) * F::STAGE;
       Sums<NT> acc;
       if constexpr (FMT == F_E4M3) acc.clear();
-      half_item<FMT, GROUP, HALF, NT, PASSES, 0>(sums, acc, stage, acts, g, t, zeros);
-      half_item<FMT, GROUP, HALF, NT, PASSES, 1>(sums, acc, stage, acts, g, t, zeros);
+      half_item<FMT, GROUP, HALF, NT, PASSES, 0>(sums, acc, st, acts, lane, zeros);
+      half_item<FMT, GROUP, HALF, NT, PASSES, 1>(sums, acc, st, acts, lane, zeros);
       if constexpr (FMT == F_E4M3) {
         // an item is one 128-column scale block
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float s = *reinterpret_cast<const float*>(stage + 4096 + h * 16);
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int q = 0; q < NT; ++q)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sums.v[q][h][j] = fmaf(s, acc.v[q][h][j], sums.v[q][h][j]);
-        }
+            for (int j = 0; j < 4; ++j) sums.v[q][h][j] = fmaf(h ? f1 : f0, acc.v[q][h][j], sums.v[q][h][j]);
       }
       __syncwarp();     // the stage may be filled again
-      out = out + 1 == STAGES ? 0 : out + 1;
+      ++stage;          // bit 0: the stage; bit 1: its phase
 #pragma unroll
       for (int p = 0; p < PASSES; ++p)
 #pragma unroll
         for (int q = 0; q < NT; ++q)
-          if (x[p][q]) x[p][q] += F::KI;
+          if (xp[p][q]) xp[p][q] += F::KI;
       kleft -= F::KI;
     }
   }
 };
+
+// The scheduler warp.  Src says what the CTA's sequence of tiles is: tile() the next one (its number,
+// negative past the end), cut(tile), describe(tile, part, unit), and idle(), called every time
+// round (true if it got something done).
+template <int WORKERS, class Src>
+__device__ __forceinline__ void schedule(Feed<WORKERS>& f, Src& src, int lane, int32_t* dev_status) {
+  volatile int* use = f.use;
+  int units = 0;
+  bool end = false;
+  unsigned long long t0 = clock_ns();
+  while (!end || !src.done()) {
+    bool moved = src.idle(lane);
+    const int slowest = __reduce_min_sync(0xffffffffu, lane < WORKERS ? use[lane] : 0x7fffffff);
+    if (!end && units < slowest + AHEAD) {
+      const int t = src.tile(lane);
+      if (t < 0) {
+        end = true;
+        if (lane == 0) *static_cast<volatile int*>(&f.total) = units;
+      } else {
+        const Cut c = src.cut(t);
+        if (lane < c.parts) src.describe(t, lane, c, f.unit[(units + lane) & (FEED - 1)]);
+        __threadfence_block();
+        __syncwarp();
+        units += c.parts;
+        if (lane == 0) *static_cast<volatile int*>(&f.published) = units;
+      }
+      moved = true;
+    }
+    if (moved) {
+      t0 = clock_ns();
+    } else {
+      if (__any_sync(0xffffffffu, clock_ns() - t0 > TIMEOUT_NS)) {   // let the workers go
+        if (lane == 0) {
+          if (dev_status) atomicOr(dev_status, MOE_DEV_PIPELINE_TIMEOUT);
+          if (!end) *static_cast<volatile int*>(&f.total) = units;
+        }
+        src.give_up(lane);
+        return;
+      }
+      __nanosleep(60);
+    }
+  }
+}
 
 // ---------------------------------------------------------------------------------- join
 constexpr int MAX_SLOTS = 48;
@@ -512,9 +586,6 @@ __device__ __forceinline__ bool join(Sums<NT>& sums, JoinShared& j, float4* part
 // ---------------------------------------------------------------------- host-side layout
 __host__ __device__ __forceinline__ long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
-
-// The packed 4-bit layout (moe_pack_w4): blocks of 16 rows x 256 columns, 2 KB of codes.
-__host__ __device__ __forceinline__ long long w4_slices(int k) { return (k + 255) / 256; }
 
 }  // namespace few
 }  // namespace moe

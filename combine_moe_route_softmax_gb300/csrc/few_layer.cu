@@ -16,7 +16,9 @@ inline bool plan_few(const moe_few_desc_t* d, FewPlan* p) {
       (d->has_shared != 0 && d->has_shared != 1) || (d->weight_tiles != 0 && d->weight_tiles != 1))
     return false;
   if (d->dtype != MOE_BF16 && d->dtype != MOE_E4M3 && d->dtype != MOE_W4) return false;
-  if (d->dtype == MOE_W4 ? (d->group != 32 && d->group != 64 && d->group != 128) || d->weight_tiles : d->group != 0)
+  if (d->zeros != 0 && d->zeros != 1) return false;
+  if (d->dtype == MOE_W4 ? (d->group != 32 && d->group != 64 && d->group != 128) || d->weight_tiles
+                         : d->group != 0 || d->zeros != 0)
     return false;
   const size_t slots = (size_t)d->T * d->K + d->T;
   const bool half = d->dtype != MOE_BF16;
@@ -59,38 +61,39 @@ extern "C" moe_status_t moe_layer_few(const moe_few_desc_t* d, const moe_few_wei
   if (d->T == 0) return MOE_OK;
   if (!x || !topk_idx || !topk_w || !out || !w->w13 || !w->w2) return MOE_ERR_ARG;
   if (w->w_router && logits) return MOE_ERR_ARG;          // one source of the routing
-  if (d->dtype != MOE_BF16 && (!w->w13_scales || !w->w2_scales)) return MOE_ERR_ARG;
-  const bool zeros = w->w13_zeros != nullptr;
-  if (zeros != (w->w2_zeros != nullptr) || (zeros && d->dtype != MOE_W4)) return MOE_ERR_ARG;
+  if (d->dtype == MOE_E4M3 && (!w->w13_scales || !w->w2_scales)) return MOE_ERR_ARG;
   if (d->has_shared) {
     if (!w->shared_w13 || !w->shared_w2) return MOE_ERR_ARG;
-    if (d->dtype != MOE_BF16 && (!w->shared_w13_scales || !w->shared_w2_scales)) return MOE_ERR_ARG;
-    if (zeros != (w->shared_w13_zeros != nullptr) || zeros != (w->shared_w2_zeros != nullptr)) return MOE_ERR_ARG;
+    if (d->dtype == MOE_E4M3 && (!w->shared_w13_scales || !w->shared_w2_scales)) return MOE_ERR_ARG;
   }
-  const void* al16[] = {x, w->w_router};
-  for (const void* q : al16)
+  const void* al[] = {x, w->w_router, w->w13, w->w2, d->has_shared ? w->shared_w13 : nullptr,
+                      d->has_shared ? w->shared_w2 : nullptr};
+  for (const void* q : al)
     if (reinterpret_cast<uintptr_t>(q) & 15) return MOE_ERR_ARG;
-  const void* al32[] = {w->w13, w->w2, d->has_shared ? w->shared_w13 : nullptr, d->has_shared ? w->shared_w2 : nullptr};
-  for (const void* q : al32)
-    if (reinterpret_cast<uintptr_t>(q) & 31) return MOE_ERR_ARG;
-  if (d->dtype == MOE_W4) {
-    const void* al[] = {w->w13_scales, w->w2_scales, w->w13_zeros, w->w2_zeros,
-                        d->has_shared ? w->shared_w13_scales : nullptr, d->has_shared ? w->shared_w2_scales : nullptr,
-                        d->has_shared ? w->shared_w13_zeros : nullptr, d->has_shared ? w->shared_w2_zeros : nullptr};
-    for (const void* q : al)
-      if (reinterpret_cast<uintptr_t>(q) & 15) return MOE_ERR_ARG;
-  }
+  // weight coordinates are int32: rows, or lines of 128 bytes for tiled weights
+  const long long wide = d->H > 2 * d->I ? d->H : 2 * d->I;
+  const long long bytes_per = d->dtype == MOE_BF16 ? 2 : 1;
+  if ((d->weight_tiles ? 2ll * d->I * d->H * bytes_per / 128 : wide) * d->E > 0x7fffffffll) return MOE_ERR_ARG;
   uint8_t* b = static_cast<uint8_t*>(ws);
   LayerArgs a;
   a.T = d->T; a.H = d->H; a.I = d->I; a.E = d->E; a.K = d->K;
   a.shared = d->has_shared;
   a.tiled = d->weight_tiles;
-  a.w13 = static_cast<const uint8_t*>(w->w13);
-  a.w2 = static_cast<const uint8_t*>(w->w2);
-  a.sw13 = static_cast<const uint8_t*>(w->shared_w13);
-  a.sw2 = static_cast<const uint8_t*>(w->shared_w2);
-  a.w13_s = w->w13_scales; a.w2_s = w->w2_scales; a.sw13_s = w->shared_w13_scales; a.sw2_s = w->shared_w2_scales;
-  a.w13_z = w->w13_zeros; a.w2_z = w->w2_zeros; a.sw13_z = w->shared_w13_zeros; a.sw2_z = w->shared_w2_zeros;
+  a.zeros = d->zeros;
+  const void* wp[4] = {w->w13, w->w2, w->shared_w13, w->shared_w2};
+  const float* sp[4] = {w->w13_scales, w->w2_scales, w->shared_w13_scales, w->shared_w2_scales};
+  for (int i = 0; i < 4; ++i) {
+    const bool used = i < 2 || d->has_shared;
+    a.w[i] = used ? static_cast<const uint8_t*>(wp[i]) : nullptr;
+    a.scales[i] = used ? sp[i] : nullptr;
+    if (used && d->dtype != MOE_W4) {
+      const uint64_t rows = (uint64_t)(i % 2 ? d->H : 2 * d->I) * (i < 2 ? d->E : 1);
+      const uint64_t bytes = (uint64_t)(i % 2 ? d->I : d->H) * bytes_per;
+      const bool ok = d->weight_tiles ? gg::make_map(&a.map[i], wp[i], true, 128, rows * bytes / 128, 16)
+                                      : gg::make_map(&a.map[i], wp[i], true, bytes, rows, 16);
+      if (!ok) return MOE_ERR_CUDA;
+    }
+  }
   a.w_router = w->w_router;
   a.router_bias = w->router_bias;
   a.logits_in = logits;

@@ -12,7 +12,7 @@
 //      columns of the same tensor instruction up to 4 tokens, two instructions above; the
 //      SM that completes a row tile's last expert sums its rows over the slots in the
 //      combine's order.
-// All tiles, phase 1 then phase 2, expert by expert, are one queue.  A scheduler warp per SM takes
+// All tiles, phase 1 then phase 2, expert by expert, are one queue.  The scheduler warp of an SM takes
 // the next tile when its workers are about to need it, so SMs stay level whatever the experts
 // cost, and phase 2 begins on the first experts while phase 1 ends on the last: a tile of phase 2
 // waits for its expert's h alone (its weights are loaded meanwhile).  Tiles in the queue are
@@ -34,21 +34,18 @@ namespace few {
 constexpr int WARPS = 16;
 constexpr int THREADS = WARPS * 32;
 constexpr int WORKERS = WARPS - 1;          // the last warp schedules
-constexpr int STAGES = 2;
 constexpr int PARTS_BYTES = 40 * 1024;      // slots of the joins
 constexpr int kMaxSlots = kMaxTokens * kMaxTopK;
 // one entry = up to COLS columns of one expert; at most one per routed slot, plus the shared ones
 constexpr int kMaxEntries = kMaxSlots + kMaxTokens / COLS;
 constexpr int kMaxWidth = 1 << 17;          // H and I
-constexpr int SEQ = 128;                    // places of a CTA's tile sequence kept at a time
-constexpr int AHEAD = 48;                   // units scheduled past the slowest worker's
 
 struct LayerArgs {
+  CUtensorMap map[4];          // BF16, E4M3: w13, w2, shared w13, shared w2 (boxes of 16 rows x 128 bytes)
   int T, H, I, E, K;
-  int shared, tiled;
-  const uint8_t *w13, *w2, *sw13, *sw2;
-  const void *w13_s, *w2_s, *sw13_s, *sw2_s;
-  const void *w13_z, *w2_z, *sw13_z, *sw2_z;
+  int shared, tiled, zeros;
+  const uint8_t* w[4];         // the same four, for W4
+  const float* scales[4];      // E4M3
   const uint16_t* w_router;    // [E, H] or null
   const float* router_bias;    // [E] or null
   const float* logits_in;      // [T, E] or null
@@ -78,18 +75,16 @@ struct LayerShared {
   int max_cols;
   int n1, n_all;               // tiles of phase 1, of both phases
   int tiles1, tiles2;          // row tiles of one expert
-  Strides st[2];
-  long long mat_bytes[2], mat_sc[2];   // one matrix's weights (bytes) and scales (elements)
-  int seq[SEQ];                // tile numbers of the CTA's sequence
-  int published;               // places filled
+  Cut cut[2];
+  Feed<WORKERS> feed;
   int ready;                   // leading entries whose h is ready
-  int use[WORKERS];            // unit each worker is at
   int go;
   float block[WARPS];
   short expert[kMaxEntries];   // E for the shared expert
   short first[kMaxEntries];    // first column in cols
   int ncols[kMaxEntries];
   short cols[kMaxSlots + kMaxTokens];   // slot ids t*K + k, or T*K + t for the shared expert
+  short toks[kMaxSlots + kMaxTokens];   // and their tokens
   short count[kMaxExperts];    // listing: slots of the expert so far
   short open[kMaxExperts];     // listing: its entry being filled
   short slot_entry[kMaxSlots];
@@ -188,7 +183,10 @@ __device__ __forceinline__ void list_entries(const LayerArgs& a, LayerShared& s)
     // first: with the most columns, its h takes longest to be ready
     const bool v = lane < a.T && s.alive[lane];
     const unsigned m = __ballot_sync(0xffffffffu, v);
-    if (v) s.cols[__popc(m & lanemask_lt())] = (short)(n + lane);
+    if (v) {
+      s.cols[__popc(m & lanemask_lt())] = (short)(n + lane);
+      s.toks[__popc(m & lanemask_lt())] = (short)lane;
+    }
     const int c = __popc(m);
 #pragma unroll 1
     for (; col < c; col += COLS, ++ent) {
@@ -248,163 +246,122 @@ __device__ __forceinline__ void list_entries(const LayerArgs& a, LayerShared& s)
   __syncwarp();
 #pragma unroll 1
   for (int i = lane; i < n; i += 32)
-    if (s.id[i] >= 0) s.cols[s.first[s.slot_entry[i]] + s.slot_rank[i]] = (short)i;
+    if (s.id[i] >= 0) {
+      const int c = s.first[s.slot_entry[i]] + s.slot_rank[i];
+      s.cols[c] = (short)i;
+      s.toks[c] = (short)(i / a.K);
+    }
   if (lane == 0) {
     s.n_entries = ent;
     s.max_cols = most;
   }
 }
 
-// The CTA's tile sequence as the stream's source of items.
+__device__ __forceinline__ int atom_add_release(int32_t* p, int v) {
+  int old;
+  asm volatile("atom.add.release.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
+}
+
+// The scheduler's side: tiles off the queue (the first two of a CTA are its own; the others are
+// asked for one ahead), and which entries' h are ready, as far as tiles of phase 2 need them.
 template <int FMT, int GROUP>
-struct LayerSrc {
+struct LayerSched {
   const LayerArgs& a;
   LayerShared& s;
+  const int h_ready;           // entry_done of an entry whose h is ready
+  int q, pending, ready, want;
 
-  __device__ __forceinline__ int tile(int q) const {
-    volatile int* published = &s.published;
-    if (!wait_for([&] { return *published > q; }, a.dev_status)) return -1;
-    __threadfence_block();
-    return s.seq[q & (SEQ - 1)];
+  __device__ __forceinline__ int tile(int lane) {
+    int t = 0;
+    if (lane == 0) {
+      t = q < 2 ? (int)(blockIdx.x + q * gridDim.x) : (int)(2 * gridDim.x) + pending;
+      if (q >= 1) pending = (int)atomicAdd(&a.ctl[2], 1u);
+    }
+    ++q;
+    t = __shfl_sync(0xffffffffu, t, 0);
+    if (t >= s.n_all) return -1;
+    if (t >= s.n1) want = max(want, (t - s.n1) / s.tiles2 + 1);
+    return t;
   }
-  __device__ __forceinline__ bool down(int tile_) const { return tile_ >= s.n1; }
-  __device__ __forceinline__ const Strides& strides(int tile_) const { return s.st[down(tile_)]; }
-  __device__ __forceinline__ bool zeros() const { return a.w13_z != nullptr; }
-  // tile number -> entry and row tile
-  __device__ __forceinline__ void split(int tile_, int& entry, int& row) const {
-    const int n = down(tile_) ? s.tiles2 : s.tiles1, i = down(tile_) ? tile_ - s.n1 : tile_;
-    entry = i / n;
-    row = i - entry * n;
+  __device__ __forceinline__ Cut cut(int t) const { return s.cut[t >= s.n1]; }
+  __device__ __forceinline__ bool done() const { return ready >= want; }
+  __device__ __forceinline__ bool idle(int lane) {
+    if (ready >= want) return false;
+    const int e = ready + lane;
+    int v = 0;
+    if (e < want) asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(a.entry_done + e) : "memory");
+    const unsigned m = __ballot_sync(0xffffffffu, e < want && v == h_ready);
+    const int n = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
+    if (n == 0) return false;
+    ready += n;
+    __threadfence();
+    __syncwarp();
+    if (lane == 0) *static_cast<volatile int*>(&s.ready) = ready;
+    return true;
   }
-  __device__ __forceinline__ Tile where(int tile_, int s0) const {
-    const bool d = down(tile_);
-    const Strides& st = s.st[d];
-    int entry, row;
-    split(tile_, entry, row);
+  __device__ __forceinline__ void give_up(int lane) {
+    if (lane == 0) *static_cast<volatile int*>(&s.ready) = s.n_entries;
+  }
+  __device__ __forceinline__ void describe(int t, int part, const Cut& c, Unit& u) const {
+    const bool d = t >= s.n1;
+    const int tiles = d ? s.tiles2 : s.tiles1, i = d ? t - s.n1 : t;
+    const int entry = i / tiles, row = i - entry * tiles;
     const int e = s.expert[entry];
     const bool sh = e == a.E;
-    const uint8_t* w = d ? (sh ? a.sw2 : a.w2) : (sh ? a.sw13 : a.w13);
+    const int which = (sh ? 2 : 0) + d;
     const long long m = sh ? 0 : e;
-    w += m * s.mat_bytes[d];
-    Tile r;
-    r.sc = r.zp = nullptr;
+    const int s0 = part * c.len;
+    const int rows = d ? a.H : 2 * a.I, k = d ? a.I : a.H;
+    u.entry = entry;
+    u.row = row;
+    u.s0 = (short)s0;
+    u.n = (short)min(c.len, c.nsl - s0);
+    u.part = (short)part;
+    u.parts = (short)c.parts;
+    u.down = d;
+    // the half tiles: 16 rows each, side by side in phase 2, gate and up rows in phase 1
+    const int r0 = d ? row * 32 : row * 16, r1 = d ? r0 + 16 : a.I + r0;
     if constexpr (FMT == F_W4) {
-      constexpr int NG = Format<FMT, GROUP>::NG;
-      const void* sc = d ? (sh ? a.sw2_s : a.w2_s) : (sh ? a.sw13_s : a.w13_s);
-      const void* zp = d ? (sh ? a.sw2_z : a.w2_z) : (sh ? a.sw13_z : a.w13_z);
-      const long long blk = (long long)row * (d ? 2 : 1) * st.nsl + s0;
-      w += blk * 2048;
-      r.sc = static_cast<const uint32_t*>(sc) + m * s.mat_sc[d] + blk * 8 * NG;
-      if (zp) r.zp = static_cast<const uint16_t*>(zp) + m * s.mat_sc[d] + blk * 8 * NG;
+      const int block = w4_block(GROUP, a.zeros);
+      const uint8_t* w = a.w[which] + m * (rows / 16) * c.nsl * block;
+      u.p0 = w + ((long long)(r0 / 16) * c.nsl + s0) * block;
+      u.p1 = w + ((long long)(r1 / 16) * c.nsl + s0) * block;
     } else {
-      const long long bytes = FMT == F_BF16 ? 2ll * st.k : st.k;
-      const int r0 = row * (d ? 32 : 16);
-      if (a.tiled)
-        w += (long long)(r0 >> 7) * (bytes * 128) + (long long)s0 * 16384 + (r0 & 127) * 128;
-      else
-        w += r0 * bytes + (long long)s0 * 128;
+      u.map = &a.map[which];
+      if (a.tiled) {
+        // boxes of 128 rows x 128 bytes, one after the other along K: row y of 128-byte lines
+        u.x = 0;
+        u.y0 = (int)(((m * (rows / 128) + r0 / 128) * c.nsl + s0) * 128 + r0 % 128);
+        u.y1 = (int)(((m * (rows / 128) + r1 / 128) * c.nsl + s0) * 128 + r1 % 128);
+      } else {
+        u.x = s0 * 128;
+        u.y0 = (int)(m * rows + r0);
+        u.y1 = (int)(m * rows + r1);
+      }
       if constexpr (FMT == F_E4M3) {
-        const void* sc = d ? (sh ? a.sw2_s : a.w2_s) : (sh ? a.sw13_s : a.w13_s);
-        r.sc = static_cast<const float*>(sc) + m * s.mat_sc[d] + (long long)(r0 >> 7) * (st.k / 128) + s0;
+        const float* sc = a.scales[which] + m * (rows / 128) * (k / 128) + s0;
+        u.p0 = reinterpret_cast<const uint8_t*>(sc + (long long)(r0 / 128) * (k / 128));
+        u.p1 = reinterpret_cast<const uint8_t*>(sc + (long long)(r1 / 128) * (k / 128));
       }
     }
-    r.w = w;
-    return r;
   }
 };
 
-// Strides and cuts of both phases (one thread).
-template <int FMT, int GROUP>
+// Cuts of both phases (one thread).
+template <int FMT>
 __device__ __forceinline__ void plan_phases(const LayerArgs& a, LayerShared& s) {
-#pragma unroll 1
-  for (int d = 0; d < 2; ++d) {
-    Strides& st = s.st[d];
-    const int rows = d ? a.H : 2 * a.I, half_rows = d ? 16 : a.I;
-    st.k = d ? a.I : a.H;
-    if constexpr (FMT == F_W4) {
-      st.nsl = (int)w4_slices(st.k);
-      st.step = 2048;
-      st.pitch = 128;
-      st.half = (long long)(half_rows / 16) * st.nsl * 2048;
-      st.sc_half = (long long)(half_rows / 16) * st.nsl * 8 * Format<FMT, GROUP>::NG;
-      s.mat_bytes[d] = (long long)(rows / 16) * st.nsl * 2048;
-      s.mat_sc[d] = (long long)(rows / 16) * st.nsl * 8 * Format<FMT, GROUP>::NG;
-    } else {
-      const long long bytes = FMT == F_BF16 ? 2ll * st.k : st.k;
-      st.nsl = (int)(bytes / 128);
-      st.step = a.tiled ? 16384 : 128;
-      st.pitch = a.tiled ? 128 : bytes;
-      // 16 rows on inside a 128-row box, or I (a multiple of 128) rows on in either layout
-      st.half = d ? 16 * st.pitch : a.I * bytes;
-      st.sc_half = d ? 0 : (long long)(a.I / 128) * (st.k / 128);
-      s.mat_bytes[d] = rows * bytes;
-      s.mat_sc[d] = (long long)(rows / 128) * (st.k / 128);
-    }
-    const int n = rows / 32 * s.n_entries;
-    st.cut(WORKERS, n <= (int)gridDim.x);
-  }
   s.tiles1 = a.I / 16;
   s.tiles2 = a.H / 32;
   s.n1 = s.n_entries * s.tiles1;
   s.n_all = s.n1 + s.n_entries * s.tiles2;
-  s.published = 0;
-  s.ready = 0;
-}
-
-// The scheduler warp: keeps the sequence AHEAD units past the slowest worker, and passes on which
-// entries' h are ready.  The first two tiles of a CTA are its own, the rest come off the queue.
-__device__ __forceinline__ void schedule(const LayerArgs& a, LayerShared& s, int h_ready, int lane) {
-  volatile int* use = s.use;
-  int q = 0, units = 0, ready = 0;
-  bool end = false;
-  unsigned long long t0 = clock_ns();
-  while (!end || ready < s.n_entries) {
-    bool moved = false;
-    if (ready < s.n_entries) {
-      const int e = ready + lane;
-      int v = 0;
-      if (e < s.n_entries) asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(a.entry_done + e) : "memory");
-      const unsigned m = __ballot_sync(0xffffffffu, e < s.n_entries && v == h_ready);
-      const int n = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
-      if (n > 0) {
-        ready += n;
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) *static_cast<volatile int*>(&s.ready) = ready;
-        moved = true;
-      }
-    }
-    if (!end) {
-      const int slowest = __reduce_min_sync(0xffffffffu, lane < WORKERS ? use[lane] : 0x7fffffff);
-      if (units < slowest + AHEAD) {
-        int t = 0;
-        if (lane == 0) {
-          t = q < 2 ? (int)(blockIdx.x + q * gridDim.x) : (int)(2 * gridDim.x + atomicAdd(&a.ctl[2], 1u));
-          if (t >= s.n_all) t = -1;
-          s.seq[q & (SEQ - 1)] = t;
-          __threadfence_block();
-          *static_cast<volatile int*>(&s.published) = q + 1;
-        }
-        t = __shfl_sync(0xffffffffu, t, 0);
-        end = t < 0;
-        if (!end) units += s.st[t >= s.n1].parts;
-        ++q;
-        moved = true;
-      }
-    }
-    if (moved) {
-      t0 = clock_ns();
-    } else if (__any_sync(0xffffffffu, clock_ns() - t0 > TIMEOUT_NS)) {   // nothing for two seconds: let the workers go
-      if (lane == 0) {
-        if (a.dev_status) atomicOr(a.dev_status, MOE_DEV_PIPELINE_TIMEOUT);
-        s.seq[q & (SEQ - 1)] = -1;
-        __threadfence_block();
-        if (!end) *static_cast<volatile int*>(&s.published) = q + 1;
-        *static_cast<volatile int*>(&s.ready) = s.n_entries;
-      }
-      return;
-    }
+#pragma unroll 1
+  for (int d = 0; d < 2; ++d) {
+    const int k = d ? a.I : a.H;
+    const int items = FMT == F_W4 ? w4_slices(k) : FMT == F_BF16 ? k / 64 : k / 128;
+    s.cut[d].set(items, WORKERS, (d ? s.n_all - s.n1 : s.n1) <= (int)gridDim.x);
   }
+  s.ready = 0;
 }
 
 // Phase 1's result for one tile: h of 16 intermediate rows; two BF16 terms, or float32 with the
@@ -420,7 +377,7 @@ __device__ __forceinline__ void store_h(const LayerArgs& a, const LayerShared& s
       const int c = n * 8 + 2 * t + j;
       const int slot = c < nc ? s.cols[c0 + c] : -1;
       float unit = 1.0f;
-      if (HALF && slot >= 0) unit = __ldcg(&a.x_unit[slot < a.T * a.K ? slot / a.K : slot - a.T * a.K]);
+      if (HALF && slot >= 0) unit = __ldcg(&a.x_unit[s.toks[c0 + c]]);
       uint32_t most = 0;
 #pragma unroll
       for (int i = j; i < 4; i += 2) {
@@ -533,16 +490,16 @@ __device__ __forceinline__ void combine_tile(const LayerArgs& a, const LayerShar
 }
 
 template <int FMT, int GROUP>
-using LayerStream = Stream<FMT, GROUP, FMT != F_BF16, STAGES, WORKERS, LayerSrc<FMT, GROUP>>;
+using LayerStream = Stream<FMT, GROUP, FMT != F_BF16, WORKERS>;
 
-// The unit at in.usec with NT column groups: columns, sums, join, result.
+// The unit in use with NT column groups: columns, sums, join, result.
 template <int FMT, int GROUP, int NT, int PASSES>
-__device__ __forceinline__ void do_unit(const LayerSrc<FMT, GROUP>& src, LayerStream<FMT, GROUP>& in, bool down,
-                                        int entry, int row, float4* parts, int slots, int stride) {
+__device__ __forceinline__ void do_unit(const LayerArgs& a, LayerShared& s, LayerStream<FMT, GROUP>& in, bool down,
+                                        float4* parts, int slots, int stride) {
   constexpr bool HALF = FMT != F_BF16;
-  const LayerArgs& a = src.a;
-  LayerShared& s = src.s;
   const int lane = in.lane, g = lane >> 2;
+  const Unit& un = in.unit();
+  const int entry = un.entry, row = un.row, part = un.part, n = un.parts;
   const int nc = s.ncols[entry], c0 = s.first[entry];
   const uint16_t* x[PASSES][NT];
 #pragma unroll
@@ -553,38 +510,32 @@ __device__ __forceinline__ void do_unit(const LayerSrc<FMT, GROUP>& src, LayerSt
       const bool pairs = down && PASSES == 1;              // hi and lo as columns of one group
       const int c = pairs ? (g & 3) : i * 8 + g;
       if (c < nc) {
-        const int slot = s.cols[c0 + c];
         if (!down)
-          x[p][i] = (HALF ? a.x16 : a.x) + (size_t)(slot < a.T * a.K ? slot / a.K : slot - a.T * a.K) * a.H;
+          x[p][i] = (HALF ? a.x16 : a.x) + (size_t)s.toks[c0 + c] * a.H;
         else
-          x[p][i] = ((pairs ? g >= 4 : p == 1) ? a.h_lo : a.h_hi) + (size_t)slot * a.I;
+          x[p][i] = ((pairs ? g >= 4 : p == 1) ? a.h_lo : a.h_hi) + (size_t)s.cols[c0 + c] * a.I;
       }
     }
-  const Strides& st = s.st[down];
   Sums<NT> sums;
-  in.template run<NT, PASSES>(sums, st, x);
-  if (!join<NT>(sums, s.join, parts, slots, stride, in.usec.u, in.usec.u - in.usec.part, st.parts, lane, a.dev_status))
-    return;
+  in.template run<NT, PASSES>(sums, down ? a.I : a.H, x);
+  if (!join<NT>(sums, s.join, parts, slots, stride, in.cur, in.cur - part, n, lane, a.dev_status)) return;
   if (!down) {
     store_h<HALF, NT>(a, s, sums, entry, row, lane);
-    __threadfence();
     __syncwarp();
     int old = 0;
-    if (lane == 0) old = atomicAdd(&a.entry_done[entry], 1);
+    if (lane == 0) old = atom_add_release(&a.entry_done[entry], 1);
     if (HALF && __shfl_sync(0xffffffffu, old, 0) == s.tiles1 - 1) {
       __threadfence();
       entry_to_half(a, s, entry, lane);
-      __threadfence();
       __syncwarp();
-      if (lane == 0) atomicAdd(&a.entry_done[entry], 1);
+      if (lane == 0) atom_add_release(&a.entry_done[entry], 1);
     }
     return;
   }
   store_y<HALF, NT>(a, s, sums, entry, row, lane);
-  __threadfence();
   __syncwarp();
   int old = 0;
-  if (lane == 0) old = atomicAdd(&a.tile_count[row], 1);
+  if (lane == 0) old = atom_add_release(&a.tile_count[row], 1);
   if (__shfl_sync(0xffffffffu, old, 0) != s.n_entries - 1) return;
   __threadfence();
   if (lane == 0) a.tile_count[row] = 0;
@@ -592,10 +543,10 @@ __device__ __forceinline__ void do_unit(const LayerSrc<FMT, GROUP>& src, LayerSt
 }
 
 template <int FMT, int GROUP>
-__global__ void __launch_bounds__(THREADS, 1) layer_kernel(const LayerArgs a) {
+__global__ void __launch_bounds__(THREADS, 1) layer_kernel(const __grid_constant__ LayerArgs a) {
   constexpr bool HALF = FMT != F_BF16;
   __shared__ LayerShared s;
-  extern __shared__ __align__(128) uint8_t rings[];
+  extern __shared__ __align__(1024) uint8_t rings[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = a.T * a.K;
   const bool sync = HALF || a.w_router;
@@ -643,12 +594,12 @@ __global__ void __launch_bounds__(THREADS, 1) layer_kernel(const LayerArgs a) {
   __syncthreads();
   list_entries(a, s);
   if (tid == 0) {
-    plan_phases<FMT, GROUP>(a, s);
+    plan_phases<FMT>(a, s);
     if (!sync) s.go = 1;
     else if (!a.w_router) s.go = barrier_wait(a.ctl, gen, a.dev_status);
   }
   join_init(s.join);
-  if (tid < WORKERS) s.use[tid] = tid;
+  feed_init(s.feed);
   __syncthreads();
   if (!s.go) return;
   if (s.n_entries == 0) {   // no valid slot in the batch: every output is +0
@@ -657,36 +608,41 @@ __global__ void __launch_bounds__(THREADS, 1) layer_kernel(const LayerArgs a) {
     return;
   }
   if (warp == WORKERS) {
-    schedule(a, s, s.tiles1 + (HALF ? 1 : 0), lane);
+    LayerSched<FMT, GROUP> src{a, s, s.tiles1 + (HALF ? 1 : 0), 0, 0, 0, 0};
+    schedule(s.feed, src, lane, a.dev_status);
   } else {
-    constexpr int RING = STAGES * Format<FMT, GROUP>::STAGE;
+    constexpr int RING = 2 * Format<FMT, GROUP>::STAGE;
     float4* parts = reinterpret_cast<float4*>(rings + WORKERS * RING);
     const int stride = s.max_cols <= 8 ? 64 : 128;       // a slot is 1 KB for each 8 columns
     const int slots = min(MAX_SLOTS, PARTS_BYTES / (stride * 16));
-    const LayerSrc<FMT, GROUP> src{a, s};
-    LayerStream<FMT, GROUP> in(src, rings + warp * RING, warp, lane);
+    LayerStream<FMT, GROUP> in{s.feed, rings + warp * RING};
+    in.ring_addr = gg::smem_u32(in.ring);
+    in.bars = gg::smem_u32(&s.feed.full[warp][0]);
+    in.lane = lane;
+    in.worker = warp;
+    in.dev_status = a.dev_status;
+    in.dx = a.tiled ? 0 : 128;
+    in.dy = a.tiled ? 128 : 0;
+    in.block = FMT == F_W4 ? w4_block(GROUP, a.zeros) : 0;
+    in.zeros = a.zeros;
+    in.start();
     volatile int* ready = &s.ready;
-    while (in.usec.tile >= 0) {
-      if (lane == 0) *static_cast<volatile int*>(&s.use[warp]) = in.usec.u;
-      const bool down = src.down(in.usec.tile);
-      int entry, row;
-      src.split(in.usec.tile, entry, row);
+    while (in.take()) {
+      const int entry = in.unit().entry;
       const int nc = s.ncols[entry];
-      if (!down) {
-        if (nc <= 8) do_unit<FMT, GROUP, 1, 1>(src, in, down, entry, row, parts, slots, stride);
-        else do_unit<FMT, GROUP, 2, 1>(src, in, down, entry, row, parts, slots, stride);
-      } else {
-        wait_for([&] { return *ready > entry; }, a.dev_status);
+      if (in.unit().down) {
+        if (!wait_for([&] { return *ready > entry; }, a.dev_status)) in.dead = true;
         __threadfence_block();
         __syncwarp();
-        if (nc <= 4) do_unit<FMT, GROUP, 1, 1>(src, in, down, entry, row, parts, slots, stride);
-        else if (nc <= 8) do_unit<FMT, GROUP, 1, 2>(src, in, down, entry, row, parts, slots, stride);
-        else do_unit<FMT, GROUP, 2, 2>(src, in, down, entry, row, parts, slots, stride);
+        if (nc <= 4) do_unit<FMT, GROUP, 1, 1>(a, s, in, true, parts, slots, stride);
+        else if (nc <= 8) do_unit<FMT, GROUP, 1, 2>(a, s, in, true, parts, slots, stride);
+        else do_unit<FMT, GROUP, 2, 2>(a, s, in, true, parts, slots, stride);
+      } else {
+        if (nc <= 8) do_unit<FMT, GROUP, 1, 1>(a, s, in, false, parts, slots, stride);
+        else do_unit<FMT, GROUP, 2, 1>(a, s, in, false, parts, slots, stride);
       }
-      in.hop(in.usec);
     }
-    cp_wait<0>();
-    if (lane == 0) *static_cast<volatile int*>(&s.use[warp]) = 0x7fffff00;
+    in.finish();
   }
   // the last CTA leaves the counters zero for the next launch
   __syncthreads();
@@ -703,7 +659,7 @@ __global__ void __launch_bounds__(THREADS, 1) layer_kernel(const LayerArgs a) {
 
 template <int FMT, int GROUP>
 cudaError_t launch_layer(const LayerArgs& a, cudaStream_t stream) {
-  constexpr int smem = WORKERS * STAGES * Format<FMT, GROUP>::STAGE + PARTS_BYTES;
+  constexpr int smem = WORKERS * 2 * Format<FMT, GROUP>::STAGE + PARTS_BYTES;
   static std::atomic<unsigned long long> done{0};
   if (!once_per_device(done, [] {
         return cudaFuncSetAttribute(layer_kernel<FMT, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ==

@@ -11,20 +11,20 @@ namespace few {
 
 constexpr int LIN_COLS = 32;
 constexpr int LIN_WARPS = 16;
-constexpr int LIN_STAGES = 2;
+constexpr int LIN_WORKERS = LIN_WARPS - 1;   // the last warp schedules
 constexpr int LIN_PARTS = 64 * 1024;
 
 struct LinearArgs {
   const uint16_t* x;
   long long x_stride, out_stride;
-  int T, N;
-  const uint8_t* q;
-  const void *scales, *zeros;
+  int T, N, K;
+  const uint8_t* w;
+  int zeros;
   const float* bias;
   void* out;
   int out_f32;
   int32_t* dev_status;
-  Strides st;
+  Cut cut;
   int tiles;                   // row tiles x blocks of x
   int blocks;                  // blocks of LIN_COLS rows of x
 };
@@ -32,39 +32,44 @@ struct LinearArgs {
 // CTA c takes tiles c, c + CTAs, ...; tile = (row tile, block of x rows), blocks inner, so that the
 // second block of a row tile finds its weights in L2.
 template <int GROUP>
-struct LinearSrc {
+struct LinearSched {
   const LinearArgs& a;
-  __device__ __forceinline__ int tile(int q) const {
-    const long long n = blockIdx.x + (long long)q * gridDim.x;
+  int q;
+  __device__ __forceinline__ int tile(int) {
+    const long long n = blockIdx.x + (long long)q++ * gridDim.x;
     return n < a.tiles ? (int)n : -1;
   }
-  __device__ __forceinline__ const Strides& strides(int) const { return a.st; }
-  __device__ __forceinline__ bool zeros() const { return a.zeros != nullptr; }
-  __device__ __forceinline__ Tile where(int tile_, int s0) const {
-    constexpr int NG = Format<F_W4, GROUP>::NG;
-    const long long b = (long long)(tile_ / a.blocks) * 2 * a.st.nsl + s0;
-    Tile r;
-    r.w = a.q + b * 2048;
-    r.sc = static_cast<const uint32_t*>(a.scales) + b * 8 * NG;
-    r.zp = a.zeros ? static_cast<const uint16_t*>(a.zeros) + b * 8 * NG : nullptr;
-    return r;
+  __device__ __forceinline__ Cut cut(int) const { return a.cut; }
+  __device__ __forceinline__ bool done() const { return true; }
+  __device__ __forceinline__ bool idle(int) { return false; }
+  __device__ __forceinline__ void give_up(int) {}
+  __device__ __forceinline__ void describe(int t, int part, const Cut& c, Unit& u) const {
+    const int row = t / a.blocks, s0 = part * c.len, block = w4_block(GROUP, a.zeros);
+    u.entry = t - row * a.blocks;
+    u.row = row;
+    u.s0 = (short)s0;
+    u.n = (short)min(c.len, c.nsl - s0);
+    u.part = (short)part;
+    u.parts = (short)c.parts;
+    u.p0 = a.w + ((long long)row * 2 * c.nsl + s0) * block;
+    u.p1 = u.p0 + (long long)c.nsl * block;
   }
 };
 template <int GROUP>
-using LinearStream = Stream<F_W4, GROUP, false, LIN_STAGES, LIN_WARPS, LinearSrc<GROUP>>;
+using LinearStream = Stream<F_W4, GROUP, false, LIN_WORKERS>;
 
 template <int GROUP, int NT>
 __device__ __forceinline__ void linear_unit(const LinearArgs& a, LinearStream<GROUP>& in, JoinShared& j, float4* parts,
                                             int slots, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  const int row = in.usec.tile / a.blocks, t0 = (in.usec.tile - row * a.blocks) * LIN_COLS;
+  const Unit& un = in.unit();
+  const int row = un.row, t0 = un.entry * LIN_COLS, part = un.part;
   const uint16_t* x[1][NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) x[0][n] = t0 + n * 8 + g < a.T ? a.x + (t0 + n * 8 + g) * a.x_stride : nullptr;
   Sums<NT> sums;
-  in.template run<NT, 1>(sums, a.st, x);
-  if (!join<NT>(sums, j, parts, slots, NT * 64, in.usec.u, in.usec.u - in.usec.part, a.st.parts, lane, a.dev_status))
-    return;
+  in.template run<NT, 1>(sums, a.K, x);
+  if (!join<NT>(sums, j, parts, slots, NT * 64, in.cur, in.cur - part, a.cut.parts, lane, a.dev_status)) return;
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -88,20 +93,32 @@ __device__ __forceinline__ void linear_unit(const LinearArgs& a, LinearStream<GR
 
 template <int GROUP, int NT>
 __global__ void __launch_bounds__(LIN_WARPS * 32, 1) linear_w4_kernel(const LinearArgs a) {
-  extern __shared__ __align__(128) uint8_t rings[];
+  extern __shared__ __align__(1024) uint8_t rings[];
   __shared__ JoinShared j;
+  __shared__ Feed<LIN_WORKERS> feed;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int RING = LIN_STAGES * Format<F_W4, GROUP>::STAGE;
+  constexpr int RING = 2 * Format<F_W4, GROUP>::STAGE;
   constexpr int SLOTS = LIN_PARTS / 1024 / NT < MAX_SLOTS ? LIN_PARTS / 1024 / NT : MAX_SLOTS;
-  float4* parts = reinterpret_cast<float4*>(rings + LIN_WARPS * RING);
   join_init(j);
-  const LinearSrc<GROUP> src{a};
-  LinearStream<GROUP> in(src, rings + warp * RING, warp, lane);
+  feed_init(feed);
   __syncthreads();
-  while (in.usec.tile >= 0) {
-    linear_unit<GROUP, NT>(a, in, j, parts, SLOTS, lane);
-    in.hop(in.usec);
+  if (warp == LIN_WORKERS) {
+    LinearSched<GROUP> src{a, 0};
+    schedule(feed, src, lane, a.dev_status);
+    return;
   }
+  float4* parts = reinterpret_cast<float4*>(rings + LIN_WORKERS * RING);
+  LinearStream<GROUP> in{feed, rings + warp * RING};
+  in.ring_addr = gg::smem_u32(in.ring);
+  in.bars = gg::smem_u32(&feed.full[warp][0]);
+  in.lane = lane;
+  in.worker = warp;
+  in.dev_status = a.dev_status;
+  in.block = w4_block(GROUP, a.zeros);
+  in.zeros = a.zeros;
+  in.start();
+  while (in.take()) linear_unit<GROUP, NT>(a, in, j, parts, SLOTS, lane);
+  in.finish();
 }
 
 // ------------------------------------------------------------------- weight preparation
@@ -147,42 +164,46 @@ __global__ void __launch_bounds__(256) quant_w4_kernel(const uint16_t* __restric
   if (zeros) zeros[o] = (uint8_t)z;
 }
 
-// One warp per (matrix, 16-row block, 256-column slice): lane (g, t) writes the 32 bytes it will
-// load for row g and for row g + 8; rows past N and columns past K are code 0 with scale 0.
+// One warp per block (16 rows x 256 columns).  Codes: for row g (then g + 8) and J = 0, 1, lane (g, t)'s
+// 16 bytes: word i holds columns (4 J + i) * 32 + t * 8 .. + 8, even ones in nibbles 0-3, odd ones in
+// nibbles 4-7.  Then the scales, [g][group][row g, row g + 8], and the zero points likewise.  Rows
+// past N and columns past K are code 0 with scale 0.
 __global__ void __launch_bounds__(256) pack_w4_kernel(const uint8_t* __restrict__ q, const uint16_t* __restrict__ sc,
                                                       const uint8_t* __restrict__ zp, long long blocks, int N, int K,
-                                                      int group, uint8_t* __restrict__ oq, uint32_t* __restrict__ osc,
-                                                      uint16_t* __restrict__ ozp) {
+                                                      int group, uint8_t* __restrict__ out) {
   const long long blk = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (blk >= blocks) return;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int nsl = (int)w4_slices(K), nrb = (int)ceil_div(N, 32) * 2;
+  const int nsl = w4_slices(K), nrb = (int)ceil_div(N, 32) * 2;
   const int s = (int)(blk % nsl);
   const long long mrb = blk / nsl;
   const int rb = (int)(mrb % nrb);
   const long long m = mrb / nrb;
+  uint8_t* dst = out + blk * w4_block(group, zp != nullptr);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int row = rb * 16 + h * 8 + g;
-    uint32_t out[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int k = s * 256 + j * 32 + t * 8;
-      uint32_t v = 0;
-      if (row < N && k < K) {
-        const uint32_t u = *reinterpret_cast<const uint32_t*>(q + ((m * N + row) * K + k) / 2);
-        // even columns to nibbles 0-3, odd ones to nibbles 4-7
+    for (int J = 0; J < 2; ++J) {
+      uint32_t o[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          v |= ((u >> (8 * i)) & 15u) << (4 * i) | ((u >> (8 * i + 4)) & 15u) << (4 * i + 16);
+      for (int i = 0; i < 4; ++i) {
+        const int k = s * 256 + (4 * J + i) * 32 + t * 8;
+        uint32_t v = 0;
+        if (row < N && k < K) {
+          const uint32_t u = *reinterpret_cast<const uint32_t*>(q + ((m * N + row) * K + k) / 2);
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            v |= ((u >> (8 * b)) & 15u) << (4 * b) | ((u >> (8 * b + 4)) & 15u) << (4 * b + 16);
+        }
+        o[i] = v;
       }
-      out[j] = v;
+      *reinterpret_cast<uint4*>(dst + h * 1024 + J * 512 + lane * 16) = make_uint4(o[0], o[1], o[2], o[3]);
     }
-    uint4* d = reinterpret_cast<uint4*>(oq + blk * 2048 + h * 1024 + lane * 32);
-    d[0] = make_uint4(out[0], out[1], out[2], out[3]);
-    d[1] = make_uint4(out[4], out[5], out[6], out[7]);
   }
   const int ng = 256 / group, kg = K / group;
+  uint32_t* osc = reinterpret_cast<uint32_t*>(dst + 2048);
+  uint16_t* ozp = reinterpret_cast<uint16_t*>(dst + 2048 + 8 * ng * 4);
   for (int i = lane; i < 8 * ng; i += 32) {
     const int gg = i / ng, gi = i % ng, kgi = s * ng + gi;
     uint32_t sv = 0, zv = 0;
@@ -195,14 +216,14 @@ __global__ void __launch_bounds__(256) pack_w4_kernel(const uint8_t* __restrict_
         if (zp) zv |= (uint32_t)(zp[o] & 15) << (8 * h);
       }
     }
-    osc[(blk * 8 + gg) * ng + gi] = sv;
-    if (zp) ozp[(blk * 8 + gg) * ng + gi] = (uint16_t)zv;
+    osc[gg * ng + gi] = sv;
+    if (zp) ozp[gg * ng + gi] = (uint16_t)zv;
   }
 }
 
 template <int GROUP, int NT>
 moe_status_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
-  constexpr int smem = LIN_WARPS * LIN_STAGES * Format<F_W4, GROUP>::STAGE + LIN_PARTS;
+  constexpr int smem = LIN_WORKERS * 2 * Format<F_W4, GROUP>::STAGE + LIN_PARTS;
   static std::atomic<unsigned long long> done{0};
   if (!once_per_device(done, [] {
         return cudaFuncSetAttribute(linear_w4_kernel<GROUP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ==
@@ -224,7 +245,7 @@ moe_status_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
 
 inline bool w4_shape_ok(int mats, int N, int K, int group) {
   return mats >= 0 && N > 0 && K > 0 && (group == 32 || group == 64 || group == 128) && K % 128 == 0 &&
-         N <= (1 << 24) && K <= (1 << 24);
+         N <= (1 << 24) && K <= (1 << 22);
 }
 inline uintptr_t bits_of(const void* p) { return reinterpret_cast<uintptr_t>(p); }
 
@@ -246,32 +267,28 @@ extern "C" moe_status_t moe_quantize_weight_w4(const uint16_t* w, int mats, int 
   return MOE_OK;
 }
 
-extern "C" size_t moe_w4_packed_bytes(int N, int K) {
+extern "C" size_t moe_w4_packed_bytes(int N, int K, int group, int zeros) {
   using namespace moe::few;
-  if (!w4_shape_ok(0, N, K, 32)) return 0;
+  if (!w4_shape_ok(0, N, K, group) || (zeros != 0 && zeros != 1)) return 0;
   // whole 32-row tiles, so that the last tile's second half is there to be read
-  return (size_t)(ceil_div(N, 32) * 2 * w4_slices(K) * 2048);
+  return (size_t)(ceil_div(N, 32) * 2 * w4_slices(K) * w4_block(group, zeros));
 }
 
 extern "C" moe_status_t moe_pack_w4(const uint8_t* q, const uint16_t* scales, const uint8_t* zeros, int mats, int N,
-                                    int K, int group, uint8_t* q_packed, uint16_t* scales_packed,
-                                    uint8_t* zeros_packed, void* stream) {
+                                    int K, int group, uint8_t* packed, void* stream) {
   using namespace moe;
   using namespace moe::few;
   if (!w4_shape_ok(mats, N, K, group)) return MOE_ERR_ARG;
   if (mats == 0) return MOE_OK;
-  if (!q || !scales || !q_packed || !scales_packed || (zeros != nullptr) != (zeros_packed != nullptr))
-    return MOE_ERR_ARG;
-  if ((bits_of(q) & 3) || (bits_of(q_packed) & 31) || (bits_of(scales_packed) & 15) || (bits_of(zeros_packed) & 15))
-    return MOE_ERR_ARG;
-  const size_t in = (size_t)mats * N * K / 2, outb = (size_t)mats * moe_w4_packed_bytes(N, K);
-  if (bits_of(q) < bits_of(q_packed) + outb && bits_of(q_packed) < bits_of(q) + in) return MOE_ERR_ARG;   // overlap
+  if (!q || !scales || !packed) return MOE_ERR_ARG;
+  if ((bits_of(q) & 3) || (bits_of(scales) & 1) || (bits_of(packed) & 15)) return MOE_ERR_ARG;
+  const size_t in = (size_t)mats * N * K / 2, outb = (size_t)mats * moe_w4_packed_bytes(N, K, group, zeros != nullptr);
+  if (bits_of(q) < bits_of(packed) + outb && bits_of(packed) < bits_of(q) + in) return MOE_ERR_ARG;   // overlap
   if (mats > 1 && N % 32) return MOE_ERR_ARG;     // a stack of matrices is addressed by whole tiles
-  const long long blocks = (long long)(outb / 2048);
+  const long long blocks = (long long)(outb / w4_block(group, zeros != nullptr));
   if (ceil_div(blocks, 8) > 0x7fffffffll) return MOE_ERR_ARG;
-  pack_w4_kernel<<<(unsigned)ceil_div(blocks, 8), 256, 0, as_stream(stream)>>>(
-      q, scales, zeros, blocks, N, K, group, q_packed, reinterpret_cast<uint32_t*>(scales_packed),
-      reinterpret_cast<uint16_t*>(zeros_packed));
+  pack_w4_kernel<<<(unsigned)ceil_div(blocks, 8), 256, 0, as_stream(stream)>>>(q, scales, zeros, blocks, N, K, group,
+                                                                               packed);
   MOE_CHECK_LAUNCH();
   return MOE_OK;
 }
@@ -282,21 +299,20 @@ extern "C" size_t moe_linear_w4_workspace_bytes(int T, int N, int K) {
   return 256;
 }
 
-extern "C" moe_status_t moe_linear_w4(const uint16_t* x, int T, int K, long long x_stride, const uint8_t* q_packed,
-                                      const uint16_t* scales_packed, const uint8_t* zeros_packed, int N, int group,
-                                      const float* bias, void* out, int out_f32, long long out_stride, void* ws,
-                                      size_t ws_bytes, int32_t* dev_status, void* stream) {
+extern "C" moe_status_t moe_linear_w4(const uint16_t* x, int T, int K, long long x_stride, const uint8_t* packed, int N,
+                                      int group, int zeros, const float* bias, void* out, int out_f32,
+                                      long long out_stride, void* ws, size_t ws_bytes, int32_t* dev_status,
+                                      void* stream) {
   using namespace moe;
   using namespace moe::few;
-  if (T < 0 || !w4_shape_ok(0, N, K, group) || x_stride < K || x_stride % 8 || out_stride < N ||
-      (out_f32 != 0 && out_f32 != 1))
+  if (T < 0 || !w4_shape_ok(0, N, K, group) || (zeros != 0 && zeros != 1) || x_stride < K || x_stride % 8 ||
+      out_stride < N || (out_f32 != 0 && out_f32 != 1))
     return MOE_ERR_ARG;
   if (!ws || ws_bytes < moe_linear_w4_workspace_bytes(T, N, K)) return MOE_ERR_WORKSPACE;
   if (bits_of(ws) & 255) return MOE_ERR_ARG;
   if (T == 0) return MOE_OK;
-  if (!x || !q_packed || !scales_packed || !out) return MOE_ERR_ARG;
-  if ((bits_of(x) & 15) || (bits_of(q_packed) & 31) || (bits_of(scales_packed) & 15) || (bits_of(zeros_packed) & 15) ||
-      (bits_of(out) & (out_f32 ? 3 : 1)) || (bits_of(bias) & 3))
+  if (!x || !packed || !out) return MOE_ERR_ARG;
+  if ((bits_of(x) & 15) || (bits_of(packed) & 15) || (bits_of(out) & (out_f32 ? 3 : 1)) || (bits_of(bias) & 3))
     return MOE_ERR_ARG;
   LinearArgs a;
   a.x = x;
@@ -304,23 +320,17 @@ extern "C" moe_status_t moe_linear_w4(const uint16_t* x, int T, int K, long long
   a.out_stride = out_stride;
   a.T = T;
   a.N = N;
-  a.q = q_packed;
-  a.scales = scales_packed;
-  a.zeros = zeros_packed;
+  a.K = K;
+  a.w = packed;
+  a.zeros = zeros;
   a.bias = bias;
   a.out = out;
   a.out_f32 = out_f32;
-  a.st.k = K;
-  a.st.nsl = (int)w4_slices(K);
-  a.st.step = 2048;
-  a.st.pitch = 128;
-  a.st.half = (long long)a.st.nsl * 2048;
-  a.st.sc_half = (long long)a.st.nsl * 8 * (256 / group);
   a.blocks = (int)ceil_div(T, LIN_COLS);
   const long long tiles = ceil_div(N, 32) * a.blocks;
   if (tiles > 0x7fffffffll) return MOE_ERR_ARG;
   a.tiles = (int)tiles;
-  a.st.cut(LIN_WARPS, a.tiles <= num_sms());
+  a.cut.set(w4_slices(K), LIN_WORKERS, a.tiles <= num_sms());
   a.dev_status = dev_status;
   cudaStream_t st = as_stream(stream);
   return group == 32 ? launch_linear<32>(a, st) : group == 64 ? launch_linear<64>(a, st) : launch_linear<128>(a, st);

@@ -510,25 +510,23 @@ moe_status_t moe_layer_forward(const moe_layer_desc_t* d, const moe_layer_weight
  *   zero points: lo = min(0, min w), hi = max(0, max w), s = bf16_rn((hi - lo) / 15),
  *                z = clamp(rn(-lo / s), 0, 15), code = clamp(rn(w / s) + z, 0, 15);
  *   s is 1 where that is not positive; IEEE float32 steps, ties to even; w finite.
- * moe_pack_w4: the same values in the order the kernels read them, once per model:
- *   q_packed      mats * moe_w4_packed_bytes(N, K) bytes, 32-byte aligned;
- *   scales_packed mats * moe_w4_packed_bytes(N, K) * 2 / group elements (two bytes each), and
- *   zeros_packed  as many single bytes, both 16-byte aligned.
- *   Blocks of 16 rows x 256 columns, row block major, whole pairs of row blocks and whole
- *   slices of 256 columns (the padding has scale 0).  zeros and zeros_packed: both or neither.
- * K (cols) % 128 == 0, N and K at most 2^24; N % 32 == 0 when mats > 1.
- * Errors: MOE_ERR_ARG for sizes, null pointers, alignment, overlapping q and q_packed. */
+ * moe_pack_w4: the same values in the order the kernels read them, once per model: mats *
+ *   moe_w4_packed_bytes(N, K, group, zeros given) bytes, 16-byte aligned, of blocks of 16 rows
+ *   x 256 columns (codes, then the scales, then the zero points), row block major, whole
+ *   pairs of row blocks and whole 256 columns (the padding has scale 0).
+ * K (cols) % 128 == 0, N at most 2^24, K at most 2^22; N % 32 == 0 when mats > 1.
+ * Errors: MOE_ERR_ARG for sizes, null pointers, alignment, overlapping q and packed. */
 moe_status_t moe_quantize_weight_w4(const uint16_t* w, int mats, int rows, int cols, int group, uint8_t* q,
                                     uint16_t* scales, uint8_t* zeros, void* stream);
-size_t moe_w4_packed_bytes(int N, int K);
+size_t moe_w4_packed_bytes(int N, int K, int group, int zeros);
 moe_status_t moe_pack_w4(const uint8_t* q, const uint16_t* scales, const uint8_t* zeros, int mats, int N, int K,
-                         int group, uint8_t* q_packed, uint16_t* scales_packed, uint8_t* zeros_packed, void* stream);
+                         int group, uint8_t* packed, void* stream);
 
 /* out[t, n] = sum_k x[t, k] * value(n, k) (+ bias[n]), BF16 products, float32 sums, one
  * rounding.  Made for few rows: every 32 rows of x read the weights again.
  *   x          BF16 [T, K], row t at x + t * x_stride (elements, a multiple of 8, >= K),
  *              16-byte aligned.
- *   q_packed, scales_packed, zeros_packed (nullable)  one matrix from moe_pack_w4.
+ *   packed     one matrix from moe_pack_w4 (of this group; zeros: 1 if it has zero points).
  *   bias       nullable float32 [N].
  *   out        BF16 (out_f32 = 0) or float32 (1) [T, N], row t at out + t * out_stride (>= N).
  *   ws         moe_linear_w4_workspace_bytes(T, N, K) bytes, 256-byte aligned, zero at first use.
@@ -536,10 +534,9 @@ moe_status_t moe_pack_w4(const uint8_t* q, const uint16_t* scales, const uint8_t
  * Any N >= 1 (mats = 1), K % 128 == 0.  The result does not depend on timing.
  * Errors: MOE_ERR_ARG, MOE_ERR_WORKSPACE. */
 size_t moe_linear_w4_workspace_bytes(int T, int N, int K);
-moe_status_t moe_linear_w4(const uint16_t* x, int T, int K, long long x_stride, const uint8_t* q_packed,
-                           const uint16_t* scales_packed, const uint8_t* zeros_packed, int N, int group,
-                           const float* bias, void* out, int out_f32, long long out_stride, void* ws,
-                           size_t ws_bytes, int32_t* dev_status, void* stream);
+moe_status_t moe_linear_w4(const uint16_t* x, int T, int K, long long x_stride, const uint8_t* packed, int N,
+                           int group, int zeros, const float* bias, void* out, int out_f32, long long out_stride,
+                           void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
 
 /* The router from hidden states, T <= MOE_FEW_MAX_TOKENS:
  *   logits[t, e] = float32(sum_h x[t, h] * w_router[e, h] + bias[e]), the sum carried to about
@@ -570,21 +567,18 @@ typedef struct {
   int has_shared;     /* 1: one shared expert of the same I and format */
   int weight_tiles;   /* 1: BF16 / E4M3 weights in the tile layout of moe_pack_weights */
   int group;          /* MOE_W4: 32, 64 or 128; else 0 */
+  int zeros;          /* MOE_W4: 1 if the packed weights have zero points; else 0 */
 } moe_few_desc_t;
 
 typedef struct {
-  const void* w13;         /* [E, 2I, H] gate rows then up rows, 32-byte aligned; W4: packed */
-  const void* w13_scales;  /* E4M3: float32 [E, 2I/128, H/128]; W4: packed scales */
-  const void* w13_zeros;   /* W4: packed zeros or NULL (for all four matrices or for none) */
-  const void* w2;          /* [E, H, I] */
-  const void* w2_scales;
-  const void* w2_zeros;
-  const void* shared_w13;  /* has_shared: [2I, H] */
-  const void* shared_w13_scales;
-  const void* shared_w13_zeros;
-  const void* shared_w2;   /* has_shared: [H, I] */
-  const void* shared_w2_scales;
-  const void* shared_w2_zeros;
+  const void* w13;            /* [E, 2I, H] gate rows then up rows, 16-byte aligned; W4: packed */
+  const float* w13_scales;    /* E4M3: [E, 2I/128, H/128] */
+  const void* w2;             /* [E, H, I] */
+  const float* w2_scales;
+  const void* shared_w13;     /* has_shared: [2I, H] */
+  const float* shared_w13_scales;
+  const void* shared_w2;      /* has_shared: [H, I] */
+  const float* shared_w2_scales;
   const uint16_t* w_router;   /* nullable BF16 [E, H]: route inside the layer (moe_route_hidden) */
   const float* router_bias;   /* nullable float32 [E] */
 } moe_few_weights_t;
@@ -600,7 +594,8 @@ size_t moe_layer_few_workspace_bytes(const moe_few_desc_t* d);
  *              id is one more slot).
  *   out        BF16 [T, H], every row written.
  *   ws         moe_layer_few_workspace_bytes(d) bytes, 256-byte aligned, zero at first use.
- *   dev_status nullable; MOE_DEV_BAD_EXPERT, MOE_DEV_PIPELINE_TIMEOUT (a grid barrier gave up).
+ *   dev_status nullable; MOE_DEV_BAD_EXPERT, MOE_DEV_PIPELINE_TIMEOUT (a wait gave up; the
+ *              output is invalid).
  * Errors: MOE_ERR_ARG, MOE_ERR_WORKSPACE; MOE_ERR_CUDA if the launch fails (it needs every SM
  * of the GPU to itself: one block per SM). */
 moe_status_t moe_layer_few(const moe_few_desc_t* d, const moe_few_weights_t* w, const uint16_t* x,

@@ -102,8 +102,7 @@ def route(x, w_router, bias, K):
 
 
 def pack_w4(q, scales, zeros=None):
-    """moe_pack_w4 of one matrix, from the layout's definition: numpy arrays (codes uint8
-    [bytes], scales uint16 [n], zeros uint8 [n] or None)."""
+    """moe_pack_w4 of one matrix, from the layout's definition: numpy uint8 bytes."""
     import numpy as np
     N, K = q.shape[0], 2 * q.shape[1]
     group = K // scales.shape[0]
@@ -112,22 +111,25 @@ def pack_w4(q, scales, zeros=None):
     code[:N, 0:K:2] = q & 15
     code[:N, 1:K:2] = q >> 4
     nsl, nrb = K256 // 256, N32 // 16
-    oq = np.zeros((nrb, nsl, 2, 8, 4, 8), np.uint32)      # [row block][slice][half][g][t][word]
+    oq = np.zeros((nrb, nsl, 2, 2, 8, 4, 4), np.uint32)      # [row block][slice][half][J][g][t][word]
     for h in range(2):
-        for g in range(8):
-            for t in range(4):
-                for j in range(8):
+        for j in range(8):
+            for g in range(8):
+                for t in range(4):
                     for i in range(8):
                         nib = i // 2 + 4 * (i % 2)
-                        c = code[h * 8 + g::16, j * 32 + t * 8 + i::256]
-                        oq[:, :, h, g, t, j] |= c << (4 * nib)
+                        oq[:, :, h, j // 4, g, t, j % 4] |= code[h * 8 + g::16, j * 32 + t * 8 + i::256] << (4 * nib)
+
     def params(p, dt):
         full = np.zeros((K256 // group, N32), dt)
         full[:K // group, :N] = p
         # [slice][group][row block][half][g] -> [row block][slice][g][group][half]
-        return np.ascontiguousarray(full.reshape(nsl, ng, nrb, 2, 8).transpose(2, 0, 4, 1, 3)).reshape(-1)
-    return (oq.reshape(-1).view(np.uint8), params(scales, np.uint16),
-            None if zeros is None else params(zeros, np.uint8))
+        v = np.ascontiguousarray(full.reshape(nsl, ng, nrb, 2, 8).transpose(2, 0, 4, 1, 3))
+        return v.reshape(nrb, nsl, -1).view(np.uint8)
+    parts = [oq.reshape(nrb, nsl, -1).view(np.uint8), params(scales, np.uint16)]
+    if zeros is not None:
+        parts.append(params(zeros, np.uint8))
+    return np.concatenate(parts, axis=2).reshape(-1)
 
 
 def quantize_w4(w, group, with_zeros):

@@ -58,10 +58,8 @@ def test_pack_w4_layout(mats, N, K, group, zeros):
         normal(g, mats, K // group, N), torch.randint(0, 16, (mats, K // group, N), generator=g, device="cuda", dtype=torch.uint8))
     p = moe.moe_pack_w4(q, s, z)
     for m in range(mats):
-        oq, os_, oz = ref.pack_w4(q[m].cpu().numpy(), bits(s[m]), None if z is None else z[m].cpu().numpy())
-        assert np.array_equal(p.q[m].cpu().numpy(), oq)
-        assert np.array_equal(bits(p.scales[m]), os_)
-        assert z is None or np.array_equal(p.zeros[m].cpu().numpy(), oz)
+        want = ref.pack_w4(q[m].cpu().numpy(), bits(s[m]), None if z is None else z[m].cpu().numpy())
+        assert np.array_equal(p.data[m].cpu().numpy(), want)
 
 
 # ----------------------------------------------------------------------------------- linear
