@@ -57,6 +57,12 @@ __device__ __forceinline__ bool wait_for(Done done, int32_t* dev_status) {
   return true;
 }
 
+// The same for a whole warp: one answer for all lanes.
+template <class Done>
+__device__ __forceinline__ bool warp_wait_for(Done done, int32_t* dev_status) {
+  return __all_sync(0xffffffffu, wait_for(done, dev_status));
+}
+
 // HALF: operands are FP16, else BF16.
 template <bool HALF>
 __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -320,42 +326,50 @@ struct Stream {
   int block;                   // W4: bytes of a block
   bool zeros;
   int stage;                   // of the item in use: bit 0, and its barriers' phase above
-  int filled;                  // unit of the item on its way, or past the end
+  static constexpr int END = 0x7fffffff;
+  int filled;                  // unit of the item on its way; END past the last
+  bool pending;                // ... which is not written down yet
   int left, x, y0, y1;         // its items still to be asked for, and where they are
   const uint8_t *p0, *p1;
   const CUtensorMap* map;
   int cur;                     // unit in use
   bool dead;                   // a wait gave up
 
-  // the next unit off the feed, for filling
-  __device__ __forceinline__ void grab() {
-    int u = 0;
-    if (lane == 0) u = atomicAdd(&feed.next, 1);
-    u = __shfl_sync(0xffffffffu, u, 0);
-    volatile int *published = &feed.published, *total = &feed.total;
-    if (!wait_for([&] { return *published > u || *total <= u; }, dev_status)) dead = true;
-    __threadfence_block();
-    filled = u;
-    if (dead || *total <= u) {
-      filled = 0x7fffffff;
-      return;
-    }
-    const Unit& k = feed.unit[u & (FEED - 1)];
-    left = k.n;
-    p0 = k.p0;
-    p1 = k.p1;
-    if constexpr (FMT != F_W4) {
-      x = k.x;
-      y0 = k.y0;
-      y1 = k.y1;
-      map = k.map;
-    }
-  }
+  // Asks for the next item, into stage st.  It never waits while a unit is in use: the scheduler waits
+  // for the slowest worker, which must not wait for it in turn.  If the next unit is not written
+  // down yet, take() waits for it, when this worker holds nothing up.
   __device__ __forceinline__ void fill(int st) {
     if (left == 0) {
-      if (filled == 0x7fffffff) return;
-      grab();
-      if (filled == 0x7fffffff) return;
+      if (filled == END) return;
+      if (!pending) {            // the next unit
+        int u = 0;
+        if (lane == 0) u = atomicAdd(&feed.next, 1);
+        filled = __shfl_sync(0xffffffffu, u, 0);
+        pending = true;
+      }
+      int go = 0;
+      if (lane == 0) {
+        volatile int *published = &feed.published, *total = &feed.total;
+        go = *published > filled ? 1 : *total <= filled ? 2 : 0;
+      }
+      go = __shfl_sync(0xffffffffu, go, 0);
+      if (go == 0) return;
+      pending = false;
+      if (go == 2) {
+        filled = END;
+        return;
+      }
+      __threadfence_block();
+      const Unit& k = feed.unit[filled & (FEED - 1)];
+      left = k.n;
+      p0 = k.p0;
+      p1 = k.p1;
+      if constexpr (FMT != F_W4) {
+        x = k.x;
+        y0 = k.y0;
+        y1 = k.y1;
+        map = k.map;
+      }
     }
     if (lane == 0) {
       const uint32_t d = ring_addr + st * F::STAGE, bar = bars + st * 8;
@@ -383,18 +397,33 @@ struct Stream {
     stage = 0;
     left = 0;
     filled = 0;
+    pending = false;
     dead = false;
     fill(0);
   }
   __device__ __forceinline__ bool take() {
+    if (lane == 0 && filled != END) *static_cast<volatile int*>(&feed.use[worker]) = filled;
+    if (pending) {
+      const unsigned long long t0 = clock_ns();
+      while (true) {             // the lanes stay together: fill() is the whole warp's
+        fill(stage & 1);
+        if (!pending) break;
+        __nanosleep(40);
+        if (__any_sync(0xffffffffu, clock_ns() - t0 > TIMEOUT_NS)) {
+          if (lane == 0 && dev_status) atomicOr(dev_status, MOE_DEV_PIPELINE_TIMEOUT);
+          dead = true;
+          break;
+        }
+      }
+    }
     cur = filled;
-    if (dead || cur == 0x7fffffff) return false;
-    if (lane == 0) *static_cast<volatile int*>(&feed.use[worker]) = cur;
-    return true;
+    return !dead && cur != END;
   }
   __device__ __forceinline__ const Unit& unit() const { return feed.unit[cur & (FEED - 1)]; }
   __device__ __forceinline__ void finish() {
-    if (lane == 0) *static_cast<volatile int*>(&feed.use[worker]) = 0x7fffff00;
+    // given up: the item on its way arrives before the block ends
+    if (dead && !pending && filled != END) gg::mbar_drain(bars + (stage & 1) * 8, (stage >> 1) & 1);
+    if (lane == 0) *static_cast<volatile int*>(&feed.use[worker]) = 0x7fffff00;    // far past any unit
   }
 
   // sums = weights x activations over the unit in use.  x0[p][n] is this lane's column of group n,
@@ -446,9 +475,7 @@ struct Stream {
         }
       };
       const uint32_t bar = bars + (stage & 1) * 8, phase = (stage >> 1) & 1;
-      if (!gg::mbar_try_wait(bar, phase) &&
-          !wait_for([&] { return gg::mbar_try_wait(bar, phase); }, dev_status))
-        dead = true;
+      if (!warp_wait_for([&] { return gg::mbar_try_wait(bar, phase); }, dev_status)) dead = true;
       const uint8_t* st = ring + (stage & 1) * F::STAGE;
       Sums<NT> acc;
       if constexpr (FMT == F_E4M3) acc.clear();
@@ -542,7 +569,7 @@ __device__ __forceinline__ bool join(Sums<NT>& sums, JoinShared& j, float4* part
                                      int n, int lane, int32_t* dev_status) {
   const int mine = u % slots;
   volatile int* turn = j.turn;
-  if (!__all_sync(0xffffffffu, wait_for([&] { return turn[mine] == u; }, dev_status))) return false;
+  if (!warp_wait_for([&] { return turn[mine] == u; }, dev_status)) return false;
   if (n > 1) {
     float4* p = parts + mine * stride;
 #pragma unroll

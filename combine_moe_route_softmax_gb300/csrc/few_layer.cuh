@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(THREADS, 1) layer_kernel(const __grid_constant
       const int entry = in.unit().entry;
       const int nc = s.ncols[entry];
       if (in.unit().down) {
-        if (!wait_for([&] { return *ready > entry; }, a.dev_status)) in.dead = true;
+        if (!warp_wait_for([&] { return *ready > entry; }, a.dev_status)) in.dead = true;
         __threadfence_block();
         __syncwarp();
         if (nc <= 4) do_unit<FMT, GROUP, 1, 1>(a, s, in, true, parts, slots, stride);

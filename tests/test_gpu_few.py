@@ -67,7 +67,8 @@ LINEAR = [(1, 512, 256, 32, False, False, False), (1, 32, 128, 128, False, False
           (3, 50, 384, 32, True, True, False), (8, 272, 1408, 128, False, False, True),
           (9, 4096, 640, 64, True, False, False), (17, 1000, 2048, 128, True, True, True),
           (32, 2048, 896, 32, False, True, False), (33, 96, 512, 64, True, False, True),
-          (100, 160, 256, 128, False, False, True), (5, 7168, 4096, 128, False, False, False)]
+          (100, 160, 256, 128, False, False, True), (5, 7168, 4096, 128, False, False, False),
+          (2, 40960, 2048, 64, True, True, True)]
 
 
 @pytest.mark.parametrize("T,N,K,group,zeros,bias,f32", LINEAR)
@@ -84,7 +85,9 @@ def test_linear_w4(T, N, K, group, zeros, bias, f32):
     p = moe.moe_pack_w4(q, s, z)
     ws = moe.moe_linear_w4_workspace(T, N, K)
     dt = torch.float32 if f32 else torch.bfloat16
-    y = moe.moe_linear_w4(x, p, bias=b, out_dtype=dt, ws=ws)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = moe.moe_linear_w4(x, p, bias=b, out_dtype=dt, ws=ws, dev_status=status)
+    assert status.item() == 0
     want, err = ref.linear(x, ref.w4_values(q[0], s[0], None if z is None else z[0]), b)
     assert y.dtype == dt and ref.close(y, want, err) <= 1
     again = moe.moe_linear_w4(x, p, bias=b, out_dtype=dt, ws=ws)
@@ -214,6 +217,10 @@ LAYER = [
     (6, 1152, 384, 9, 4, "w4", True, 0.2, 128, True, False),
     (20, 512, 640, 3, 2, "w4", True, 0.1, 32, True, False),
     (32, 256, 256, 64, 8, "w4", False, 0.0, 128, False, False),
+    # many units per SM: the sequence of units goes round its ring many times
+    (1, 7168, 2048, 4, 3, "e4m3", True, 0.0, 0, False, False),
+    (3, 4096, 2048, 8, 4, "w4", True, 0.0, 32, True, False),
+    (2, 2048, 4096, 6, 3, "bf16", False, 0.0, 0, False, True),
 ]
 
 
