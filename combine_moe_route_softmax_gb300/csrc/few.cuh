@@ -87,11 +87,11 @@ __device__ __forceinline__ void e4m3x4_to_half(uint32_t v, uint32_t& lo, uint32_
 // Eight 4-bit codes of one word minus their zero point -> four pairs (columns 0 1, 2 3, 4 5, 6 7).
 // Column 2i sits at nibble i and 2i + 1 at nibble i + 4, so a mask leaves a pair of codes in
 // the low mantissa bits of two 16-bit halves.  BF16: 0x4300 | c is exactly 128 + c, and minus
-// (128 + z) is exact.  FP16: 0x6400 | c is 1024 + c, and 0x6400 | 16 c is 1024 + 16 c, a
+// (128 + z) is exact (as a multiply-add by one: BF16 has no plain addition).  FP16: 0x6400 | c is 1024 + c, and 0x6400 | 16 c is 1024 + 16 c, a
 // sixteenth of which minus (64 + z) is exact in one multiply-add: two shifts fewer.
 template <bool HALF>
 struct W4Zero {
-  uint32_t a, b;               // 128 + z; or 1024 + z and -(64 + z)
+  uint32_t a, b;               // -(128 + z); or 1024 + z and -(64 + z)
   // z in byte `sel` of the word
   __device__ __forceinline__ W4Zero(uint32_t z, int sel) {
     if (HALF) {
@@ -99,7 +99,7 @@ struct W4Zero {
       a = p | 0x64006400u;
       b = (p << 4) | 0xd400d400u;
     } else {
-      a = __byte_perm(z, 0x43u, 0x4040 | sel * 0x0101);
+      a = __byte_perm(z, 0xc3u, 0x4040 | sel * 0x0101);
       b = 0;
     }
   }
@@ -118,7 +118,7 @@ __device__ __forceinline__ void w4_pairs(uint32_t v, const W4Zero<HALF>& z, uint
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t c = ((v >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-      asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(p[i]) : "r"(c), "r"(z.a));
+      asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(p[i]) : "r"(c), "r"(0x3f803f80u), "r"(z.a));
     }
   }
 }
@@ -216,8 +216,8 @@ __device__ __forceinline__ void mma_step(Sums<NT>& acc, const uint32_t (&a)[4][4
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 // Half an item: sums += weights x activations.  acc: E4M3 sums of the item so far, unscaled.
-template <int FMT, int GROUP, bool HALF, int NT, int PASSES, int J, class Acts>
-__device__ __forceinline__ void half_item(Sums<NT>& sums, Sums<NT>& acc, const uint8_t* stage, Acts acts, int lane,
+template <int FMT, int GROUP, bool HALF, int NT, int PASSES, class Acts>
+__device__ __forceinline__ void half_item(Sums<NT>& sums, Sums<NT>& acc, const uint8_t* stage, int J, Acts acts, int lane,
                                           bool zeros) {
   using F = Format<FMT, GROUP>;
   const int g = lane >> 2, t = lane & 3;
@@ -233,14 +233,14 @@ __device__ __forceinline__ void half_item(Sums<NT>& sums, Sums<NT>& acc, const u
 #pragma unroll
     for (int r = 0; r < 4; ++r) { a[r][0] = q[r].x; a[r][1] = q[r].y; a[r][2] = q[r].z; a[r][3] = q[r].w; }
     uint4 b[PASSES][NT];
-    acts(b, J, 0);
+    acts(b, 0);
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) mma_step<HALF, NT>(sums, a, b[p]);
   } else if constexpr (FMT == F_E4M3) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       uint4 b[PASSES][NT];
-      acts(b, J, i);
+      acts(b, i);
       uint32_t a[4][4];
 #pragma unroll
       for (int r = 0; r < 4; ++r)
@@ -252,11 +252,11 @@ __device__ __forceinline__ void half_item(Sums<NT>& sums, Sums<NT>& acc, const u
   } else {
     // word j of the lane's 8 holds columns j*32 + t*8 .. + 8
     constexpr int WPG = GROUP / 32;   // words per scale group
-    const uint32_t* scales = reinterpret_cast<const uint32_t*>(stage + 2048) + g * F::NG;
-    const uint16_t* zps = reinterpret_cast<const uint16_t*>(stage + 2048 + F::SC) + g * F::NG;
+    const uint32_t* scales = reinterpret_cast<const uint32_t*>(stage + 2048) + g * F::NG + J * (F::NG / 2);
+    const uint16_t* zps = reinterpret_cast<const uint16_t*>(stage + 2048 + F::SC) + g * F::NG + J * (F::NG / 2);
 #pragma unroll
     for (int i0 = 0; i0 < 4; i0 += WPG) {
-      const int gi = (4 * J + i0) / WPG;
+      const int gi = i0 / WPG;
       const uint32_t za = zeros ? zps[gi] : 0x0808u, zb = zeros ? zps[F::HALF / 2 + gi] : 0x0808u;
       const W4Zero<HALF> z[4] = {{za, 0}, {za, 1}, {zb, 0}, {zb, 1}};
       Sums<NT> part;
@@ -264,7 +264,7 @@ __device__ __forceinline__ void half_item(Sums<NT>& sums, Sums<NT>& acc, const u
 #pragma unroll
       for (int i = i0; i < i0 + WPG; ++i) {
         uint4 b[PASSES][NT];
-        acts(b, J, i);
+        acts(b, i);
         uint32_t a[4][4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) w4_pairs<HALF>(word(q[r], i), z[r], a[r]);
@@ -427,9 +427,13 @@ struct Stream {
   }
 
   // sums = weights x activations over the unit in use.  x0[p][n] is this lane's column of group n,
-  // or null; PASSES sets of columns are added into the same sums.  k: columns of the matrix.
+  // or null; PASSES sets of columns are added into the same sums.  k: columns of the matrix.  With
+  // scaled (FP16 only), 16 values of a column share an exponent: ex[n] are those of the lane's column, and
+  // they count from top[n].
   template <int NT, int PASSES>
-  __device__ __forceinline__ void run(Sums<NT>& sums, int k, const uint16_t* const (&x0)[PASSES][NT]) {
+  __device__ __forceinline__ void run(Sums<NT>& sums, int k, const uint16_t* const (&x0)[PASSES][NT],
+                                      bool scaled = false, const uint8_t* const* ex = nullptr,
+                                      const int* top = nullptr) {
     const int t = lane & 3;
     const Unit& un = unit();
     const int s0 = un.s0, n = un.n;
@@ -447,40 +451,82 @@ struct Stream {
     sums.clear();
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
+      // the first half's activations are on their way before the weights are waited for
+      uint4 b[F::HALF_CHUNKS][PASSES][NT];
+      uint2 e8[NT];
+      auto ask = [&](int J) {
+#pragma unroll
+        for (int q = 0; q < F::HALF_CHUNKS; ++q)
+#pragma unroll
+          for (int p = 0; p < PASSES; ++p) load_acts<FMT, NT>(b[q][p], xp[p], J, q, t, kleft);
+      };
+      // exponents of half J: E4M3 one (the lane's 16 columns), W4 eight (words 4J.. of two blocks each)
+      auto ask_exps = [&](int J) {
+        if constexpr (HALF) {
+          if (!scaled) return;
+          const int at = (s0 + i) * (F::KI / 16) + (FMT == F_E4M3 ? t * 2 + J : 8 * J);
+#pragma unroll
+          for (int q = 0; q < NT; ++q) {
+            e8[q] = make_uint2(0, 0);
+            if (ex[q]) {
+              if constexpr (FMT == F_E4M3) e8[q].x = ex[q][at];
+              else e8[q] = *reinterpret_cast<const uint2*>(ex[q] + at);
+            }
+          }
+        }
+      };
+      constexpr bool EARLY = F::HALF_CHUNKS * NT * PASSES <= 8;   // else as they are used: registers
+      if constexpr (EARLY) ask(0);
+      ask_exps(0);
       fill((stage ^ 1) & 1);
-      // few columns: the item's activations are on their way before its weights are waited for
-      constexpr bool EARLY = F::HALF_CHUNKS * NT * PASSES <= 4;
-      uint4 early[EARLY ? 2 * F::HALF_CHUNKS : 1][PASSES][NT];
-      if constexpr (EARLY) {
-#pragma unroll
-        for (int q = 0; q < 2 * F::HALF_CHUNKS; ++q)
-#pragma unroll
-          for (int p = 0; p < PASSES; ++p)
-            load_acts<FMT, NT>(early[q][p], xp[p], q / F::HALF_CHUNKS, q % F::HALF_CHUNKS, t, kleft);
-      }
       float f0 = 1.0f, f1 = 1.0f;
       if constexpr (FMT == F_E4M3) {
         f0 = __ldg(sc0 + i);
         f1 = __ldg(sc1 + i);
       }
-      auto acts = [&](uint4(&b)[PASSES][NT], int J, int I) {
-#pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-          if constexpr (EARLY) {
-#pragma unroll
-            for (int q = 0; q < NT; ++q) b[p][q] = early[J * F::HALF_CHUNKS + I][p][q];
-          } else {
-            load_acts<FMT, NT>(b[p], xp[p], J, I, t, kleft);
-          }
-        }
-      };
       const uint32_t bar = bars + (stage & 1) * 8, phase = (stage >> 1) & 1;
       if (!warp_wait_for([&] { return gg::mbar_try_wait(bar, phase); }, dev_status)) dead = true;
       const uint8_t* st = ring + (stage & 1) * F::STAGE;
       Sums<NT> acc;
       if constexpr (FMT == F_E4M3) acc.clear();
-      half_item<FMT, GROUP, HALF, NT, PASSES, 0>(sums, acc, st, acts, lane, zeros);
-      half_item<FMT, GROUP, HALF, NT, PASSES, 1>(sums, acc, st, acts, lane, zeros);
+      // rolled: one copy of the arithmetic, which several variants of this function share the
+      // instruction cache with
+#pragma unroll 1
+      for (int J = 0; J < 2; ++J) {
+        auto acts = [&](uint4(&v)[PASSES][NT], int I) {
+#pragma unroll
+          for (int p = 0; p < PASSES; ++p) {
+            if constexpr (EARLY) {
+#pragma unroll
+              for (int q = 0; q < NT; ++q) v[p][q] = b[I][p][q];
+            } else {
+              load_acts<FMT, NT>(v[p], xp[p], J, I, t, kleft);
+            }
+          }
+          if constexpr (HALF) {
+            if (scaled) {
+#pragma unroll
+              for (int q = 0; q < NT; ++q) {
+                // bytes 2 I + (t >> 1) of the eight; 2^(exponent - top), 0 where FP16 ends
+                const int e = FMT == F_E4M3 ? e8[q].x : ((I < 2 ? e8[q].x : e8[q].y) >> (16 * (I & 1) + 8 * (t >> 1))) & 255;
+                const float f = __uint_as_float((uint32_t)(127 + max(min(e - top[q], 0), -30)) << 23);
+                const __half2 h = __float2half2_rn(f);
+#pragma unroll
+                for (int p = 0; p < PASSES; ++p) {
+                  __half2* w = reinterpret_cast<__half2*>(&v[p][q]);
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) w[j] = __hmul2(w[j], h);
+                }
+              }
+            }
+          }
+        };
+        half_item<FMT, GROUP, HALF, NT, PASSES>(sums, acc, st, J, acts, lane, zeros);
+        if (J == 0) {
+          if constexpr (EARLY) ask(1);
+          ask_exps(1);
+        }
+      }
       if constexpr (FMT == F_E4M3) {
         // an item is one 128-column scale block
 #pragma unroll
@@ -502,30 +548,34 @@ struct Stream {
   }
 };
 
-// The scheduler warp.  Src says what the CTA's sequence of tiles is: tile() the next one (its number,
-// negative past the end), cut(tile), describe(tile, part, unit), and idle(), called every time
-// round (true if it got something done).
+// The scheduler warp.  Src says what the CTA's sequence of tiles is: next(t, n) the next run of tiles
+// t, t + 1, ... (false past the end), cut(t), same(t) (how many from t on are cut alike),
+// describe(t, part, cut, unit), and idle(), called every time round (true if it got something done).
+constexpr int BATCH = 16;            // units written down at a time
 template <int WORKERS, class Src>
 __device__ __forceinline__ void schedule(Feed<WORKERS>& f, Src& src, int lane, int32_t* dev_status) {
   volatile int* use = f.use;
-  int units = 0;
+  int units = 0, t = 0, n = 0;
   bool end = false;
   unsigned long long t0 = clock_ns();
   while (!end || !src.done()) {
     bool moved = src.idle(lane);
     const int slowest = __reduce_min_sync(0xffffffffu, lane < WORKERS ? use[lane] : 0x7fffffff);
     if (!end && units < slowest + AHEAD) {
-      const int t = src.tile(lane);
-      if (t < 0) {
+      if (n == 0 && !src.next(lane, t, n)) {
         end = true;
         if (lane == 0) *static_cast<volatile int*>(&f.total) = units;
       } else {
         const Cut c = src.cut(t);
-        if (lane < c.parts) src.describe(t, lane, c, f.unit[(units + lane) & (FEED - 1)]);
+        const int m = min(min(n, src.same(t)), max(1, BATCH / c.parts));
+        const int i = lane / c.parts;
+        if (i < m) src.describe(t + i, lane - i * c.parts, c, f.unit[(units + lane) & (FEED - 1)]);
         __threadfence_block();
         __syncwarp();
-        units += c.parts;
+        units += m * c.parts;
         if (lane == 0) *static_cast<volatile int*>(&f.published) = units;
+        t += m;
+        n -= m;
       }
       moved = true;
     }

@@ -5,8 +5,7 @@ namespace moe {
 namespace few {
 
 struct FewPlan {
-  size_t off_tile, off_entry, off_hmax, off_logits, off_x16, off_xunit, off_h32, off_hunit, off_hhi, off_hlo, off_y,
-      total;
+  size_t off_tile, off_entry, off_htop, off_logits, off_x16, off_xunit, off_hexp, off_hhi, off_hlo, off_y, total;
 };
 
 inline bool plan_few(const moe_few_desc_t* d, FewPlan* p) {
@@ -26,13 +25,12 @@ inline bool plan_few(const moe_few_desc_t* d, FewPlan* p) {
   // zero between calls; at the same places for every T
   p->off_tile = o;   o = align256(o + 4 * (size_t)(d->H / 32));
   p->off_entry = o;  o = align256(o + 4 * (size_t)kMaxEntries);
-  p->off_hmax = o;   o = align256(o + 4 * (size_t)kMaxTokens * (d->K + 1));
+  p->off_htop = o;   o = align256(o + 4 * (size_t)kMaxTokens * (d->K + 1));
   // not kept
   p->off_logits = o; o = align256(o + 4 * (size_t)d->T * d->E);
   p->off_x16 = o;    o = align256(o + (half ? 2 * (size_t)d->T * d->H : 0));
   p->off_xunit = o;  o = align256(o + 4 * (size_t)d->T);
-  p->off_h32 = o;    o = align256(o + (half ? 4 * slots * d->I : 0));
-  p->off_hunit = o;  o = align256(o + 4 * slots);
+  p->off_hexp = o;   o = align256(o + (half ? slots * exp_pitch(d->I) : 0));
   p->off_hhi = o;    o = align256(o + 2 * slots * d->I);
   p->off_hlo = o;    o = align256(o + 2 * slots * d->I);
   p->off_y = o;      o = align256(o + 4 * slots * d->H);
@@ -107,11 +105,10 @@ extern "C" moe_status_t moe_layer_few(const moe_few_desc_t* d, const moe_few_wei
   a.ctl = reinterpret_cast<uint32_t*>(b);
   a.tile_count = reinterpret_cast<int32_t*>(b + p.off_tile);
   a.entry_done = reinterpret_cast<int32_t*>(b + p.off_entry);
-  a.h_max = reinterpret_cast<uint32_t*>(b + p.off_hmax);
+  a.h_top = reinterpret_cast<int32_t*>(b + p.off_htop);
   a.x16 = reinterpret_cast<uint16_t*>(b + p.off_x16);
   a.x_unit = reinterpret_cast<float*>(b + p.off_xunit);
-  a.h32 = reinterpret_cast<float*>(b + p.off_h32);
-  a.h_unit = reinterpret_cast<float*>(b + p.off_hunit);
+  a.h_exp = b + p.off_hexp;
   a.h_hi = reinterpret_cast<uint16_t*>(b + p.off_hhi);
   a.h_lo = reinterpret_cast<uint16_t*>(b + p.off_hlo);
   a.y = reinterpret_cast<float*>(b + p.off_y);

@@ -20,9 +20,11 @@
 //
 // 16-bit operands: BF16 weights take BF16 activations.  E4M3 and 4-bit weights become FP16 in
 // fewer instructions than BF16 (the conversion unit gives FP16 pairs), so their activations
-// are FP16, scaled by a power of two per token (x) or per slot (h) that brings the largest
-// value to 2^14: FP16 then holds every BF16 value above 2^-28 of the largest exactly, and the
-// rest to 2^-39 of it.
+// are FP16, scaled by powers of two: x per token, so that its largest value comes to 2^14 (FP16
+// then holds every BF16 value above 2^-28 of the largest exactly, and the rest to 2^-39 of it);
+// h per slot and tile of phase 1 (16 values, whose largest comes to 2^14), as each tile is
+// finished.  Phase 2 brings these to the slot's largest scale as it reads them, by a product with a
+// power of two, so nothing has to wait for the whole of h but the largest exponent.
 #pragma once
 
 #include "few.cuh"
@@ -39,6 +41,11 @@ constexpr int kMaxSlots = kMaxTokens * kMaxTopK;
 // one entry = up to COLS columns of one expert; at most one per routed slot, plus the shared ones
 constexpr int kMaxEntries = kMaxSlots + kMaxTokens / COLS;
 constexpr int kMaxWidth = 1 << 17;          // H and I
+
+// Exponents of h are kept as 121 + log2(what 1 in a FP16 term stands for), 1 .. 234; a slot's row of
+// them is padded to 16 bytes.
+constexpr int EXP_BIAS = 121;
+__host__ __device__ __forceinline__ int exp_pitch(int i) { return (i / 16 + 15) / 16 * 16; }
 
 struct LayerArgs {
   CUtensorMap map[4];          // BF16, E4M3: w13, w2, shared w13, shared w2 (boxes of 16 rows x 128 bytes)
@@ -59,14 +66,13 @@ struct LayerArgs {
   // workspace, zero between launches
   uint32_t* ctl;               // barrier arrivals, barrier generation, next tile, CTAs done
   int32_t* tile_count;         // [H / 32] experts done of a row tile
-  int32_t* entry_done;         // [kMaxEntries] row tiles done of an expert's h, plus one when it is ready
-  uint32_t* h_max;             // [T*K + T] largest finite |h| of a slot, as bits
+  int32_t* entry_done;         // [kMaxEntries] row tiles done of an expert's h
+  int32_t* h_top;              // [T*K + T] largest exponent of a slot's h (FP16)
   // workspace
   uint16_t* x16;               // [T, H] FP16
   float* x_unit;               // [T] what 1 in x16 stands for
-  float* h32;                  // [T*K + T, I]
-  float* h_unit;               // [T*K + T]
   uint16_t *h_hi, *h_lo;       // [T*K + T, I]
+  uint8_t* h_exp;              // [T*K + T, ex_pitch] exponent of each 16 values of h (FP16)
   float* y;                    // [T*K + T, H]
 };
 
@@ -264,34 +270,41 @@ __device__ __forceinline__ int atom_add_release(int32_t* p, int v) {
 }
 
 // The scheduler's side: tiles off the queue (the first two of a CTA are its own; the others are
-// asked for one ahead), and which entries' h are ready, as far as tiles of phase 2 need them.
+// asked for one run ahead), and which entries' h are ready, as far as tiles of phase 2 need them.
 template <int FMT, int GROUP>
 struct LayerSched {
   const LayerArgs& a;
   LayerShared& s;
-  const int h_ready;           // entry_done of an entry whose h is ready
-  int q, pending, ready, want;
+  int q, pending, run, ready, want;
 
-  __device__ __forceinline__ int tile(int lane) {
-    int t = 0;
-    if (lane == 0) {
-      t = q < 2 ? (int)(blockIdx.x + q * gridDim.x) : (int)(2 * gridDim.x) + pending;
-      if (q >= 1) pending = (int)atomicAdd(&a.ctl[2], 1u);
+  __device__ __forceinline__ bool next(int lane, int& t, int& n) {
+    // runs of four (smaller) tiles in phase 2 as long as there are plenty: a look at the queue takes
+    // about as long as an SM needs for 32 KB
+    if (q < 2) {
+      t = blockIdx.x + q * gridDim.x;
+      n = 1;
+    } else {
+      t = __shfl_sync(0xffffffffu, pending, 0);
+      n = run;
     }
-    ++q;
-    t = __shfl_sync(0xffffffffu, t, 0);
-    if (t >= s.n_all) return -1;
-    if (t >= s.n1) want = max(want, (t - s.n1) / s.tiles2 + 1);
-    return t;
+    if (++q >= 2) {
+      run = t >= s.n1 && s.n_all - t > 16 * (int)gridDim.x ? 4 : 1;
+      if (lane == 0) pending = (int)(2 * gridDim.x + atomicAdd(&a.ctl[2], (unsigned)run));
+    }
+    n = min(n, s.n_all - t);
+    if (n <= 0) return false;
+    if (t + n > s.n1) want = max(want, (t + n - 1 - s.n1) / s.tiles2 + 1);
+    return true;
   }
   __device__ __forceinline__ Cut cut(int t) const { return s.cut[t >= s.n1]; }
+  __device__ __forceinline__ int same(int t) const { return t < s.n1 ? s.n1 - t : s.n_all - t; }
   __device__ __forceinline__ bool done() const { return ready >= want; }
   __device__ __forceinline__ bool idle(int lane) {
     if (ready >= want) return false;
     const int e = ready + lane;
     int v = 0;
     if (e < want) asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(a.entry_done + e) : "memory");
-    const unsigned m = __ballot_sync(0xffffffffu, e < want && v == h_ready);
+    const unsigned m = __ballot_sync(0xffffffffu, e < want && v == s.tiles1);
     const int n = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
     if (n == 0) return false;
     ready += n;
@@ -364,8 +377,7 @@ __device__ __forceinline__ void plan_phases(const LayerArgs& a, LayerShared& s) 
   s.ready = 0;
 }
 
-// Phase 1's result for one tile: h of 16 intermediate rows; two BF16 terms, or float32 with the
-// largest magnitude of each slot kept (its FP16 terms are made when the expert is complete).
+// Phase 1's result for one tile: h of 16 intermediate rows as two BF16 or scaled FP16 terms.
 template <bool HALF, int NT>
 __device__ __forceinline__ void store_h(const LayerArgs& a, const LayerShared& s, const Sums<NT>& sums, int entry,
                                         int tile, int lane) {
@@ -376,62 +388,46 @@ __device__ __forceinline__ void store_h(const LayerArgs& a, const LayerShared& s
     for (int j = 0; j < 2; ++j) {
       const int c = n * 8 + 2 * t + j;
       const int slot = c < nc ? s.cols[c0 + c] : -1;
-      float unit = 1.0f;
+      float unit = 1.0f, h[2];
       if (HALF && slot >= 0) unit = __ldcg(&a.x_unit[s.toks[c0 + c]]);
-      uint32_t most = 0;
 #pragma unroll
-      for (int i = j; i < 4; i += 2) {
-        const float gate = sums.v[n][0][i] * unit, up = sums.v[n][1][i] * unit;
-        const float h = gate / (1.0f + expf(-gate)) * up;
-        const size_t o = (size_t)slot * a.I + tile * 16 + g + (i >> 1) * 8;
-        if (slot >= 0) {
-          if (HALF) {
-            __stcg(&a.h32[o], h);
-            const uint32_t b = __float_as_uint(h) & 0x7fffffffu;
-            if (b < 0x7f800000u) most = max(most, b);
-          } else {
-            const uint16_t hi = f32_to_bf16(h);
-            a.h_hi[o] = hi;
-            a.h_lo[o] = f32_to_bf16((hi & 0x7fffu) >= 0x7f80u ? 0.0f : h - bf16_to_f32(hi));   // inf, NaN: hi alone
-          }
-        }
+      for (int i = 0; i < 2; ++i) {
+        const float gate = sums.v[n][0][2 * i + j] * unit, up = sums.v[n][1][2 * i + j] * unit;
+        h[i] = gate / (1.0f + expf(-gate)) * up;
       }
+      float sc = 1.0f;
       if (HALF) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t b = __float_as_uint(h[i]) & 0x7fffffffu;
+          if (b < 0x7f800000u) most = max(most, b);
+        }
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-        if (g == 0 && slot >= 0) atomicMax(&a.h_max[slot], most);
+        sc = to_half_scale(most);
+        if (g == 0 && slot >= 0) {
+          const int e = EXP_BIAS + 127 - (int)(__float_as_uint(sc) >> 23);
+          a.h_exp[(size_t)slot * exp_pitch(a.I) + tile] = (uint8_t)e;
+          atomicMax(&a.h_top[slot], e);
+        }
       }
-    }
-}
-
-// The h of a complete entry as two FP16 terms per value (one warp).
-__device__ __forceinline__ void entry_to_half(const LayerArgs& a, const LayerShared& s, int entry, int lane) {
-#pragma unroll 1
-  for (int c = 0; c < s.ncols[entry]; ++c) {
-    const int slot = s.cols[s.first[entry] + c];
-    const float sc = to_half_scale(__ldcg(&a.h_max[slot]));
-    const float4* src = reinterpret_cast<const float4*>(a.h32 + (size_t)slot * a.I);
-    uint2* hi = reinterpret_cast<uint2*>(a.h_hi + (size_t)slot * a.I);
-    uint2* lo = reinterpret_cast<uint2*>(a.h_lo + (size_t)slot * a.I);
-#pragma unroll 4
-    for (int i = lane; i < a.I / 4; i += 32) {
-      const float4 v = __ldcg(src + i);
-      const float f[4] = {v.x * sc, v.y * sc, v.z * sc, v.w * sc};
-      uint16_t p[4], r[4];
+      if (slot < 0) continue;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        p[j] = half_bits(f[j]);
-        r[j] = (p[j] & 0x7fffu) >= 0x7c00u ? 0 : half_bits(f[j] - __half2float(__ushort_as_half(p[j])));
+      for (int i = 0; i < 2; ++i) {
+        const size_t o = (size_t)slot * a.I + tile * 16 + g + i * 8;
+        if (HALF) {
+          const float v = h[i] * sc;
+          const uint16_t hi = half_bits(v);
+          a.h_hi[o] = hi;
+          a.h_lo[o] = (hi & 0x7fffu) >= 0x7c00u ? 0 : half_bits(v - __half2float(__ushort_as_half(hi)));
+        } else {
+          const uint16_t hi = f32_to_bf16(h[i]);
+          a.h_hi[o] = hi;
+          a.h_lo[o] = f32_to_bf16((hi & 0x7fffu) >= 0x7f80u ? 0.0f : h[i] - bf16_to_f32(hi));   // inf, NaN: hi alone
+        }
       }
-      hi[i] = make_uint2(p[0] | (uint32_t)p[1] << 16, p[2] | (uint32_t)p[3] << 16);
-      lo[i] = make_uint2(r[0] | (uint32_t)r[1] << 16, r[2] | (uint32_t)r[3] << 16);
     }
-    __syncwarp();
-    if (lane == 0) {
-      a.h_unit[slot] = 1.0f / sc;
-      a.h_max[slot] = 0;
-    }
-  }
 }
 
 // Phase 2's result for one (row tile, expert): y rows; up to 4 columns come as hi and lo columns
@@ -453,7 +449,7 @@ __device__ __forceinline__ void store_y(const LayerArgs& a, const LayerShared& s
       const int c = n * 8 + 2 * t + (i & 1);
       if (c < nc) {
         const int slot = s.cols[c0 + c];
-        const float unit = HALF ? __ldcg(&a.h_unit[slot]) : 1.0f;
+        const float unit = HALF ? __uint_as_float((uint32_t)(127 - EXP_BIAS + __ldcg(&a.h_top[slot])) << 23) : 1.0f;
         float* p = a.y + (size_t)slot * a.H + tile * 32 + g + (i >> 1) * 8;
         __stcg(p, sums.v[n][0][i] * unit);
         __stcg(p + 16, sums.v[n][1][i] * unit);
@@ -502,34 +498,37 @@ __device__ __forceinline__ void do_unit(const LayerArgs& a, LayerShared& s, Laye
   const int entry = un.entry, row = un.row, part = un.part, n = un.parts;
   const int nc = s.ncols[entry], c0 = s.first[entry];
   const uint16_t* x[PASSES][NT];
+  const uint8_t* ex[NT];
+  int top[NT];
 #pragma unroll
-  for (int p = 0; p < PASSES; ++p)
+  for (int i = 0; i < NT; ++i) {
+    const bool pairs = down && PASSES == 1;              // hi and lo as columns of one group
+    const int c = pairs ? (g & 3) : i * 8 + g;
+    const int slot = c < nc ? s.cols[c0 + c] : -1;
+    ex[i] = nullptr;
+    top[i] = 0;
+    if (HALF && down && slot >= 0) {
+      ex[i] = a.h_exp + (size_t)slot * exp_pitch(a.I);
+      top[i] = __ldcg(&a.h_top[slot]);
+    }
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
+    for (int p = 0; p < PASSES; ++p) {
       x[p][i] = nullptr;
-      const bool pairs = down && PASSES == 1;              // hi and lo as columns of one group
-      const int c = pairs ? (g & 3) : i * 8 + g;
-      if (c < nc) {
+      if (slot >= 0) {
         if (!down)
           x[p][i] = (HALF ? a.x16 : a.x) + (size_t)s.toks[c0 + c] * a.H;
         else
-          x[p][i] = ((pairs ? g >= 4 : p == 1) ? a.h_lo : a.h_hi) + (size_t)s.cols[c0 + c] * a.I;
+          x[p][i] = ((pairs ? g >= 4 : p == 1) ? a.h_lo : a.h_hi) + (size_t)slot * a.I;
       }
     }
+  }
   Sums<NT> sums;
-  in.template run<NT, PASSES>(sums, down ? a.I : a.H, x);
+  in.template run<NT, PASSES>(sums, down ? a.I : a.H, x, HALF && down, ex, top);
   if (!join<NT>(sums, s.join, parts, slots, stride, in.cur, in.cur - part, n, lane, a.dev_status)) return;
   if (!down) {
     store_h<HALF, NT>(a, s, sums, entry, row, lane);
     __syncwarp();
-    int old = 0;
-    if (lane == 0) old = atom_add_release(&a.entry_done[entry], 1);
-    if (HALF && __shfl_sync(0xffffffffu, old, 0) == s.tiles1 - 1) {
-      __threadfence();
-      entry_to_half(a, s, entry, lane);
-      __syncwarp();
-      if (lane == 0) atom_add_release(&a.entry_done[entry], 1);
-    }
+    if (lane == 0) atom_add_release(&a.entry_done[entry], 1);
     return;
   }
   store_y<HALF, NT>(a, s, sums, entry, row, lane);
@@ -552,7 +551,8 @@ __global__ void __launch_bounds__(THREADS, 1) layer_kernel(const __grid_constant
   const bool sync = HALF || a.w_router;
   uint32_t gen = 0;
   if (HALF)
-    for (int t = blockIdx.x; t < a.T; t += gridDim.x) token_to_half(a, s, t, tid);
+    // by the last CTAs, which have the fewest router rows
+    for (int t = gridDim.x - 1 - blockIdx.x; t < a.T; t += gridDim.x) token_to_half(a, s, t, tid);
   if (a.w_router)
     router_logits<WARPS>(a.x, a.w_router, a.router_bias, a.T, a.H, a.E, a.logits, s.scratch, blockIdx.x, gridDim.x,
                          warp, lane);
@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(THREADS, 1) layer_kernel(const __grid_constant
     return;
   }
   if (warp == WORKERS) {
-    LayerSched<FMT, GROUP> src{a, s, s.tiles1 + (HALF ? 1 : 0), 0, 0, 0, 0};
+    LayerSched<FMT, GROUP> src{a, s, 0, 0, 0, 0, 0};
     schedule(s.feed, src, lane, a.dev_status);
   } else {
     constexpr int RING = 2 * Format<FMT, GROUP>::STAGE;
@@ -629,17 +629,20 @@ __global__ void __launch_bounds__(THREADS, 1) layer_kernel(const __grid_constant
     volatile int* ready = &s.ready;
     while (in.take()) {
       const int entry = in.unit().entry;
+      const bool down = in.unit().down;
       const int nc = s.ncols[entry];
-      if (in.unit().down) {
+      if (down) {
         if (!warp_wait_for([&] { return *ready > entry; }, a.dev_status)) in.dead = true;
         __threadfence_block();
         __syncwarp();
-        if (nc <= 4) do_unit<FMT, GROUP, 1, 1>(a, s, in, true, parts, slots, stride);
-        else if (nc <= 8) do_unit<FMT, GROUP, 1, 2>(a, s, in, true, parts, slots, stride);
-        else do_unit<FMT, GROUP, 2, 2>(a, s, in, true, parts, slots, stride);
+      }
+      // up to 4 columns in phase 2: hi and lo side by side in one group of 8, else one after the other
+      if (nc > 8) {
+        if (down) do_unit<FMT, GROUP, 2, 2>(a, s, in, down, parts, slots, stride);
+        else do_unit<FMT, GROUP, 2, 1>(a, s, in, down, parts, slots, stride);
       } else {
-        if (nc <= 8) do_unit<FMT, GROUP, 1, 1>(a, s, in, false, parts, slots, stride);
-        else do_unit<FMT, GROUP, 2, 1>(a, s, in, false, parts, slots, stride);
+        if (down && nc > 4) do_unit<FMT, GROUP, 1, 2>(a, s, in, down, parts, slots, stride);
+        else do_unit<FMT, GROUP, 1, 1>(a, s, in, down, parts, slots, stride);
       }
     }
     in.finish();
@@ -654,6 +657,7 @@ __global__ void __launch_bounds__(THREADS, 1) layer_kernel(const __grid_constant
   if (!s.go) return;
   __threadfence();
   for (int i = tid; i < s.n_entries; i += THREADS) a.entry_done[i] = 0;
+  for (int i = tid; i < a.T * (a.K + 1); i += THREADS) a.h_top[i] = 0;
   if (tid < 2) a.ctl[2 + tid] = 0;
 }
 

@@ -35,10 +35,13 @@ template <int GROUP>
 struct LinearSched {
   const LinearArgs& a;
   int q;
-  __device__ __forceinline__ int tile(int) {
-    const long long n = blockIdx.x + (long long)q++ * gridDim.x;
-    return n < a.tiles ? (int)n : -1;
+  __device__ __forceinline__ bool next(int, int& t, int& n) {
+    const long long i = blockIdx.x + (long long)q++ * gridDim.x;
+    t = (int)i;
+    n = 1;
+    return i < a.tiles;
   }
+  __device__ __forceinline__ int same(int) const { return 1; }
   __device__ __forceinline__ Cut cut(int) const { return a.cut; }
   __device__ __forceinline__ bool done() const { return true; }
   __device__ __forceinline__ bool idle(int) { return false; }
