@@ -95,9 +95,8 @@ struct W4Zero {
   // z in byte `sel` of the word
   __device__ __forceinline__ W4Zero(uint32_t z, int sel) {
     if (HALF) {
-      const uint32_t p = __byte_perm(z, 0, 0x4040 | sel * 0x0101);
-      a = p | 0x64006400u;
-      b = (p << 4) | 0xd400d400u;
+      a = __byte_perm(z, 0x64u, 0x4040 | sel * 0x0101);
+      asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(b) : "r"(a), "r"(0xbc00bc00u), "r"(0x63806380u));   // 960 - a
     } else {
       a = __byte_perm(z, 0xc3u, 0x4040 | sel * 0x0101);
       b = 0;
@@ -252,13 +251,31 @@ __device__ __forceinline__ void half_item(Sums<NT>& sums, Sums<NT>& acc, const u
   } else {
     // word j of the lane's 8 holds columns j*32 + t*8 .. + 8
     constexpr int WPG = GROUP / 32;   // words per scale group
-    const uint32_t* scales = reinterpret_cast<const uint32_t*>(stage + 2048) + g * F::NG + J * (F::NG / 2);
-    const uint16_t* zps = reinterpret_cast<const uint16_t*>(stage + 2048 + F::SC) + g * F::NG + J * (F::NG / 2);
+    constexpr int HG = F::NG / 2;     // groups of half an item
+    uint32_t scs[2][HG], zps[2][(HG + 1) / 2];     // by half tile: BF16 pairs; bytes, two groups a word
+    const uint8_t* par = stage + 2048 + (g * F::NG + J * HG) * 4;
+    const uint8_t* zpar = stage + 2048 + F::SC + (g * F::NG + J * HG) * 2;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (HG == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(par + h * F::HALF);
+        scs[h][0] = v.x; scs[h][1] = v.y; scs[h][2] = v.z; scs[h][3] = v.w;
+        const uint2 z = zeros ? *reinterpret_cast<const uint2*>(zpar + h * F::HALF) : make_uint2(0x08080808u, 0x08080808u);
+        zps[h][0] = z.x; zps[h][1] = z.y;
+      } else if constexpr (HG == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(par + h * F::HALF);
+        scs[h][0] = v.x; scs[h][1] = v.y;
+        zps[h][0] = zeros ? *reinterpret_cast<const uint32_t*>(zpar + h * F::HALF) : 0x08080808u;
+      } else {
+        scs[h][0] = *reinterpret_cast<const uint32_t*>(par + h * F::HALF);
+        zps[h][0] = zeros ? *reinterpret_cast<const uint16_t*>(zpar + h * F::HALF) : 0x0808u;
+      }
+    }
 #pragma unroll
     for (int i0 = 0; i0 < 4; i0 += WPG) {
-      const int gi = i0 / WPG;
-      const uint32_t za = zeros ? zps[gi] : 0x0808u, zb = zeros ? zps[F::HALF / 2 + gi] : 0x0808u;
-      const W4Zero<HALF> z[4] = {{za, 0}, {za, 1}, {zb, 0}, {zb, 1}};
+      const int gi = i0 / WPG, zb = (gi & 1) * 2;
+      const W4Zero<HALF> z[4] = {{zps[0][gi >> 1], zb}, {zps[0][gi >> 1], zb + 1}, {zps[1][gi >> 1], zb},
+                                 {zps[1][gi >> 1], zb + 1}};
       Sums<NT> part;
       part.clear();
 #pragma unroll
@@ -273,8 +290,7 @@ __device__ __forceinline__ void half_item(Sums<NT>& sums, Sums<NT>& acc, const u
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t sc = scales[h * (F::HALF / 4) + gi];
-        const float s0 = bf_lo(sc), s1 = bf_hi(sc);
+        const float s0 = bf_lo(scs[h][gi]), s1 = bf_hi(scs[h][gi]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           sums.v[n][h][0] = fmaf(s0, part.v[n][h][0], sums.v[n][h][0]);
@@ -552,8 +568,8 @@ struct Stream {
 // t, t + 1, ... (false past the end), cut(t), same(t) (how many from t on are cut alike),
 // describe(t, part, cut, unit), and idle(), called every time round (true if it got something done).
 constexpr int BATCH = 16;            // units written down at a time
-template <int WORKERS, class Src>
-__device__ __forceinline__ void schedule(Feed<WORKERS>& f, Src& src, int lane, int32_t* dev_status) {
+template <int WORKERS, int SIZE, class Src>
+__device__ __forceinline__ void schedule(Feed<SIZE>& f, Src& src, int lane, int32_t* dev_status) {
   volatile int* use = f.use;
   int units = 0, t = 0, n = 0;
   bool end = false;

@@ -32,7 +32,7 @@ inline bool plan_few(const moe_few_desc_t* d, FewPlan* p) {
   p->off_xunit = o;  o = align256(o + 4 * (size_t)d->T);
   p->off_hexp = o;   o = align256(o + (half ? slots * exp_pitch(d->I) : 0));
   p->off_hhi = o;    o = align256(o + 2 * slots * d->I);
-  p->off_hlo = o;    o = align256(o + 2 * slots * d->I);
+  p->off_hlo = o;    o = align256(o + (half ? 0 : 2 * slots * d->I));
   p->off_y = o;      o = align256(o + 4 * slots * d->H);
   p->total = o;
   return true;
@@ -58,6 +58,7 @@ extern "C" moe_status_t moe_layer_few(const moe_few_desc_t* d, const moe_few_wei
   if (reinterpret_cast<uintptr_t>(ws) & 255) return MOE_ERR_ARG;
   if (d->T == 0) return MOE_OK;
   if (!x || !topk_idx || !topk_w || !out || !w->w13 || !w->w2) return MOE_ERR_ARG;
+  if (reinterpret_cast<uintptr_t>(out) & 7) return MOE_ERR_ARG;
   if (w->w_router && logits) return MOE_ERR_ARG;          // one source of the routing
   if (d->dtype == MOE_E4M3 && (!w->w13_scales || !w->w2_scales)) return MOE_ERR_ARG;
   if (d->has_shared) {

@@ -5,13 +5,9 @@
 //   0  the router logits (with w_router), and for 4- and 8-bit weights the tokens as FP16 (below);
 //      one grid barrier.  Every SM then selects the top-k itself (T x E logits from L2) and
 //      lists the experts met with their columns.
-//   1  tiles of 16 gate + 16 up rows of an expert: h = silu(g) * u of a (token, slot), kept as
-//      two 16-bit terms h = hi + lo (one BF16 term would cost half of the layer's error
-//      budget).
-//   2  tiles of 32 output rows of an expert: y = W2 (hi + lo) in float32, hi and lo as two
-//      columns of the same tensor instruction up to 4 tokens, two instructions above; the
-//      SM that completes a row tile's last expert sums its rows over the slots in the
-//      combine's order.
+//   1  tiles of 16 gate + 16 up rows of an expert: h = silu(g) * u of a (token, slot).
+//   2  tiles of 32 output rows of an expert: y = W2 h in float32; the SM that completes a row
+//      tile's last expert sums its rows over the slots in the combine's order.
 // All tiles, phase 1 then phase 2, expert by expert, are one queue.  The scheduler warp of an SM takes
 // the next tile when its workers are about to need it, so SMs stay level whatever the experts
 // cost, and phase 2 begins on the first experts while phase 1 ends on the last: a tile of phase 2
@@ -25,6 +21,11 @@
 // h per slot and tile of phase 1 (16 values, whose largest comes to 2^14), as each tile is
 // finished.  Phase 2 brings these to the slot's largest scale as it reads them, by a product with a
 // power of two, so nothing has to wait for the whole of h but the largest exponent.
+//
+// Roundings of h: one FP16 term keeps 11 bits, an error of 1.4e-4 of the output beside the 1.7e-3
+// of its BF16 rounding.  One BF16 term would add 1.2e-3, so BF16 layers keep two, h = hi + lo (16
+// bits): side by side as two columns of one tensor instruction up to 4 tokens, as two
+// instructions above.
 #pragma once
 
 #include "few.cuh"
@@ -33,9 +34,13 @@
 namespace moe {
 namespace few {
 
-constexpr int WARPS = 16;
-constexpr int THREADS = WARPS * 32;
-constexpr int WORKERS = WARPS - 1;          // the last warp schedules
+constexpr int MAX_WARPS = 16;
+// Warps of a CTA, the last of which schedules.  W4's unpacking wants more than the 128 registers a
+// thread has with 16 warps: 162 us with 12 warps against 182 on 32 tokens at H = 2048, I = 1408, E = 64,
+// top-8, groups of 32; E4M3's does not: 720 us with 16 against 796 on 16 tokens at H = 7168, I = 2048,
+// E = 256, top-8.
+template <int FMT>
+__host__ __device__ constexpr int warps_of() { return FMT == F_W4 ? 12 : MAX_WARPS; }
 constexpr int PARTS_BYTES = 40 * 1024;      // slots of the joins
 constexpr int kMaxSlots = kMaxTokens * kMaxTopK;
 // one entry = up to COLS columns of one expert; at most one per routed slot, plus the shared ones
@@ -71,7 +76,7 @@ struct LayerArgs {
   // workspace
   uint16_t* x16;               // [T, H] FP16
   float* x_unit;               // [T] what 1 in x16 stands for
-  uint16_t *h_hi, *h_lo;       // [T*K + T, I]
+  uint16_t *h_hi, *h_lo;       // [T*K + T, I]; FP16: h_hi alone
   uint8_t* h_exp;              // [T*K + T, ex_pitch] exponent of each 16 values of h (FP16)
   float* y;                    // [T*K + T, H]
 };
@@ -82,10 +87,10 @@ struct LayerShared {
   int n1, n_all;               // tiles of phase 1, of both phases
   int tiles1, tiles2;          // row tiles of one expert
   Cut cut[2];
-  Feed<WORKERS> feed;
+  Feed<MAX_WARPS - 1> feed;
   int ready;                   // leading entries whose h is ready
   int go;
-  float block[WARPS];
+  float block[MAX_WARPS];
   short expert[kMaxEntries];   // E for the shared expert
   short first[kMaxEntries];    // first column in cols
   int ncols[kMaxEntries];
@@ -99,7 +104,7 @@ struct LayerShared {
   float w[kMaxSlots];
   uint8_t alive[kMaxTokens];   // token has a valid slot
   JoinShared join;
-  float2 scratch[WARPS][ROUTE_TOKENS];
+  float2 scratch[MAX_WARPS][ROUTE_TOKENS];
 };
 
 // Grid barrier in two halves (thread 0; the CTA synchronises around them).  The generation word
@@ -137,10 +142,11 @@ __device__ __forceinline__ float to_half_scale(uint32_t m) {
 __device__ __forceinline__ uint16_t half_bits(float v) { return __half_as_ushort(__float2half_rn(v)); }
 
 // Token t as FP16 (all threads of one CTA).
+template <int WARPS>
 __device__ __forceinline__ void token_to_half(const LayerArgs& a, LayerShared& s, int t, int tid) {
   const uint4* src = reinterpret_cast<const uint4*>(a.x + (size_t)t * a.H);
   uint32_t m = 0;
-  for (int i = tid; i < a.H / 8; i += THREADS) {
+  for (int i = tid; i < a.H / 8; i += WARPS * 32) {
     const uint4 v = __ldg(src + i);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -157,7 +163,7 @@ __device__ __forceinline__ void token_to_half(const LayerArgs& a, LayerShared& s
 #pragma unroll
   for (int i = 0; i < WARPS; ++i) m = max(m, __float_as_uint(s.block[i]));
   const float sc = to_half_scale(m);
-  for (int i = tid; i < a.H / 8; i += THREADS) {
+  for (int i = tid; i < a.H / 8; i += WARPS * 32) {
     const uint4 v = __ldg(src + i);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t o[4];
@@ -173,9 +179,10 @@ __device__ __forceinline__ void token_to_half(const LayerArgs& a, LayerShared& s
 // Lists the experts met -- the shared one, then in the order of their first slots -- and their
 // columns (all threads; every CTA gets the same lists).  Loops are kept rolled: the code runs
 // once per launch and is bound by fetching it.
+template <int WARPS>
 __device__ __forceinline__ void list_entries(const LayerArgs& a, LayerShared& s) {
   const int n = a.T * a.K, tid = threadIdx.x, lane = tid & 31;
-  for (int e = tid; e < a.E; e += THREADS) s.count[e] = 0;
+  for (int e = tid; e < a.E; e += WARPS * 32) s.count[e] = 0;
   if (tid < a.T) {
     bool any = false;
 #pragma unroll 1
@@ -372,12 +379,12 @@ __device__ __forceinline__ void plan_phases(const LayerArgs& a, LayerShared& s) 
   for (int d = 0; d < 2; ++d) {
     const int k = d ? a.I : a.H;
     const int items = FMT == F_W4 ? w4_slices(k) : FMT == F_BF16 ? k / 64 : k / 128;
-    s.cut[d].set(items, WORKERS, (d ? s.n_all - s.n1 : s.n1) <= (int)gridDim.x);
+    s.cut[d].set(items, warps_of<FMT>() - 1, (d ? s.n_all - s.n1 : s.n1) <= (int)gridDim.x);
   }
   s.ready = 0;
 }
 
-// Phase 1's result for one tile: h of 16 intermediate rows as two BF16 or scaled FP16 terms.
+// Phase 1's result for one tile: h of 16 intermediate rows as two BF16 terms or one scaled FP16 term.
 template <bool HALF, int NT>
 __device__ __forceinline__ void store_h(const LayerArgs& a, const LayerShared& s, const Sums<NT>& sums, int entry,
                                         int tile, int lane) {
@@ -417,10 +424,7 @@ __device__ __forceinline__ void store_h(const LayerArgs& a, const LayerShared& s
       for (int i = 0; i < 2; ++i) {
         const size_t o = (size_t)slot * a.I + tile * 16 + g + i * 8;
         if (HALF) {
-          const float v = h[i] * sc;
-          const uint16_t hi = half_bits(v);
-          a.h_hi[o] = hi;
-          a.h_lo[o] = (hi & 0x7fffu) >= 0x7c00u ? 0 : half_bits(v - __half2float(__ushort_as_half(hi)));
+          a.h_hi[o] = half_bits(h[i] * sc);
         } else {
           const uint16_t hi = f32_to_bf16(h[i]);
           a.h_hi[o] = hi;
@@ -430,13 +434,13 @@ __device__ __forceinline__ void store_h(const LayerArgs& a, const LayerShared& s
     }
 }
 
-// Phase 2's result for one (row tile, expert): y rows; up to 4 columns come as hi and lo columns
-// of one group (hi in columns 0-3, lanes t = 0, 1; lo in 4-7, t = 2, 3).
+// Phase 2's result for one (row tile, expert): y rows.  BF16: up to 4 columns come as hi and lo
+// columns of one group (hi in columns 0-3, lanes t = 0, 1; lo in 4-7, t = 2, 3).
 template <bool HALF, int NT>
 __device__ __forceinline__ void store_y(const LayerArgs& a, const LayerShared& s, Sums<NT>& sums, int entry, int tile,
                                         int lane) {
   const int g = lane >> 2, t = lane & 3, nc = s.ncols[entry], c0 = s.first[entry];
-  if (nc <= 4) {
+  if (!HALF && nc <= 4) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -457,36 +461,50 @@ __device__ __forceinline__ void store_y(const LayerArgs& a, const LayerShared& s
     }
 }
 
-// One row tile's outputs, lane = row, in the combine's order: ascending slot, float32 product and
-// sum from +0, the shared row last, one BF16 rounding.
-__device__ __forceinline__ void combine_tile(const LayerArgs& a, const LayerShared& s, int tile, int lane) {
-  const int row = tile * 32 + lane;
-#pragma unroll 2
-  for (int t = 0; t < a.T; ++t) {
-    float acc = 0.0f;
+// One row tile's outputs in the combine's order: ascending slot, float32 product and sum from +0,
+// the shared row last, one BF16 rounding.  Lane = (token of four, four rows): a warp has up to eight
+// 16-byte loads in flight per lane, since this is the tail of the layer.  Not inlined: its registers
+// are not the streaming loop's.
+static __device__ __noinline__ void combine_tile(const LayerArgs& a, const LayerShared& s, int tile, int lane) {
+  const int row = tile * 32 + (lane & 7) * 4;
+#pragma unroll 1
+  for (int t = lane >> 3; t < a.T; t += 4) {
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     const bool sh = a.shared && s.alive[t];
-    const float sv = sh ? __ldcg(a.y + (size_t)(a.T * a.K + t) * a.H + row) : 0.0f;
+    float4 sv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (sh) sv = __ldcg(reinterpret_cast<const float4*>(a.y + (size_t)(a.T * a.K + t) * a.H + row));
 #pragma unroll 1
     for (int k0 = 0; k0 < a.K; k0 += 8) {
-      float v[8];
+      // every row is read, used or not (they all exist): a load behind a condition waits for the one before
+      float4 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[j] = __ldcg(reinterpret_cast<const float4*>(a.y + (size_t)(t * a.K + min(k0 + j, a.K - 1)) * a.H + row));
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int k = k0 + j;
-        v[j] = k < a.K && s.id[t * a.K + k] >= 0 ? __ldcg(&a.y[(size_t)(t * a.K + k) * a.H + row]) : 0.0f;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int k = k0 + j;
-        if (k < a.K && s.id[t * a.K + k] >= 0) acc = __fadd_rn(acc, __fmul_rn(v[j], s.w[t * a.K + k]));
+        const int i = t * a.K + min(k0 + j, a.K - 1);
+        const bool use = k0 + j < a.K && s.id[i] >= 0;
+        const float w = s.w[i];
+        acc[0] = use ? __fadd_rn(acc[0], __fmul_rn(v[j].x, w)) : acc[0];
+        acc[1] = use ? __fadd_rn(acc[1], __fmul_rn(v[j].y, w)) : acc[1];
+        acc[2] = use ? __fadd_rn(acc[2], __fmul_rn(v[j].z, w)) : acc[2];
+        acc[3] = use ? __fadd_rn(acc[3], __fmul_rn(v[j].w, w)) : acc[3];
       }
     }
-    if (sh) acc = __fadd_rn(acc, sv);
-    a.out[(size_t)t * a.H + row] = f32_to_bf16(acc);
+    if (sh) {
+      acc[0] = __fadd_rn(acc[0], sv.x);
+      acc[1] = __fadd_rn(acc[1], sv.y);
+      acc[2] = __fadd_rn(acc[2], sv.z);
+      acc[3] = __fadd_rn(acc[3], sv.w);
+    }
+    const uint32_t lo = f32_to_bf16(acc[0]) | (uint32_t)f32_to_bf16(acc[1]) << 16;
+    const uint32_t hi = f32_to_bf16(acc[2]) | (uint32_t)f32_to_bf16(acc[3]) << 16;
+    *reinterpret_cast<uint2*>(a.out + (size_t)t * a.H + row) = make_uint2(lo, hi);
   }
 }
 
 template <int FMT, int GROUP>
-using LayerStream = Stream<FMT, GROUP, FMT != F_BF16, WORKERS>;
+using LayerStream = Stream<FMT, GROUP, FMT != F_BF16, MAX_WARPS - 1>;
 
 // The unit in use with NT column groups: columns, sums, join, result.
 template <int FMT, int GROUP, int NT, int PASSES>
@@ -502,7 +520,7 @@ __device__ __forceinline__ void do_unit(const LayerArgs& a, LayerShared& s, Laye
   int top[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    const bool pairs = down && PASSES == 1;              // hi and lo as columns of one group
+    const bool pairs = !HALF && down && PASSES == 1;     // hi and lo as columns of one group
     const int c = pairs ? (g & 3) : i * 8 + g;
     const int slot = c < nc ? s.cols[c0 + c] : -1;
     ex[i] = nullptr;
@@ -542,8 +560,9 @@ __device__ __forceinline__ void do_unit(const LayerArgs& a, LayerShared& s, Laye
 }
 
 template <int FMT, int GROUP>
-__global__ void __launch_bounds__(THREADS, 1) layer_kernel(const __grid_constant__ LayerArgs a) {
+__global__ void __launch_bounds__(warps_of<FMT>() * 32, 1) layer_kernel(const __grid_constant__ LayerArgs a) {
   constexpr bool HALF = FMT != F_BF16;
+  constexpr int WARPS = warps_of<FMT>(), THREADS = WARPS * 32, WORKERS = WARPS - 1;
   __shared__ LayerShared s;
   extern __shared__ __align__(1024) uint8_t rings[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -552,7 +571,7 @@ __global__ void __launch_bounds__(THREADS, 1) layer_kernel(const __grid_constant
   uint32_t gen = 0;
   if (HALF)
     // by the last CTAs, which have the fewest router rows
-    for (int t = gridDim.x - 1 - blockIdx.x; t < a.T; t += gridDim.x) token_to_half(a, s, t, tid);
+    for (int t = gridDim.x - 1 - blockIdx.x; t < a.T; t += gridDim.x) token_to_half<WARPS>(a, s, t, tid);
   if (a.w_router)
     router_logits<WARPS>(a.x, a.w_router, a.router_bias, a.T, a.H, a.E, a.logits, s.scratch, blockIdx.x, gridDim.x,
                          warp, lane);
@@ -592,7 +611,7 @@ __global__ void __launch_bounds__(THREADS, 1) layer_kernel(const __grid_constant
     }
   }
   __syncthreads();
-  list_entries(a, s);
+  list_entries<WARPS>(a, s);
   if (tid == 0) {
     plan_phases<FMT>(a, s);
     if (!sync) s.go = 1;
@@ -609,7 +628,7 @@ __global__ void __launch_bounds__(THREADS, 1) layer_kernel(const __grid_constant
   }
   if (warp == WORKERS) {
     LayerSched<FMT, GROUP> src{a, s, 0, 0, 0, 0, 0};
-    schedule(s.feed, src, lane, a.dev_status);
+    schedule<WORKERS>(s.feed, src, lane, a.dev_status);
   } else {
     constexpr int RING = 2 * Format<FMT, GROUP>::STAGE;
     float4* parts = reinterpret_cast<float4*>(rings + WORKERS * RING);
@@ -636,13 +655,16 @@ __global__ void __launch_bounds__(THREADS, 1) layer_kernel(const __grid_constant
         __threadfence_block();
         __syncwarp();
       }
-      // up to 4 columns in phase 2: hi and lo side by side in one group of 8, else one after the other
-      if (nc > 8) {
-        if (down) do_unit<FMT, GROUP, 2, 2>(a, s, in, down, parts, slots, stride);
-        else do_unit<FMT, GROUP, 2, 1>(a, s, in, down, parts, slots, stride);
+      // BF16, phase 2: hi and lo side by side in one group of 8 up to 4 columns, else one after the other
+      if (!HALF && down && nc > 4) {
+        if constexpr (!HALF) {
+          if (nc > 8) do_unit<FMT, GROUP, 2, 2>(a, s, in, down, parts, slots, stride);
+          else do_unit<FMT, GROUP, 1, 2>(a, s, in, down, parts, slots, stride);
+        }
+      } else if (nc > 8) {
+        do_unit<FMT, GROUP, 2, 1>(a, s, in, down, parts, slots, stride);
       } else {
-        if (down && nc > 4) do_unit<FMT, GROUP, 1, 2>(a, s, in, down, parts, slots, stride);
-        else do_unit<FMT, GROUP, 1, 1>(a, s, in, down, parts, slots, stride);
+        do_unit<FMT, GROUP, 1, 1>(a, s, in, down, parts, slots, stride);
       }
     }
     in.finish();
@@ -663,7 +685,7 @@ __global__ void __launch_bounds__(THREADS, 1) layer_kernel(const __grid_constant
 
 template <int FMT, int GROUP>
 cudaError_t launch_layer(const LayerArgs& a, cudaStream_t stream) {
-  constexpr int smem = WORKERS * 2 * Format<FMT, GROUP>::STAGE + PARTS_BYTES;
+  constexpr int smem = (warps_of<FMT>() - 1) * 2 * Format<FMT, GROUP>::STAGE + PARTS_BYTES;
   static std::atomic<unsigned long long> done{0};
   if (!once_per_device(done, [] {
         return cudaFuncSetAttribute(layer_kernel<FMT, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ==
@@ -672,7 +694,7 @@ cudaError_t launch_layer(const LayerArgs& a, cudaStream_t stream) {
     return cudaErrorUnknown;
   void* args[] = {const_cast<LayerArgs*>(&a)};
   return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(&layer_kernel<FMT, GROUP>), dim3(num_sms()),
-                                     dim3(THREADS), args, smem, stream);
+                                     dim3(warps_of<FMT>() * 32), args, smem, stream);
 }
 
 cudaError_t launch_layer_bf16(const LayerArgs& a, cudaStream_t stream);

@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 1) linear_w4_kernel(const Line
   __syncthreads();
   if (warp == LIN_WORKERS) {
     LinearSched<GROUP> src{a, 0};
-    schedule(feed, src, lane, a.dev_status);
+    schedule<LIN_WORKERS>(feed, src, lane, a.dev_status);
     return;
   }
   float4* parts = reinterpret_cast<float4*>(rings + LIN_WORKERS * RING);

@@ -42,7 +42,7 @@ constexpr int ROUTE_TOKENS = 4;   // tokens of one task
 // tasks, so that every SM has some.  By sizes alone: the logits are the same bits in any grid.
 __device__ __forceinline__ int router_split(int tasks, int H) {
   if (tasks > 1024) return 1;
-  return H >= 2048 ? 8 : H >= 1024 ? 4 : H >= 512 ? 2 : 1;
+  return H >= 1024 ? 4 : H >= 512 ? 2 : 1;
 }
 
 // This warp's share of one task: columns of chunks (8 each) first, first + step, ...  Lane 8 * j
@@ -95,7 +95,8 @@ __device__ __forceinline__ void router_dot(const uint16_t* __restrict__ x, const
   rc = c[0];
 }
 
-// All logits, by every CTA of a grid (NW warps each, all threads call).
+// All logits, by every CTA of a grid (NW warps each, all threads call; NW need not be a multiple of
+// the split).
 template <int NW>
 __device__ __forceinline__ void router_logits(const uint16_t* x, const uint16_t* wr, const float* bias, int T, int H,
                                               int E, float* logits, float2 (*scratch)[ROUTE_TOKENS], int cta, int ctas,
@@ -107,7 +108,7 @@ __device__ __forceinline__ void router_logits(const uint16_t* x, const uint16_t*
     const int task = r + mine;
     const int e = task / groups, t0 = (task - e * groups) * ROUTE_TOKENS;
     float s = 0.0f, c = 0.0f;
-    if (task < tasks) {
+    if (mine < per && task < tasks) {
       const uint16_t* row = wr + (size_t)e * H;
       if (T == 1) router_dot<1>(x, row, T, H, 0, slice * 32 + lane, 32 * S, lane, s, c);
       else router_dot<ROUTE_TOKENS>(x, row, T, H, t0, slice * 32 + lane, 32 * S, lane, s, c);
@@ -115,7 +116,7 @@ __device__ __forceinline__ void router_logits(const uint16_t* x, const uint16_t*
     const int j = lane >> 3;       // this lane's token
     if (S > 1) {
       __syncthreads();
-      if ((lane & 7) == 0) scratch[warp][j] = make_float2(s, c);
+      if (mine < per && (lane & 7) == 0) scratch[warp][j] = make_float2(s, c);
       __syncthreads();
       if (slice != 0) continue;
       for (int q = 1; q < S; ++q) {
@@ -123,7 +124,7 @@ __device__ __forceinline__ void router_logits(const uint16_t* x, const uint16_t*
         join_pair(s, c, v.x, v.y);
       }
     }
-    if (task < tasks && (lane & 7) == 0 && j < (T == 1 ? 1 : ROUTE_TOKENS) && t0 + j < T) {
+    if (mine < per && task < tasks && (lane & 7) == 0 && j < (T == 1 ? 1 : ROUTE_TOKENS) && t0 + j < T) {
       if (bias) add_pair(s, c, __ldg(bias + e));
       logits[(size_t)(t0 + j) * E + e] = __fadd_rn(s, c);
     }

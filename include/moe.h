@@ -554,8 +554,9 @@ moe_status_t moe_route_hidden(const uint16_t* x, int T, int H, const uint16_t* w
 
 /* The whole layer for T <= MOE_FEW_MAX_TOKENS tokens in one cooperative launch: (router ->)
  * gate/up + SwiGLU -> down -> combine.  It computes moe_layer_forward's layer with fewer
- * roundings: activations stay BF16 with every weight format (no FP8 activations), h is kept
- * to 16 bits of mantissa and the expert rows in float32, so
+ * roundings: activations stay at 16 bits with every weight format (no FP8 activations), h is
+ * kept to 16 bits of mantissa (BF16 weights) or 11 (FP16, scaled, with the other formats) and
+ * the expert rows in float32, so
  *     out[t] = bf16_rn( sum over ascending k of w_tk * (W2_e silu(g) u), float32 from +0,
  *                       the shared expert's row last )
  * and a token with no valid slot gets +0 and no shared row.  The result does not depend on
@@ -592,7 +593,7 @@ size_t moe_layer_few_workspace_bytes(const moe_few_desc_t* d);
  *   topk_idx, topk_w  [T, K]: written when routed here, else inputs (slots -1 are padding; an
  *              id outside [-1, E) sets MOE_DEV_BAD_EXPERT and counts as padding; a repeated
  *              id is one more slot).
- *   out        BF16 [T, H], every row written.
+ *   out        BF16 [T, H], 8-byte aligned, every row written.
  *   ws         moe_layer_few_workspace_bytes(d) bytes, 256-byte aligned, zero at first use.
  *   dev_status nullable; MOE_DEV_BAD_EXPERT, MOE_DEV_PIPELINE_TIMEOUT (a wait gave up; the
  *              output is invalid).

@@ -5,7 +5,9 @@ Rounding counted: one rounding to the output's type (half a step, finfo.eps / 2 
 float32 sums on the tensor cores, at most one step (2^-23) of the largest partial sum per
 tensor instruction and per scale group -- a partial sum is at most |row| * |column|
 (Cauchy-Schwarz) and a row of k columns takes at most k/8 of them; silu and the
-product, 2^-20 of h; h as two BF16 terms, 2^-16 of h; the combine, one float32 step per slot."""
+product, 2^-20 of h; h as two BF16 terms, 2^-16 of h, or as one FP16 term whose block of 16
+is scaled to its largest value, half a step (2^-11) of h and 2^-25 of the slot's largest; the
+combine, one float32 step per slot."""
 import torch
 
 STEP = 2.0 ** -23
@@ -50,20 +52,22 @@ def linear(x, w, bias=None):
     return y, err
 
 
-def swiglu(x, w13, w2):
-    """(y, allowed error) of one expert for rows x."""
+def swiglu(x, w13, w2, half=False):
+    """(y, allowed error) of one expert for rows x; half: h as one FP16 term."""
     x = x.double()
     i = w13.shape[0] // 2
     z, dz = linear(x, w13)
     g, u = z[:, :i], z[:, i:]
     silu = g * torch.sigmoid(g)
     h = silu * u
-    dh = 1.1 * u.abs() * dz[:, :i] + silu.abs() * dz[:, i:] + 1.1 * dz[:, :i] * dz[:, i:] + h.abs() * (2.0 ** -16 + 2.0 ** -20)
+    dh = 1.1 * u.abs() * dz[:, :i] + silu.abs() * dz[:, i:] + 1.1 * dz[:, :i] * dz[:, i:] + h.abs() * ((2.0 ** -11 if half else 2.0 ** -16) + 2.0 ** -20)
+    if half:
+        dh = dh + 2.0 ** -25 * h.abs().amax(1, keepdim=True)
     y, dy = linear(h, w2)
     return y, dy + dh @ w2.abs().T
 
 
-def layer(x, idx, wt, w13, w2, shared=None):
+def layer(x, idx, wt, w13, w2, shared=None, half=False):
     """(out, allowed error) [T, H]; w13(e), w2(e) give an expert's float64 matrices, shared is a pair."""
     T, K = idx.shape
     H = x.shape[1]
@@ -72,14 +76,14 @@ def layer(x, idx, wt, w13, w2, shared=None):
     size = torch.zeros_like(out)
     for e in sorted(set(idx.flatten().tolist()) - {-1}):
         t, k = (idx == e).nonzero(as_tuple=True)
-        y, d = swiglu(x[t], w13(e), w2(e))
+        y, d = swiglu(x[t], w13(e), w2(e), half)
         w = wt[t, k].double().unsqueeze(1)
         out.index_add_(0, t, w * y)
         err.index_add_(0, t, w.abs() * d)
         size.index_add_(0, t, (w * y).abs())
     if shared is not None:
         some = (idx >= 0).any(1)
-        y, d = swiglu(x[some], *shared)
+        y, d = swiglu(x[some], *shared, half)
         out[some] += y
         err[some] += d
         size[some] += y.abs()

@@ -162,6 +162,7 @@ class Weights:
     def __init__(self, g, dtype, H, I, E, shared, group=0, zeros=False, tiled=False):
         self.kw = dict(dtype={"bf16": moe.MOE_BF16, "e4m3": moe.MOE_E4M3, "w4": moe.MOE_W4}[dtype])
         self.val = {}
+        self.half = dtype != "bf16"
         for name, mats, n, k in (("w13", E, 2 * I, H), ("w2", E, H, I)) + (
                 (("shared_w13", 1, 2 * I, H), ("shared_w2", 1, H, I)) if shared else ()):
             one = name.startswith("shared")
@@ -190,7 +191,7 @@ class Weights:
     def want(self, x, idx, wt):
         v = self.val
         sh = (v["shared_w13"](0), v["shared_w2"](0)) if "shared_w13" in v else None
-        return ref.layer(x, idx, wt, v["w13"], v["w2"], sh)
+        return ref.layer(x, idx, wt, v["w13"], v["w2"], sh, self.half)
 
 
 def random_routing(g, T, K, E, pad):
