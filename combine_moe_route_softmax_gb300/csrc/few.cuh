@@ -122,6 +122,42 @@ __device__ __forceinline__ void w4_pairs(uint32_t v, const W4Zero<HALF>& z, uint
   }
 }
 
+// The power of two that brings a positive finite float (bits m) to [2^14, 2^15), as far as float32
+// can hold it and its inverse (2^-113 .. 2^120).
+__device__ __forceinline__ float to_half_scale(uint32_t m) {
+  const int e = (int)(m >> 23);                            // biased exponent, 0 for 0 and subnormals
+  return __uint_as_float((uint32_t)min(127 + 14 - (e - 127), 127 + 120) << 23);
+}
+__device__ __forceinline__ uint16_t half_bits(float v) { return __half_as_ushort(__float2half_rn(v)); }
+
+// Largest finite magnitude of eight BF16 values, as float bits.
+__device__ __forceinline__ uint32_t bf16_max(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t lo = (w[j] << 16) & 0x7fffffffu, hi = w[j] & 0x7fff0000u;
+    if (lo < 0x7f800000u) m = max(m, lo);
+    if (hi < 0x7f800000u) m = max(m, hi);
+  }
+  return m;
+}
+// Eight BF16 values times sc as FP16.
+__device__ __forceinline__ uint4 bf16_to_half8(const uint4& v, float sc) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    o[j] = half_bits(__uint_as_float(w[j] << 16) * sc) |
+           (uint32_t)half_bits(__uint_as_float(w[j] & 0xffff0000u) * sc) << 16;
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ int atom_add_release(int32_t* p, int v) {
+  int old;
+  asm volatile("atom.add.release.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
+}
+
 // --------------------------------------------------------------------------------- items
 // How the tiles of a phase are cut: units of `len` items, `parts` to a tile (at most `most`), of
 // at least four items unless there is little work.
@@ -143,7 +179,7 @@ struct __align__(16) Unit {
   const CUtensorMap* map;
   int x, y0, y1;
   int entry, row;
-  short s0, n, part, parts;
+  short s0, n, part, parts;   // first item, items, place in the tile, units of the tile
   int down;            // layer: phase 2
 };
 
@@ -328,15 +364,43 @@ __device__ __forceinline__ void feed_init(Feed<WORKERS>& f) {
   if (threadIdx.x < WORKERS) f.use[threadIdx.x] = 0;
 }
 
+// Units off the feed, as one worker takes them.
+template <int WORKERS>
+struct FeedSource {
+  Feed<WORKERS>& feed;
+  int worker;
+  __device__ __forceinline__ int claim(int lane) {
+    int u = 0;
+    if (lane == 0) u = atomicAdd(&feed.next, 1);
+    return __shfl_sync(0xffffffffu, u, 0);
+  }
+  // 1: unit u is written down, 2: there is no such unit, 0: not known yet
+  __device__ __forceinline__ int state(int u, int lane) const {
+    int go = 0;
+    if (lane == 0) {
+      volatile int *published = &feed.published, *total = &feed.total;
+      go = *published > u ? 1 : *total <= u ? 2 : 0;
+    }
+    go = __shfl_sync(0xffffffffu, go, 0);
+    __threadfence_block();
+    return go;
+  }
+  __device__ __forceinline__ const Unit& unit(int u) const { return feed.unit[u & (FEED - 1)]; }
+  __device__ __forceinline__ void at(int u, int lane) const {
+    if (lane == 0) *static_cast<volatile int*>(&feed.use[worker]) = u;
+  }
+};
+
 // A worker warp's stream of units: take() moves to the next one (false at the end), run() multiplies
-// it.  The item after the one in use is always on its way.
-template <int FMT, int GROUP, bool HALF, int WORKERS>
+// it.  The item after the one in use is always on its way.  Src gives the units (FeedSource, or one
+// that works them out).
+template <int FMT, int GROUP, bool HALF, class Src>
 struct Stream {
   using F = Format<FMT, GROUP>;
-  Feed<WORKERS>& feed;
+  Src src;
   uint8_t* ring;               // two stages
   uint32_t ring_addr, bars;    // shared addresses of the ring and of its two barriers
-  int lane, worker;
+  int lane;
   int32_t* dev_status;
   int dx, dy;                  // tensor maps: from one item to the next
   int block;                   // W4: bytes of a block
@@ -358,25 +422,17 @@ struct Stream {
     if (left == 0) {
       if (filled == END) return;
       if (!pending) {            // the next unit
-        int u = 0;
-        if (lane == 0) u = atomicAdd(&feed.next, 1);
-        filled = __shfl_sync(0xffffffffu, u, 0);
+        filled = src.claim(lane);
         pending = true;
       }
-      int go = 0;
-      if (lane == 0) {
-        volatile int *published = &feed.published, *total = &feed.total;
-        go = *published > filled ? 1 : *total <= filled ? 2 : 0;
-      }
-      go = __shfl_sync(0xffffffffu, go, 0);
+      const int go = src.state(filled, lane);
       if (go == 0) return;
       pending = false;
       if (go == 2) {
         filled = END;
         return;
       }
-      __threadfence_block();
-      const Unit& k = feed.unit[filled & (FEED - 1)];
+      const Unit& k = src.unit(filled);
       left = k.n;
       p0 = k.p0;
       p1 = k.p1;
@@ -418,7 +474,7 @@ struct Stream {
     fill(0);
   }
   __device__ __forceinline__ bool take() {
-    if (lane == 0 && filled != END) *static_cast<volatile int*>(&feed.use[worker]) = filled;
+    if (filled != END) src.at(filled, lane);
     if (pending) {
       const unsigned long long t0 = clock_ns();
       while (true) {             // the lanes stay together: fill() is the whole warp's
@@ -435,11 +491,10 @@ struct Stream {
     cur = filled;
     return !dead && cur != END;
   }
-  __device__ __forceinline__ const Unit& unit() const { return feed.unit[cur & (FEED - 1)]; }
   __device__ __forceinline__ void finish() {
     // given up: the item on its way arrives before the block ends
     if (dead && !pending && filled != END) gg::mbar_drain(bars + (stage & 1) * 8, (stage >> 1) & 1);
-    if (lane == 0) *static_cast<volatile int*>(&feed.use[worker]) = 0x7fffff00;    // far past any unit
+    src.at(0x7fffff00, lane);    // far past any unit
   }
 
   // sums = weights x activations over the unit in use.  x0[p][n] is this lane's column of group n,
@@ -451,7 +506,7 @@ struct Stream {
                                       bool scaled = false, const uint8_t* const* ex = nullptr,
                                       const int* top = nullptr) {
     const int t = lane & 3;
-    const Unit& un = unit();
+    const Unit& un = src.unit(cur);
     const int s0 = un.s0, n = un.n;
     const uint16_t* xp[PASSES][NT];
 #pragma unroll

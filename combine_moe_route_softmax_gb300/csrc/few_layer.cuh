@@ -133,28 +133,13 @@ __device__ __forceinline__ bool barrier_wait(uint32_t* bar, uint32_t gen, int32_
   return ok;
 }
 
-// The power of two that brings a positive finite float (bits m) to [2^14, 2^15), as far as float32
-// can hold it and its inverse (2^-113 .. 2^120).
-__device__ __forceinline__ float to_half_scale(uint32_t m) {
-  const int e = (int)(m >> 23);                            // biased exponent, 0 for 0 and subnormals
-  return __uint_as_float((uint32_t)min(127 + 14 - (e - 127), 127 + 120) << 23);
-}
-__device__ __forceinline__ uint16_t half_bits(float v) { return __half_as_ushort(__float2half_rn(v)); }
-
 // Token t as FP16 (all threads of one CTA).
 template <int WARPS>
 __device__ __forceinline__ void token_to_half(const LayerArgs& a, LayerShared& s, int t, int tid) {
   const uint4* src = reinterpret_cast<const uint4*>(a.x + (size_t)t * a.H);
   uint32_t m = 0;
   for (int i = tid; i < a.H / 8; i += WARPS * 32) {
-    const uint4 v = __ldg(src + i);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t lo = (w[j] << 16) & 0x7fffffffu, hi = w[j] & 0x7fff0000u;
-      if (lo < 0x7f800000u) m = max(m, lo);
-      if (hi < 0x7f800000u) m = max(m, hi);
-    }
+    m = max(m, bf16_max(__ldg(src + i)));
   }
   m = __reduce_max_sync(0xffffffffu, m);
   if ((tid & 31) == 0) s.block[tid >> 5] = __uint_as_float(m);
@@ -164,13 +149,7 @@ __device__ __forceinline__ void token_to_half(const LayerArgs& a, LayerShared& s
   for (int i = 0; i < WARPS; ++i) m = max(m, __float_as_uint(s.block[i]));
   const float sc = to_half_scale(m);
   for (int i = tid; i < a.H / 8; i += WARPS * 32) {
-    const uint4 v = __ldg(src + i);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t o[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      o[j] = half_bits(bf_lo(w[j]) * sc) | (uint32_t)half_bits(bf_hi(w[j]) * sc) << 16;
-    reinterpret_cast<uint4*>(a.x16 + (size_t)t * a.H)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+    reinterpret_cast<uint4*>(a.x16 + (size_t)t * a.H)[i] = bf16_to_half8(__ldg(src + i), sc);
   }
   if (tid == 0) a.x_unit[t] = 1.0f / sc;
   __syncthreads();
@@ -268,12 +247,6 @@ __device__ __forceinline__ void list_entries(const LayerArgs& a, LayerShared& s)
     s.n_entries = ent;
     s.max_cols = most;
   }
-}
-
-__device__ __forceinline__ int atom_add_release(int32_t* p, int v) {
-  int old;
-  asm volatile("atom.add.release.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
-  return old;
 }
 
 // The scheduler's side: tiles off the queue (the first two of a CTA are its own; the others are
@@ -504,7 +477,7 @@ static __device__ __noinline__ void combine_tile(const LayerArgs& a, const Layer
 }
 
 template <int FMT, int GROUP>
-using LayerStream = Stream<FMT, GROUP, FMT != F_BF16, MAX_WARPS - 1>;
+using LayerStream = Stream<FMT, GROUP, FMT != F_BF16, FeedSource<MAX_WARPS - 1>>;
 
 // The unit in use with NT column groups: columns, sums, join, result.
 template <int FMT, int GROUP, int NT, int PASSES>
@@ -512,7 +485,7 @@ __device__ __forceinline__ void do_unit(const LayerArgs& a, LayerShared& s, Laye
                                         float4* parts, int slots, int stride) {
   constexpr bool HALF = FMT != F_BF16;
   const int lane = in.lane, g = lane >> 2;
-  const Unit& un = in.unit();
+  const Unit& un = in.src.unit(in.cur);
   const int entry = un.entry, row = un.row, part = un.part, n = un.parts;
   const int nc = s.ncols[entry], c0 = s.first[entry];
   const uint16_t* x[PASSES][NT];
@@ -634,11 +607,10 @@ __global__ void __launch_bounds__(warps_of<FMT>() * 32, 1) layer_kernel(const __
     float4* parts = reinterpret_cast<float4*>(rings + WORKERS * RING);
     const int stride = s.max_cols <= 8 ? 64 : 128;       // a slot is 1 KB for each 8 columns
     const int slots = min(MAX_SLOTS, PARTS_BYTES / (stride * 16));
-    LayerStream<FMT, GROUP> in{s.feed, rings + warp * RING};
+    LayerStream<FMT, GROUP> in{{s.feed, warp}, rings + warp * RING};
     in.ring_addr = gg::smem_u32(in.ring);
     in.bars = gg::smem_u32(&s.feed.full[warp][0]);
     in.lane = lane;
-    in.worker = warp;
     in.dev_status = a.dev_status;
     in.dx = a.tiled ? 0 : 128;
     in.dy = a.tiled ? 128 : 0;
@@ -647,8 +619,8 @@ __global__ void __launch_bounds__(warps_of<FMT>() * 32, 1) layer_kernel(const __
     in.start();
     volatile int* ready = &s.ready;
     while (in.take()) {
-      const int entry = in.unit().entry;
-      const bool down = in.unit().down;
+      const int entry = in.src.unit(in.cur).entry;
+      const bool down = in.src.unit(in.cur).down;
       const int nc = s.ncols[entry];
       if (down) {
         if (!warp_wait_for([&] { return *ready > entry; }, a.dev_status)) in.dead = true;

@@ -1,7 +1,13 @@
 // moe_linear_w4: y = x W^T (+ bias) for a few rows of BF16 x and 4-bit weights with a BF16
 // scale (and optionally a zero point) per group of 32, 64 or 128 columns.  The weight
-// stream, the work division and the arithmetic are those of few.cuh, with one matrix and the
-// rows of x as columns, 32 at a time (each pass over the weights serves 32 rows of x).
+// stream and the arithmetic are those of few.cuh, with one matrix and the rows of x as columns,
+// 32 at a time (each pass over the weights serves 32 rows of x).
+//
+// A CTA keeps its rows of x in shared memory as FP16, scaled by a power of two per row that brings
+// the largest value to 2^14 (exact for values above 2^-28 of it): FP16 codes unpack in fewer
+// instructions than BF16 ones, and 24 rows read from L2 beside every item are three times the
+// weights' bytes.  Where the rows are too long for that, K is shared between CTAs, whose sums the
+// last of them adds up in order.
 //
 // Also the one-time preparation of such weights: moe_quantize_weight_w4 and moe_pack_w4.
 #include "few.cuh"
@@ -10,9 +16,8 @@ namespace moe {
 namespace few {
 
 constexpr int LIN_COLS = 32;
-constexpr int LIN_WARPS = 16;
-constexpr int LIN_WORKERS = LIN_WARPS - 1;   // the last warp schedules
-constexpr int LIN_PARTS = 64 * 1024;
+constexpr int LIN_WARPS = 12;                // as the layer's W4 kernels: registers
+constexpr int LIN_SMEM = 224 * 1024;
 
 struct LinearArgs {
   const uint16_t* x;
@@ -24,60 +29,128 @@ struct LinearArgs {
   void* out;
   int out_f32;
   int32_t* dev_status;
-  Cut cut;
-  int tiles;                   // row tiles x blocks of x
-  int blocks;                  // blocks of LIN_COLS rows of x
+  int nsl;                     // items per tile row
+  int splits, split_len;       // shares of K, items per share
+  Cut cut;                     // of a share
+  int rows, blocks;            // row tiles, blocks of LIN_COLS rows of x
+  int pitch;                   // elements from one row of x to the next in shared memory
+  int slots;                   // of the joins
+  int32_t* count;              // [rows x blocks] shares done, zero between launches
+  float* part;                 // [rows x blocks][splits][NT * 256]
 };
 
-// CTA c takes tiles c, c + CTAs, ...; tile = (row tile, block of x rows), blocks inner, so that the
-// second block of a row tile finds its weights in L2.
+// CTA c has share c % splits of K and, of the tiles (row tile, block of x), c / splits and every
+// (CTAs / splits)-th on; its warps take the units of that sequence in turn.
 template <int GROUP>
-struct LinearSched {
+struct LinearSource {
   const LinearArgs& a;
-  int q;
-  __device__ __forceinline__ bool next(int, int& t, int& n) {
-    const long long i = blockIdx.x + (long long)q++ * gridDim.x;
-    t = (int)i;
-    n = 1;
-    return i < a.tiles;
+  int share, items, parts, first, step, total;   // items of a tile here, its units; units in all
+  int next;
+  __device__ __forceinline__ int claim(int) {
+    const int u = next;
+    next += LIN_WARPS;
+    return u;
   }
-  __device__ __forceinline__ int same(int) const { return 1; }
-  __device__ __forceinline__ Cut cut(int) const { return a.cut; }
-  __device__ __forceinline__ bool done() const { return true; }
-  __device__ __forceinline__ bool idle(int) { return false; }
-  __device__ __forceinline__ void give_up(int) {}
-  __device__ __forceinline__ void describe(int t, int part, const Cut& c, Unit& u) const {
-    const int row = t / a.blocks, s0 = part * c.len, block = w4_block(GROUP, a.zeros);
-    u.entry = t - row * a.blocks;
-    u.row = row;
-    u.s0 = (short)s0;
-    u.n = (short)min(c.len, c.nsl - s0);
-    u.part = (short)part;
-    u.parts = (short)c.parts;
-    u.p0 = a.w + ((long long)row * 2 * c.nsl + s0) * block;
-    u.p1 = u.p0 + (long long)c.nsl * block;
+  __device__ __forceinline__ int state(int u, int) const { return u < total ? 1 : 2; }
+  __device__ __forceinline__ void at(int, int) const {}
+  __device__ __forceinline__ Unit unit(int u) const {
+    const int len = a.cut.len;
+    const int q = u / parts, tile = first + q * step, row = tile / a.blocks;
+    const int block = w4_block(GROUP, a.zeros);
+    Unit k;
+    k.part = (short)(u - q * parts);
+    k.parts = (short)parts;
+    const int s0 = k.part * len;                         // within the share
+    k.s0 = (short)s0;
+    k.n = (short)min(len, items - s0);
+    k.entry = tile - row * a.blocks;
+    k.row = row;
+    k.p0 = a.w + ((long long)row * 2 * a.nsl + share * a.split_len + s0) * block;
+    k.p1 = k.p0 + (long long)a.nsl * block;
+    return k;
   }
 };
 template <int GROUP>
-using LinearStream = Stream<F_W4, GROUP, false, LIN_WORKERS>;
+using LinearStream = Stream<F_W4, GROUP, true, LinearSource<GROUP>>;
+
+// The CTA's rows of x, its share of K, as FP16: warp w takes rows w, w + LIN_WARPS, ...
+__device__ __forceinline__ void stage_rows(const LinearArgs& a, uint16_t* xs, float* unit, int t0, int k0, int k,
+                                           int warp, int lane) {
+  const int n = min(LIN_COLS, a.T - t0);
+#pragma unroll 1
+  for (int r = warp; r < n; r += LIN_WARPS) {
+    const uint4* src = reinterpret_cast<const uint4*>(a.x + (t0 + r) * a.x_stride + k0);
+    uint32_t m = 0;
+#pragma unroll 4
+    for (int i = lane; i < k / 8; i += 32) {
+      const uint4 v = __ldg(src + i);
+      m = max(m, bf16_max(v));
+    }
+    const float sc = to_half_scale(__reduce_max_sync(0xffffffffu, m));
+#pragma unroll 4
+    for (int i = lane; i < k / 8; i += 32)
+      reinterpret_cast<uint4*>(xs + r * a.pitch)[i] = bf16_to_half8(__ldg(src + i), sc);
+    if (lane == 0) unit[r] = 1.0f / sc;
+  }
+}
 
 template <int GROUP, int NT>
 __device__ __forceinline__ void linear_unit(const LinearArgs& a, LinearStream<GROUP>& in, JoinShared& j, float4* parts,
-                                            int slots, int lane) {
+                                            const uint16_t* xs, const float* unit, int k, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  const Unit& un = in.unit();
-  const int row = un.row, t0 = un.entry * LIN_COLS, part = un.part;
+  const Unit un = in.src.unit(in.cur);
+  const int t0 = un.entry * LIN_COLS;
   const uint16_t* x[1][NT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) x[0][n] = t0 + n * 8 + g < a.T ? a.x + (t0 + n * 8 + g) * a.x_stride : nullptr;
+  for (int n = 0; n < NT; ++n) x[0][n] = t0 + n * 8 + g < a.T ? xs + (n * 8 + g) * a.pitch : nullptr;
   Sums<NT> sums;
-  in.template run<NT, 1>(sums, a.K, x);
-  if (!join<NT>(sums, j, parts, slots, NT * 64, in.cur, in.cur - part, a.cut.parts, lane, a.dev_status)) return;
+  in.template run<NT, 1>(sums, k, x);
+  if (!join<NT>(sums, j, parts, a.slots, NT * 64, in.cur, in.cur - un.part, un.parts, lane, a.dev_status)) return;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float f = unit[n * 8 + 2 * t + i];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        sums.v[n][h][i] *= f;
+        sums.v[n][h][i + 2] *= f;
+      }
+    }
+  if (a.splits > 1) {
+    const int tile = un.row * a.blocks + un.entry;
+    float4* p = reinterpret_cast<float4*>(a.part) + (size_t)tile * a.splits * (NT * 64);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        __stcg(&p[in.src.share * (NT * 64) + (n * 2 + h) * 32 + lane],
+               make_float4(sums.v[n][h][0], sums.v[n][h][1], sums.v[n][h][2], sums.v[n][h][3]));
+    __syncwarp();
+    int old = 0;
+    if (lane == 0) old = atom_add_release(&a.count[tile], 1);
+    if (__shfl_sync(0xffffffffu, old, 0) != a.splits - 1) return;
+    __threadfence();
+    if (lane == 0) a.count[tile] = 0;
+    sums.clear();
+#pragma unroll 1
+    for (int s = 0; s < a.splits; ++s)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4 v = __ldcg(&p[s * (NT * 64) + (n * 2 + h) * 32 + lane]);
+          sums.v[n][h][0] += v.x;
+          sums.v[n][h][1] += v.y;
+          sums.v[n][h][2] += v.z;
+          sums.v[n][h][3] += v.w;
+        }
+  }
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = row * 32 + h * 16 + (i >> 1) * 8 + g;
+      const int r = un.row * 32 + h * 16 + (i >> 1) * 8 + g;
       if (r >= a.N) continue;
       const float b = a.bias ? __ldg(a.bias + r) : 0.0f;
 #pragma unroll
@@ -95,32 +168,39 @@ __device__ __forceinline__ void linear_unit(const LinearArgs& a, LinearStream<GR
 }
 
 template <int GROUP, int NT>
-__global__ void __launch_bounds__(LIN_WARPS * 32, 1) linear_w4_kernel(const LinearArgs a) {
+__global__ void __launch_bounds__(LIN_WARPS * 32, 1) linear_w4_kernel(const __grid_constant__ LinearArgs a) {
   extern __shared__ __align__(1024) uint8_t rings[];
   __shared__ JoinShared j;
-  __shared__ Feed<LIN_WORKERS> feed;
+  __shared__ float unit[LIN_COLS];
+  __shared__ __align__(8) unsigned long long full[LIN_WARPS][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int RING = 2 * Format<F_W4, GROUP>::STAGE;
-  constexpr int SLOTS = LIN_PARTS / 1024 / NT < MAX_SLOTS ? LIN_PARTS / 1024 / NT : MAX_SLOTS;
-  join_init(j);
-  feed_init(feed);
-  __syncthreads();
-  if (warp == LIN_WORKERS) {
-    LinearSched<GROUP> src{a, 0};
-    schedule<LIN_WORKERS>(feed, src, lane, a.dev_status);
-    return;
-  }
-  float4* parts = reinterpret_cast<float4*>(rings + LIN_WORKERS * RING);
-  LinearStream<GROUP> in{feed, rings + warp * RING};
+  float4* parts = reinterpret_cast<float4*>(rings + LIN_WARPS * RING);
+  uint16_t* xs = reinterpret_cast<uint16_t*>(rings + LIN_WARPS * RING + a.slots * NT * 1024);
+  const int share = blockIdx.x % a.splits, first = blockIdx.x / a.splits, step = gridDim.x / a.splits;
+  const int tiles = a.rows * a.blocks;
+  const int mine = first < tiles ? (tiles - first + step - 1) / step : 0;
+  const int items = min(a.split_len, a.nsl - share * a.split_len), n_parts = (items + a.cut.len - 1) / a.cut.len;
+  LinearStream<GROUP> in{{a, share, items, n_parts, first, step, mine * n_parts, warp}, rings + warp * RING};
   in.ring_addr = gg::smem_u32(in.ring);
-  in.bars = gg::smem_u32(&feed.full[warp][0]);
+  in.bars = gg::smem_u32(&full[warp][0]);
   in.lane = lane;
-  in.worker = warp;
   in.dev_status = a.dev_status;
   in.block = w4_block(GROUP, a.zeros);
   in.zeros = a.zeros;
-  in.start();
-  while (in.take()) linear_unit<GROUP, NT>(a, in, j, parts, SLOTS, lane);
+  if (lane == 0) {
+    gg::mbar_init(in.bars, 1);
+    gg::mbar_init(in.bars + 8, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncwarp();
+  in.start();                  // the weights are on their way while x is converted
+  join_init(j);
+  const int k0 = share * a.split_len * 256, k = min(a.K - k0, a.split_len * 256);
+  // one block of x at a time stays in shared memory: with more blocks every CTA has one (launch_linear)
+  stage_rows(a, xs, unit, (first % a.blocks) * LIN_COLS, k0, k, warp, lane);
+  __syncthreads();
+  while (in.take()) linear_unit<GROUP, NT>(a, in, j, parts, xs, unit, k, lane);
   in.finish();
 }
 
@@ -224,26 +304,57 @@ __global__ void __launch_bounds__(256) pack_w4_kernel(const uint8_t* __restrict_
   }
 }
 
+// How a product is laid out on the GPU: shares of K so that a block of x fits in shared memory
+// beside the rings and the joins' slots; a whole number of blocks of x per step of tiles, so that
+// a CTA always has the same block.
+struct LinearPlan {
+  int nt, slots, splits, split_len, pitch, ctas, smem;
+  Cut cut;
+  long long tiles;
+};
+inline LinearPlan plan_linear(int T, int N, int K, int group, int sms) {
+  LinearPlan p;
+  const int cols = T < LIN_COLS ? T : LIN_COLS;
+  p.nt = cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
+  p.slots = p.nt == 1 ? 24 : p.nt == 2 ? 16 : LIN_WARPS;   // at least a tile's units
+  const int stage = 2 * (2048 + 8 * (256 / group) * 6);
+  const int fixed = LIN_WARPS * 2 * stage + p.slots * p.nt * 1024;
+  const int room = (LIN_SMEM - fixed) / 2 / cols - 32;      // elements of a row
+  const int nsl = w4_slices(K), fit = room / 256 < 1 ? 1 : room / 256;
+  p.splits = (nsl + fit - 1) / fit;
+  p.split_len = (nsl + p.splits - 1) / p.splits;
+  p.splits = (nsl + p.split_len - 1) / p.split_len;
+  const int blocks = (T + LIN_COLS - 1) / LIN_COLS;
+  p.tiles = ceil_div(N, 32) * blocks;
+  const int len = (K + 127) / 128 * 128 < p.split_len * 256 ? (K + 127) / 128 * 128 : p.split_len * 256;
+  p.pitch = len + 32;          // rows 64 bytes past a multiple of 128: two rows' chunks in different banks
+  p.smem = fixed + cols * p.pitch * 2;
+  p.cut.set(p.split_len, LIN_WARPS, p.tiles * p.splits <= sms);
+  const int unit = p.splits * blocks;
+  p.ctas = sms / unit * unit;
+  if (p.ctas == 0) p.ctas = unit;
+  const long long most = p.tiles * p.splits;
+  if (most < p.ctas) p.ctas = (int)most;
+  return p;
+}
+
 template <int GROUP, int NT>
-moe_status_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
-  constexpr int smem = LIN_WORKERS * 2 * Format<F_W4, GROUP>::STAGE + LIN_PARTS;
+moe_status_t launch_linear(const LinearArgs& a, const LinearPlan& p, cudaStream_t stream) {
   static std::atomic<unsigned long long> done{0};
   if (!once_per_device(done, [] {
-        return cudaFuncSetAttribute(linear_w4_kernel<GROUP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ==
-               cudaSuccess;
+        return cudaFuncSetAttribute(linear_w4_kernel<GROUP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    LIN_SMEM) == cudaSuccess;
       }))
     return MOE_ERR_CUDA;
-  const int ctas = a.tiles < num_sms() ? a.tiles : num_sms();
-  linear_w4_kernel<GROUP, NT><<<ctas, LIN_WARPS * 32, smem, stream>>>(a);
+  linear_w4_kernel<GROUP, NT><<<p.ctas, LIN_WARPS * 32, p.smem, stream>>>(a);
   MOE_CHECK_LAUNCH();
   return MOE_OK;
 }
 template <int GROUP>
-moe_status_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
-  const int cols = a.T < LIN_COLS ? a.T : LIN_COLS;
-  return cols <= 8    ? launch_linear<GROUP, 1>(a, stream)
-         : cols <= 16 ? launch_linear<GROUP, 2>(a, stream)
-                      : launch_linear<GROUP, 4>(a, stream);
+moe_status_t launch_linear(const LinearArgs& a, const LinearPlan& p, cudaStream_t stream) {
+  return p.nt == 1 ? launch_linear<GROUP, 1>(a, p, stream)
+         : p.nt == 2 ? launch_linear<GROUP, 2>(a, p, stream)
+                     : launch_linear<GROUP, 4>(a, p, stream);
 }
 
 inline bool w4_shape_ok(int mats, int N, int K, int group) {
@@ -296,10 +407,14 @@ extern "C" moe_status_t moe_pack_w4(const uint8_t* q, const uint16_t* scales, co
   return MOE_OK;
 }
 
+// The counters of the tiles, then the shares' sums; for the group whose rows of x need most shares.
 extern "C" size_t moe_linear_w4_workspace_bytes(int T, int N, int K) {
+  using namespace moe;
   using namespace moe::few;
   if (T < 0 || !w4_shape_ok(0, N, K, 32)) return 0;
-  return 256;
+  if (T == 0) return 256;
+  const LinearPlan p = plan_linear(T, N, K, 32, num_sms());
+  return align256(4 * (size_t)p.tiles) + (p.splits > 1 ? (size_t)p.tiles * p.splits * p.nt * 1024 : 0);
 }
 
 extern "C" moe_status_t moe_linear_w4(const uint16_t* x, int T, int K, long long x_stride, const uint8_t* packed, int N,
@@ -329,12 +444,21 @@ extern "C" moe_status_t moe_linear_w4(const uint16_t* x, int T, int K, long long
   a.bias = bias;
   a.out = out;
   a.out_f32 = out_f32;
+  const LinearPlan p = plan_linear(T, N, K, group, num_sms());
+  if (p.tiles > 0x3fffffff / p.cut.parts) return MOE_ERR_ARG;
+  a.nsl = w4_slices(K);
+  a.splits = p.splits;
+  a.split_len = p.split_len;
+  a.cut = p.cut;
+  a.rows = (int)ceil_div(N, 32);
   a.blocks = (int)ceil_div(T, LIN_COLS);
-  const long long tiles = ceil_div(N, 32) * a.blocks;
-  if (tiles > 0x7fffffffll) return MOE_ERR_ARG;
-  a.tiles = (int)tiles;
-  a.cut.set(w4_slices(K), LIN_WORKERS, a.tiles <= num_sms());
+  a.pitch = p.pitch;
+  a.slots = p.slots;
+  a.count = static_cast<int32_t*>(ws);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align256(4 * (size_t)p.tiles));
   a.dev_status = dev_status;
   cudaStream_t st = as_stream(stream);
-  return group == 32 ? launch_linear<32>(a, st) : group == 64 ? launch_linear<64>(a, st) : launch_linear<128>(a, st);
+  return group == 32   ? launch_linear<32>(a, p, st)
+         : group == 64 ? launch_linear<64>(a, p, st)
+                       : launch_linear<128>(a, p, st);
 }
