@@ -77,6 +77,20 @@ __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, u
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same from zero: d = a b.
+template <bool HALF>
+__device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1) {
+  if (HALF)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 // Four E4M3 codes -> two FP16 pairs, exactly (FP16 holds every E4M3 value).
 __device__ __forceinline__ void e4m3x4_to_half(uint32_t v, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
@@ -103,12 +117,25 @@ struct W4Zero {
     }
   }
 };
+// (v & mask) | magic in one instruction: the magic number comes in a register, which the compiler
+// cannot see through (two constants would be two instructions).
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(v), "r"(mask), "r"(magic));
+  return r;
+}
 template <bool HALF>
-__device__ __forceinline__ void w4_pairs(uint32_t v, const W4Zero<HALF>& z, uint32_t (&p)[4]) {
+__device__ __forceinline__ uint32_t w4_magic() {
+  uint32_t r;
+  asm volatile("mov.b32 %0, %1;" : "=r"(r) : "n"(HALF ? 0x64006400 : 0x43004300));
+  return r;
+}
+template <bool HALF>
+__device__ __forceinline__ void w4_pairs(uint32_t v, const W4Zero<HALF>& z, uint32_t magic, uint32_t (&p)[4]) {
   if (HALF) {
     const uint32_t w = v >> 8;
-    const uint32_t c0 = (v & 0x000f000fu) | 0x64006400u, c1 = (v & 0x00f000f0u) | 0x64006400u;
-    const uint32_t c2 = (w & 0x000f000fu) | 0x64006400u, c3 = (w & 0x00f000f0u) | 0x64006400u;
+    const uint32_t c0 = and_or(v, 0x000f000fu, magic), c1 = and_or(v, 0x00f000f0u, magic);
+    const uint32_t c2 = and_or(w, 0x000f000fu, magic), c3 = and_or(w, 0x00f000f0u, magic);
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p[0]) : "r"(c0), "r"(z.a));
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p[1]) : "r"(c1), "r"(0x2c002c00u), "r"(z.b));   // 0x2c00 = 1/16
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p[2]) : "r"(c2), "r"(z.a));
@@ -116,7 +143,7 @@ __device__ __forceinline__ void w4_pairs(uint32_t v, const W4Zero<HALF>& z, uint
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t c = ((v >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+      const uint32_t c = and_or(v >> (4 * i), 0x000f000fu, magic);
       asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(p[i]) : "r"(c), "r"(0x3f803f80u), "r"(z.a));
     }
   }
@@ -225,26 +252,29 @@ __device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 
 
 // This lane's activations: 16-byte chunk I of half J of an item (an item's half is J's 16 of the
 // lane's 32 bytes per weight row, HALF_CHUNKS chunks of activations); x[n] is the lane's column of
-// group n at the item's first column (null: no such column, zeros).  kleft: columns to the
-// row's end (W4 rows are padded to whole items, activations are not).  Activations are kept
-// in L1, which the weights pass by; plain loads, since the layer writes some of them in the
-// same launch.
+// group n at the item's first column.  A lane without a column reads another's and its sums are
+// dropped.  last: the row's last chunk, counted from the item (W4 rows are padded to whole items,
+// activations are not: chunks past the end read the last one again, beside weights of scale 0).
+// Activations are kept in L1, which the weights pass by; plain loads, since the layer writes some
+// of them in the same launch.
 template <int FMT, int NT>
 __device__ __forceinline__ void load_acts(uint4 (&b)[NT], const uint16_t* const (&x)[NT], int J, int I, int t,
-                                          int kleft) {
-  const int k = FMT == F_BF16 ? t * 16 + 8 * J : FMT == F_E4M3 ? t * 32 + 16 * J + 8 * I : (4 * J + I) * 32 + t * 8;
+                                          int last) {
+  int k = FMT == F_BF16 ? t * 16 + 8 * J : FMT == F_E4M3 ? t * 32 + 16 * J + 8 * I : (4 * J + I) * 32 + t * 8;
+  if (FMT == F_W4) k = min(k, last);
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
-    b[n] = x[n] && (FMT != F_W4 || k < kleft) ? *reinterpret_cast<const uint4*>(x[n] + k) : make_uint4(0, 0, 0, 0);
+  for (int n = 0; n < NT; ++n) b[n] = *reinterpret_cast<const uint4*>(x[n] + k);
 }
 
 template <bool HALF, int NT>
-__device__ __forceinline__ void mma_step(Sums<NT>& acc, const uint32_t (&a)[4][4], const uint4 (&b)[NT]) {
+__device__ __forceinline__ void mma_step(Sums<NT>& acc, const uint32_t (&a)[4][4], const uint4 (&b)[NT],
+                                         bool first = false) {
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      mma16<HALF>(acc.v[n][h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b[n].x, b[n].y);
+      if (first) mma16_first<HALF>(acc.v[n][h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b[n].x, b[n].y);
+      else mma16<HALF>(acc.v[n][h], a[2 * h][0], a[2 * h + 1][0], a[2 * h][1], a[2 * h + 1][1], b[n].x, b[n].y);
       mma16<HALF>(acc.v[n][h], a[2 * h][2], a[2 * h + 1][2], a[2 * h][3], a[2 * h + 1][3], b[n].z, b[n].w);
     }
 }
@@ -288,6 +318,7 @@ __device__ __forceinline__ void half_item(Sums<NT>& sums, Sums<NT>& acc, const u
     // word j of the lane's 8 holds columns j*32 + t*8 .. + 8
     constexpr int WPG = GROUP / 32;   // words per scale group
     constexpr int HG = F::NG / 2;     // groups of half an item
+    const uint32_t magic = w4_magic<HALF>();
     uint32_t scs[2][HG], zps[2][(HG + 1) / 2];     // by half tile: BF16 pairs; bytes, two groups a word
     const uint8_t* par = stage + 2048 + (g * F::NG + J * HG) * 4;
     const uint8_t* zpar = stage + 2048 + F::SC + (g * F::NG + J * HG) * 2;
@@ -313,16 +344,15 @@ __device__ __forceinline__ void half_item(Sums<NT>& sums, Sums<NT>& acc, const u
       const W4Zero<HALF> z[4] = {{zps[0][gi >> 1], zb}, {zps[0][gi >> 1], zb + 1}, {zps[1][gi >> 1], zb},
                                  {zps[1][gi >> 1], zb + 1}};
       Sums<NT> part;
-      part.clear();
 #pragma unroll
       for (int i = i0; i < i0 + WPG; ++i) {
         uint4 b[PASSES][NT];
         acts(b, i);
         uint32_t a[4][4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) w4_pairs<HALF>(word(q[r], i), z[r], a[r]);
+        for (int r = 0; r < 4; ++r) w4_pairs<HALF>(word(q[r], i), z[r], magic, a[r]);
 #pragma unroll
-        for (int p = 0; p < PASSES; ++p) mma_step<HALF, NT>(part, a, b[p]);
+        for (int p = 0; p < PASSES; ++p) mma_step<HALF, NT>(part, a, b[p], i == i0 && p == 0);
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -497,8 +527,8 @@ struct Stream {
     src.at(0x7fffff00, lane);    // far past any unit
   }
 
-  // sums = weights x activations over the unit in use.  x0[p][n] is this lane's column of group n,
-  // or null; PASSES sets of columns are added into the same sums.  k: columns of the matrix.  With
+  // sums = weights x activations over the unit in use.  x0[p][n] is this lane's column of group n
+  // (any column, if it has none); PASSES sets of columns are added into the same sums.  k: columns of the matrix.  With
   // scaled (FP16 only), 16 values of a column share an exponent: ex[n] are those of the lane's column, and
   // they count from top[n].
   template <int NT, int PASSES>
@@ -512,8 +542,8 @@ struct Stream {
 #pragma unroll
     for (int p = 0; p < PASSES; ++p)
 #pragma unroll
-      for (int i = 0; i < NT; ++i) xp[p][i] = x0[p][i] ? x0[p][i] + (long long)s0 * F::KI : nullptr;
-    int kleft = k - s0 * F::KI;
+      for (int i = 0; i < NT; ++i) xp[p][i] = x0[p][i] + (long long)s0 * F::KI;
+    int last = k - 8 - s0 * F::KI;
     const float *sc0 = nullptr, *sc1 = nullptr;
     if constexpr (FMT == F_E4M3) {
       sc0 = reinterpret_cast<const float*>(un.p0);
@@ -529,7 +559,7 @@ struct Stream {
 #pragma unroll
         for (int q = 0; q < F::HALF_CHUNKS; ++q)
 #pragma unroll
-          for (int p = 0; p < PASSES; ++p) load_acts<FMT, NT>(b[q][p], xp[p], J, q, t, kleft);
+          for (int p = 0; p < PASSES; ++p) load_acts<FMT, NT>(b[q][p], xp[p], J, q, t, last);
       };
       // exponents of half J: E4M3 one (the lane's 16 columns), W4 eight (words 4J.. of two blocks each)
       auto ask_exps = [&](int J) {
@@ -538,11 +568,8 @@ struct Stream {
           const int at = (s0 + i) * (F::KI / 16) + (FMT == F_E4M3 ? t * 2 + J : 8 * J);
 #pragma unroll
           for (int q = 0; q < NT; ++q) {
-            e8[q] = make_uint2(0, 0);
-            if (ex[q]) {
-              if constexpr (FMT == F_E4M3) e8[q].x = ex[q][at];
-              else e8[q] = *reinterpret_cast<const uint2*>(ex[q] + at);
-            }
+            if constexpr (FMT == F_E4M3) e8[q].x = ex[q][at];
+            else e8[q] = *reinterpret_cast<const uint2*>(ex[q] + at);
           }
         }
       };
@@ -571,7 +598,7 @@ struct Stream {
 #pragma unroll
               for (int q = 0; q < NT; ++q) v[p][q] = b[I][p][q];
             } else {
-              load_acts<FMT, NT>(v[p], xp[p], J, I, t, kleft);
+              load_acts<FMT, NT>(v[p], xp[p], J, I, t, last);
             }
           }
           if constexpr (HALF) {
@@ -613,8 +640,8 @@ struct Stream {
       for (int p = 0; p < PASSES; ++p)
 #pragma unroll
         for (int q = 0; q < NT; ++q)
-          if (xp[p][q]) xp[p][q] += F::KI;
-      kleft -= F::KI;
+          xp[p][q] += F::KI;
+      last -= F::KI;
     }
   }
 };

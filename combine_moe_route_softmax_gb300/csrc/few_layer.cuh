@@ -495,22 +495,20 @@ __device__ __forceinline__ void do_unit(const LayerArgs& a, LayerShared& s, Laye
   for (int i = 0; i < NT; ++i) {
     const bool pairs = !HALF && down && PASSES == 1;     // hi and lo as columns of one group
     const int c = pairs ? (g & 3) : i * 8 + g;
-    const int slot = c < nc ? s.cols[c0 + c] : -1;
+    const int at = c0 + (c < nc ? c : 0);                // no such column: the first one again
+    const int slot = s.cols[at];
     ex[i] = nullptr;
     top[i] = 0;
-    if (HALF && down && slot >= 0) {
+    if (HALF && down) {
       ex[i] = a.h_exp + (size_t)slot * exp_pitch(a.I);
       top[i] = __ldcg(&a.h_top[slot]);
     }
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
-      x[p][i] = nullptr;
-      if (slot >= 0) {
-        if (!down)
-          x[p][i] = (HALF ? a.x16 : a.x) + (size_t)s.toks[c0 + c] * a.H;
-        else
-          x[p][i] = ((pairs ? g >= 4 : p == 1) ? a.h_lo : a.h_hi) + (size_t)slot * a.I;
-      }
+      if (!down)
+        x[p][i] = (HALF ? a.x16 : a.x) + (size_t)s.toks[at] * a.H;
+      else
+        x[p][i] = ((pairs ? g >= 4 : p == 1) ? a.h_lo : a.h_hi) + (size_t)slot * a.I;
     }
   }
   Sums<NT> sums;

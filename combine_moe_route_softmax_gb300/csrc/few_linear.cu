@@ -102,7 +102,7 @@ __device__ __forceinline__ void linear_unit(const LinearArgs& a, LinearStream<GR
   const int t0 = un.entry * LIN_COLS;
   const uint16_t* x[1][NT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) x[0][n] = t0 + n * 8 + g < a.T ? xs + (n * 8 + g) * a.pitch : nullptr;
+  for (int n = 0; n < NT; ++n) x[0][n] = xs + (t0 + n * 8 + g < a.T ? n * 8 + g : 0) * a.pitch;
   Sums<NT> sums;
   in.template run<NT, 1>(sums, k, x);
   if (!join<NT>(sums, j, parts, a.slots, NT * 64, in.cur, in.cur - un.part, un.parts, lane, a.dev_status)) return;
