@@ -250,20 +250,30 @@ struct Sums {
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-// This lane's activations: 16-byte chunk I of half J of an item (an item's half is J's 16 of the
-// lane's 32 bytes per weight row, HALF_CHUNKS chunks of activations); x[n] is the lane's column of
-// group n at the item's first column.  A lane without a column reads another's and its sums are
-// dropped.  last: the row's last chunk, counted from the item (W4 rows are padded to whole items,
-// activations are not: chunks past the end read the last one again, beside weights of scale 0).
-// Activations are kept in L1, which the weights pass by; plain loads, since the layer writes some
-// of them in the same launch.
-template <int FMT, int NT>
-__device__ __forceinline__ void load_acts(uint4 (&b)[NT], const uint16_t* const (&x)[NT], int J, int I, int t,
-                                          int last) {
-  int k = FMT == F_BF16 ? t * 16 + 8 * J : FMT == F_E4M3 ? t * 32 + 16 * J + 8 * I : (4 * J + I) * 32 + t * 8;
-  if (FMT == F_W4) k = min(k, last);
-#pragma unroll
-  for (int n = 0; n < NT; ++n) b[n] = *reinterpret_cast<const uint4*>(x[n] + k);
+// Where activations are: element offsets from one base, in global memory (kept in L1, which the
+// weights pass by; plain loads, since the layer writes some of them in the same launch) or shared.
+template <bool SMEM>
+struct Acts {
+  const uint16_t* base;              // global
+  uint32_t addr;                     // shared
+  __device__ __forceinline__ uint4 load(int off) const {
+    uint4 v;
+    if (SMEM)
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                   : "r"(addr + off * 2));
+    else
+      v = *reinterpret_cast<const uint4*>(base + off);
+    return v;
+  }
+};
+// This lane's part of an item's columns starts at acts_lane; 16-byte chunk I of half J (J's 16 of the
+// lane's 32 bytes per weight row, HALF_CHUNKS chunks of activations) is acts_chunk further on.
+template <int FMT>
+__device__ __forceinline__ int acts_lane(int t) { return FMT == F_BF16 ? t * 16 : FMT == F_E4M3 ? t * 32 : t * 8; }
+template <int FMT>
+__device__ __forceinline__ constexpr int acts_chunk(int J, int I) {
+  return FMT == F_BF16 ? 8 * J : FMT == F_E4M3 ? 16 * J + 8 * I : (4 * J + I) * 32;
 }
 
 template <bool HALF, int NT>
@@ -424,7 +434,7 @@ struct FeedSource {
 // A worker warp's stream of units: take() moves to the next one (false at the end), run() multiplies
 // it.  The item after the one in use is always on its way.  Src gives the units (FeedSource, or one
 // that works them out).
-template <int FMT, int GROUP, bool HALF, class Src>
+template <int FMT, int GROUP, bool HALF, bool SMEM, class Src>
 struct Stream {
   using F = Format<FMT, GROUP>;
   Src src;
@@ -527,23 +537,23 @@ struct Stream {
     src.at(0x7fffff00, lane);    // far past any unit
   }
 
-  // sums = weights x activations over the unit in use.  x0[p][n] is this lane's column of group n
-  // (any column, if it has none); PASSES sets of columns are added into the same sums.  k: columns of the matrix.  With
-  // scaled (FP16 only), 16 values of a column share an exponent: ex[n] are those of the lane's column, and
-  // they count from top[n].
+  // sums = weights x activations over the unit in use.  off[p][n] is where this lane's column of group n
+  // (any column, if it has none: its sums are dropped) begins; PASSES sets of columns are added
+  // into the same sums.  With scaled (FP16 only), 16 values of a column share an exponent:
+  // ex[n] are those of the lane's column, and they count from top[n].  Rows of activations reach to
+  // whole items (W4: 256 columns), with zeros.
   template <int NT, int PASSES>
-  __device__ __forceinline__ void run(Sums<NT>& sums, int k, const uint16_t* const (&x0)[PASSES][NT],
+  __device__ __forceinline__ void run(Sums<NT>& sums, const Acts<SMEM>& from, const int (&off)[PASSES][NT],
                                       bool scaled = false, const uint8_t* const* ex = nullptr,
                                       const int* top = nullptr) {
     const int t = lane & 3;
     const Unit& un = src.unit(cur);
     const int s0 = un.s0, n = un.n;
-    const uint16_t* xp[PASSES][NT];
+    int at[PASSES][NT];
 #pragma unroll
     for (int p = 0; p < PASSES; ++p)
 #pragma unroll
-      for (int i = 0; i < NT; ++i) xp[p][i] = x0[p][i] + (long long)s0 * F::KI;
-    int last = k - 8 - s0 * F::KI;
+      for (int i = 0; i < NT; ++i) at[p][i] = off[p][i] + s0 * F::KI + acts_lane<FMT>(t);
     const float *sc0 = nullptr, *sc1 = nullptr;
     if constexpr (FMT == F_E4M3) {
       sc0 = reinterpret_cast<const float*>(un.p0);
@@ -559,17 +569,19 @@ struct Stream {
 #pragma unroll
         for (int q = 0; q < F::HALF_CHUNKS; ++q)
 #pragma unroll
-          for (int p = 0; p < PASSES; ++p) load_acts<FMT, NT>(b[q][p], xp[p], J, q, t, last);
+          for (int p = 0; p < PASSES; ++p)
+#pragma unroll
+            for (int c = 0; c < NT; ++c) b[q][p][c] = from.load(at[p][c] + acts_chunk<FMT>(J, q));
       };
       // exponents of half J: E4M3 one (the lane's 16 columns), W4 eight (words 4J.. of two blocks each)
       auto ask_exps = [&](int J) {
         if constexpr (HALF) {
           if (!scaled) return;
-          const int at = (s0 + i) * (F::KI / 16) + (FMT == F_E4M3 ? t * 2 + J : 8 * J);
+          const int e0 = (s0 + i) * (F::KI / 16) + (FMT == F_E4M3 ? t * 2 + J : 8 * J);
 #pragma unroll
           for (int q = 0; q < NT; ++q) {
-            if constexpr (FMT == F_E4M3) e8[q].x = ex[q][at];
-            else e8[q] = *reinterpret_cast<const uint2*>(ex[q] + at);
+            if constexpr (FMT == F_E4M3) e8[q].x = ex[q][e0];
+            else e8[q] = *reinterpret_cast<const uint2*>(ex[q] + e0);
           }
         }
       };
@@ -598,7 +610,8 @@ struct Stream {
 #pragma unroll
               for (int q = 0; q < NT; ++q) v[p][q] = b[I][p][q];
             } else {
-              load_acts<FMT, NT>(v[p], xp[p], J, I, t, last);
+#pragma unroll
+              for (int q = 0; q < NT; ++q) v[p][q] = from.load(at[p][q] + acts_chunk<FMT>(J, I));
             }
           }
           if constexpr (HALF) {
@@ -639,9 +652,7 @@ struct Stream {
 #pragma unroll
       for (int p = 0; p < PASSES; ++p)
 #pragma unroll
-        for (int q = 0; q < NT; ++q)
-          xp[p][q] += F::KI;
-      last -= F::KI;
+        for (int q = 0; q < NT; ++q) at[p][q] += F::KI;
     }
   }
 };

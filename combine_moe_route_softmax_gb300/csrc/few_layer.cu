@@ -28,10 +28,10 @@ inline bool plan_few(const moe_few_desc_t* d, FewPlan* p) {
   p->off_htop = o;   o = align256(o + 4 * (size_t)kMaxTokens * (d->K + 1));
   // not kept
   p->off_logits = o; o = align256(o + 4 * (size_t)d->T * d->E);
-  p->off_x16 = o;    o = align256(o + (half ? 2 * (size_t)d->T * d->H : 0));
+  p->off_x16 = o;    o = align256(o + (half ? 2 * (size_t)d->T * half_pitch(d->H) : 0));
   p->off_xunit = o;  o = align256(o + 4 * (size_t)d->T);
   p->off_hexp = o;   o = align256(o + (half ? slots * exp_pitch(d->I) : 0));
-  p->off_hhi = o;    o = align256(o + 2 * slots * d->I);
+  p->off_hhi = o;    o = align256(o + 2 * slots * (half ? half_pitch(d->I) : d->I));
   p->off_hlo = o;    o = align256(o + (half ? 0 : 2 * slots * d->I));
   p->off_y = o;      o = align256(o + 4 * slots * d->H);
   p->total = o;
@@ -111,7 +111,7 @@ extern "C" moe_status_t moe_layer_few(const moe_few_desc_t* d, const moe_few_wei
   a.x_unit = reinterpret_cast<float*>(b + p.off_xunit);
   a.h_exp = b + p.off_hexp;
   a.h_hi = reinterpret_cast<uint16_t*>(b + p.off_hhi);
-  a.h_lo = reinterpret_cast<uint16_t*>(b + p.off_hlo);
+  a.h_lo = (int)((p.off_hlo - p.off_hhi) / 2);
   a.y = reinterpret_cast<float*>(b + p.off_y);
   cudaStream_t st = as_stream(stream);
   const cudaError_t e = d->dtype == MOE_BF16   ? launch_layer_bf16(a, st)

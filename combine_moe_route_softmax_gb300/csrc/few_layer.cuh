@@ -35,12 +35,13 @@ namespace moe {
 namespace few {
 
 constexpr int MAX_WARPS = 16;
+constexpr int W4W = 12;
 // Warps of a CTA, the last of which schedules.  W4's unpacking wants more than the 128 registers a
 // thread has with 16 warps: 162 us with 12 warps against 182 on 32 tokens at H = 2048, I = 1408, E = 64,
 // top-8, groups of 32; E4M3's does not: 720 us with 16 against 796 on 16 tokens at H = 7168, I = 2048,
 // E = 256, top-8.
 template <int FMT>
-__host__ __device__ constexpr int warps_of() { return FMT == F_W4 ? 12 : MAX_WARPS; }
+__host__ __device__ constexpr int warps_of() { return FMT == F_W4 ? W4W : MAX_WARPS; }
 constexpr int PARTS_BYTES = 40 * 1024;      // slots of the joins
 constexpr int kMaxSlots = kMaxTokens * kMaxTopK;
 // one entry = up to COLS columns of one expert; at most one per routed slot, plus the shared ones
@@ -51,6 +52,8 @@ constexpr int kMaxWidth = 1 << 17;          // H and I
 // them is padded to 16 bytes.
 constexpr int EXP_BIAS = 121;
 __host__ __device__ __forceinline__ int exp_pitch(int i) { return (i / 16 + 15) / 16 * 16; }
+// Rows of FP16 activations reach to whole W4 items.
+__host__ __device__ __forceinline__ int half_pitch(int k) { return (k + 255) / 256 * 256; }
 
 struct LayerArgs {
   CUtensorMap map[4];          // BF16, E4M3: w13, w2, shared w13, shared w2 (boxes of 16 rows x 128 bytes)
@@ -74,9 +77,10 @@ struct LayerArgs {
   int32_t* entry_done;         // [kMaxEntries] row tiles done of an expert's h
   int32_t* h_top;              // [T*K + T] largest exponent of a slot's h (FP16)
   // workspace
-  uint16_t* x16;               // [T, H] FP16
+  uint16_t* x16;               // [T, half_pitch(H)] FP16
   float* x_unit;               // [T] what 1 in x16 stands for
-  uint16_t *h_hi, *h_lo;       // [T*K + T, I]; FP16: h_hi alone
+  uint16_t* h_hi;              // [T*K + T, I]; FP16: rows of half_pitch(I)
+  int h_lo;                    // BF16: elements from h_hi to the second terms
   uint8_t* h_exp;              // [T*K + T, ex_pitch] exponent of each 16 values of h (FP16)
   float* y;                    // [T*K + T, H]
 };
@@ -149,8 +153,10 @@ __device__ __forceinline__ void token_to_half(const LayerArgs& a, LayerShared& s
   for (int i = 0; i < WARPS; ++i) m = max(m, __float_as_uint(s.block[i]));
   const float sc = to_half_scale(m);
   for (int i = tid; i < a.H / 8; i += WARPS * 32) {
-    reinterpret_cast<uint4*>(a.x16 + (size_t)t * a.H)[i] = bf16_to_half8(__ldg(src + i), sc);
+    reinterpret_cast<uint4*>(a.x16 + (size_t)t * half_pitch(a.H))[i] = bf16_to_half8(__ldg(src + i), sc);
   }
+  for (int i = a.H / 8 + tid; i < half_pitch(a.H) / 8; i += WARPS * 32)
+    reinterpret_cast<uint4*>(a.x16 + (size_t)t * half_pitch(a.H))[i] = make_uint4(0, 0, 0, 0);
   if (tid == 0) a.x_unit[t] = 1.0f / sc;
   __syncthreads();
 }
@@ -395,13 +401,17 @@ __device__ __forceinline__ void store_h(const LayerArgs& a, const LayerShared& s
       if (slot < 0) continue;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const size_t o = (size_t)slot * a.I + tile * 16 + g + i * 8;
+        const size_t o = (size_t)slot * (HALF ? half_pitch(a.I) : a.I) + tile * 16 + g + i * 8;
         if (HALF) {
           a.h_hi[o] = half_bits(h[i] * sc);
+          // the last tile also clears the row's end
+          if (tile == s.tiles1 - 1 && i == 0)
+            for (int z = a.I + g * 8; z < half_pitch(a.I); z += 64)
+              *reinterpret_cast<uint4*>(a.h_hi + (size_t)slot * half_pitch(a.I) + z) = make_uint4(0, 0, 0, 0);
         } else {
           const uint16_t hi = f32_to_bf16(h[i]);
           a.h_hi[o] = hi;
-          a.h_lo[o] = f32_to_bf16((hi & 0x7fffu) >= 0x7f80u ? 0.0f : h[i] - bf16_to_f32(hi));   // inf, NaN: hi alone
+          a.h_hi[o + a.h_lo] = f32_to_bf16((hi & 0x7fffu) >= 0x7f80u ? 0.0f : h[i] - bf16_to_f32(hi));   // inf, NaN: hi alone
         }
       }
     }
@@ -477,7 +487,7 @@ static __device__ __noinline__ void combine_tile(const LayerArgs& a, const Layer
 }
 
 template <int FMT, int GROUP>
-using LayerStream = Stream<FMT, GROUP, FMT != F_BF16, FeedSource<MAX_WARPS - 1>>;
+using LayerStream = Stream<FMT, GROUP, FMT != F_BF16, false, FeedSource<MAX_WARPS - 1>>;
 
 // The unit in use with NT column groups: columns, sums, join, result.
 template <int FMT, int GROUP, int NT, int PASSES>
@@ -488,7 +498,7 @@ __device__ __forceinline__ void do_unit(const LayerArgs& a, LayerShared& s, Laye
   const Unit& un = in.src.unit(in.cur);
   const int entry = un.entry, row = un.row, part = un.part, n = un.parts;
   const int nc = s.ncols[entry], c0 = s.first[entry];
-  const uint16_t* x[PASSES][NT];
+  int off[PASSES][NT];
   const uint8_t* ex[NT];
   int top[NT];
 #pragma unroll
@@ -506,13 +516,14 @@ __device__ __forceinline__ void do_unit(const LayerArgs& a, LayerShared& s, Laye
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
       if (!down)
-        x[p][i] = (HALF ? a.x16 : a.x) + (size_t)s.toks[at] * a.H;
+        off[p][i] = s.toks[at] * (HALF ? half_pitch(a.H) : a.H);
       else
-        x[p][i] = ((pairs ? g >= 4 : p == 1) ? a.h_lo : a.h_hi) + (size_t)slot * a.I;
+        off[p][i] = slot * (HALF ? half_pitch(a.I) : a.I) + ((pairs ? g >= 4 : p == 1) ? a.h_lo : 0);
     }
   }
   Sums<NT> sums;
-  in.template run<NT, PASSES>(sums, down ? a.I : a.H, x, HALF && down, ex, top);
+  const Acts<false> from{down ? a.h_hi : HALF ? a.x16 : a.x, 0};
+  in.template run<NT, PASSES>(sums, from, off, HALF && down, ex, top);
   if (!join<NT>(sums, s.join, parts, slots, stride, in.cur, in.cur - part, n, lane, a.dev_status)) return;
   if (!down) {
     store_h<HALF, NT>(a, s, sums, entry, row, lane);

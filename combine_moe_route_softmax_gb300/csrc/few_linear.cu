@@ -16,7 +16,9 @@ namespace moe {
 namespace few {
 
 constexpr int LIN_COLS = 32;
-constexpr int LIN_WARPS = 12;                // as the layer's W4 kernels: registers
+// Warps of a CTA: 16 as far as 128 registers a thread do.
+template <int NT>
+__host__ __device__ constexpr int lin_warps() { return NT == 1 ? 16 : 12; }
 constexpr int LIN_SMEM = 224 * 1024;
 
 struct LinearArgs {
@@ -41,14 +43,14 @@ struct LinearArgs {
 
 // CTA c has share c % splits of K and, of the tiles (row tile, block of x), c / splits and every
 // (CTAs / splits)-th on; its warps take the units of that sequence in turn.
-template <int GROUP>
+template <int GROUP, int NT>
 struct LinearSource {
   const LinearArgs& a;
   int share, items, parts, first, step, total;   // items of a tile here, its units; units in all
   int next;
   __device__ __forceinline__ int claim(int) {
     const int u = next;
-    next += LIN_WARPS;
+    next += lin_warps<NT>();
     return u;
   }
   __device__ __forceinline__ int state(int u, int) const { return u < total ? 1 : 2; }
@@ -70,47 +72,56 @@ struct LinearSource {
     return k;
   }
 };
-template <int GROUP>
-using LinearStream = Stream<F_W4, GROUP, true, LinearSource<GROUP>>;
+template <int GROUP, int NT>
+using LinearStream = Stream<F_W4, GROUP, true, true, LinearSource<GROUP, NT>>;
 
-// The CTA's rows of x, its share of K, as FP16: warp w takes rows w, w + LIN_WARPS, ...
-__device__ __forceinline__ void stage_rows(const LinearArgs& a, uint16_t* xs, float* unit, int t0, int k0, int k,
-                                           int warp, int lane) {
-  const int n = min(LIN_COLS, a.T - t0);
+// The CTA's rows of x, its share of K, as FP16, by all threads; zeros up to a whole item.
+template <int THREADS>
+__device__ __forceinline__ void stage_rows(const LinearArgs& a, uint16_t* xs, uint32_t* most, int t0, int k0, int k,
+                                           int tid) {
+  const int n = min(LIN_COLS, a.T - t0), chunks = (a.pitch - 32) / 8, real = k / 8;
+  if (tid < LIN_COLS) most[tid] = 0;
+  __syncthreads();
 #pragma unroll 1
-  for (int r = warp; r < n; r += LIN_WARPS) {
-    const uint4* src = reinterpret_cast<const uint4*>(a.x + (t0 + r) * a.x_stride + k0);
-    uint32_t m = 0;
-#pragma unroll 4
-    for (int i = lane; i < k / 8; i += 32) {
-      const uint4 v = __ldg(src + i);
-      m = max(m, bf16_max(v));
+  for (int pass = 0; pass < 2; ++pass) {
+    int r = 0, c = tid;
+#pragma unroll 2
+    for (int i = tid; i < n * chunks; i += THREADS) {
+      while (c >= chunks) {
+        c -= chunks;
+        ++r;
+      }
+      const uint4 v = c < real ? __ldg(reinterpret_cast<const uint4*>(a.x + (t0 + r) * a.x_stride + k0) + c)
+                               : make_uint4(0, 0, 0, 0);
+      if (pass == 0) {
+        const uint32_t m = bf16_max(v);
+        if (m > *static_cast<volatile uint32_t*>(&most[r])) atomicMax(&most[r], m);
+      } else {
+        reinterpret_cast<uint4*>(xs + r * a.pitch)[c] = bf16_to_half8(v, to_half_scale(most[r]));
+      }
+      c += THREADS;
     }
-    const float sc = to_half_scale(__reduce_max_sync(0xffffffffu, m));
-#pragma unroll 4
-    for (int i = lane; i < k / 8; i += 32)
-      reinterpret_cast<uint4*>(xs + r * a.pitch)[i] = bf16_to_half8(__ldg(src + i), sc);
-    if (lane == 0) unit[r] = 1.0f / sc;
+    __syncthreads();
   }
 }
 
 template <int GROUP, int NT>
-__device__ __forceinline__ void linear_unit(const LinearArgs& a, LinearStream<GROUP>& in, JoinShared& j, float4* parts,
-                                            const uint16_t* xs, const float* unit, int k, int lane) {
+__device__ __forceinline__ void linear_unit(const LinearArgs& a, LinearStream<GROUP, NT>& in, JoinShared& j, float4* parts,
+                                            uint32_t xs, const uint32_t* most, int lane) {
   const int g = lane >> 2, t = lane & 3;
   const Unit un = in.src.unit(in.cur);
   const int t0 = un.entry * LIN_COLS;
-  const uint16_t* x[1][NT];
+  int off[1][NT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) x[0][n] = xs + (t0 + n * 8 + g < a.T ? n * 8 + g : 0) * a.pitch;
+  for (int n = 0; n < NT; ++n) off[0][n] = (t0 + n * 8 + g < a.T ? n * 8 + g : 0) * a.pitch;
   Sums<NT> sums;
-  in.template run<NT, 1>(sums, k, x);
+  in.template run<NT, 1>(sums, Acts<true>{nullptr, xs}, off);
   if (!join<NT>(sums, j, parts, a.slots, NT * 64, in.cur, in.cur - un.part, un.parts, lane, a.dev_status)) return;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float f = unit[n * 8 + 2 * t + i];
+      const float f = 1.0f / to_half_scale(most[n * 8 + 2 * t + i]);     // a power of two
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         sums.v[n][h][i] *= f;
@@ -168,10 +179,11 @@ __device__ __forceinline__ void linear_unit(const LinearArgs& a, LinearStream<GR
 }
 
 template <int GROUP, int NT>
-__global__ void __launch_bounds__(LIN_WARPS * 32, 1) linear_w4_kernel(const __grid_constant__ LinearArgs a) {
+__global__ void __launch_bounds__(lin_warps<NT>() * 32, 1) linear_w4_kernel(const __grid_constant__ LinearArgs a) {
   extern __shared__ __align__(1024) uint8_t rings[];
   __shared__ JoinShared j;
-  __shared__ float unit[LIN_COLS];
+  constexpr int LIN_WARPS = lin_warps<NT>();
+  __shared__ uint32_t most[LIN_COLS];              // largest finite |x| of a row, as bits
   __shared__ __align__(8) unsigned long long full[LIN_WARPS][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int RING = 2 * Format<F_W4, GROUP>::STAGE;
@@ -181,7 +193,7 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 1) linear_w4_kernel(const __gr
   const int tiles = a.rows * a.blocks;
   const int mine = first < tiles ? (tiles - first + step - 1) / step : 0;
   const int items = min(a.split_len, a.nsl - share * a.split_len), n_parts = (items + a.cut.len - 1) / a.cut.len;
-  LinearStream<GROUP> in{{a, share, items, n_parts, first, step, mine * n_parts, warp}, rings + warp * RING};
+  LinearStream<GROUP, NT> in{{a, share, items, n_parts, first, step, mine * n_parts, warp}, rings + warp * RING};
   in.ring_addr = gg::smem_u32(in.ring);
   in.bars = gg::smem_u32(&full[warp][0]);
   in.lane = lane;
@@ -198,9 +210,8 @@ __global__ void __launch_bounds__(LIN_WARPS * 32, 1) linear_w4_kernel(const __gr
   join_init(j);
   const int k0 = share * a.split_len * 256, k = min(a.K - k0, a.split_len * 256);
   // one block of x at a time stays in shared memory: with more blocks every CTA has one (launch_linear)
-  stage_rows(a, xs, unit, (first % a.blocks) * LIN_COLS, k0, k, warp, lane);
-  __syncthreads();
-  while (in.take()) linear_unit<GROUP, NT>(a, in, j, parts, xs, unit, k, lane);
+  stage_rows<LIN_WARPS * 32>(a, xs, most, (first % a.blocks) * LIN_COLS, k0, k, threadIdx.x);
+  while (in.take()) linear_unit<GROUP, NT>(a, in, j, parts, gg::smem_u32(xs), most, lane);
   in.finish();
 }
 
@@ -316,9 +327,10 @@ inline LinearPlan plan_linear(int T, int N, int K, int group, int sms) {
   LinearPlan p;
   const int cols = T < LIN_COLS ? T : LIN_COLS;
   p.nt = cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
-  p.slots = p.nt == 1 ? 24 : p.nt == 2 ? 16 : LIN_WARPS;   // at least a tile's units
+  const int warps = p.nt == 1 ? lin_warps<1>() : lin_warps<4>();
+  p.slots = p.nt == 1 ? 32 : p.nt == 2 ? 16 : warps;       // at least a tile's units
   const int stage = 2 * (2048 + 8 * (256 / group) * 6);
-  const int fixed = LIN_WARPS * 2 * stage + p.slots * p.nt * 1024;
+  const int fixed = warps * 2 * stage + p.slots * p.nt * 1024;
   const int room = (LIN_SMEM - fixed) / 2 / cols - 32;      // elements of a row
   const int nsl = w4_slices(K), fit = room / 256 < 1 ? 1 : room / 256;
   p.splits = (nsl + fit - 1) / fit;
@@ -326,10 +338,9 @@ inline LinearPlan plan_linear(int T, int N, int K, int group, int sms) {
   p.splits = (nsl + p.split_len - 1) / p.split_len;
   const int blocks = (T + LIN_COLS - 1) / LIN_COLS;
   p.tiles = ceil_div(N, 32) * blocks;
-  const int len = (K + 127) / 128 * 128 < p.split_len * 256 ? (K + 127) / 128 * 128 : p.split_len * 256;
-  p.pitch = len + 32;          // rows 64 bytes past a multiple of 128: two rows' chunks in different banks
+  p.pitch = p.split_len * 256 + 32;          // rows 64 bytes past a multiple of 128: two rows' chunks in different banks
   p.smem = fixed + cols * p.pitch * 2;
-  p.cut.set(p.split_len, LIN_WARPS, p.tiles * p.splits <= sms);
+  p.cut.set(p.split_len, warps, p.tiles * p.splits <= sms);
   const int unit = p.splits * blocks;
   p.ctas = sms / unit * unit;
   if (p.ctas == 0) p.ctas = unit;
@@ -346,7 +357,7 @@ moe_status_t launch_linear(const LinearArgs& a, const LinearPlan& p, cudaStream_
                                     LIN_SMEM) == cudaSuccess;
       }))
     return MOE_ERR_CUDA;
-  linear_w4_kernel<GROUP, NT><<<p.ctas, LIN_WARPS * 32, p.smem, stream>>>(a);
+  linear_w4_kernel<GROUP, NT><<<p.ctas, lin_warps<NT>() * 32, p.smem, stream>>>(a);
   MOE_CHECK_LAUNCH();
   return MOE_OK;
 }
