@@ -131,7 +131,8 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without a Stream object around it (3 us)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -537,17 +538,24 @@ def moe_linear_w4(x, w, bias=None, out=None, out_dtype=torch.bfloat16, ws=None, 
     """x BF16 [T, K] (rows may be strided), w a W4Packed matrix -> out [T, N] = x w^T (+ bias float32
     [N]) in BF16 or float32.  ws: a workspace kept from moe_linear_w4_workspace (made here
     otherwise); calls that may overlap need one each."""
-    assert x.is_cuda and x.dim() == 2 and x.stride(1) == 1 and x.dtype == torch.bfloat16, "x is BF16 [T, K] on the GPU"
     T, K = x.shape
+    N = w.N
+    assert x.is_cuda and x.dtype is torch.bfloat16 and x.stride(1) == 1, "x is BF16 [T, K] on the GPU, rows dense"
     assert w.mats == 1 and w.K == K, "w is one matrix with x's K"
     if out is None:
-        out = torch.empty(T, w.N, dtype=out_dtype, device=x.device)
-    assert out.shape == (T, w.N) and out.stride(1) == 1 and out.dtype in (torch.bfloat16, torch.float32)
+        out = torch.empty(T, N, dtype=out_dtype, device=x.device)
+        os = N
+    else:
+        assert out.shape == (T, N) and out.stride(1) == 1
+        os = out.stride(0) if T > 1 else N
+        out_dtype = out.dtype
+    assert out_dtype is torch.bfloat16 or out_dtype is torch.float32, "out is BF16 or float32"
     if ws is None:
-        ws = moe_linear_w4_workspace(T, w.N, K, x.device)
-    _check("moe_linear_w4", lib().moe_linear_w4(
-        x.data_ptr(), T, K, x.stride(0) if T > 1 else K, w.data.data_ptr(), w.N, w.group, w.zeros, _ptr(bias), out.data_ptr(), int(out.dtype == torch.float32), out.stride(0) if T > 1 else w.N,
-        ws.data_ptr(), ws.numel(), _ptr(dev_status), _stream(stream)))
+        ws = moe_linear_w4_workspace(T, N, K, x.device)
+    _check("moe_linear_w4", (_lib or lib()).moe_linear_w4(
+        x.data_ptr(), T, K, x.stride(0) if T > 1 else K, w.data.data_ptr(), N, w.group, w.zeros,
+        None if bias is None else bias.data_ptr(), out.data_ptr(), out_dtype is torch.float32, os, ws.data_ptr(),
+        ws.numel(), None if dev_status is None else dev_status.data_ptr(), _stream(stream)))
     return out
 
 
@@ -560,9 +568,8 @@ def moe_route_hidden(x, w_router, K, bias=None, num_tokens=None, logits=None, to
                      stream=None):
     """The router from hidden states: x BF16 [T, H], w_router BF16 [E, H] -> (topk_idx int32 [T, K],
     topk_w float32 [T, K], logits float32 [T, E])."""
-    _dev(x)
-    _dev(w_router)
-    assert x.dtype == torch.bfloat16 and w_router.dtype == torch.bfloat16
+    assert x.is_cuda and x.is_contiguous() and w_router.is_contiguous(), "expected contiguous CUDA tensors"
+    assert x.dtype is torch.bfloat16 and w_router.dtype is torch.bfloat16
     T, H = x.shape
     E = w_router.shape[0]
     if logits is None:
@@ -573,7 +580,7 @@ def moe_route_hidden(x, w_router, K, bias=None, num_tokens=None, logits=None, to
         topk_w = torch.empty(T, K, dtype=torch.float32, device=x.device)
     if ws is None:
         ws = moe_route_hidden_workspace(device=x.device)
-    _check("moe_route_hidden", lib().moe_route_hidden(
+    _check("moe_route_hidden", (_lib or lib()).moe_route_hidden(
         x.data_ptr(), T, H, w_router.data_ptr(), _ptr(bias), E, K, _ptr(num_tokens), logits.data_ptr(),
         topk_idx.data_ptr(), topk_w.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
     return topk_idx, topk_w, logits
@@ -607,19 +614,21 @@ class MoeLayerFew:
         self.ws = _zeroed(nbytes, device)
         self.max_tokens = T
         self._descs = {T: self.desc}
+        self._w = ctypes.byref(self.weights)
+        self._ws = self.ws.data_ptr(), self.ws.numel()
 
     def forward(self, x, out=None, topk_idx=None, topk_w=None, logits=None, num_tokens=None, dev_status=None,
                 stream=None):
         """x BF16 [t, H], t <= T -> (out [t, H], topk_idx, topk_w).  topk_idx / topk_w are inputs
         unless the layer routes (w_router, or logits [t, E])."""
-        _dev(x)
+        assert x.is_cuda and x.is_contiguous() and x.dtype is torch.bfloat16, "x is BF16, contiguous, on the GPU"
         t, H = x.shape
         d = self._descs.get(t)
         if d is None:
             if t > self.max_tokens:
                 raise ValueError("more tokens than the layer was made for")
             d = self._descs[t] = FewDesc(t, *(getattr(self.desc, f) for f, _ in FewDesc._fields_[1:]))
-        assert x.dtype == torch.bfloat16 and H == d.H
+        assert H == d.H
         if out is None:
             out = torch.empty_like(x)
         if topk_idx is None:
@@ -627,8 +636,7 @@ class MoeLayerFew:
                 raise ValueError("topk_idx and topk_w are needed: the layer has no router and no logits")
             topk_idx = torch.empty(t, d.K, dtype=torch.int32, device=x.device)
             topk_w = torch.empty(t, d.K, dtype=torch.float32, device=x.device)
-        _check("moe_layer_few", lib().moe_layer_few(
-            ctypes.byref(d), ctypes.byref(self.weights), x.data_ptr(), _ptr(logits), _ptr(num_tokens),
-            topk_idx.data_ptr(), topk_w.data_ptr(), out.data_ptr(), self.ws.data_ptr(), self.ws.numel(),
-            _ptr(dev_status), _stream(stream)))
+        _check("moe_layer_few", (_lib or lib()).moe_layer_few(
+            ctypes.byref(d), self._w, x.data_ptr(), _ptr(logits), _ptr(num_tokens), topk_idx.data_ptr(),
+            topk_w.data_ptr(), out.data_ptr(), *self._ws, _ptr(dev_status), _stream(stream)))
         return out, topk_idx, topk_w
