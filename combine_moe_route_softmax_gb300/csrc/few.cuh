@@ -190,10 +190,10 @@ __device__ __forceinline__ int atom_add_release(int32_t* p, int v) {
 // at least four items unless there is little work.
 struct Cut {
   int nsl, len, parts;
-  __host__ __device__ __forceinline__ void set(int items, int most, bool little) {
+  __host__ __device__ __forceinline__ void set(int items, int most, bool little, int least = 4) {
     nsl = items;
     len = (nsl + most - 1) / most;
-    if (len < 4 && !little) len = nsl < 4 ? nsl : 4;
+    if (len < least && !little) len = nsl < least ? nsl : least;
     parts = (nsl + len - 1) / len;
   }
 };
@@ -382,6 +382,7 @@ __device__ __forceinline__ void half_item(Sums<NT>& sums, Sums<NT>& acc, const u
 // -------------------------------------------------------------------------------- feed
 constexpr int FEED = 64;             // units written down at a time
 constexpr int AHEAD = 40;            // ... past the slowest worker's
+constexpr int STOCK = 10;            // ... that no worker has taken
 template <int WORKERS>
 struct Feed {
   Unit unit[FEED];
@@ -670,7 +671,8 @@ __device__ __forceinline__ void schedule(Feed<SIZE>& f, Src& src, int lane, int3
   while (!end || !src.done()) {
     bool moved = src.idle(lane);
     const int slowest = __reduce_min_sync(0xffffffffu, lane < WORKERS ? use[lane] : 0x7fffffff);
-    if (!end && units < slowest + AHEAD) {
+    // few units in stock: what an SM holds ready at the end, the others do without
+    if (!end && units < min(slowest + AHEAD, *static_cast<volatile int*>(&f.next) + STOCK)) {
       if (n == 0 && !src.next(lane, t, n)) {
         end = true;
         if (lane == 0) *static_cast<volatile int*>(&f.total) = units;

@@ -35,13 +35,12 @@ namespace moe {
 namespace few {
 
 constexpr int MAX_WARPS = 16;
-constexpr int W4W = 12;
 // Warps of a CTA, the last of which schedules.  W4's unpacking wants more than the 128 registers a
 // thread has with 16 warps: 162 us with 12 warps against 182 on 32 tokens at H = 2048, I = 1408, E = 64,
 // top-8, groups of 32; E4M3's does not: 720 us with 16 against 796 on 16 tokens at H = 7168, I = 2048,
 // E = 256, top-8.
 template <int FMT>
-__host__ __device__ constexpr int warps_of() { return FMT == F_W4 ? W4W : MAX_WARPS; }
+__host__ __device__ constexpr int warps_of() { return FMT == F_W4 ? 12 : MAX_WARPS; }
 constexpr int PARTS_BYTES = 40 * 1024;      // slots of the joins
 constexpr int kMaxSlots = kMaxTokens * kMaxTopK;
 // one entry = up to COLS columns of one expert; at most one per routed slot, plus the shared ones
@@ -264,7 +263,7 @@ struct LayerSched {
   int q, pending, run, ready, want;
 
   __device__ __forceinline__ bool next(int lane, int& t, int& n) {
-    // runs of four (smaller) tiles in phase 2 as long as there are plenty: a look at the queue takes
+    // runs of a few (smaller) tiles in phase 2 as long as there are plenty: a look at the queue takes
     // about as long as an SM needs for 32 KB
     if (q < 2) {
       t = blockIdx.x + q * gridDim.x;
@@ -274,7 +273,8 @@ struct LayerSched {
       n = run;
     }
     if (++q >= 2) {
-      run = t >= s.n1 && s.n_all - t > 16 * (int)gridDim.x ? 4 : 1;
+      const int left = (s.n_all - t) / (int)gridDim.x;
+      run = t < s.n1 || left < 3 ? 1 : left < 20 ? 2 : 4;
       if (lane == 0) pending = (int)(2 * gridDim.x + atomicAdd(&a.ctl[2], (unsigned)run));
     }
     n = min(n, s.n_all - t);
@@ -358,7 +358,11 @@ __device__ __forceinline__ void plan_phases(const LayerArgs& a, LayerShared& s) 
   for (int d = 0; d < 2; ++d) {
     const int k = d ? a.I : a.H;
     const int items = FMT == F_W4 ? w4_slices(k) : FMT == F_BF16 ? k / 64 : k / 128;
-    s.cut[d].set(items, warps_of<FMT>() - 1, (d ? s.n_all - s.n1 : s.n1) <= (int)gridDim.x);
+    // Longer units cost less per item, shorter ones level the end of the layer.  One token at the
+    // decode sizes (E4M3), 4 / 8 items in phase 1: 86.4 / 82.6 us, then 4 / 8 in phase 2: 82.6 / 83.3;
+    // 16 tokens: 719 / 698 and 698 / 689.
+    const int tiles = d ? s.n_all - s.n1 : s.n1, sms = gridDim.x;
+    s.cut[d].set(items, warps_of<FMT>() - 1, tiles <= sms, d == 0 || tiles >= 20 * sms ? 8 : 4);
   }
   s.ready = 0;
 }
