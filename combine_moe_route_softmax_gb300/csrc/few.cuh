@@ -195,6 +195,7 @@ struct Cut {
     len = (nsl + most - 1) / most;
     if (len < least && !little) len = nsl < least ? nsl : least;
     parts = (nsl + len - 1) / len;
+    len = (nsl + parts - 1) / parts;
   }
 };
 

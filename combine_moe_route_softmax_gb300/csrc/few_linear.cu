@@ -19,7 +19,7 @@ constexpr int LIN_COLS = 32;
 // Warps of a CTA: 16 as far as 128 registers a thread do.
 template <int NT>
 __host__ __device__ constexpr int lin_warps() { return NT == 1 ? 16 : 12; }
-constexpr int LIN_SMEM = 224 * 1024;
+constexpr int LIN_SMEM = 225 * 1024;
 
 struct LinearArgs {
   const uint16_t* x;
@@ -75,39 +75,61 @@ struct LinearSource {
 template <int GROUP, int NT>
 using LinearStream = Stream<F_W4, GROUP, true, true, LinearSource<GROUP, NT>>;
 
-// The CTA's rows of x, its share of K, as FP16, by all threads; zeros up to a whole item.
-template <int THREADS>
-__device__ __forceinline__ void stage_rows(const LinearArgs& a, uint16_t* xs, uint32_t* most, int t0, int k0, int k,
-                                           int tid) {
+// The CTA's rows of x, its share of K, as FP16, by all warps: several to a row, or several rows to a
+// warp, each lane with BATCH loads in flight.  Zeros up to a whole item.
+template <int WARPS, int BATCH>
+__device__ __forceinline__ void stage_rows(const LinearArgs& a, uint16_t* xs, uint32_t* most, float* unit, int t0,
+                                           int k0, int k, int warp, int lane) {
   const int n = min(LIN_COLS, a.T - t0), chunks = (a.pitch - 32) / 8, real = k / 8;
-  if (tid < LIN_COLS) most[tid] = 0;
-  __syncthreads();
-#pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-    int r = 0, c = tid;
-#pragma unroll 2
-    for (int i = tid; i < n * chunks; i += THREADS) {
-      while (c >= chunks) {
-        c -= chunks;
-        ++r;
-      }
-      const uint4 v = c < real ? __ldg(reinterpret_cast<const uint4*>(a.x + (t0 + r) * a.x_stride + k0) + c)
-                               : make_uint4(0, 0, 0, 0);
-      if (pass == 0) {
-        const uint32_t m = bf16_max(v);
-        if (m > *static_cast<volatile uint32_t*>(&most[r])) atomicMax(&most[r], m);
-      } else {
-        reinterpret_cast<uint4*>(xs + r * a.pitch)[c] = bf16_to_half8(v, to_half_scale(most[r]));
-      }
-      c += THREADS;
-    }
+  const int lg = WARPS == 16 ? max(0, 4 - (32 - __clz(n - 1))) : 0;
+  const int share = 1 << lg, at_once = WARPS >> lg;      // warps to a row (a power of two), rows at a time
+  const int row = warp >> lg, first = (warp & (share - 1)) * 32 + lane, step = share * 32;
+  if (share > 1) {
+    if (warp == 0) most[lane] = 0;
     __syncthreads();
   }
+  for (int r0 = 0; r0 < n; r0 += at_once) {       // once if share > 1
+    const int r = r0 + row;
+    const bool mine = r < n;
+    const uint4* src = reinterpret_cast<const uint4*>(a.x + (t0 + (mine ? r : 0)) * a.x_stride + k0);
+    uint4* dst = reinterpret_cast<uint4*>(xs + (mine ? r : 0) * a.pitch);
+    uint4 v[BATCH];
+    auto load = [&](int c0) {
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const int c = c0 + first + i * step;
+        v[i] = c < real ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    uint32_t m = 0;
+    for (int c0 = (chunks - 1) & -(BATCH * step); c0 >= 0; c0 -= BATCH * step) {   // the first chunks last: they stay
+      load(c0);
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) m = max(m, bf16_max(v[i]));
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (share > 1) {
+      if (lane == 0 && mine) atomicMax(&most[r], m);
+      __syncthreads();
+      if (mine) m = most[r];
+    }
+    const float sc = to_half_scale(m);
+    if (first == 0 && mine) unit[r] = 1.0f / sc;   // a power of two
+    for (int c0 = 0; c0 < chunks; c0 += BATCH * step) {
+      if (c0) load(c0);
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const int c = c0 + first + i * step;
+        if (c < chunks && mine) dst[c] = bf16_to_half8(v[i], sc);
+      }
+    }
+  }
+  __syncthreads();
 }
 
 template <int GROUP, int NT>
 __device__ __forceinline__ void linear_unit(const LinearArgs& a, LinearStream<GROUP, NT>& in, JoinShared& j, float4* parts,
-                                            uint32_t xs, const uint32_t* most, int lane) {
+                                            uint32_t xs, const float* unit, int lane) {
   const int g = lane >> 2, t = lane & 3;
   const Unit un = in.src.unit(in.cur);
   const int t0 = un.entry * LIN_COLS;
@@ -121,7 +143,7 @@ __device__ __forceinline__ void linear_unit(const LinearArgs& a, LinearStream<GR
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float f = 1.0f / to_half_scale(most[n * 8 + 2 * t + i]);     // a power of two
+      const float f = unit[n * 8 + 2 * t + i];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         sums.v[n][h][i] *= f;
@@ -157,23 +179,32 @@ __device__ __forceinline__ void linear_unit(const LinearArgs& a, LinearStream<GR
           sums.v[n][h][3] += v.w;
         }
   }
+  const int r0 = un.row * 32 + g;               // rows r0 + 8 q, q = 2 h + i / 2
+  if (a.bias) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+    for (int q = 0; q < 4; ++q) {
+      const float b = r0 + 8 * q < a.N ? __ldg(a.bias + r0 + 8 * q) : 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = un.row * 32 + h * 16 + (i >> 1) * 8 + g;
-      if (r >= a.N) continue;
-      const float b = a.bias ? __ldg(a.bias + r) : 0.0f;
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int c = t0 + n * 8 + 2 * t + (i & 1);
-        if (c >= a.T) continue;
-        const float v = a.bias ? sums.v[n][h][i] + b : sums.v[n][h][i];
-        const long long o = c * a.out_stride + r;
+        for (int j = 0; j < 2; ++j) sums.v[n][q >> 1][(q & 1) * 2 + j] += b;
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int c = t0 + n * 8 + 2 * t + j;
+      if (c >= a.T) continue;
+      const long long o = c * a.out_stride + r0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float v = sums.v[n][q >> 1][(q & 1) * 2 + j];
+        if (r0 + 8 * q >= a.N) break;
         if (a.out_f32)
-          static_cast<float*>(a.out)[o] = v;
+          static_cast<float*>(a.out)[o + 8 * q] = v;
         else
-          static_cast<uint16_t*>(a.out)[o] = f32_to_bf16(v);
+          static_cast<uint16_t*>(a.out)[o + 8 * q] = f32_to_bf16(v);
       }
     }
 }
@@ -184,6 +215,7 @@ __global__ void __launch_bounds__(lin_warps<NT>() * 32, 1) linear_w4_kernel(cons
   __shared__ JoinShared j;
   constexpr int LIN_WARPS = lin_warps<NT>();
   __shared__ uint32_t most[LIN_COLS];              // largest finite |x| of a row, as bits
+  __shared__ float unit[LIN_COLS];                 // what 1 in the FP16 row stands for
   __shared__ __align__(8) unsigned long long full[LIN_WARPS][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int RING = 2 * Format<F_W4, GROUP>::STAGE;
@@ -210,8 +242,8 @@ __global__ void __launch_bounds__(lin_warps<NT>() * 32, 1) linear_w4_kernel(cons
   join_init(j);
   const int k0 = share * a.split_len * 256, k = min(a.K - k0, a.split_len * 256);
   // one block of x at a time stays in shared memory: with more blocks every CTA has one (launch_linear)
-  stage_rows<LIN_WARPS * 32>(a, xs, most, (first % a.blocks) * LIN_COLS, k0, k, threadIdx.x);
-  while (in.take()) linear_unit<GROUP, NT>(a, in, j, parts, gg::smem_u32(xs), most, lane);
+  stage_rows<LIN_WARPS, NT == 1 ? 2 : 8>(a, xs, most, unit, (first % a.blocks) * LIN_COLS, k0, k, warp, lane);
+  while (in.take()) linear_unit<GROUP, NT>(a, in, j, parts, gg::smem_u32(xs), unit, lane);
   in.finish();
 }
 
@@ -326,9 +358,11 @@ struct LinearPlan {
 inline LinearPlan plan_linear(int T, int N, int K, int group, int sms) {
   LinearPlan p;
   const int cols = T < LIN_COLS ? T : LIN_COLS;
-  p.nt = cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
+  p.nt = (cols + 7) / 8;
   const int warps = p.nt == 1 ? lin_warps<1>() : lin_warps<4>();
-  p.slots = p.nt == 1 ? 32 : p.nt == 2 ? 16 : warps;       // at least a tile's units
+  // At least a tile's units.  9 with 24 columns leave room for half of K = 4096: 53 us for 24 x 40960,
+  // against 56 with 12 slots and thirds.
+  p.slots = p.nt == 1 ? 32 : p.nt == 2 ? 16 : p.nt == 3 ? 9 : 12;
   const int stage = 2 * (2048 + 8 * (256 / group) * 6);
   const int fixed = warps * 2 * stage + p.slots * p.nt * 1024;
   const int room = (LIN_SMEM - fixed) / 2 / cols - 32;      // elements of a row
@@ -340,7 +374,10 @@ inline LinearPlan plan_linear(int T, int N, int K, int group, int sms) {
   p.tiles = ceil_div(N, 32) * blocks;
   p.pitch = p.split_len * 256 + 32;          // rows 64 bytes past a multiple of 128: two rows' chunks in different banks
   p.smem = fixed + cols * p.pitch * 2;
-  p.cut.set(p.split_len, warps, p.tiles * p.splits <= sms);
+  // Units of 8 items where a CTA has many tiles, 4 where it has few: 42.7 against 45.6 us for 24 x 40960
+  // x 4096, and 12.1 against 9.9 for 7 x 7168 x 2048.
+  p.cut.set(p.split_len, p.slots < warps ? p.slots : warps, p.tiles * p.splits <= sms,
+            p.tiles * p.splits >= 8 * sms ? 8 : 4);
   const int unit = p.splits * blocks;
   p.ctas = sms / unit * unit;
   if (p.ctas == 0) p.ctas = unit;
@@ -365,6 +402,7 @@ template <int GROUP>
 moe_status_t launch_linear(const LinearArgs& a, const LinearPlan& p, cudaStream_t stream) {
   return p.nt == 1 ? launch_linear<GROUP, 1>(a, p, stream)
          : p.nt == 2 ? launch_linear<GROUP, 2>(a, p, stream)
+         : p.nt == 3 ? launch_linear<GROUP, 3>(a, p, stream)
                      : launch_linear<GROUP, 4>(a, p, stream);
 }
 
