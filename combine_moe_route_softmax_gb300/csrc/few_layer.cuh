@@ -107,7 +107,6 @@ struct LayerShared {
   float w[kMaxSlots];
   uint8_t alive[kMaxTokens];   // token has a valid slot
   JoinShared join;
-  float2 scratch[MAX_WARPS][ROUTE_TOKENS];
 };
 
 // Grid barrier in two halves (thread 0; the CTA synchronises around them).  The generation word
@@ -554,12 +553,15 @@ __global__ void __launch_bounds__(warps_of<FMT>() * 32, 1) layer_kernel(const __
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = a.T * a.K;
   const bool sync = HALF || a.w_router;
+  // where the joins' slots will be
+  float2* scratch = reinterpret_cast<float2*>(rings + WORKERS * 2 * Format<FMT, GROUP>::STAGE);
+  static_assert(route_scratch(WARPS) * 8 <= PARTS_BYTES, "");
   uint32_t gen = 0;
   if (HALF)
     // by the last CTAs, which have the fewest router rows
     for (int t = gridDim.x - 1 - blockIdx.x; t < a.T; t += gridDim.x) token_to_half<WARPS>(a, s, t, tid);
   if (a.w_router)
-    router_logits<WARPS>(a.x, a.w_router, a.router_bias, a.T, a.H, a.E, a.logits, s.scratch, blockIdx.x, gridDim.x,
+    router_logits<WARPS>(a.x, a.w_router, a.router_bias, a.T, a.H, a.E, a.logits, scratch, blockIdx.x, gridDim.x,
                          warp, lane);
   if (sync) {
     __syncthreads();

@@ -9,33 +9,37 @@
 namespace moe {
 namespace few {
 
-constexpr int ROUTE_WARPS = 8;
+constexpr int ROUTE_WARPS = 16;
 
+// A CTA per task beyond ROUTE_TOKENS tokens; the last CTA of each 16 tokens selects for them, one warp
+// a token.
 __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_hidden_kernel(
     const uint16_t* x, const uint16_t* wr, const float* bias, int T, int H, int E, int K, const int32_t* num_tokens,
     float* logits, int32_t* topk_idx, float* topk_w, uint32_t* count) {
   __shared__ bool last;
-  __shared__ float2 scratch[ROUTE_WARPS][ROUTE_TOKENS];
+  __shared__ float2 scratch[route_scratch(ROUTE_WARPS)];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   router_logits<ROUTE_WARPS>(x, wr, bias, T, H, E, logits, scratch, blockIdx.x, gridDim.x, warp, lane);
+  const int groups = mma_groups(T), group = blockIdx.x % groups;     // of tokens (the grid is whole rounds of them)
   __threadfence();
   __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(count, 1u) == gridDim.x - 1;
+  if (threadIdx.x == 0) last = atomicAdd(&count[group], 1u) == gridDim.x / groups - 1;
   __syncthreads();
   if (!last) return;
   __threadfence();
-  if (threadIdx.x == 0) *count = 0;
+  if (threadIdx.x == 0) count[group] = 0;
   const int n = num_tokens ? *num_tokens : T;
-  for (int t = warp; t < T; t += ROUTE_WARPS) {
-    int id = -1;
-    float w = 0.0f;
-    if (t < n) select_topk(logits + (size_t)t * E, E, K, lane, id, w);
-    if (lane < K) {
-      topk_idx[t * K + lane] = id;
-      topk_w[t * K + lane] = w;
-    }
+  const int t = group * MMA_TOKENS + warp;
+  if (t >= T) return;
+  int id = -1;
+  float w = 0.0f;
+  if (t < n) select_topk(logits + (size_t)t * E, E, K, lane, id, w);
+  if (lane < K) {
+    topk_idx[t * K + lane] = id;
+    topk_w[t * K + lane] = w;
   }
 }
+static_assert(ROUTE_WARPS == MMA_TOKENS, "a warp per token");
 
 }  // namespace few
 }  // namespace moe
@@ -55,8 +59,7 @@ extern "C" moe_status_t moe_route_hidden(const uint16_t* x, int T, int H, const 
   if (T == 0) return MOE_OK;
   if (!x || !w_router || !logits || !topk_idx || !topk_w) return MOE_ERR_ARG;
   if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w_router)) & 15) return MOE_ERR_ARG;
-  const int tasks = E * ((T + ROUTE_TOKENS - 1) / ROUTE_TOKENS);
-  const int ctas = std::min(tasks, num_sms() * 2);
+  const int ctas = T > ROUTE_TOKENS ? mma_tasks(T, E) : std::min(E, num_sms() * 2);
   route_hidden_kernel<<<ctas, ROUTE_WARPS * 32, 0, as_stream(stream)>>>(
       x, w_router, bias, T, H, E, K, num_tokens, logits, topk_idx, topk_w, static_cast<uint32_t*>(ws));
   MOE_CHECK_LAUNCH();

@@ -3,12 +3,14 @@
 //
 // logits[t, e] = x[t] . wr[e] + bias[e].  A near tie between two experts is decided by the last
 // bits of the logits, so the sum is carried in two float32 words: products of BF16 are
-// exact in float32, 8 of them are summed by fused multiply-adds, and each such partial sum
-// enters the running pair by an error-free addition.  What is left of rounding is that of the
-// 8-term sums, about 1e-9 of the logits' size each, below the final float32 rounding
-// (the plain error-free sum of every product costs four times the instructions).
+// exact in float32, 8 of them are summed by fused multiply-adds, or 16 by a tensor instruction, and
+// each such partial sum enters the running pair by an error-free addition.  What is left of
+// rounding is that of the partial sums, about 1e-9 of the logits' size each; together with the final
+// rounding to float32 6e-8 of the largest logit at H = 7168 (the error-free sum of every
+// product costs four times the instructions).
 #pragma once
 
+#include "few.cuh"
 #include "route_topk.cuh"
 
 namespace moe {
@@ -36,20 +38,16 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
   }
 }
 
-constexpr int ROUTE_TOKENS = 4;   // tokens of one task
-
-// A task is one expert and up to ROUTE_TOKENS tokens; S warps share its columns when there are few
-// tasks, so that every SM has some.  By sizes alone: the logits are the same bits in any grid.
-__device__ __forceinline__ int router_split(int tasks, int H) {
-  if (tasks > 1024) return 1;
-  return H >= 1024 ? 4 : H >= 512 ? 2 : 1;
-}
+// Up to ROUTE_TOKENS tokens a task is one expert, and S warps share its columns, so that every SM has
+// some.  By sizes alone: the logits are the same bits in any grid.
+constexpr int ROUTE_TOKENS = 4;
+__device__ __forceinline__ int router_split(int H) { return H >= 1024 ? 4 : H >= 512 ? 2 : 1; }
 
 // This warp's share of one task: columns of chunks (8 each) first, first + step, ...  Lane 8 * j
-// ends with token t0 + j's pair.
+// ends with token j's pair.
 template <int TT>
 __device__ __forceinline__ void router_dot(const uint16_t* __restrict__ x, const uint16_t* __restrict__ wr, int T,
-                                           int H, int t0, int first, int step, int lane, float& rs, float& rc) {
+                                           int H, int first, int step, int lane, float& rs, float& rc) {
   float s[TT], c[TT];
 #pragma unroll
   for (int j = 0; j < TT; ++j) s[j] = c[j] = 0.0f;
@@ -57,7 +55,7 @@ __device__ __forceinline__ void router_dot(const uint16_t* __restrict__ x, const
   // tokens past T read the last one; their sums are dropped
   const uint4* x4[TT];
 #pragma unroll
-  for (int j = 0; j < TT; ++j) x4[j] = reinterpret_cast<const uint4*>(x + (size_t)min(t0 + j, T - 1) * H);
+  for (int j = 0; j < TT; ++j) x4[j] = reinterpret_cast<const uint4*>(x + (size_t)min(j, T - 1) * H);
 #pragma unroll 4
   for (int i = first; i < H / 8; i += step) {
     float w[8], v[8];
@@ -95,38 +93,91 @@ __device__ __forceinline__ void router_dot(const uint16_t* __restrict__ x, const
   rc = c[0];
 }
 
+// More than ROUTE_TOKENS tokens: a task is 16 tokens and 8 experts, its columns shared out between the
+// CTA's warps 32 at a time.  A tensor instruction (tokens as its 16 rows, experts as its 8 columns)
+// starts from zero and gives sums of 16 products, which enter the pairs as above.
+constexpr int MMA_TOKENS = 16, MMA_EXPERTS = 8;
+__host__ __device__ __forceinline__ int mma_groups(int T) { return (T + MMA_TOKENS - 1) / MMA_TOKENS; }
+__host__ __device__ __forceinline__ int mma_tasks(int T, int E) {
+  return (E + MMA_EXPERTS - 1) / MMA_EXPERTS * mma_groups(T);
+}
+__host__ __device__ constexpr int route_scratch(int warps) { return warps * MMA_TOKENS * MMA_EXPERTS; }   // float2
+template <int NW>
+__device__ __forceinline__ void router_logits_mma(const uint16_t* __restrict__ x, const uint16_t* __restrict__ wr,
+                                                  const float* bias, int T, int H, int E, float* logits,
+                                                  float2* scratch, int cta, int ctas, int warp, int lane) {
+  const int groups = mma_groups(T), tasks = mma_tasks(T, E), g = lane >> 2, t = lane & 3;
+  for (int task = cta; task < tasks; task += ctas) {
+    const int e0 = task / groups * MMA_EXPERTS, t0 = task % groups * MMA_TOKENS;
+    // tokens past T read the last one, experts past E too; their sums are dropped
+    const uint4* x0 = reinterpret_cast<const uint4*>(x + (size_t)min(t0 + g, T - 1) * H) + t;
+    const uint4* x1 = reinterpret_cast<const uint4*>(x + (size_t)min(t0 + g + 8, T - 1) * H) + t;
+    const uint4* w = reinterpret_cast<const uint4*>(wr + (size_t)min(e0 + g, E - 1) * H) + t;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int i = warp; i < H / 32; i += NW) {
+      const uint4 a = __ldg(x0 + i * 4), b = __ldg(x1 + i * 4), v = __ldg(w + i * 4);
+      float d[2][4];
+      mma16_first<false>(d[0], a.x, b.x, a.y, b.y, v.x, v.y);
+      mma16_first<false>(d[1], a.z, b.z, a.w, b.w, v.z, v.w);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) add_pair(s[q], c[q], d[j][q]);
+    }
+    __syncthreads();           // the task before is read
+#pragma unroll
+    for (int q = 0; q < 4; ++q) scratch[(warp * 4 + q) * 32 + lane] = make_float2(s[q], c[q]);
+    __syncthreads();
+    const int i = warp * 32 + lane;
+    if (i < 128) {
+      const int q = warp, tok = t0 + g + (q >> 1) * 8, e = e0 + 2 * t + (q & 1);
+      float rs = scratch[i].x, rc = scratch[i].y;
+#pragma unroll 4
+      for (int j = 1; j < NW; ++j) join_pair(rs, rc, scratch[j * 128 + i].x, scratch[j * 128 + i].y);
+      if (tok < T && e < E) {
+        if (bias) add_pair(rs, rc, __ldg(bias + e));
+        logits[(size_t)tok * E + e] = __fadd_rn(rs, rc);
+      }
+    }
+  }
+}
+
 // All logits, by every CTA of a grid (NW warps each, all threads call; NW need not be a multiple of
-// the split).
+// the split).  scratch: route_scratch(NW) of shared memory.
 template <int NW>
 __device__ __forceinline__ void router_logits(const uint16_t* x, const uint16_t* wr, const float* bias, int T, int H,
-                                              int E, float* logits, float2 (*scratch)[ROUTE_TOKENS], int cta, int ctas,
-                                              int warp, int lane) {
-  const int groups = (T + ROUTE_TOKENS - 1) / ROUTE_TOKENS, tasks = E * groups;
-  const int S = router_split(tasks, H), per = NW / S;
+                                              int E, float* logits, float2* scratch, int cta, int ctas, int warp,
+                                              int lane) {
+  if (T > ROUTE_TOKENS) {
+    router_logits_mma<NW>(x, wr, bias, T, H, E, logits, scratch, cta, ctas, warp, lane);
+    return;
+  }
+  const int tasks = E, S = router_split(H), per = NW / S;
   const int slice = warp % S, mine = warp / S;
   for (int r = cta * per; r < tasks; r += ctas * per) {
     const int task = r + mine;
-    const int e = task / groups, t0 = (task - e * groups) * ROUTE_TOKENS;
+    const int e = task;
     float s = 0.0f, c = 0.0f;
     if (mine < per && task < tasks) {
       const uint16_t* row = wr + (size_t)e * H;
-      if (T == 1) router_dot<1>(x, row, T, H, 0, slice * 32 + lane, 32 * S, lane, s, c);
-      else router_dot<ROUTE_TOKENS>(x, row, T, H, t0, slice * 32 + lane, 32 * S, lane, s, c);
+      if (T == 1) router_dot<1>(x, row, T, H, slice * 32 + lane, 32 * S, lane, s, c);
+      else router_dot<ROUTE_TOKENS>(x, row, T, H, slice * 32 + lane, 32 * S, lane, s, c);
     }
     const int j = lane >> 3;       // this lane's token
     if (S > 1) {
       __syncthreads();
-      if (mine < per && (lane & 7) == 0) scratch[warp][j] = make_float2(s, c);
+      if (mine < per && (lane & 7) == 0) scratch[warp * ROUTE_TOKENS + j] = make_float2(s, c);
       __syncthreads();
       if (slice != 0) continue;
       for (int q = 1; q < S; ++q) {
-        const float2 v = scratch[warp + q][j];
+        const float2 v = scratch[(warp + q) * ROUTE_TOKENS + j];
         join_pair(s, c, v.x, v.y);
       }
     }
-    if (mine < per && task < tasks && (lane & 7) == 0 && j < (T == 1 ? 1 : ROUTE_TOKENS) && t0 + j < T) {
+    if (mine < per && task < tasks && (lane & 7) == 0 && j < T) {
       if (bias) add_pair(s, c, __ldg(bias + e));
-      logits[(size_t)(t0 + j) * E + e] = __fadd_rn(s, c);
+      logits[(size_t)j * E + e] = __fadd_rn(s, c);
     }
   }
 }
