@@ -536,7 +536,7 @@ struct Stream {
   __device__ __forceinline__ void finish() {
     // given up: the item on its way arrives before the block ends
     if (dead && !pending && filled != END) gg::mbar_drain(bars + (stage & 1) * 8, (stage >> 1) & 1);
-    src.at(0x7fffff00, lane);    // far past any unit
+    src.at(0x7ffff000, lane);    // far past any unit
   }
 
   // sums = weights x activations over the unit in use.  off[p][n] is where this lane's column of group n
@@ -671,9 +671,11 @@ __device__ __forceinline__ void schedule(Feed<SIZE>& f, Src& src, int lane, int3
   unsigned long long t0 = clock_ns();
   while (!end || !src.done()) {
     bool moved = src.idle(lane);
-    const int slowest = __reduce_min_sync(0xffffffffu, lane < WORKERS ? use[lane] : 0x7fffffff);
     // few units in stock: what an SM holds ready at the end, the others do without
-    if (!end && units < min(slowest + AHEAD, *static_cast<volatile int*>(&f.next) + STOCK)) {
+    volatile int* next = &f.next;
+    const int most = __reduce_min_sync(
+        0xffffffffu, lane < WORKERS ? use[lane] + AHEAD : lane == WORKERS ? *next + STOCK : 0x7fffffff);
+    if (!end && units < most) {
       if (n == 0 && !src.next(lane, t, n)) {
         end = true;
         if (lane == 0) *static_cast<volatile int*>(&f.total) = units;
@@ -724,14 +726,16 @@ __device__ __forceinline__ void join_init(JoinShared& j) {
 // Joins the units [u0, u0 + n) of one tile; unit u is this warp's.  Slot i % slots of `parts`
 // (`stride` float4 each) belongs to unit i until its tile is summed; a warp that is `slots` units
 // ahead waits for it (units are taken in order and a tile has at most `slots` of them, so the wait
-// ends; it is bounded all the same).  True on the warp that has the tile's sums; false also
-// after a timeout, which sets the status bit.
+// ends; it is bounded all the same).  It also waits for the first unit's slot, whose count the tile
+// uses: where tiles of more parts follow ones of fewer, the tile that had that slot before may
+// not be the one that had this unit's.  True on the warp that has the tile's sums; false also after
+// a timeout, which sets the status bit.
 template <int NT>
 __device__ __forceinline__ bool join(Sums<NT>& sums, JoinShared& j, float4* parts, int slots, int stride, int u, int u0,
                                      int n, int lane, int32_t* dev_status) {
-  const int mine = u % slots;
+  const int mine = u % slots, head = u0 % slots;
   volatile int* turn = j.turn;
-  if (!warp_wait_for([&] { return turn[mine] == u; }, dev_status)) return false;
+  if (!warp_wait_for([&] { return turn[mine] == u && turn[head] == u0; }, dev_status)) return false;
   if (n > 1) {
     float4* p = parts + mine * stride;
 #pragma unroll
@@ -742,13 +746,13 @@ __device__ __forceinline__ bool join(Sums<NT>& sums, JoinShared& j, float4* part
     __threadfence_block();
     __syncwarp();
     int old = 0;
-    if (lane == 0) old = atomicAdd(&j.count[u0 % slots], 1);
+    if (lane == 0) old = atomicAdd(&j.count[head], 1);
     old = __shfl_sync(0xffffffffu, old, 0);
     if (old != n - 1) return false;
     __threadfence_block();
-    if (lane == 0) j.count[u0 % slots] = 0;
+    if (lane == 0) j.count[head] = 0;
     sums.clear();
-    int at = u0 % slots;
+    int at = head;
 #pragma unroll 2
     for (int i = 0; i < n; ++i) {
       const float4* v = parts + at * stride;

@@ -398,3 +398,27 @@ def test_layer_few_near_layer_forward():
     moe.MoeLayer(T, H, I, E, K, moe.MOE_BF16, **kw).forward(x, old, idx, wt)
     # three more BF16 roundings (h, the rows): within 2e-2 of the largest output, as its own tests hold it
     assert (out.float() - old.float()).abs().max() <= 2e-2 * old.float().abs().max()
+
+
+@pytest.mark.parametrize("dtype,H,I,E,K,T,group", [("bf16", 2048, 1408, 64, 8, 5, 0), ("e4m3", 2048, 1408, 64, 8, 5, 0),
+                                                   ("w4", 2048, 1408, 64, 8, 5, 32), ("e4m3", 1024, 2048, 32, 4, 20, 0)])
+def test_layer_few_behind_other_work(dtype, H, I, E, K, T, group):
+    """Right behind kernels that wrote the weights some SMs run far behind others.  Tiles of phase 2
+    have other numbers of parts than those of phase 1: the joins of a late one stay its own.  Every
+    call has other inputs than the one before, and gives the bits of a quiet call, with no wait
+    run out."""
+    g = gen(31)
+    w = Weights(g, dtype, H, I, E, False, group)
+    layer, quiet = (moe.MoeLayerFew(T, H, I, E, K, **w.kw) for _ in range(2))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    big = [t for t in layer.tensors if t is not None]
+    for i in range(16):
+        x = normal(g, T, H)
+        idx, wt = random_routing(g, T, K, E, 0.1)
+        torch.cuda.synchronize()
+        want, _, _ = quiet.forward(x, topk_idx=idx, topk_w=wt)
+        torch.cuda.synchronize()
+        for t in big if i % 2 else big[::-1]:
+            t.view(torch.uint8).bitwise_or_(0)
+        got, _, _ = layer.forward(x, topk_idx=idx, topk_w=wt, dev_status=status)
+        assert torch.equal(got, want) and status.item() == 0
