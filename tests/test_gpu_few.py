@@ -422,3 +422,29 @@ def test_layer_few_behind_other_work(dtype, H, I, E, K, T, group):
             t.view(torch.uint8).bitwise_or_(0)
         got, _, _ = layer.forward(x, topk_idx=idx, topk_w=wt, dev_status=status)
         assert torch.equal(got, want) and status.item() == 0
+
+
+@pytest.mark.parametrize("weights", ["bf16", "e4m3", "w4"])
+def test_decode_few_example(weights):
+    """The operators together: 12 greedy steps, routed inside the layers and ahead of them."""
+    need_gpu()
+    from combine_moe_route_softmax_gb300 import decode_few
+    ms, same = decode_few.run(tokens=5, layers=2, H=512, I=256, E=16, K=4, vocab=1024, weights=weights, group=64, steps=12)
+    assert same and all(t > 0 for t in ms.values())
+
+
+def test_decode_few_step_values():
+    """One BF16 layer and the head against the 64-bit forms of each, fed each other's outputs."""
+    need_gpu()
+    from combine_moe_route_softmax_gb300 import decode_few
+    step = decode_few.DecodeStep(3, 1, 512, 256, 16, 4, 640, "bf16", 32, shared=False)
+    x = step.table[:3].contiguous()
+    logits, ids = step(x)
+    layer = step.inside[0]
+    y, idx, w = layer.forward(x)
+    assert torch.equal(idx, ids[0])
+    val = lambda t: (lambda e: t[e].double())
+    want, err = ref.layer(x, idx, w, val(layer.tensors[0]), val(layer.tensors[2]), None, False)
+    assert ref.close(y, want, err) <= 1
+    again = moe.moe_linear_w4(x + y, step.head, out_dtype=torch.float32)
+    assert torch.equal(again, logits)
