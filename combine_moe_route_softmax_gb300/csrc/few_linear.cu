@@ -9,14 +9,22 @@
 // weights' bytes.  Where the rows are too long for that, K is shared between CTAs, whose sums the
 // last of them adds up in order.
 //
+// Bound: reading W once; in fact the unpacking and, with 24 columns, the tensor instructions.  Measured
+// (group 128 unless said otherwise): 24 x 40960 x 4096, float32 out 42 us (2.1 TB/s); 1 x 4096 x 7168
+// 7.8 us; 7 x 7168 x 2048, group 64, zero points, bias 8.1 us; 1 x 512 x 256, group 32 4.2 us
+// (launch and latency).
+//
 // Also the one-time preparation of such weights: moe_quantize_weight_w4 and moe_pack_w4.
+#include <algorithm>
+
 #include "few.cuh"
 
 namespace moe {
 namespace few {
 
 constexpr int LIN_COLS = 32;
-// Warps of a CTA: 16 as far as 128 registers a thread do.
+// Warps of a CTA: 16 as far as 128 registers a thread do; 12 otherwise (24 columns: 42.0 us with 12, 45 to
+// 47 with 13 to 15, whose rings leave less room for x).
 template <int NT>
 __host__ __device__ constexpr int lin_warps() { return NT == 1 ? 16 : 12; }
 constexpr int LIN_SMEM = 225 * 1024;
@@ -76,7 +84,8 @@ template <int GROUP, int NT>
 using LinearStream = Stream<F_W4, GROUP, true, true, LinearSource<GROUP, NT>>;
 
 // The CTA's rows of x, its share of K, as FP16, by all warps: several to a row, or several rows to a
-// warp, each lane with BATCH loads in flight.  Zeros up to a whole item.
+// warp, each lane with BATCH loads in flight (8 with many rows: 42.7 us against 52.5 for 24 x 40960 x 4096
+// with one row after the other; 2 with few: less code, and 1 x 512 x 256 is fetching code).  Zeros up to a whole item.
 template <int WARPS, int BATCH>
 __device__ __forceinline__ void stage_rows(const LinearArgs& a, uint16_t* xs, uint32_t* most, float* unit, int t0,
                                            int k0, int k, int warp, int lane) {
@@ -354,6 +363,7 @@ struct LinearPlan {
   int nt, slots, splits, split_len, pitch, ctas, smem;
   Cut cut;
   long long tiles;
+  size_t sum_bytes() const { return splits > 1 ? (size_t)tiles * splits * nt * 1024 : 0; }
 };
 inline LinearPlan plan_linear(int T, int N, int K, int group, int sms) {
   LinearPlan p;
@@ -456,14 +466,18 @@ extern "C" moe_status_t moe_pack_w4(const uint8_t* q, const uint16_t* scales, co
   return MOE_OK;
 }
 
-// The counters of the tiles, then the shares' sums; for the group whose rows of x need most shares.
+// The counters of the tiles at the start, the shares' sums at the end of what the caller has: a workspace
+// made for T serves fewer rows too, whose sums must not lie where more rows have counters.  So the sums get
+// what any T up to this one needs, with the group whose items leave least room for x.
 extern "C" size_t moe_linear_w4_workspace_bytes(int T, int N, int K) {
   using namespace moe;
   using namespace moe::few;
   if (T < 0 || !w4_shape_ok(0, N, K, 32)) return 0;
   if (T == 0) return 256;
+  size_t sums = 0;
+  for (int t = 8; t < T && t < LIN_COLS; t += 8) sums = std::max(sums, plan_linear(t, N, K, 32, num_sms()).sum_bytes());
   const LinearPlan p = plan_linear(T, N, K, 32, num_sms());
-  return align256(4 * (size_t)p.tiles) + (p.splits > 1 ? (size_t)p.tiles * p.splits * p.nt * 1024 : 0);
+  return align256(4 * (size_t)p.tiles) + std::max(sums, p.sum_bytes());
 }
 
 extern "C" moe_status_t moe_linear_w4(const uint16_t* x, int T, int K, long long x_stride, const uint8_t* packed, int N,
@@ -504,7 +518,7 @@ extern "C" moe_status_t moe_linear_w4(const uint16_t* x, int T, int K, long long
   a.pitch = p.pitch;
   a.slots = p.slots;
   a.count = static_cast<int32_t*>(ws);
-  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align256(4 * (size_t)p.tiles));
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + (ws_bytes - p.sum_bytes()) / 256 * 256);
   a.dev_status = dev_status;
   cudaStream_t st = as_stream(stream);
   return group == 32   ? launch_linear<32>(a, p, st)

@@ -522,14 +522,16 @@ size_t moe_w4_packed_bytes(int N, int K, int group, int zeros);
 moe_status_t moe_pack_w4(const uint8_t* q, const uint16_t* scales, const uint8_t* zeros, int mats, int N, int K,
                          int group, uint8_t* packed, void* stream);
 
-/* out[t, n] = sum_k x[t, k] * value(n, k) (+ bias[n]), BF16 products, float32 sums, one
- * rounding.  Made for few rows: every 32 rows of x read the weights again.
+/* out[t, n] = sum_k x[t, k] * value(n, k) (+ bias[n]), float32 sums, one rounding.  x is
+ * held as FP16 scaled by a power of two per row, exact for values above 2^-28 of the row's largest.
+ * Made for few rows: every 32 rows of x read the weights again.
  *   x          BF16 [T, K], row t at x + t * x_stride (elements, a multiple of 8, >= K),
  *              16-byte aligned.
  *   packed     one matrix from moe_pack_w4 (of this group; zeros: 1 if it has zero points).
  *   bias       nullable float32 [N].
  *   out        BF16 (out_f32 = 0) or float32 (1) [T, N], row t at out + t * out_stride (>= N).
- *   ws         moe_linear_w4_workspace_bytes(T, N, K) bytes, 256-byte aligned, zero at first use.
+ *   ws         moe_linear_w4_workspace_bytes(T, N, K) bytes, 256-byte aligned, zero at first use;
+ *              it serves any number of rows up to T (with ws_bytes as it was made), of this N and K.
  *   dev_status nullable; MOE_DEV_PIPELINE_TIMEOUT if a wait within the kernel gave up.
  * Any N >= 1 (mats = 1), K % 128 == 0.  The result does not depend on timing.
  * Errors: MOE_ERR_ARG, MOE_ERR_WORKSPACE. */

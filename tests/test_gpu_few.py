@@ -109,6 +109,20 @@ def test_linear_w4_strides_and_out():
     assert (out[:, N:] == 7).all()
 
 
+def test_linear_w4_workspace_for_fewer_rows():
+    """One workspace, row counts up and down: what one call leaves is not where another counts."""
+    g = gen(41)
+    N, K = 320, 7168           # K shared between CTAs at every T
+    q, s, _ = w4_random(g, 1, N, K, 32, False)
+    p = moe.moe_pack_w4(q, s)
+    ws = moe.moe_linear_w4_workspace(100, N, K)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for T in (100, 24, 100, 8, 33, 1, 64, 31, 100):
+        x = normal(g, T, K)
+        out = moe.moe_linear_w4(x, p, out_dtype=torch.float32, ws=ws, dev_status=status)
+        assert torch.equal(out, moe.moe_linear_w4(x, p, out_dtype=torch.float32)) and status.item() == 0
+
+
 def test_linear_w4_rows_are_apart():
     """A row of x with NaN or infinity leaves the other rows as they are."""
     g = gen(6)
