@@ -22,6 +22,16 @@
 // finished.  Phase 2 brings these to the slot's largest scale as it reads them, by a product with a
 // power of two, so nothing has to wait for the whole of h but the largest exponent.
 //
+// Bound: reading the weights of the experts met once.  Measured (6.68 TB/s is the copy bandwidth):
+//   E4M3, 16 tokens at H = 7168, I = 2048, E = 256, top-8 + shared: 672-685 us, 6.6-6.8 TB/s
+//   E4M3, one token at those sizes: 82 us for 400 MB -- 10 until the experts are known, 60
+//     streaming at the copy bandwidth, 8 from the average warp's last unit to the last combine, launch
+//   BF16, 5 tokens at H = 2048, I = 1408, E = 64, top-8: 84 us, 5.9 TB/s
+//   4 bits, one token at the E4M3 sizes: 72 us, 2.9 TB/s; 32 tokens at the BF16 sizes, groups of 32 with
+//     zero points: 137 us, 2.4 TB/s -- bound by unpacking (few.cuh)
+//   BF16, one token at H = 256, I = 512, E = 8, top-2: 18 us, latency throughout
+// An L2 prefetch of the shared expert while the routing is found out changed none of these.
+//
 // Roundings of h: one FP16 term keeps 11 bits, an error of 1.4e-4 of the output beside the 1.7e-3
 // of its BF16 rounding.  One BF16 term would add 1.2e-3, so BF16 layers keep two, h = hi + lo (16
 // bits): side by side as two columns of one tensor instruction up to 4 tokens, as two
@@ -36,8 +46,8 @@ namespace few {
 
 constexpr int MAX_WARPS = 16;
 // Warps of a CTA, the last of which schedules.  W4's unpacking wants more than the 128 registers a
-// thread has with 16 warps: 162 us with 12 warps against 182 on 32 tokens at H = 2048, I = 1408, E = 64,
-// top-8, groups of 32; E4M3's does not: 720 us with 16 against 796 on 16 tokens at H = 7168, I = 2048,
+// thread has with 16 warps: 144 us with 12 warps, 157 with 14, 168 with 16 on 32 tokens at H = 2048,
+// I = 1408, E = 64, top-8, groups of 32; E4M3's does not: 720 us with 16 against 796 on 16 tokens at H = 7168, I = 2048,
 // E = 256, top-8.
 template <int FMT>
 __host__ __device__ constexpr int warps_of() { return FMT == F_W4 ? 12 : MAX_WARPS; }
@@ -263,7 +273,7 @@ struct LayerSched {
 
   __device__ __forceinline__ bool next(int lane, int& t, int& n) {
     // runs of a few (smaller) tiles in phase 2 as long as there are plenty: a look at the queue takes
-    // about as long as an SM needs for 32 KB
+    // about as long as an SM needs for 32 KB (16 tokens, E4M3 as above: 685 us, 699 with two at most)
     if (q < 2) {
       t = blockIdx.x + q * gridDim.x;
       n = 1;
