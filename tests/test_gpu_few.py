@@ -399,6 +399,37 @@ def test_few_streams_and_graph():
         assert all(torch.equal(a, b) for a, b in zip(outs, want[i]))
 
 
+def test_few_two_streams_at_once():
+    """Two layers and two products on two streams, each with a workspace of its own: the bits of calls
+    one after the other."""
+    g = gen(23)
+    T, H, I, E, K = 6, 512, 384, 16, 4
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    sides = []
+    for dtype, group in (("e4m3", 0), ("w4", 64)):
+        w = Weights(g, dtype, H, I, E, True, group)
+        q, sc, z = w4_random(g, 1, 416, H, 64, True)
+        sides.append((moe.MoeLayerFew(T, H, I, E, K, w_router=normal(g, E, H, std=H ** -0.5), **w.kw),
+                      moe.moe_pack_w4(q, sc, z), moe.moe_linear_w4_workspace(T, 416, H),
+                      [normal(g, T, H) for _ in range(12)], torch.zeros(1, dtype=torch.int32, device="cuda")))
+
+    def one(side, i):
+        layer, p, ws, xs, status = side
+        out, idx, w = layer.forward(xs[i], dev_status=status)
+        return out, idx, w, moe.moe_linear_w4(out, p, ws=ws, dev_status=status)
+    want = [[one(side, i) for i in range(12)] for side in sides]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for i in range(12):
+        for k in range(2):
+            with torch.cuda.stream(streams[k]):
+                got[k].append(one(sides[k], i))
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert sides[k][4].item() == 0
+        assert all(torch.equal(a, b) for x, y in zip(got[k], want[k]) for a, b in zip(x, y))
+
+
 def test_layer_few_near_layer_forward():
     """The same layer through moe_layer_forward (BF16 h and rows): equal to its extra roundings."""
     g = gen(14)
