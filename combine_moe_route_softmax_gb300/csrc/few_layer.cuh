@@ -23,12 +23,12 @@
 // power of two, so nothing has to wait for the whole of h but the largest exponent.
 //
 // Bound: reading the weights of the experts met once.  Measured (6.68 TB/s is the copy bandwidth):
-//   E4M3, 16 tokens at H = 7168, I = 2048, E = 256, top-8 + shared: 672-685 us, 6.6-6.8 TB/s
+//   E4M3, 16 tokens at H = 7168, I = 2048, E = 256, top-8 + shared: 667-681 us, 6.7-6.8 TB/s
 //   E4M3, one token at those sizes: 82 us for 400 MB -- 10 until the experts are known, 60
 //     streaming at the copy bandwidth, 8 from the average warp's last unit to the last combine, launch
 //   BF16, 5 tokens at H = 2048, I = 1408, E = 64, top-8: 84 us, 5.9 TB/s
 //   4 bits, one token at the E4M3 sizes: 72 us, 2.9 TB/s; 32 tokens at the BF16 sizes, groups of 32 with
-//     zero points: 137 us, 2.4 TB/s -- bound by unpacking (few.cuh)
+//     zero points: 136 us, 2.4 TB/s -- bound by unpacking (few.cuh)
 //   BF16, one token at H = 256, I = 512, E = 8, top-2: 18 us, latency throughout
 // An L2 prefetch of the shared expert while the routing is found out changed none of these.
 //
@@ -458,44 +458,61 @@ __device__ __forceinline__ void store_y(const LayerArgs& a, const LayerShared& s
 }
 
 // One row tile's outputs in the combine's order: ascending slot, float32 product and sum from +0,
-// the shared row last, one BF16 rounding.  Lane = (token of four, four rows): a warp has up to eight
-// 16-byte loads in flight per lane, since this is the tail of the layer.  Not inlined: its registers
-// are not the streaming loop's.
+// the shared row last, one BF16 rounding.  Lane = (token of four, four rows), G such tokens at a time:
+// a warp has up to 8 G 16-byte loads in flight per lane, since this is the tail of the layer.  Not
+// inlined: its registers are not the streaming loop's.  G = 2 beyond 8 tokens: 139.9 -> 135.9 us for 32
+// (4 bits, H = 2048), 670.6 -> 667.2 for 16 (E4M3, H = 7168); with 5, 83.6 -> 85.8 (BF16, H = 2048).
+template <int G>
 static __device__ __noinline__ void combine_tile(const LayerArgs& a, const LayerShared& s, int tile, int lane) {
   const int row = tile * 32 + (lane & 7) * 4;
 #pragma unroll 1
-  for (int t = lane >> 3; t < a.T; t += 4) {
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    const bool sh = a.shared && s.alive[t];
-    float4 sv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (sh) sv = __ldcg(reinterpret_cast<const float4*>(a.y + (size_t)(a.T * a.K + t) * a.H + row));
+  for (int t0 = lane >> 3; t0 < a.T; t0 += 4 * G) {
+    float acc[G][4];
+    float4 sv[G];
+    int tok[G];
+    bool sh[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      tok[g] = min(t0 + 4 * g, a.T - 1);         // past the end: the last one again, not stored
+      sh[g] = a.shared && s.alive[tok[g]];
+      acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.0f;
+      sv[g] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (sh[g]) sv[g] = __ldcg(reinterpret_cast<const float4*>(a.y + (size_t)(a.T * a.K + tok[g]) * a.H + row));
+    }
 #pragma unroll 1
     for (int k0 = 0; k0 < a.K; k0 += 8) {
       // every row is read, used or not (they all exist): a load behind a condition waits for the one before
-      float4 v[8];
+      float4 v[G][8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        v[j] = __ldcg(reinterpret_cast<const float4*>(a.y + (size_t)(t * a.K + min(k0 + j, a.K - 1)) * a.H + row));
+      for (int g = 0; g < G; ++g)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int i = t * a.K + min(k0 + j, a.K - 1);
-        const bool use = k0 + j < a.K && s.id[i] >= 0;
-        const float w = s.w[i];
-        acc[0] = use ? __fadd_rn(acc[0], __fmul_rn(v[j].x, w)) : acc[0];
-        acc[1] = use ? __fadd_rn(acc[1], __fmul_rn(v[j].y, w)) : acc[1];
-        acc[2] = use ? __fadd_rn(acc[2], __fmul_rn(v[j].z, w)) : acc[2];
-        acc[3] = use ? __fadd_rn(acc[3], __fmul_rn(v[j].w, w)) : acc[3];
+        for (int j = 0; j < 8; ++j)
+          v[g][j] = __ldcg(reinterpret_cast<const float4*>(a.y + (size_t)(tok[g] * a.K + min(k0 + j, a.K - 1)) * a.H + row));
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int i = tok[g] * a.K + min(k0 + j, a.K - 1);
+          const bool use = k0 + j < a.K && s.id[i] >= 0;
+          const float w = s.w[i];
+          acc[g][0] = use ? __fadd_rn(acc[g][0], __fmul_rn(v[g][j].x, w)) : acc[g][0];
+          acc[g][1] = use ? __fadd_rn(acc[g][1], __fmul_rn(v[g][j].y, w)) : acc[g][1];
+          acc[g][2] = use ? __fadd_rn(acc[g][2], __fmul_rn(v[g][j].z, w)) : acc[g][2];
+          acc[g][3] = use ? __fadd_rn(acc[g][3], __fmul_rn(v[g][j].w, w)) : acc[g][3];
+        }
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      if (sh[g]) {
+        acc[g][0] = __fadd_rn(acc[g][0], sv[g].x);
+        acc[g][1] = __fadd_rn(acc[g][1], sv[g].y);
+        acc[g][2] = __fadd_rn(acc[g][2], sv[g].z);
+        acc[g][3] = __fadd_rn(acc[g][3], sv[g].w);
       }
+      const uint32_t lo = f32_to_bf16(acc[g][0]) | (uint32_t)f32_to_bf16(acc[g][1]) << 16;
+      const uint32_t hi = f32_to_bf16(acc[g][2]) | (uint32_t)f32_to_bf16(acc[g][3]) << 16;
+      if (t0 + 4 * g < a.T) *reinterpret_cast<uint2*>(a.out + (size_t)tok[g] * a.H + row) = make_uint2(lo, hi);
     }
-    if (sh) {
-      acc[0] = __fadd_rn(acc[0], sv.x);
-      acc[1] = __fadd_rn(acc[1], sv.y);
-      acc[2] = __fadd_rn(acc[2], sv.z);
-      acc[3] = __fadd_rn(acc[3], sv.w);
-    }
-    const uint32_t lo = f32_to_bf16(acc[0]) | (uint32_t)f32_to_bf16(acc[1]) << 16;
-    const uint32_t hi = f32_to_bf16(acc[2]) | (uint32_t)f32_to_bf16(acc[3]) << 16;
-    *reinterpret_cast<uint2*>(a.out + (size_t)t * a.H + row) = make_uint2(lo, hi);
   }
 }
 
@@ -551,7 +568,8 @@ __device__ __forceinline__ void do_unit(const LayerArgs& a, LayerShared& s, Laye
   if (__shfl_sync(0xffffffffu, old, 0) != s.n_entries - 1) return;
   __threadfence();
   if (lane == 0) a.tile_count[row] = 0;
-  combine_tile(a, s, row, lane);
+  if (a.T > 8) combine_tile<2>(a, s, row, lane);
+  else combine_tile<1>(a, s, row, lane);
 }
 
 template <int FMT, int GROUP>
