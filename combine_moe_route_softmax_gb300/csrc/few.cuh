@@ -386,7 +386,7 @@ __device__ __forceinline__ void half_item(Sums<NT>& sums, Sums<NT>& acc, const u
 // -------------------------------------------------------------------------------- feed
 constexpr int FEED = 64;             // units written down at a time
 constexpr int AHEAD = 40;            // ... past the slowest worker's
-constexpr int STOCK = 10;            // ... that no worker has taken
+constexpr int STOCK = 4;             // ... that no worker has taken
 template <int WORKERS>
 struct Feed {
   Unit unit[FEED];
