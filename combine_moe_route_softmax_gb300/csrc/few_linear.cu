@@ -11,7 +11,7 @@
 //
 // Bound: reading W once; in fact the unpacking and, with 24 columns, the tensor instructions.  Measured
 // (group 128 unless said otherwise): 24 x 40960 x 4096, float32 out 42 us (2.1 TB/s); 1 x 4096 x 7168
-// 7.8 us; 7 x 7168 x 2048, group 64, zero points, bias 8.1 us; 1 x 512 x 256, group 32 4.2 us
+// 7.8 us; 7 x 7168 x 2048, group 64, zero points, bias 7.5 us; 1 x 512 x 256, group 32 4.2 us
 // (launch and latency).
 //
 // Also the one-time preparation of such weights: moe_quantize_weight_w4 and moe_pack_w4.
@@ -384,15 +384,27 @@ inline LinearPlan plan_linear(int T, int N, int K, int group, int sms) {
   p.tiles = ceil_div(N, 32) * blocks;
   p.pitch = p.split_len * 256 + 32;          // rows 64 bytes past a multiple of 128: two rows' chunks in different banks
   p.smem = fixed + cols * p.pitch * 2;
-  // Units of 8 items where a CTA has many tiles, 4 where it has few: 42.7 against 45.6 us for 24 x 40960
-  // x 4096, and 12.1 against 9.9 for 7 x 7168 x 2048.
-  p.cut.set(p.split_len, p.slots < warps ? p.slots : warps, p.tiles * p.splits <= sms,
-            p.tiles * p.splits >= 8 * sms ? 8 : 4);
   const int unit = p.splits * blocks;
   p.ctas = sms / unit * unit;
   if (p.ctas == 0) p.ctas = unit;
   const long long most = p.tiles * p.splits;
   if (most < p.ctas) p.ctas = (int)most;
+  // Warps take units in turn, so a CTA works in rounds of a unit per warp; a unit costs its items and
+  // about four more (join, result).  Against units of four items, eight with many tiles: 12 x 16384 x 4096 18.2
+  // and 22.9 us, 7 x 7168 x 2048 7.5 and 8.1, others the same; with a cost of two instead of four 24 x 40960 x
+  // 4096 takes 44.5 instead of 42.3.
+  constexpr int UNIT_COST = 4;
+  const long long mine = (p.tiles + p.ctas / p.splits - 1) / (p.ctas / p.splits);      // tiles of a CTA
+  long long best = 0;
+  for (int parts = 1; parts <= p.slots && parts <= p.split_len; ++parts) {
+    const int len = (p.split_len + parts - 1) / parts;
+    const long long cost = (mine * parts + warps - 1) / warps * (len + UNIT_COST);
+    if (parts > 1 && cost >= best) continue;
+    best = cost;
+    p.cut.nsl = p.split_len;
+    p.cut.len = len;
+    p.cut.parts = (p.split_len + len - 1) / len;
+  }
   return p;
 }
 
