@@ -189,18 +189,17 @@ __device__ __forceinline__ int atom_add_release(int32_t* p, int v) {
 }
 
 // --------------------------------------------------------------------------------- items
-// How the tiles of a phase are cut: units of `len` items, `parts` to a tile (at most `most`), of
-// at least four items unless there is little work.
+// How tiles are cut: into `parts` units of `len` items (the last may have fewer).
 struct Cut {
   int nsl, len, parts;
-  __host__ __device__ __forceinline__ void set(int items, int most, bool little, int least = 4) {
+  __host__ __device__ __forceinline__ void set(int items, int n) {
     nsl = items;
-    len = (nsl + most - 1) / most;
-    if (len < least && !little) len = nsl < least ? nsl : least;
-    parts = (nsl + len - 1) / len;
-    len = (nsl + parts - 1) / parts;
+    len = (items + n - 1) / n;
+    parts = (items + len - 1) / len;
   }
 };
+// What a unit costs beside its items (join, result), in items.
+constexpr int UNIT_COST = 4;
 
 // One unit, as the scheduler writes it down.  BF16 and E4M3 items are boxes of a tensor map (128
 // bytes of column, rows y0.. and y1.. for the two half tiles; per item x or the rows go on by dx,

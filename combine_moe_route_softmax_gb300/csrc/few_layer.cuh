@@ -356,24 +356,34 @@ struct LayerSched {
   }
 };
 
-// Cuts of both phases (one thread).
+// Cuts of both phases (one warp, a lane per number of parts): the least rounds of a unit per worker, times
+// what a unit takes.
 template <int FMT>
-__device__ __forceinline__ void plan_phases(const LayerArgs& a, LayerShared& s) {
-  s.tiles1 = a.I / 16;
-  s.tiles2 = a.H / 32;
-  s.n1 = s.n_entries * s.tiles1;
-  s.n_all = s.n1 + s.n_entries * s.tiles2;
+__device__ __forceinline__ void plan_phases(const LayerArgs& a, LayerShared& s, int lane) {
+  constexpr int WORKERS = warps_of<FMT>() - 1;
+  const int tiles1 = a.I / 16, tiles2 = a.H / 32, workers = gridDim.x * WORKERS;
 #pragma unroll 1
   for (int d = 0; d < 2; ++d) {
     const int k = d ? a.I : a.H;
     const int items = FMT == F_W4 ? w4_slices(k) : FMT == F_BF16 ? k / 64 : k / 128;
+    const int tiles = s.n_entries * (d ? tiles2 : tiles1);
     // Longer units cost less per item, shorter ones level the end of the layer.  One token at the
     // decode sizes (E4M3), 4 / 8 items in phase 1: 86.4 / 82.6 us, then 4 / 8 in phase 2: 82.6 / 83.3;
     // 16 tokens: 719 / 698 and 698 / 689.
-    const int tiles = d ? s.n_all - s.n1 : s.n1, sms = gridDim.x;
-    s.cut[d].set(items, warps_of<FMT>() - 1, tiles <= sms, d == 0 || tiles >= 20 * sms ? 8 : 4);
+    const int longest = d == 0 || tiles >= 20 * (int)gridDim.x ? 8 : 4;
+    const int n = min(lane + 1, min(WORKERS, items)), len = (items + n - 1) / n;
+    const unsigned rounds = (unsigned)((tiles * n + workers - 1) / workers);
+    const unsigned cost = len <= longest || n == min(WORKERS, items) ? rounds * (len + UNIT_COST) * 32 + n : 0xffffffffu;
+    const int best = (int)(__reduce_min_sync(0xffffffffu, cost) & 31u);
+    if (lane == 0) s.cut[d].set(items, best);
   }
-  s.ready = 0;
+  if (lane == 0) {
+    s.tiles1 = tiles1;
+    s.tiles2 = tiles2;
+    s.n1 = s.n_entries * tiles1;
+    s.n_all = s.n1 + s.n_entries * tiles2;
+    s.ready = 0;
+  }
 }
 
 // Phase 1's result for one tile: h of 16 intermediate rows as two BF16 terms or one scaled FP16 term.
@@ -628,8 +638,11 @@ __global__ void __launch_bounds__(warps_of<FMT>() * 32, 1) layer_kernel(const __
   }
   __syncthreads();
   list_entries<WARPS>(a, s);
+  if (warp == 0) {
+    __syncwarp();
+    plan_phases<FMT>(a, s, lane);
+  }
   if (tid == 0) {
-    plan_phases<FMT>(a, s);
     if (!sync) s.go = 1;
     else if (!a.w_router) s.go = barrier_wait(a.ctl, gen, a.dev_status);
   }

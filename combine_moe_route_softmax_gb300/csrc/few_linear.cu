@@ -390,10 +390,9 @@ inline LinearPlan plan_linear(int T, int N, int K, int group, int sms) {
   const long long most = p.tiles * p.splits;
   if (most < p.ctas) p.ctas = (int)most;
   // Warps take units in turn, so a CTA works in rounds of a unit per warp; a unit costs its items and
-  // about four more (join, result).  Against units of four items, eight with many tiles: 12 x 16384 x 4096 18.2
+  // UNIT_COST.  Against units of four items, eight with many tiles: 12 x 16384 x 4096 18.2
   // and 22.9 us, 7 x 7168 x 2048 7.5 and 8.1, others the same; with a cost of two instead of four 24 x 40960 x
   // 4096 takes 44.5 instead of 42.3.
-  constexpr int UNIT_COST = 4;
   const long long mine = (p.tiles + p.ctas / p.splits - 1) / (p.ctas / p.splits);      // tiles of a CTA
   long long best = 0;
   for (int parts = 1; parts <= p.slots && parts <= p.split_len; ++parts) {
@@ -401,9 +400,7 @@ inline LinearPlan plan_linear(int T, int N, int K, int group, int sms) {
     const long long cost = (mine * parts + warps - 1) / warps * (len + UNIT_COST);
     if (parts > 1 && cost >= best) continue;
     best = cost;
-    p.cut.nsl = p.split_len;
-    p.cut.len = len;
-    p.cut.parts = (p.split_len + len - 1) / len;
+    p.cut.set(p.split_len, parts);
   }
   return p;
 }
