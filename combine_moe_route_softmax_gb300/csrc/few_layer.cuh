@@ -273,8 +273,9 @@ struct LayerSched {
   int q, pending, run, ready, want;
 
   __device__ __forceinline__ bool next(int lane, int& t, int& n) {
-    // runs of a few (smaller) tiles in phase 2 as long as there are plenty: a look at the queue takes
-    // about as long as an SM needs for 32 KB (16 tokens, E4M3 as above: 685 us, 699 with two at most)
+    // runs of a few (smaller) tiles in phase 2 as long as there are plenty, about 32 items of small ones: a
+    // look at the queue takes about as long as an SM needs for 32 KB (16 tokens, E4M3 as above: 685 us,
+    // 699 with two at most; 32 tokens in 4 bits, H = 1024, I = 512, E = 128: 67.7, 74.4 with four)
     if (q < s.own) {
       t = blockIdx.x + q * gridDim.x;
       n = 1;
@@ -284,7 +285,7 @@ struct LayerSched {
     }
     if (++q >= s.own) {
       const int left = (s.n_all - t) / (int)gridDim.x;
-      run = t < s.n1 || left < 3 ? 1 : left < 20 ? 2 : 4;
+      run = t < s.n1 || left < 3 ? 1 : min(left / 2, max(left < 20 ? 2 : 4, 32 / s.cut[1].nsl));
       if (lane == 0) pending = (int)(s.own * gridDim.x + atomicAdd(&a.ctl[2], (unsigned)run));
     }
     n = min(n, s.n_all - t);
