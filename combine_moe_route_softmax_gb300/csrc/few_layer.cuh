@@ -28,7 +28,7 @@
 //     streaming at the copy bandwidth, 8 from the average warp's last unit to the last combine, launch
 //   BF16, 5 tokens at H = 2048, I = 1408, E = 64, top-8: 84 us, 5.9 TB/s
 //   4 bits, one token at the E4M3 sizes: 72 us, 2.9 TB/s; 32 tokens at the BF16 sizes, groups of 32 with
-//     zero points: 131 us, 2.5 TB/s -- bound by unpacking (few.cuh)
+//     zero points: 126 us, 2.6 TB/s -- bound by unpacking (few.cuh)
 //   BF16, one token at H = 256, I = 512, E = 8, top-2: 18 us, latency throughout
 // An L2 prefetch of the shared expert while the routing is found out changed none of these.
 //

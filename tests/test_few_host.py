@@ -149,3 +149,11 @@ def test_reference_pack_keeps_values(group, zeros):
         o = ((r % 8) * ng + kk // group) * 2 + r // 8
         assert b[2048:2048 + 32 * ng].view(np.uint16)[o] == s[k // group, n]
         assert z is None or b[2048 + 32 * ng + o] == z[k // group, n]
+
+
+@pytest.mark.parametrize("N,K", [(16, 128), (320, 7168), (4096, 2048), (40960, 4096), (1000, 16384)])
+def test_linear_workspace_serves_fewer_rows(lib, N, K):
+    """A workspace made for T rows is enough for any fewer."""
+    sizes = [lib.moe_linear_w4_workspace_bytes(t, N, K) for t in range(130)]
+    assert all(b and b % 256 == 0 for b in sizes)
+    assert all(b >= a for a, b in zip(sizes, sizes[1:]))
