@@ -32,7 +32,7 @@ inline bool plan_few(const moe_few_desc_t* d, FewPlan* p) {
   p->off_xunit = o;  o = align256(o + 4 * (size_t)d->T);
   p->off_hexp = o;   o = align256(o + (half ? slots * exp_pitch(d->I) : 0));
   p->off_hhi = o;    o = align256(o + 2 * slots * (half ? half_pitch(d->I) : d->I));
-  p->off_hlo = o;    o = align256(o + (half ? 0 : 2 * slots * d->I));
+  p->off_hlo = o;    o = align256(o + 2 * slots * (half ? half_pitch(d->I) : d->I));
   p->off_y = o;      o = align256(o + 4 * slots * d->H);
   p->total = o;
   return true;

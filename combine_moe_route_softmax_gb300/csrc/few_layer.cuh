@@ -32,10 +32,10 @@
 //   BF16, one token at H = 256, I = 512, E = 8, top-2: 18 us, latency throughout
 // An L2 prefetch of the shared expert while the routing is found out changed none of these.
 //
-// Roundings of h: one FP16 term keeps 11 bits, an error of 1.4e-4 of the output beside the 1.7e-3
-// of its BF16 rounding.  One BF16 term would add 1.2e-3, so BF16 layers keep two, h = hi + lo (16
-// bits): side by side as two columns of one tensor instruction up to 4 tokens, as two
-// instructions above.
+// Roundings of h: one FP16 term keeps 11 bits, an error of 1.4e-4 of the output that moves one BF16
+// output in thirty to its neighbour (9e-4 of the outputs' size); one BF16 term 1.2e-3.  So h is
+// kept in two terms, h = hi + lo (BF16: 16 bits, FP16: 22): side by side as two columns of one tensor
+// instruction up to 4 columns of an expert, as two instructions above.
 #pragma once
 
 #include "few.cuh"
@@ -89,7 +89,7 @@ struct LayerArgs {
   uint16_t* x16;               // [T, half_pitch(H)] FP16
   float* x_unit;               // [T] what 1 in x16 stands for
   uint16_t* h_hi;              // [T*K + T, I]; FP16: rows of half_pitch(I)
-  int h_lo;                    // BF16: elements from h_hi to the second terms
+  int h_lo;                    // elements from h_hi to the second terms
   uint8_t* h_exp;              // [T*K + T, ex_pitch] exponent of each 16 values of h (FP16)
   float* y;                    // [T*K + T, H]
 };
@@ -391,7 +391,7 @@ __device__ __forceinline__ void plan_phases(const LayerArgs& a, LayerShared& s, 
   }
 }
 
-// Phase 1's result for one tile: h of 16 intermediate rows as two BF16 terms or one scaled FP16 term.
+// Phase 1's result for one tile: h of 16 intermediate rows as two BF16 or two scaled FP16 terms.
 template <bool HALF, int NT>
 __device__ __forceinline__ void store_h(const LayerArgs& a, const LayerShared& s, const Sums<NT>& sums, int entry,
                                         int tile, int lane) {
@@ -431,11 +431,17 @@ __device__ __forceinline__ void store_h(const LayerArgs& a, const LayerShared& s
       for (int i = 0; i < 2; ++i) {
         const size_t o = (size_t)slot * (HALF ? half_pitch(a.I) : a.I) + tile * 16 + g + i * 8;
         if (HALF) {
-          a.h_hi[o] = half_bits(h[i] * sc);
-          // the last tile also clears the row's end
+          const float v = h[i] * sc;
+          const uint16_t hi = half_bits(v);
+          a.h_hi[o] = hi;
+          a.h_hi[o + a.h_lo] = (hi & 0x7fffu) >= 0x7c00u ? 0 : half_bits(v - __half2float(__ushort_as_half(hi)));   // inf, NaN: hi alone
+          // the last tile also clears the rows' ends
           if (tile == s.tiles1 - 1 && i == 0)
-            for (int z = a.I + g * 8; z < half_pitch(a.I); z += 64)
-              *reinterpret_cast<uint4*>(a.h_hi + (size_t)slot * half_pitch(a.I) + z) = make_uint4(0, 0, 0, 0);
+            for (int z = a.I + g * 8; z < half_pitch(a.I); z += 64) {
+              uint16_t* p = a.h_hi + (size_t)slot * half_pitch(a.I) + z;
+              *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(p + a.h_lo) = make_uint4(0, 0, 0, 0);
+            }
         } else {
           const uint16_t hi = f32_to_bf16(h[i]);
           a.h_hi[o] = hi;
@@ -445,13 +451,13 @@ __device__ __forceinline__ void store_h(const LayerArgs& a, const LayerShared& s
     }
 }
 
-// Phase 2's result for one (row tile, expert): y rows.  BF16: up to 4 columns come as hi and lo
-// columns of one group (hi in columns 0-3, lanes t = 0, 1; lo in 4-7, t = 2, 3).
+// Phase 2's result for one (row tile, expert): y rows.  Up to 4 columns come as hi and lo columns of
+// one group (hi in columns 0-3, lanes t = 0, 1; lo in 4-7, t = 2, 3).
 template <bool HALF, int NT>
 __device__ __forceinline__ void store_y(const LayerArgs& a, const LayerShared& s, Sums<NT>& sums, int entry, int tile,
                                         int lane) {
   const int g = lane >> 2, t = lane & 3, nc = s.ncols[entry], c0 = s.first[entry];
-  if (!HALF && nc <= 4) {
+  if (nc <= 4) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -548,7 +554,7 @@ __device__ __forceinline__ void do_unit(const LayerArgs& a, LayerShared& s, Laye
   int top[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    const bool pairs = !HALF && down && PASSES == 1;     // hi and lo as columns of one group
+    const bool pairs = down && PASSES == 1;              // hi and lo as columns of one group
     const int c = pairs ? (g & 3) : i * 8 + g;
     const int at = c0 + (c < nc ? c : 0);                // no such column: the first one again
     const int slot = s.cols[at];
@@ -688,12 +694,10 @@ __global__ void __launch_bounds__(warps_of<FMT>() * 32, 1) layer_kernel(const __
         __threadfence_block();
         __syncwarp();
       }
-      // BF16, phase 2: hi and lo side by side in one group of 8 up to 4 columns, else one after the other
-      if (!HALF && down && nc > 4) {
-        if constexpr (!HALF) {
-          if (nc > 8) do_unit<FMT, GROUP, 2, 2>(a, s, in, down, parts, slots, stride);
-          else do_unit<FMT, GROUP, 1, 2>(a, s, in, down, parts, slots, stride);
-        }
+      // phase 2: hi and lo side by side in one group of 8 up to 4 columns, else one after the other
+      if (down && nc > 4) {
+        if (nc > 8) do_unit<FMT, GROUP, 2, 2>(a, s, in, down, parts, slots, stride);
+        else do_unit<FMT, GROUP, 1, 2>(a, s, in, down, parts, slots, stride);
       } else if (nc > 8) {
         do_unit<FMT, GROUP, 2, 1>(a, s, in, down, parts, slots, stride);
       } else {

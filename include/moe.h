@@ -557,7 +557,7 @@ moe_status_t moe_route_hidden(const uint16_t* x, int T, int H, const uint16_t* w
 /* The whole layer for T <= MOE_FEW_MAX_TOKENS tokens in one cooperative launch: (router ->)
  * gate/up + SwiGLU -> down -> combine.  It computes moe_layer_forward's layer with fewer
  * roundings: activations stay at 16 bits with every weight format (no FP8 activations), h is
- * kept to 16 bits of mantissa (BF16 weights) or 11 (FP16, scaled, with the other formats) and
+ * kept in two 16-bit terms (16 bits of mantissa with BF16 weights, 22 with the other formats) and
  * the expert rows in float32, so
  *     out[t] = bf16_rn( sum over ascending k of w_tk * (W2_e silu(g) u), float32 from +0,
  *                       the shared expert's row last )
