@@ -411,12 +411,11 @@ __device__ __forceinline__ void store_h(const LayerArgs& a, const LayerShared& s
       }
       float sc = 1.0f;
       if (HALF) {
+        // infinities and NaN count as the largest finite value: their block sets the slot's scale, so phase 2
+        // takes them times 1, never times a power of two that FP16 has no room for (infinity times 0)
         uint32_t most = 0;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t b = __float_as_uint(h[i]) & 0x7fffffffu;
-          if (b < 0x7f800000u) most = max(most, b);
-        }
+        for (int i = 0; i < 2; ++i) most = max(most, min(__float_as_uint(h[i]) & 0x7fffffffu, 0x7f7fffffu));
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
         sc = to_half_scale(most);

@@ -1,0 +1,54 @@
+"""The few-token operators on the GPU at values and calls where they can go wrong: infinities, masked
+experts, NaN, zero points of a whole byte, streams, waits that run out."""
+import numpy as np
+import pytest
+import torch
+
+import combine_moe_route_softmax_gb300 as moe
+import few_ref as ref
+from gpu_helpers import bits
+from test_gpu_few import Weights, gen, normal, random_routing, w4_random
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------- infinite intermediate values
+def infinite_h_layer(dtype):
+    """An E4M3 or 4-bit layer whose h is infinite in row 0 for tokens with x[0] = 1 and 1 in row 16 for those
+    with x[128] = 1 (silu(40) * 0.025 to within BF16); the other rows of h are 0."""
+    H, I = 256, 128
+    up, down = 40.0, 0.025
+    if dtype == "e4m3":
+        code = lambda v: torch.tensor(v, device="cuda").to(torch.float8_e4m3fn).view(torch.uint8)
+        w13 = torch.zeros(1, 2 * I, H, dtype=torch.uint8, device="cuda")
+        w13[0, 0, 0] = w13[0, I, 0] = w13[0, 16, 128] = w13[0, I + 16, 128] = code(1.0)
+        s13 = torch.tensor([[[2.0 ** 70, up], [2.0 ** 70, down]]], device="cuda")
+        w2 = torch.zeros(1, H, I, dtype=torch.uint8, device="cuda")
+        w2[0, :, 0] = w2[0, :, 16] = code(1.0)
+        kw = dict(w13=w13, w13_scales=s13, w2=w2, w2_scales=torch.ones(1, 2, 1, device="cuda"))
+        return moe.MoeLayerFew(4, H, I, 1, 1, moe.MOE_E4M3, **kw), H
+    def packed(n, k, entries):
+        q = torch.full((1, n, k // 2), 0x88, dtype=torch.uint8, device="cuda")
+        s = torch.ones(1, k // 128, n, dtype=torch.bfloat16, device="cuda")
+        for r, c, v in entries:
+            q[0, r, c // 2] = 0x89                  # 1 in the even column
+            s[0, c // 128, r] = v
+        return moe.moe_pack_w4(q, s)
+    w13 = packed(2 * I, H, [(0, 0, 2.0 ** 70), (I, 0, 2.0 ** 70), (16, 128, up), (I + 16, 128, down)])
+    w2 = packed(H, I, [(r, c, 1.0) for r in range(H) for c in (0, 16)])
+    return moe.MoeLayerFew(4, H, I, 1, 1, moe.MOE_W4, w13=w13, w2=w2), H
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "w4"])
+def test_layer_few_infinite_beside_finite(dtype):
+    """h infinite in a block of small values, beside a block of larger ones: infinity, not NaN; tokens without
+    it have their values."""
+    gen(0)
+    layer, H = infinite_h_layer(dtype)
+    x = torch.zeros(4, H, dtype=torch.bfloat16, device="cuda")
+    x[0, 0] = x[1, 128] = 1.0
+    x[2, 0] = x[2, 128] = 1.0
+    idx = torch.zeros(4, 1, dtype=torch.int32, device="cuda")
+    out, _, _ = layer.forward(x, topk_idx=idx, topk_w=torch.ones(4, 1, device="cuda"))
+    assert torch.isposinf(out[0]).all() and torch.isposinf(out[2]).all()
+    assert ((out[1].float() - 1).abs() <= 2.0 ** -6).all() and (out[3] == 0).all()
