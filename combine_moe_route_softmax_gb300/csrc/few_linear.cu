@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(256) pack_w4_kernel(const uint8_t* __restrict_
       if (row < N && kgi < kg) {
         const long long o = (m * kg + kgi) * N + row;
         sv |= (uint32_t)sc[o] << (16 * h);
-        if (zp) zv |= (uint32_t)(zp[o] & 15) << (8 * h);
+        if (zp) zv |= (uint32_t)zp[o] << (8 * h);
       }
     }
     osc[gg * ng + gi] = sv;

@@ -501,7 +501,7 @@ moe_status_t moe_layer_forward(const moe_layer_desc_t* d, const moe_layer_weight
 
 /* ------------------------------------------------------------------- 4-bit weights (W4)
  * value(n, k) = (code(n, k) - zero(k / group, n)) * scale(k / group, n), codes 0..15,
- * group 32, 64 or 128; zero is 8 everywhere when there is no zero tensor.
+ * group 32, 64 or 128; zero is any byte, and 8 everywhere when there is no zero tensor.
  *
  * moe_quantize_weight_w4: BF16 w [mats, rows, cols] -> codes q [mats, rows, cols/2] (column 2i
  * in the low nibble of byte i), scales BF16 [mats, cols/group, rows], zeros (nullable) uint8

@@ -52,3 +52,35 @@ def test_layer_few_infinite_beside_finite(dtype):
     out, _, _ = layer.forward(x, topk_idx=idx, topk_w=torch.ones(4, 1, device="cuda"))
     assert torch.isposinf(out[0]).all() and torch.isposinf(out[2]).all()
     assert ((out[1].float() - 1).abs() <= 2.0 ** -6).all() and (out[3] == 0).all()
+
+
+
+# ------------------------------------------------------------------------ zero points of a whole byte
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_w4_zero_points_above_15(group):
+    """A zero point is any byte (formats that store z - 1 have 16): kept by the packing, used by the product
+    and the layer."""
+    g = gen(group)
+    N, K = 96, 384
+    q, s, _ = w4_random(g, 1, N, K, group, False)
+    z = torch.randint(0, 256, s.shape, generator=g, device="cuda", dtype=torch.uint8)
+    z[:, :, ::3] = 16
+    p = moe.moe_pack_w4(q, s, z)
+    assert np.array_equal(p.data[0].cpu().numpy(), ref.pack_w4(q[0].cpu().numpy(), bits(s[0]), z[0].cpu().numpy()))
+    for T in (1, 5, 20):
+        x = normal(g, T, K)
+        y = moe.moe_linear_w4(x, p, out_dtype=torch.float32)
+        want, err = ref.linear(x, ref.w4_values(q[0], s[0], z[0]))
+        assert ref.close(y, want, err) <= 1
+    H, I, E = 256, 128, 3
+    val, kw = {}, {}
+    for name, n, k in (("w13", 2 * I, H), ("w2", H, I)):
+        q, s, _ = w4_random(g, E, n, k, group, False)
+        z = torch.randint(0, 40, s.shape, generator=g, device="cuda", dtype=torch.uint8)
+        kw[name] = moe.moe_pack_w4(q, s, z)
+        val[name] = lambda e, q=q, s=s, z=z: ref.w4_values(q[e], s[e], z[e])
+    x = normal(g, 6, H)
+    idx, wt = random_routing(g, 6, 2, E, 0.0)
+    out, _, _ = moe.MoeLayerFew(6, H, I, E, 2, moe.MOE_W4, **kw).forward(x, topk_idx=idx, topk_w=wt)
+    want, err = ref.layer(x, idx, wt, val["w13"], val["w2"], None, True)
+    assert ref.close(out, want, err) <= 1
