@@ -28,6 +28,11 @@ __device__ __forceinline__ void join_pair(float& s, float& c, float s2, float c2
   c = __fadd_rn(c, c2);
   add_pair(s, c, s2);
 }
+// The pair's value.  An infinite or NaN sum (an expert masked by a bias of -infinity) is s alone: it is the plain
+// sum then, and what the error-free addition left in c is NaN.
+__device__ __forceinline__ float pair_value(float s, float c) {
+  return (__float_as_uint(s) & 0x7fffffffu) < 0x7f800000u ? __fadd_rn(s, c) : s;
+}
 
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -138,7 +143,7 @@ __device__ __forceinline__ void router_logits_mma(const uint16_t* __restrict__ x
       for (int j = 1; j < NW; ++j) join_pair(rs, rc, scratch[j * 128 + i].x, scratch[j * 128 + i].y);
       if (tok < T && e < E) {
         if (bias) add_pair(rs, rc, __ldg(bias + e));
-        logits[(size_t)tok * E + e] = __fadd_rn(rs, rc);
+        logits[(size_t)tok * E + e] = pair_value(rs, rc);
       }
     }
   }
@@ -178,7 +183,7 @@ __device__ __forceinline__ void router_logits(const uint16_t* x, const uint16_t*
     }
     if (mine < per && task < tasks && (lane & 7) == 0 && j < T) {
       if (bias) add_pair(s, c, __ldg(bias + e));
-      logits[(size_t)j * E + e] = __fadd_rn(s, c);
+      logits[(size_t)j * E + e] = pair_value(s, c);
     }
   }
 }

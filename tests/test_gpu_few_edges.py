@@ -84,3 +84,62 @@ def test_w4_zero_points_above_15(group):
     out, _, _ = moe.MoeLayerFew(6, H, I, E, 2, moe.MOE_W4, **kw).forward(x, topk_idx=idx, topk_w=wt)
     want, err = ref.layer(x, idx, wt, val["w13"], val["w2"], None, True)
     assert ref.close(out, want, err) <= 1
+
+
+# ----------------------------------------------------------------------------- masked experts, NaN
+@pytest.mark.parametrize("T,H,E,K", [(1, 256, 12, 4), (4, 2048, 64, 8), (5, 640, 40, 3), (32, 1024, 300, 8)])
+def test_route_hidden_masked_experts(T, H, E, K):
+    """A bias of -infinity takes an expert out, one of +infinity puts it first; the logits are what a plain sum
+    gives, and the other experts' bits do not change."""
+    g = gen(T + E)
+    x, w = normal(g, T, H), normal(g, E, H, std=H ** -0.5)
+    b = torch.randn(E, generator=g, device="cuda") * 0.1
+    _, _, plain = moe.moe_route_hidden(x, w, K, bias=b)
+    masked = torch.arange(E, device="cuda") % 3 == 1
+    b2 = torch.where(masked, float("-inf"), b)
+    idx, wt, logits = moe.moe_route_hidden(x, w, K, bias=b2)
+    assert torch.equal(logits, torch.where(masked, float("-inf"), plain))
+    oi, ow, _ = ref.route(x, w, b2, K)
+    assert torch.equal(idx, oi) and not masked[idx.long()].any()
+    assert ((wt.double() - ow).abs() <= 2.0 ** -20 * ow).all()
+    b3 = b.clone()
+    b3[E - 1] = float("inf")
+    idx, _, logits = moe.moe_route_hidden(x, w, K, bias=b3)
+    assert torch.isposinf(logits[:, E - 1]).all() and (idx[:, 0] == E - 1).all()
+    assert torch.equal(logits[:, :E - 1], plain[:, :E - 1])
+
+
+@pytest.mark.parametrize("T", [1, 3, 9])
+def test_route_hidden_infinite_and_nan_inputs(T):
+    """An infinite or NaN element of x: what a plain sum of the products gives, in that token alone."""
+    g = gen(T)
+    H, E, K = 512, 24, 4
+    x, w = normal(g, T, H), normal(g, E, H, std=H ** -0.5)
+    w[w == 0] = 0.01
+    _, _, plain = moe.moe_route_hidden(x, w, K)
+    for v in (float("inf"), float("-inf"), float("nan")):
+        y = x.clone()
+        y[T - 1, 77] = v
+        _, _, logits = moe.moe_route_hidden(y, w, K)
+        want = y.double() @ w.double().T
+        assert torch.equal(logits[:T - 1], plain[:T - 1])
+        assert torch.equal(logits[T - 1].isnan(), want[T - 1].isnan())
+        if v == v:
+            assert torch.equal(logits[T - 1], want[T - 1].float())
+
+
+def test_layer_few_masked_experts():
+    """The same mask inside the layer: the masked experts' weights are not read."""
+    g = gen(21)
+    T, H, I, E, K = 6, 256, 128, 9, 3
+    w = Weights(g, "bf16", H, I, E, True)
+    wr = normal(g, E, H, std=H ** -0.5)
+    b = torch.zeros(E, device="cuda")
+    b[::2] = float("-inf")
+    w.kw["w13"][::2] = float("nan")
+    x = normal(g, T, H)
+    out, idx, wt = moe.MoeLayerFew(T, H, I, E, K, w_router=wr, router_bias=b, **w.kw).forward(x)
+    oi, ow, _ = ref.route(x, wr, b, K)
+    assert torch.equal(idx, oi) and ((wt.double() - ow).abs() <= 2.0 ** -20 * ow).all()
+    want, err = w.want(x, idx, wt)
+    assert ref.close(out, want, err) <= 1
