@@ -188,15 +188,25 @@ __device__ __forceinline__ void router_logits(const uint16_t* x, const uint16_t*
   }
 }
 
+// A logit's place in the float order of route_key, from 1 on (0: no logit): that order has a value to spare, as -0 is
+// keyed as +0.
+__device__ __forceinline__ uint32_t logit_place(float v) {
+  const uint32_t o = (uint32_t)(route_key(v, 0) >> 32);
+  return o & 0x80000000u ? o : o + 1;
+}
+__device__ __forceinline__ float place_logit(uint32_t p) {
+  return key_logit((unsigned long long)(p & 0x80000000u ? p : p - 1) << 32);
+}
+
 // One warp: the selection of route_topk_warp (its order, ties and weights, bit for bit) by warp-wide
 // integer reductions; `load` reads a logit.
 template <int EPL, class Load>
 __device__ __forceinline__ void select_topk_warp(Load load, int E, int K, int lane, int& my_id, float& my_w) {
-  uint32_t key[EPL];             // the logit's place in float order, 0 when taken
+  uint32_t key[EPL];             // 0 when taken
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     const int e = lane + 32 * j;
-    key[j] = e < E ? (uint32_t)(route_key(load(e), e) >> 32) : 0u;
+    key[j] = e < E ? logit_place(load(e)) : 0u;
   }
   my_id = -1;
   float my_logit = 0.0f, top = 0.0f;
@@ -214,9 +224,9 @@ __device__ __forceinline__ void select_topk_warp(Load load, int E, int K, int la
 #pragma unroll
     for (int j = 0; j < EPL; ++j)
       if (lane + 32 * j == (int)id) key[j] = 0u;
-    const float v = key_logit((unsigned long long)m << 32);
+    const float v = place_logit(m);
     if (lane == k) {
-      my_id = m ? (int)id : -1;   // nothing left to choose (a NaN keyed as an empty place)
+      my_id = (int)id;
       my_logit = v;
     }
     if (k == 0) top = v;

@@ -143,3 +143,28 @@ def test_layer_few_masked_experts():
     assert torch.equal(idx, oi) and ((wt.double() - ow).abs() <= 2.0 ** -20 * ow).all()
     want, err = w.want(x, idx, wt)
     assert ref.close(out, want, err) <= 1
+
+
+@pytest.mark.parametrize("E,K", [(6, 6), (40, 5), (300, 32)])
+def test_layer_few_selects_as_route_topk_does(E, K):
+    """Given logits with infinities, zeros of both signs and every kind of NaN, the layer's choice is
+    moe_route_topk's: ids, and weights bit for bit (NaN or not)."""
+    g = gen(E)
+    T, H, I = 8, 128, 128
+    logits = torch.randn(T, E, generator=g, device="cuda")
+    logits[1, ::2] = float("-inf")
+    logits[2] = float("-inf")
+    logits[3, 1::2] = 0.0
+    logits[3, ::2] = -0.0
+    nan = torch.tensor([0x7fc00000, 0x7f800001, -1, -2, -0x400000], dtype=torch.int32, device="cuda").view(torch.float32)
+    logits[4, :5] = nan
+    logits[5] = nan[2]                     # all bits set: the lowest place in the order
+    logits[6, ::3] = nan[2]
+    logits[6, 1::3] = nan[3]
+    logits[7, ::2] = nan[4]
+    w13 = torch.zeros(E, 2 * I, H, dtype=torch.bfloat16, device="cuda")
+    w2 = torch.zeros(E, H, I, dtype=torch.bfloat16, device="cuda")
+    _, idx, wt = moe.MoeLayerFew(T, H, I, E, K, w13=w13, w2=w2).forward(normal(g, T, H), logits=logits)
+    oi, ow = moe.moe_route_topk(logits, K)
+    assert torch.equal(idx, oi)
+    assert torch.equal(wt.isnan(), ow.isnan()) and torch.equal(wt[~wt.isnan()], ow[~ow.isnan()])
