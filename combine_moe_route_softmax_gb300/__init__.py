@@ -471,6 +471,17 @@ class MoeLayer:
 
 
 # ------------------------------------------------------------------------ a few tokens
+# These calls' workspaces have to be zero at first use, so what a call makes itself (a workspace, its outputs)
+# is made on the stream it runs on: with stream=s a call is what it is inside torch.cuda.stream(s).
+# As with any tensor, what was made on another stream (inputs, weights, a workspace or layer object) has to
+# be finished there first.
+def _run_on(stream, f, *args, **kw):
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return f(*args, **kw)
+
+
 class W4Packed:
     """4-bit weights in the kernels' order (moe_pack_w4): `mats` matrices of N rows, K columns,
     scales per `group` columns, zero points or not; data uint8 [mats, bytes].  [i] is one
@@ -488,6 +499,8 @@ class W4Packed:
 def moe_quantize_weight_w4(w, group, zeros=False, stream=None):
     """w BF16 [..., rows, cols] -> (codes uint8 [..., rows, cols/2], scales BF16 [..., cols/group,
     rows], zero points uint8 like scales, or None)."""
+    if stream is not None:
+        return _run_on(stream, moe_quantize_weight_w4, w, group, zeros)
     _dev(w)
     rows, cols = w.shape[-2:]
     lead = w.shape[:-2]
@@ -496,13 +509,15 @@ def moe_quantize_weight_w4(w, group, zeros=False, stream=None):
     s = torch.empty(*lead, cols // group, rows, dtype=torch.bfloat16, device=w.device)
     z = torch.empty(*lead, cols // group, rows, dtype=torch.uint8, device=w.device) if zeros else None
     _check("moe_quantize_weight_w4", lib().moe_quantize_weight_w4(_ptr(w), mats, rows, cols, group, _ptr(q), _ptr(s),
-                                                                  _ptr(z), _stream(stream)))
+                                                                  _ptr(z), _stream(None)))
     return q, s, z
 
 
 def moe_pack_w4(q, scales, zeros=None, stream=None):
     """Codes [..., N, K/2], scales BF16 [..., K/group, N] and zero points (uint8, like scales, or
     None) -> W4Packed."""
+    if stream is not None:
+        return _run_on(stream, moe_pack_w4, q, scales, zeros)
     _dev(q)
     _dev(scales)
     N, K = q.shape[-2], 2 * q.shape[-1]
@@ -518,7 +533,7 @@ def moe_pack_w4(q, scales, zeros=None, stream=None):
     nbytes = lib().moe_w4_packed_bytes(N, K, group, int(zeros is not None))
     data = torch.empty(mats, nbytes, dtype=torch.uint8, device=q.device)
     _check("moe_pack_w4", lib().moe_pack_w4(_ptr(q), _ptr(scales), _ptr(zeros), mats, N, K, group, _ptr(data),
-                                            _stream(stream)))
+                                            _stream(None)))
     return W4Packed(data, mats, N, K, group, zeros is not None)
 
 
@@ -538,6 +553,8 @@ def moe_linear_w4(x, w, bias=None, out=None, out_dtype=torch.bfloat16, ws=None, 
     """x BF16 [T, K] (rows may be strided), w a W4Packed matrix -> out [T, N] = x w^T (+ bias float32
     [N]) in BF16 or float32.  ws: a workspace kept from moe_linear_w4_workspace (made here
     otherwise); calls that may overlap need one each."""
+    if stream is not None:
+        return _run_on(stream, moe_linear_w4, x, w, bias, out, out_dtype, ws, dev_status)
     T, K = x.shape
     N = w.N
     assert x.is_cuda and x.dtype is torch.bfloat16 and x.stride(1) == 1, "x is BF16 [T, K] on the GPU, rows dense"
@@ -555,7 +572,7 @@ def moe_linear_w4(x, w, bias=None, out=None, out_dtype=torch.bfloat16, ws=None, 
     _check("moe_linear_w4", (_lib or lib()).moe_linear_w4(
         x.data_ptr(), T, K, x.stride(0) if T > 1 else K, w.data.data_ptr(), N, w.group, w.zeros,
         None if bias is None else bias.data_ptr(), out.data_ptr(), out_dtype is torch.float32, os, ws.data_ptr(),
-        ws.numel(), None if dev_status is None else dev_status.data_ptr(), _stream(stream)))
+        ws.numel(), None if dev_status is None else dev_status.data_ptr(), _stream(None)))
     return out
 
 
@@ -568,6 +585,8 @@ def moe_route_hidden(x, w_router, K, bias=None, num_tokens=None, logits=None, to
                      stream=None):
     """The router from hidden states: x BF16 [T, H], w_router BF16 [E, H] -> (topk_idx int32 [T, K],
     topk_w float32 [T, K], logits float32 [T, E])."""
+    if stream is not None:
+        return _run_on(stream, moe_route_hidden, x, w_router, K, bias, num_tokens, logits, topk_idx, topk_w, ws)
     assert x.is_cuda and x.is_contiguous() and w_router.is_contiguous(), "expected contiguous CUDA tensors"
     assert x.dtype is torch.bfloat16 and w_router.dtype is torch.bfloat16
     T, H = x.shape
@@ -582,7 +601,7 @@ def moe_route_hidden(x, w_router, K, bias=None, num_tokens=None, logits=None, to
         ws = moe_route_hidden_workspace(device=x.device)
     _check("moe_route_hidden", (_lib or lib()).moe_route_hidden(
         x.data_ptr(), T, H, w_router.data_ptr(), _ptr(bias), E, K, _ptr(num_tokens), logits.data_ptr(),
-        topk_idx.data_ptr(), topk_w.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
+        topk_idx.data_ptr(), topk_w.data_ptr(), ws.data_ptr(), ws.numel(), _stream(None)))
     return topk_idx, topk_w, logits
 
 
@@ -621,6 +640,8 @@ class MoeLayerFew:
                 stream=None):
         """x BF16 [t, H], t <= T -> (out [t, H], topk_idx, topk_w).  topk_idx / topk_w are inputs
         unless the layer routes (w_router, or logits [t, E])."""
+        if stream is not None:
+            return _run_on(stream, self.forward, x, out, topk_idx, topk_w, logits, num_tokens, dev_status)
         assert x.is_cuda and x.is_contiguous() and x.dtype is torch.bfloat16, "x is BF16, contiguous, on the GPU"
         t, H = x.shape
         d = self._descs.get(t)
@@ -638,5 +659,5 @@ class MoeLayerFew:
             topk_w = torch.empty(t, d.K, dtype=torch.float32, device=x.device)
         _check("moe_layer_few", (_lib or lib()).moe_layer_few(
             ctypes.byref(d), self._w, x.data_ptr(), _ptr(logits), _ptr(num_tokens), topk_idx.data_ptr(),
-            topk_w.data_ptr(), out.data_ptr(), *self._ws, _ptr(dev_status), _stream(stream)))
+            topk_w.data_ptr(), out.data_ptr(), *self._ws, _ptr(dev_status), _stream(None)))
         return out, topk_idx, topk_w

@@ -168,3 +168,33 @@ def test_layer_few_selects_as_route_topk_does(E, K):
     oi, ow = moe.moe_route_topk(logits, K)
     assert torch.equal(idx, oi)
     assert torch.equal(wt.isnan(), ow.isnan()) and torch.equal(wt[~wt.isnan()], ow[~ow.isnan()])
+
+
+# ------------------------------------------------------------------------------------------- streams
+@pytest.mark.parametrize("raw", [False, True], ids=["object", "handle"])
+def test_few_calls_on_another_stream_than_the_current(raw):
+    """stream=s while the current stream is busy: nothing of the call waits for it, and the workspace that the call
+    makes is zero when its kernel starts."""
+    g = gen(17)
+    T, H, E, K, N, KL = 20, 1024, 64, 8, 160, 7168       # the product's K is shared between CTAs
+    x, w = normal(g, T, H), normal(g, E, H, std=H ** -0.5)
+    q, s, z = w4_random(g, 1, N, KL, 32, True)
+    p, xl = moe.moe_pack_w4(q, s, z), normal(g, T, KL)
+    lw = Weights(g, "e4m3", 256, 128, 6, True)
+    layer = moe.MoeLayerFew(T, 256, 128, 6, 2, w_router=normal(g, 6, 256), **lw.kw)
+    xs = normal(g, T, 256)
+
+    def calls(**k):
+        return (*moe.moe_route_hidden(x, w, K, **k), moe.moe_linear_w4(xl, p, **k), *layer.forward(xs, **k),
+                *[t for t in moe.moe_quantize_weight_w4(w, 32, True, **k)])
+    want = calls()
+    side = torch.cuda.Stream()
+    for stream in (side, torch.cuda.current_stream()):
+        with torch.cuda.stream(stream):                    # memory that a workspace is likely to get
+            junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in (256, 4096, 1 << 20, 1 << 22) * 3]
+            del junk
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    got = calls(stream=side.cuda_stream if raw else side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
