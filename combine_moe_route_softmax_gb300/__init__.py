@@ -482,18 +482,51 @@ def _run_on(stream, f, *args, **kw):
         return f(*args, **kw)
 
 
+# The kernels read what they are given by its address: type, size and layout are compared here.
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _need_tensor(t, dtype, shape, what):
+    """t: a contiguous GPU tensor of dtype and shape (one dimension: that many values), an address, or None."""
+    if t is None or isinstance(t, int):
+        return
+    fits = t.shape == shape if len(shape) > 1 else t.numel() == shape[0]
+    if not (fits and t.dtype is dtype and t.is_cuda and t.is_contiguous()):
+        raise ValueError(f"{what}: expected a contiguous {dtype} GPU tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _need_word(t, what):
+    """t: an int32 on the GPU, an address, or None."""
+    if t is None or isinstance(t, int):
+        return
+    if not (t.dtype is torch.int32 and t.is_cuda and t.numel() >= 1):
+        raise ValueError(f"{what} is an int32 on the GPU")
+
+
+def _need_ws(ws):
+    if not (ws.is_cuda and ws.is_contiguous()):
+        raise ValueError("a workspace is a contiguous GPU tensor")
+
+
 class W4Packed:
     """4-bit weights in the kernels' order (moe_pack_w4): `mats` matrices of N rows, K columns,
     scales per `group` columns, zero points or not; data uint8 [mats, bytes].  [i] is one
     matrix of a stack."""
 
     def __init__(self, data, mats, N, K, group, zeros):
+        if data is not None:
+            nbytes = lib().moe_w4_packed_bytes(N, K, group, int(zeros))
+            _need(nbytes > 0, "no such packed matrix: N, K or group")
+            _need_tensor(data, torch.uint8, (mats, nbytes), "packed weights")
         self.data, self.mats, self.N, self.K, self.group, self.zeros = data, mats, N, K, group, zeros
 
     def __getitem__(self, i):
         if not 0 <= i < self.mats:
             raise IndexError(i)
-        return W4Packed(self.data[i:i + 1], 1, self.N, self.K, self.group, self.zeros)
+        return W4Packed(None if self.data is None else self.data[i:i + 1], 1, self.N, self.K, self.group, self.zeros)
 
 
 def moe_quantize_weight_w4(w, group, zeros=False, stream=None):
@@ -502,7 +535,10 @@ def moe_quantize_weight_w4(w, group, zeros=False, stream=None):
     if stream is not None:
         return _run_on(stream, moe_quantize_weight_w4, w, group, zeros)
     _dev(w)
+    _need(w.dtype is torch.bfloat16, "w is BF16")
     rows, cols = w.shape[-2:]
+    _need(rows > 0 and group in (32, 64, 128) and cols > 0 and cols % group == 0,
+          "group is 32, 64 or 128 and divides the columns")
     lead = w.shape[:-2]
     mats = w.numel() // (rows * cols)
     q = torch.empty(*lead, rows, cols // 2, dtype=torch.uint8, device=w.device)
@@ -520,17 +556,20 @@ def moe_pack_w4(q, scales, zeros=None, stream=None):
         return _run_on(stream, moe_pack_w4, q, scales, zeros)
     _dev(q)
     _dev(scales)
+    _need(q.dtype is torch.uint8 and q.numel() > 0, "codes are uint8, two to a byte")
     N, K = q.shape[-2], 2 * q.shape[-1]
     mats = q.numel() // (N * q.shape[-1])
     if scales.dtype != torch.bfloat16 or scales.shape[-1] != N or scales.numel() % (mats * N):
         raise ValueError("scales are BF16 [..., K / group, N]")
     kg = scales.numel() // (mats * N)
+    _need(0 < kg <= K, "scales are BF16 [..., K / group, N]")
     group = K // kg
     if zeros is not None and (_dev(zeros).dtype != torch.uint8 or zeros.numel() != scales.numel()):
         raise ValueError("zeros are uint8 with the shape of scales")
     if group * kg != K:
         raise ValueError("the scales' rows do not divide K")
     nbytes = lib().moe_w4_packed_bytes(N, K, group, int(zeros is not None))
+    _need(nbytes > 0, "no such packed matrix: N, K or group")
     data = torch.empty(mats, nbytes, dtype=torch.uint8, device=q.device)
     _check("moe_pack_w4", lib().moe_pack_w4(_ptr(q), _ptr(scales), _ptr(zeros), mats, N, K, group, _ptr(data),
                                             _stream(None)))
@@ -559,16 +598,21 @@ def moe_linear_w4(x, w, bias=None, out=None, out_dtype=torch.bfloat16, ws=None, 
     N = w.N
     assert x.is_cuda and x.dtype is torch.bfloat16 and x.stride(1) == 1, "x is BF16 [T, K] on the GPU, rows dense"
     assert w.mats == 1 and w.K == K, "w is one matrix with x's K"
+    _need_tensor(bias, torch.float32, (N,), "bias")
+    _need_word(dev_status, "dev_status")
     if out is None:
         out = torch.empty(T, N, dtype=out_dtype, device=x.device)
         os = N
     else:
         assert out.shape == (T, N) and out.stride(1) == 1
+        _need(out.is_cuda, "out is on the GPU")
         os = out.stride(0) if T > 1 else N
         out_dtype = out.dtype
     assert out_dtype is torch.bfloat16 or out_dtype is torch.float32, "out is BF16 or float32"
     if ws is None:
         ws = moe_linear_w4_workspace(T, N, K, x.device)
+    else:
+        _need_ws(ws)
     _check("moe_linear_w4", (_lib or lib()).moe_linear_w4(
         x.data_ptr(), T, K, x.stride(0) if T > 1 else K, w.data.data_ptr(), N, w.group, w.zeros,
         None if bias is None else bias.data_ptr(), out.data_ptr(), out_dtype is torch.float32, os, ws.data_ptr(),
@@ -591,14 +635,25 @@ def moe_route_hidden(x, w_router, K, bias=None, num_tokens=None, logits=None, to
     assert x.dtype is torch.bfloat16 and w_router.dtype is torch.bfloat16
     T, H = x.shape
     E = w_router.shape[0]
+    _need_tensor(w_router, torch.bfloat16, (E, H), "w_router")
+    _need_tensor(bias, torch.float32, (E,), "bias")
+    _need_word(num_tokens, "num_tokens")
     if logits is None:
         logits = torch.empty(T, E, dtype=torch.float32, device=x.device)
+    else:
+        _need_tensor(logits, torch.float32, (T, E), "logits")
     if topk_idx is None:
         topk_idx = torch.empty(T, K, dtype=torch.int32, device=x.device)
+    else:
+        _need_tensor(topk_idx, torch.int32, (T, K), "topk_idx")
     if topk_w is None:
         topk_w = torch.empty(T, K, dtype=torch.float32, device=x.device)
+    else:
+        _need_tensor(topk_w, torch.float32, (T, K), "topk_w")
     if ws is None:
         ws = moe_route_hidden_workspace(device=x.device)
+    else:
+        _need_ws(ws)
     _check("moe_route_hidden", (_lib or lib()).moe_route_hidden(
         x.data_ptr(), T, H, w_router.data_ptr(), _ptr(bias), E, K, _ptr(num_tokens), logits.data_ptr(),
         topk_idx.data_ptr(), topk_w.data_ptr(), ws.data_ptr(), ws.numel(), _stream(None)))

@@ -81,3 +81,71 @@ def test_calls_make_what_they_need_on_their_stream(here, stream):
     layer.forward(x, stream=s)
     assert len(log) == 7
     assert all(at == want for _, at in log), log
+
+
+# -------------------------------------------------------------------------- what is refused, and what is not
+def refused(here, f, *a, **k):
+    log = here[0]
+    before = len(log)
+    with pytest.raises((ValueError, AssertionError, moe.MoeError)):
+        f(*a, **k)
+    assert not [name for name, _ in log[before:] if name != "zeros"], "it was launched"
+
+
+def test_linear_arguments(here):
+    log, make = here
+    x, w = make(4, 256), packed(make)
+    cpu = torch.empty(64, dtype=F32)
+    for bad in (dict(bias=make(64)), dict(bias=make(63, dtype=F32)), dict(bias=cpu),
+                dict(bias=make(128, dtype=F32)[::2]), dict(out=torch.empty(4, 64, dtype=BF)), dict(out=make(4, 64, dtype=I32)),
+                dict(out=make(3, 64)), dict(ws=torch.empty(4096, dtype=U8)), dict(ws=make(8192, dtype=U8)[::2]),
+                dict(dev_status=make(1, dtype=torch.int64)), dict(dev_status=torch.zeros(1, dtype=I32)),
+                dict(out_dtype=torch.float16)):
+        refused(here, moe.moe_linear_w4, x, w, **bad)
+    for bad in (make(4, 256, dtype=torch.float16), torch.empty(4, 256, dtype=BF), make(4, 128), make(256, 4).T, make(256)):
+        refused(here, moe.moe_linear_w4, bad, w)
+    refused(here, moe.moe_linear_w4, x, packed(make, mats=2))
+    moe.moe_linear_w4(x, w, bias=make(1, 64, dtype=F32), out=make(4, 80, dtype=F32)[:, :64], ws=make(4096, dtype=U8),
+                      dev_status=make(1, dtype=I32))
+    moe.moe_linear_w4(make(4, 300)[:, 8:264], w)
+    assert [n for n, _ in log].count("moe_linear_w4") == 2
+
+
+def test_packed_weights(here):
+    log, make = here
+    for bad in (make(1, 4095, dtype=U8), make(2, 4096, dtype=U8), make(1, 4096, dtype=torch.int8), torch.empty(1, 4096, dtype=U8),
+                make(4096, dtype=U8)):
+        refused(here, moe.W4Packed, bad, 1, 64, 256, 64, False)
+    assert moe.W4Packed(make(3, 4096, dtype=U8), 3, 64, 256, 64, False)[2].mats == 1
+
+
+def test_weight_preparation_arguments(here):
+    log, make = here
+    for bad in (dict(w=make(64, 256, dtype=F32)), dict(w=make(64, 256, dtype=torch.float16)), dict(group=0), dict(group=48),
+                dict(group=16), dict(w=make(64, 0)), dict(w=make(0, 256)), dict(w=torch.empty(64, 256, dtype=BF)),
+                dict(w=make(256, 64).T), dict(w=make(64, 160), group=64)):
+        refused(here, moe.moe_quantize_weight_w4, **{**dict(w=make(64, 256), group=64), **bad})
+    q, s, z = make(64, 128, dtype=U8), make(4, 64), make(4, 64, dtype=U8)
+    for bad in (dict(q=make(64, 128, dtype=I32)), dict(q=make(64, 128)), dict(scales=make(4, 64, dtype=F32)),
+                dict(scales=make(4, 63)), dict(scales=make(0, 64)), dict(scales=make(3, 64)), dict(zeros=make(4, 64)),
+                dict(zeros=make(3, 64, dtype=U8)), dict(zeros=torch.empty(4, 64, dtype=U8)), dict(q=make(0, 128, dtype=U8)),
+                dict(q=make(128, 64, dtype=U8).T)):
+        refused(here, moe.moe_pack_w4, **{**dict(q=q, scales=s, zeros=z), **bad})
+    moe.moe_pack_w4(q, s, z)
+    moe.moe_quantize_weight_w4(make(2, 64, 256), 32, True)
+
+
+def test_route_hidden_arguments(here):
+    log, make = here
+    x, w = make(4, 256), make(8, 256)
+    for bad in (dict(w_router=make(8, 128)), dict(w_router=make(8, 512)), dict(w_router=make(8, 256, dtype=F32)),
+                dict(w_router=torch.empty(8, 256, dtype=BF)), dict(w_router=make(256, 8).T), dict(w_router=make(2048)),
+                dict(bias=make(8)), dict(bias=make(7, dtype=F32)), dict(bias=torch.empty(8, dtype=F32)),
+                dict(num_tokens=make(1, dtype=torch.int64)), dict(num_tokens=torch.tensor([4], dtype=I32)),
+                dict(logits=make(4, 8)), dict(logits=make(4, 9, dtype=F32)), dict(logits=make(8, 4, dtype=F32).T),
+                dict(topk_idx=make(4, 2, dtype=torch.int64)), dict(topk_idx=make(4, 3, dtype=I32)),
+                dict(topk_w=make(4, 2)), dict(topk_w=make(2, 4, dtype=F32).T), dict(ws=torch.empty(256, dtype=U8))):
+        refused(here, moe.moe_route_hidden, **{**dict(x=x, w_router=w, K=2), **bad})
+    moe.moe_route_hidden(x, w, 2, bias=make(8, dtype=F32), num_tokens=make(1, dtype=I32), logits=make(4, 8, dtype=F32),
+                         topk_idx=make(4, 2, dtype=I32), topk_w=make(4, 2, dtype=F32), ws=make(256, dtype=U8))
+    assert log[-1][0] == "moe_route_hidden"
