@@ -498,6 +498,25 @@ def _need_tensor(t, dtype, shape, what):
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
+def _need_rows(t, dtype, rows, cols, what):
+    """t: a contiguous GPU tensor of dtype with `rows` rows or more (the rest is left alone), an address, or None."""
+    if t is None or isinstance(t, int):
+        return
+    if not (t.dim() == 2 and t.shape[0] >= rows and t.shape[1] == cols and t.dtype is dtype and t.is_cuda and
+            t.is_contiguous()):
+        raise ValueError(f"{what}: expected a contiguous {dtype} GPU tensor of {rows} rows of {cols}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _need_matrices(t, dtypes, mats, n, k, what):
+    """t: `mats` matrices of n rows and k columns, [mats, n, k] or for one [n, k]; an address, or None."""
+    if t is None or isinstance(t, int):
+        return
+    if not (t.shape[-2:] == (n, k) and t.numel() == mats * n * k and t.dtype in dtypes and t.is_cuda and t.is_contiguous()):
+        raise ValueError(f"{what}: expected {mats} x {n} x {k} of {dtypes[0]}, contiguous, on the GPU, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
 def _need_word(t, what):
     """t: an int32 on the GPU, an address, or None."""
     if t is None or isinstance(t, int):
@@ -641,15 +660,15 @@ def moe_route_hidden(x, w_router, K, bias=None, num_tokens=None, logits=None, to
     if logits is None:
         logits = torch.empty(T, E, dtype=torch.float32, device=x.device)
     else:
-        _need_tensor(logits, torch.float32, (T, E), "logits")
+        _need_rows(logits, torch.float32, T, E, "logits")
     if topk_idx is None:
         topk_idx = torch.empty(T, K, dtype=torch.int32, device=x.device)
     else:
-        _need_tensor(topk_idx, torch.int32, (T, K), "topk_idx")
+        _need_rows(topk_idx, torch.int32, T, K, "topk_idx")
     if topk_w is None:
         topk_w = torch.empty(T, K, dtype=torch.float32, device=x.device)
     else:
-        _need_tensor(topk_w, torch.float32, (T, K), "topk_w")
+        _need_rows(topk_w, torch.float32, T, K, "topk_w")
     if ws is None:
         ws = moe_route_hidden_workspace(device=x.device)
     else:
@@ -670,10 +689,22 @@ class MoeLayerFew:
                  w13_scales=None, w2_scales=None, shared_w13_scales=None, shared_w2_scales=None, w_router=None,
                  router_bias=None, weight_tiles=False, device="cuda"):
         w4 = dtype == MOE_W4
-        if w4:
-            for m, e, n, k in ((w13, E, 2 * I, H), (w2, E, H, I), (shared_w13, 1, 2 * I, H), (shared_w2, 1, H, I)):
+        _need((shared_w13 is None) == (shared_w2 is None), "a shared expert has both matrices")
+        _need(not w4 or all(isinstance(m, W4Packed) for m in (w13, w2) + (() if shared_w13 is None else (shared_w13, shared_w2))),
+              "MOE_W4 takes W4Packed matrices")
+        for what, m, sc, e, n, k in (("w13", w13, w13_scales, E, 2 * I, H), ("w2", w2, w2_scales, E, H, I),
+                                     ("shared_w13", shared_w13, shared_w13_scales, 1, 2 * I, H),
+                                     ("shared_w2", shared_w2, shared_w2_scales, 1, H, I)):
+            if w4:
                 if m is not None and (m.mats, m.N, m.K, m.group, m.zeros) != (e, n, k, w13.group, w13.zeros):
                     raise ValueError("a packed matrix has another shape, group or zero points than the layer")
+            elif dtype == MOE_E4M3:
+                _need_matrices(m, (torch.uint8, torch.float8_e4m3fn), e, n, k, what)
+                _need_matrices(sc, (torch.float32,), e, n // 128, k // 128, what + "_scales")
+            else:
+                _need_matrices(m, (torch.bfloat16,), e, n, k, what)
+        _need_tensor(w_router, torch.bfloat16, (E, H), "w_router")
+        _need_tensor(router_bias, torch.float32, (E,), "router_bias")
         self.desc = FewDesc(T, H, I, E, K, dtype, int(shared_w13 is not None), int(weight_tiles),
                             w13.group if w4 else 0, int(w13.zeros) if w4 else 0)
         parts = []
@@ -707,11 +738,21 @@ class MoeLayerFew:
         assert H == d.H
         if out is None:
             out = torch.empty_like(x)
+        else:
+            _need_rows(out, torch.bfloat16, t, H, "out")
+        _need_rows(logits, torch.float32, t, d.E, "logits")
+        _need_word(num_tokens, "num_tokens")
+        _need_word(dev_status, "dev_status")
+        if (topk_idx is None or topk_w is None) and self.weights.w_router is None and logits is None:
+            raise ValueError("topk_idx and topk_w are needed: the layer has no router and no logits")
         if topk_idx is None:
-            if self.weights.w_router is None and logits is None:
-                raise ValueError("topk_idx and topk_w are needed: the layer has no router and no logits")
             topk_idx = torch.empty(t, d.K, dtype=torch.int32, device=x.device)
+        else:
+            _need_rows(topk_idx, torch.int32, t, d.K, "topk_idx")
+        if topk_w is None:
             topk_w = torch.empty(t, d.K, dtype=torch.float32, device=x.device)
+        else:
+            _need_rows(topk_w, torch.float32, t, d.K, "topk_w")
         _check("moe_layer_few", (_lib or lib()).moe_layer_few(
             ctypes.byref(d), self._w, x.data_ptr(), _ptr(logits), _ptr(num_tokens), topk_idx.data_ptr(),
             topk_w.data_ptr(), out.data_ptr(), *self._ws, _ptr(dev_status), _stream(None)))

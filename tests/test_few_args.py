@@ -149,3 +149,66 @@ def test_route_hidden_arguments(here):
     moe.moe_route_hidden(x, w, 2, bias=make(8, dtype=F32), num_tokens=make(1, dtype=I32), logits=make(4, 8, dtype=F32),
                          topk_idx=make(4, 2, dtype=I32), topk_w=make(4, 2, dtype=F32), ws=make(256, dtype=U8))
     assert log[-1][0] == "moe_route_hidden"
+
+
+def layer_weights(make, dtype, E=8, H=256, I=128, shared=True):
+    kw = {}
+    for name, e, n, k in (("w13", E, 2 * I, H), ("w2", E, H, I), ("shared_w13", 1, 2 * I, H), ("shared_w2", 1, H, I)):
+        if name.startswith("shared") and not shared:
+            continue
+        lead = () if name.startswith("shared") else (e,)
+        if dtype == moe.MOE_W4:
+            kw[name] = packed(make, n, k, 64, e)
+        elif dtype == moe.MOE_E4M3:
+            kw[name] = make(*lead, n, k, dtype=U8)
+            kw[name + "_scales"] = make(*lead, n // 128, k // 128, dtype=F32)
+        else:
+            kw[name] = make(*lead, n, k)
+    return kw
+
+
+@pytest.mark.parametrize("dtype", [moe.MOE_BF16, moe.MOE_E4M3, moe.MOE_W4])
+def test_layer_weights(here, dtype):
+    log, make = here
+    good = layer_weights(make, dtype)
+    new = lambda **k: moe.MoeLayerFew(4, 256, 128, 8, 2, dtype, **{**good, **k})
+    one = U8 if dtype == moe.MOE_E4M3 else BF
+    for bad in (dict(w13=make(8, 256, 128, dtype=one)), dict(w13=make(7, 256, 256, dtype=one)), dict(w2=make(8, 128, 256, dtype=one)),
+                dict(w2=make(8, 256, 128, dtype=F32)), dict(w2=torch.empty(8, 256, 128, dtype=one)),
+                dict(w13=make(256, 256, 8, dtype=one).permute(2, 0, 1)), dict(shared_w2=None), dict(shared_w13=None),
+                dict(shared_w13=make(2, 256, 256, dtype=one)), dict(w_router=make(8, 128)), dict(w_router=make(8, 256, dtype=F32)),
+                dict(w_router=torch.empty(8, 256, dtype=BF)), dict(w_router=make(8, 256), router_bias=make(8)),
+                dict(w_router=make(8, 256), router_bias=make(7, dtype=F32))):
+        refused(here, new, **bad)
+    if dtype == moe.MOE_E4M3:
+        for bad in (make(8, 1, 2, dtype=F32), make(8, 2, 2), make(7, 2, 2, dtype=F32), torch.empty(8, 2, 2, dtype=F32)):
+            refused(here, new, w13_scales=bad)
+        new(w13=make(8, 256, 256, dtype=torch.float8_e4m3fn), shared_w2=make(1, 256, 128, dtype=U8))
+    else:
+        refused(here, new, w13=make(8, 256, 256, dtype=U8))
+    new(w_router=make(8, 256), router_bias=make(8, dtype=F32))
+
+
+@pytest.mark.parametrize("dtype", [moe.MOE_BF16, moe.MOE_E4M3, moe.MOE_W4])
+def test_layer_forward_arguments(here, dtype):
+    log, make = here
+    layer = moe.MoeLayerFew(4, 256, 128, 8, 2, dtype, **layer_weights(make, dtype, shared=False))
+    x = make(3, 256)
+    i, w = make(3, 2, dtype=I32), make(3, 2, dtype=F32)
+    for bad in (dict(topk_idx=make(3, 2, dtype=torch.int64)),         # as torch.topk returns them
+                dict(topk_idx=None), dict(topk_w=None), dict(topk_idx=None, topk_w=None), dict(topk_w=make(3, 2)),
+                dict(topk_idx=make(2, 3, dtype=I32).T), dict(topk_idx=make(2, 2, dtype=I32)), dict(topk_idx=make(3, 3, dtype=I32)),
+                dict(topk_idx=torch.empty(3, 2, dtype=I32)), dict(topk_w=make(3, 4, dtype=F32)[:, ::2]),
+                dict(out=make(3, 256, dtype=F32)), dict(out=make(3, 512)[:, ::2]), dict(out=make(2, 256)), dict(out=torch.empty(3, 256, dtype=BF)),
+                dict(logits=make(3, 8)), dict(logits=make(3, 7, dtype=F32)), dict(logits=make(8, 3, dtype=F32).T),
+                dict(num_tokens=make(1, dtype=torch.int64)), dict(num_tokens=torch.zeros(1, dtype=I32)),
+                dict(dev_status=make(1, dtype=torch.int64))):
+        refused(here, layer.forward, x, **{**dict(topk_idx=i, topk_w=w), **bad})
+    for bad in (make(5, 256), make(3, 128), make(3, 256, dtype=F32), make(256, 3).T, torch.empty(3, 256, dtype=BF)):
+        refused(here, layer.forward, bad, topk_idx=i, topk_w=w)
+    # rows past the call's in a buffer are left alone
+    layer.forward(x, out=make(4, 256), topk_idx=make(4, 2, dtype=I32), topk_w=make(4, 2, dtype=F32), logits=make(4, 8, dtype=F32),
+                  num_tokens=make(1, dtype=I32), dev_status=make(1, dtype=I32))
+    layer.forward(x, logits=make(3, 8, dtype=F32))
+    layer.forward(x, logits=make(3, 8, dtype=F32), topk_w=make(3, 2, dtype=F32))
+    assert [n for n, _ in log].count("moe_layer_few") == 3
