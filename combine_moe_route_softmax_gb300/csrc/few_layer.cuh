@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(warps_of<FMT>() * 32, 1) layer_kernel(const __
   const bool sync = HALF || a.w_router;
   // where the joins' slots will be
   float2* scratch = reinterpret_cast<float2*>(rings + WORKERS * 2 * Format<FMT, GROUP>::STAGE);
-  static_assert(route_scratch(WARPS) * 8 <= PARTS_BYTES, "");
+  static_assert(ROUTE_SCRATCH * 8 <= PARTS_BYTES, "");
   uint32_t gen = 0;
   if (HALF)
     // by the last CTAs, which have the fewest router rows

@@ -18,7 +18,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_hidden_kernel(
     const uint16_t* x, const uint16_t* wr, const float* bias, int T, int H, int E, int K, const int32_t* num_tokens,
     float* logits, int32_t* topk_idx, float* topk_w, uint32_t* count) {
   __shared__ bool last;
-  __shared__ float2 scratch[route_scratch(ROUTE_WARPS)];
+  __shared__ float2 scratch[ROUTE_SCRATCH];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   router_logits<ROUTE_WARPS>(x, wr, bias, T, H, E, logits, scratch, blockIdx.x, gridDim.x, warp, lane);
   const int groups = mma_groups(T), group = blockIdx.x % groups;     // of tokens (the grid is whole rounds of them)

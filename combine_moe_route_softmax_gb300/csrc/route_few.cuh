@@ -3,11 +3,13 @@
 //
 // logits[t, e] = x[t] . wr[e] + bias[e].  A near tie between two experts is decided by the last
 // bits of the logits, so the sum is carried in two float32 words: products of BF16 are
-// exact in float32, 8 of them are summed by fused multiply-adds, or 16 by a tensor instruction, and
-// each such partial sum enters the running pair by an error-free addition.  What is left of
-// rounding is that of the partial sums, about 1e-9 of the logits' size each; together with the final
-// rounding to float32 6e-8 of the largest logit at H = 7168 (the error-free sum of every
-// product costs four times the instructions).
+// exact in float32, 8 of them are summed by fused multiply-adds (up to 4 tokens), or 16 by a tensor
+// instruction (more), and each such partial sum enters the running pair by an error-free addition.  What
+// is left of rounding is that of the partial sums, 7 half steps of 8 products (2^-21 of their magnitudes at
+// worst) or 15 steps of 16 (2^-19), and the final one to float32.  Measured at H = 7168: an error of 9e-8 of the
+// logits' size, of which a correctly rounded sum has 5e-8.  So the bits of a token's logits depend on its row,
+// the sizes and on which side of 4 tokens the call is, not on the grid, the warps or the other tokens
+// (the error-free sum of every product would cost four times the instructions).
 #pragma once
 
 #include "few.cuh"
@@ -43,8 +45,9 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
   }
 }
 
-// Up to ROUTE_TOKENS tokens a task is one expert, and S warps share its columns, so that every SM has
-// some.  By sizes alone: the logits are the same bits in any grid.
+// Up to ROUTE_TOKENS tokens a task is one expert, and S warps share its columns; a CTA has NW / S experts at
+// a time, so 64 experts at H >= 1024 lie on 16 SMs, 256 on 64.  S goes by sizes alone: the logits are the
+// same bits in any grid.
 constexpr int ROUTE_TOKENS = 4;
 __device__ __forceinline__ int router_split(int H) { return H >= 1024 ? 4 : H >= 512 ? 2 : 1; }
 
@@ -98,16 +101,17 @@ __device__ __forceinline__ void router_dot(const uint16_t* __restrict__ x, const
   rc = c[0];
 }
 
-// More than ROUTE_TOKENS tokens: a task is 16 tokens and 8 experts, its columns shared out between the
-// CTA's warps 32 at a time.  A tensor instruction (tokens as its 16 rows, experts as its 8 columns)
+// More than ROUTE_TOKENS tokens: a task is 16 tokens and 8 experts, its columns shared out in MMA_SLICES
+// slices, 32 columns at a time in turn, and the slices between the CTA's warps (16 of them, whatever the
+// warps: 12 in a 4-bit layer).  A tensor instruction (tokens as its 16 rows, experts as its 8 columns)
 // starts from zero and gives sums of 16 products, which enter the pairs as above.  At H = 7168, E = 256:
 // 11.2 us against 8.7 on the other path for 4 tokens, 12.8 against 20.2 for 32.
-constexpr int MMA_TOKENS = 16, MMA_EXPERTS = 8;
+constexpr int MMA_TOKENS = 16, MMA_EXPERTS = 8, MMA_SLICES = 16;
 __host__ __device__ __forceinline__ int mma_groups(int T) { return (T + MMA_TOKENS - 1) / MMA_TOKENS; }
 __host__ __device__ __forceinline__ int mma_tasks(int T, int E) {
   return (E + MMA_EXPERTS - 1) / MMA_EXPERTS * mma_groups(T);
 }
-__host__ __device__ constexpr int route_scratch(int warps) { return warps * MMA_TOKENS * MMA_EXPERTS; }   // float2
+constexpr int ROUTE_SCRATCH = MMA_SLICES * MMA_TOKENS * MMA_EXPERTS;   // float2
 template <int NW>
 __device__ __forceinline__ void router_logits_mma(const uint16_t* __restrict__ x, const uint16_t* __restrict__ wr,
                                                   const float* bias, int T, int H, int E, float* logits,
@@ -119,28 +123,36 @@ __device__ __forceinline__ void router_logits_mma(const uint16_t* __restrict__ x
     const uint4* x0 = reinterpret_cast<const uint4*>(x + (size_t)min(t0 + g, T - 1) * H) + t;
     const uint4* x1 = reinterpret_cast<const uint4*>(x + (size_t)min(t0 + g + 8, T - 1) * H) + t;
     const uint4* w = reinterpret_cast<const uint4*>(wr + (size_t)min(e0 + g, E - 1) * H) + t;
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto sums = [&](int slice, bool wait) {
+      float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
-    for (int i = warp; i < H / 32; i += NW) {
-      const uint4 a = __ldg(x0 + i * 4), b = __ldg(x1 + i * 4), v = __ldg(w + i * 4);
-      float d[2][4];
-      mma16_first<false>(d[0], a.x, b.x, a.y, b.y, v.x, v.y);
-      mma16_first<false>(d[1], a.z, b.z, a.w, b.w, v.z, v.w);
+      for (int i = slice; i < H / 32; i += MMA_SLICES) {
+        const uint4 a = __ldg(x0 + i * 4), b = __ldg(x1 + i * 4), v = __ldg(w + i * 4);
+        float d[2][4];
+        mma16_first<false>(d[0], a.x, b.x, a.y, b.y, v.x, v.y);
+        mma16_first<false>(d[1], a.z, b.z, a.w, b.w, v.z, v.w);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) add_pair(s[q], c[q], d[j][q]);
+          for (int q = 0; q < 4; ++q) add_pair(s[q], c[q], d[j][q]);
+      }
+      if (wait) __syncthreads();           // the task before is read
+#pragma unroll
+      for (int q = 0; q < 4; ++q) scratch[(slice * 4 + q) * 32 + lane] = make_float2(s[q], c[q]);
+    };
+    if constexpr (NW == MMA_SLICES) {
+      sums(warp, true);
+    } else {
+#pragma unroll 1
+      for (int slice = warp; slice < MMA_SLICES; slice += NW) sums(slice, slice < NW);
     }
-    __syncthreads();           // the task before is read
-#pragma unroll
-    for (int q = 0; q < 4; ++q) scratch[(warp * 4 + q) * 32 + lane] = make_float2(s[q], c[q]);
     __syncthreads();
     const int i = warp * 32 + lane;
     if (i < 128) {
       const int q = warp, tok = t0 + g + (q >> 1) * 8, e = e0 + 2 * t + (q & 1);
       float rs = scratch[i].x, rc = scratch[i].y;
 #pragma unroll 4
-      for (int j = 1; j < NW; ++j) join_pair(rs, rc, scratch[j * 128 + i].x, scratch[j * 128 + i].y);
+      for (int j = 1; j < MMA_SLICES; ++j) join_pair(rs, rc, scratch[j * 128 + i].x, scratch[j * 128 + i].y);
       if (tok < T && e < E) {
         if (bias) add_pair(rs, rc, __ldg(bias + e));
         logits[(size_t)tok * E + e] = pair_value(rs, rc);
@@ -150,7 +162,7 @@ __device__ __forceinline__ void router_logits_mma(const uint16_t* __restrict__ x
 }
 
 // All logits, by every CTA of a grid (NW warps each, all threads call; NW need not be a multiple of
-// the split).  scratch: route_scratch(NW) of shared memory.
+// the split).  scratch: ROUTE_SCRATCH of shared memory.
 template <int NW>
 __device__ __forceinline__ void router_logits(const uint16_t* x, const uint16_t* wr, const float* bias, int T, int H,
                                               int E, float* logits, float2* scratch, int cta, int ctas, int warp,

@@ -541,9 +541,12 @@ moe_status_t moe_linear_w4(const uint16_t* x, int T, int K, long long x_stride, 
                            void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
 
 /* The router from hidden states, T <= MOE_FEW_MAX_TOKENS:
- *   logits[t, e] = float32(sum_h x[t, h] * w_router[e, h] + bias[e]), the sum carried to about
- *   48 bits before its one rounding, so which expert wins a near tie does not hang on the
- *   order of the sum; then the selection and weights of moe_route_topk.
+ *   logits[t, e] = float32(sum_h x[t, h] * w_router[e, h] + bias[e]); then the selection and weights
+ *   of moe_route_topk.  Sums of 8 products (up to 4 tokens) or 16 (more) are float32; these are
+ *   added up to about 48 bits and rounded once.  Error: at most 2^-21 (up to 4 tokens) or 2^-19 (more) of
+ *   sum_h |x w| and one float32 rounding; 9e-8 of the logits' size at H = 7168.  The bits of a
+ *   row of logits depend on that row of x, the sizes, and on whether T is above 4: experts whose
+ *   logits are that close may change places between a call of 4 tokens and one of 5.
  *   x BF16 [T, H], w_router BF16 [E, H] (both 16-byte aligned), bias nullable float32 [E],
  *   logits out float32 [T, E]; num_tokens, topk_idx, topk_w as moe_route_topk (the logits of
  *   rows past num_tokens are written too).

@@ -198,3 +198,34 @@ def test_few_calls_on_another_stream_than_the_current(raw):
     got = calls(stream=side.cuda_stream if raw else side)
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ------------------------------------------------------------------------------- logits by row
+@pytest.mark.parametrize("H,E,K", [(7168, 256, 8), (640, 60, 4), (2048, 1000, 32)])
+def test_route_hidden_rows_by_themselves(H, E, K):
+    """A token's logits are the same bits in any call of up to 4 tokens, and in any of more, at any place; the two
+    differ by the errors that moe.h states; both keep near ties that are further apart than that in order."""
+    g = gen(H)
+    x, w = normal(g, 32, H), normal(g, E, H, std=H ** -0.5)
+    w[1::2] = w[::2][:E // 2]
+    w[1::2, 5] += 2.0 ** -9 * w[1::2, 5].abs() + 2.0 ** -12      # near ties: one weight a little larger
+    z = x.double() @ w.double().T
+    size = x.double().abs() @ w.double().abs().T
+    few = torch.cat([moe.moe_route_hidden(x[i:i + n], w, K)[2] for i, n in ((0, 1), (1, 2), (3, 3), (6, 4), (10, 1))])
+    assert torch.equal(few, torch.cat([moe.moe_route_hidden(x[i:i + 1], w, K)[2] for i in range(11)]))
+    idx, _, many = moe.moe_route_hidden(x, w, K)
+    assert torch.equal(many[3:9], moe.moe_route_hidden(x[3:9].contiguous(), w, K)[2])
+    assert torch.equal(many[11:], moe.moe_route_hidden(x[11:].contiguous(), w, K)[2])
+    for logits, rows, eps in ((few, slice(0, 11), 2.0 ** -21), (many, slice(0, 32), 2.0 ** -19)):
+        err = eps * size[rows] + 2.0 ** -24 * z[rows].abs()
+        assert ((logits.double() - z[rows]).abs() <= err).all()
+        far = (z[rows, 1::2] - z[rows, ::2][:, :E // 2]).abs() > err[:, 1::2] + err[:, ::2][:, :E // 2]
+        up = logits[:, 1::2] > logits[:, ::2][:, :E // 2]
+        assert torch.equal(up[far], (z[rows, 1::2] > z[rows, ::2][:, :E // 2])[far])
+    # the layers' own router: 12 warps with 4-bit weights, 16 with the others
+    for dtype, group in (("w4", 128), ("e4m3", 0), ("bf16", 0)):
+        lw = Weights(g, dtype, H, 128, K, False, group)
+        n = moe.MoeLayerFew(32, H, 128, K, K, w_router=w[:K].contiguous(), **lw.kw)
+        _, i2, w2 = n.forward(x)
+        i1, w1, _ = moe.moe_route_hidden(x, w[:K].contiguous(), K)
+        assert torch.equal(i1, i2) and torch.equal(w1, w2)
