@@ -45,25 +45,36 @@ __device__ __forceinline__ unsigned long long clock_ns() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
-// Bounded wait for done(): false (and the status bit) after TIMEOUT_NS.
+// How long the waits of a CTA last.  The first that runs out sets the status bit and gave_up, which ends
+// all others, those still to come at their first look: a launch that cannot go on is over one limit later.
+struct Patience {
+  int* gave_up;                // shared, 0 at first
+  int32_t* dev_status;         // nullable
+  unsigned long long limit_ns;
+  __device__ __forceinline__ bool over() const { return *static_cast<volatile int*>(gave_up) != 0; }
+  __device__ __forceinline__ bool ran_out(unsigned long long t0) const {
+    if (clock_ns() - t0 <= limit_ns) return false;
+    *static_cast<volatile int*>(gave_up) = 1;
+    if (dev_status) atomicOr(dev_status, MOE_DEV_PIPELINE_TIMEOUT);
+    return true;
+  }
+};
+// Bounded wait for done(): false if this or another wait of the CTA ran out.
 template <class Done>
-__device__ __forceinline__ bool wait_for(Done done, int32_t* dev_status) {
+__device__ __forceinline__ bool wait_for(Done done, const Patience& p) {
   if (done()) return true;
   const unsigned long long t0 = clock_ns();
   while (!done()) {
     __nanosleep(40);     // a waiting warp leaves the issue slots to the others
-    if (clock_ns() - t0 > TIMEOUT_NS) {
-      if (dev_status) atomicOr(dev_status, MOE_DEV_PIPELINE_TIMEOUT);
-      return false;
-    }
+    if (p.over() || p.ran_out(t0)) return false;
   }
   return true;
 }
 
 // The same for a whole warp: one answer for all lanes.
 template <class Done>
-__device__ __forceinline__ bool warp_wait_for(Done done, int32_t* dev_status) {
-  return __all_sync(0xffffffffu, wait_for(done, dev_status));
+__device__ __forceinline__ bool warp_wait_for(Done done, const Patience& p) {
+  return __all_sync(0xffffffffu, wait_for(done, p));
 }
 
 // HALF: operands are FP16, else BF16.
@@ -445,7 +456,7 @@ struct Stream {
   uint8_t* ring;               // two stages
   uint32_t ring_addr, bars;    // shared addresses of the ring and of its two barriers
   int lane;
-  int32_t* dev_status;
+  Patience patience;
   int dx, dy;                  // tensor maps: from one item to the next
   int block;                   // W4: bytes of a block
   bool zeros;
@@ -457,7 +468,9 @@ struct Stream {
   const uint8_t *p0, *p1;
   const CUtensorMap* map;
   int cur;                     // unit in use
-  bool dead;                   // a wait gave up
+  // Set when a wait gave up: 1 with at most the item after the last one run on its way (filled, pending), 2
+  // with the item that was waited for, 3 with that and the next.
+  int dead;
 
   // Asks for the next item, into stage st.  It never waits while a unit is in use: the scheduler waits
   // for the slowest worker, which must not wait for it in turn.  If the next unit is not written
@@ -514,10 +527,11 @@ struct Stream {
     left = 0;
     filled = 0;
     pending = false;
-    dead = false;
+    dead = 0;
     fill(0);
   }
   __device__ __forceinline__ bool take() {
+    if (dead) return false;
     if (filled != END) src.at(filled, lane);
     if (pending) {
       const unsigned long long t0 = clock_ns();
@@ -525,29 +539,29 @@ struct Stream {
         fill(stage & 1);
         if (!pending) break;
         __nanosleep(40);
-        if (__any_sync(0xffffffffu, clock_ns() - t0 > TIMEOUT_NS)) {
-          if (lane == 0 && dev_status) atomicOr(dev_status, MOE_DEV_PIPELINE_TIMEOUT);
-          dead = true;
-          break;
+        if (__any_sync(0xffffffffu, patience.over() || patience.ran_out(t0))) {
+          dead = 1;
+          return false;
         }
       }
     }
     cur = filled;
-    return !dead && cur != END;
+    return cur != END;
   }
   __device__ __forceinline__ void finish() {
-    // given up: the item on its way arrives before the block ends
-    if (dead && !pending && filled != END) gg::mbar_drain(bars + (stage & 1) * 8, (stage >> 1) & 1);
+    // given up: the items on their way arrive before the block ends
+    if (dead >= 2 || (dead && !pending && filled != END)) gg::mbar_drain(bars + (stage & 1) * 8, (stage >> 1) & 1);
+    if (dead == 3) gg::mbar_drain(bars + ((stage + 1) & 1) * 8, ((stage + 1) >> 1) & 1);
     src.at(0x7ffff000, lane);    // far past any unit
   }
 
   // sums = weights x activations over the unit in use.  off[p][n] is where this lane's column of group n
   // (any column, if it has none: its sums are dropped) begins; PASSES sets of columns are added
-  // into the same sums.  With scaled (FP16 only), 16 values of a column share an exponent:
-  // ex[n] are those of the lane's column, and they count from top[n].  Rows of activations reach to
-  // whole items (W4: 256 columns), with zeros.
+  // into the same sums.  With scaled (FP16 only), 16 values of a column share an exponent: ex[n] are those
+  // of the lane's column, and they count from top[n].  Rows of activations reach to whole items (W4: 256
+  // columns), with zeros.  False if a wait gave up.
   template <int NT, int PASSES>
-  __device__ __forceinline__ void run(Sums<NT>& sums, const Acts<SMEM>& from, const int (&off)[PASSES][NT],
+  __device__ __forceinline__ bool run(Sums<NT>& sums, const Acts<SMEM>& from, const int (&off)[PASSES][NT],
                                       bool scaled = false, const uint8_t* const* ex = nullptr,
                                       const int* top = nullptr) {
     const int t = lane & 3;
@@ -599,7 +613,10 @@ struct Stream {
         f1 = __ldg(sc1 + i);
       }
       const uint32_t bar = bars + (stage & 1) * 8, phase = (stage >> 1) & 1;
-      if (!warp_wait_for([&] { return gg::mbar_try_wait(bar, phase); }, dev_status)) dead = true;
+      if (!warp_wait_for([&] { return gg::mbar_try_wait(bar, phase); }, patience)) {
+        dead = i + 1 < n || (!pending && filled != END) ? 3 : 2;
+        return false;
+      }
       const uint8_t* st = ring + (stage & 1) * F::STAGE;
       Sums<NT> acc;
       if constexpr (FMT == F_E4M3) acc.clear();
@@ -658,6 +675,7 @@ struct Stream {
 #pragma unroll
         for (int q = 0; q < NT; ++q) at[p][q] += F::KI;
     }
+    return true;
   }
 };
 
@@ -666,7 +684,7 @@ struct Stream {
 // describe(t, part, cut, unit), and idle(), called every time round (true if it got something done).
 constexpr int BATCH = 16;            // units written down at a time
 template <int WORKERS, int SIZE, class Src>
-__device__ __forceinline__ void schedule(Feed<SIZE>& f, Src& src, int lane, int32_t* dev_status) {
+__device__ __forceinline__ void schedule(Feed<SIZE>& f, Src& src, int lane, const Patience& patience) {
   volatile int* use = f.use;
   int units = 0, t = 0, n = 0;
   bool end = false;
@@ -698,14 +716,7 @@ __device__ __forceinline__ void schedule(Feed<SIZE>& f, Src& src, int lane, int3
     if (moved) {
       t0 = clock_ns();
     } else {
-      if (__any_sync(0xffffffffu, clock_ns() - t0 > TIMEOUT_NS)) {   // let the workers go
-        if (lane == 0) {
-          if (dev_status) atomicOr(dev_status, MOE_DEV_PIPELINE_TIMEOUT);
-          if (!end) *static_cast<volatile int*>(&f.total) = units;
-        }
-        src.give_up(lane);
-        return;
-      }
+      if (__any_sync(0xffffffffu, patience.over() || patience.ran_out(t0))) return;   // the workers leave too
       __nanosleep(60);
     }
   }
@@ -730,14 +741,14 @@ __device__ __forceinline__ void join_init(JoinShared& j) {
 // ahead waits for it (units are taken in order and a tile has at most `slots` of them, so the wait
 // ends; it is bounded all the same).  It also waits for the first unit's slot, whose count the tile
 // uses: where tiles of more parts follow ones of fewer, the tile that had that slot before may
-// not be the one that had this unit's.  True on the warp that has the tile's sums; false also after
-// a timeout, which sets the status bit.
+// not be the one that had this unit's.  True on the warp that has the tile's sums; false also when a
+// wait gave up: the tile is never summed, and what else the CTA waits for gives up at once.
 template <int NT>
 __device__ __forceinline__ bool join(Sums<NT>& sums, JoinShared& j, float4* parts, int slots, int stride, int u, int u0,
-                                     int n, int lane, int32_t* dev_status) {
+                                     int n, int lane, const Patience& patience) {
   const int mine = u % slots, head = u0 % slots;
   volatile int* turn = j.turn;
-  if (!warp_wait_for([&] { return turn[mine] == u && turn[head] == u0; }, dev_status)) return false;
+  if (!warp_wait_for([&] { return turn[mine] == u && turn[head] == u0; }, patience)) return false;
   if (n > 1) {
     float4* p = parts + mine * stride;
 #pragma unroll

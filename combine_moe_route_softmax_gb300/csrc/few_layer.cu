@@ -46,10 +46,10 @@ extern "C" size_t moe_layer_few_workspace_bytes(const moe_few_desc_t* d) {
   return moe::few::plan_few(d, &p) ? p.total : 0;
 }
 
-extern "C" moe_status_t moe_layer_few(const moe_few_desc_t* d, const moe_few_weights_t* w, const uint16_t* x,
-                                      const float* logits, const int32_t* num_tokens, int32_t* topk_idx,
-                                      float* topk_w, uint16_t* out, void* ws, size_t ws_bytes, int32_t* dev_status,
-                                      void* stream) {
+static moe_status_t layer_few_impl(const moe_few_desc_t* d, const moe_few_weights_t* w, const uint16_t* x,
+                                   const float* logits, const int32_t* num_tokens, int32_t* topk_idx, float* topk_w,
+                                   uint16_t* out, void* ws, size_t ws_bytes, int32_t* dev_status,
+                                   unsigned long long limit_ns, void* stream) {
   using namespace moe;
   using namespace moe::few;
   FewPlan p;
@@ -103,6 +103,7 @@ extern "C" moe_status_t moe_layer_few(const moe_few_desc_t* d, const moe_few_wei
   a.x = x;
   a.out = out;
   a.dev_status = dev_status;
+  a.limit_ns = limit_ns;
   a.ctl = reinterpret_cast<uint32_t*>(b);
   a.tile_count = reinterpret_cast<int32_t*>(b + p.off_tile);
   a.entry_done = reinterpret_cast<int32_t*>(b + p.off_entry);
@@ -122,4 +123,22 @@ extern "C" moe_status_t moe_layer_few(const moe_few_desc_t* d, const moe_few_wei
     return MOE_ERR_CUDA;
   }
   return MOE_OK;
+}
+
+extern "C" moe_status_t moe_layer_few(const moe_few_desc_t* d, const moe_few_weights_t* w, const uint16_t* x,
+                                      const float* logits, const int32_t* num_tokens, int32_t* topk_idx,
+                                      float* topk_w, uint16_t* out, void* ws, size_t ws_bytes, int32_t* dev_status,
+                                      void* stream) {
+  return layer_few_impl(d, w, x, logits, num_tokens, topk_idx, topk_w, out, ws, ws_bytes, dev_status,
+                        moe::few::TIMEOUT_NS, stream);
+}
+
+// Test hook, deliberately absent from the public header: moe_layer_few with the limit of each wait in
+// nanoseconds instead of the built-in 2 s, so that a test can make a wait run out.
+extern "C" moe_status_t moe_testing_layer_few_wait_limit(const moe_few_desc_t* d, const moe_few_weights_t* w,
+                                                         const uint16_t* x, const float* logits,
+                                                         const int32_t* num_tokens, int32_t* topk_idx, float* topk_w,
+                                                         uint16_t* out, void* ws, size_t ws_bytes, int32_t* dev_status,
+                                                         unsigned long long limit_ns, void* stream) {
+  return layer_few_impl(d, w, x, logits, num_tokens, topk_idx, topk_w, out, ws, ws_bytes, dev_status, limit_ns, stream);
 }

@@ -80,6 +80,7 @@ struct LayerArgs {
   const uint16_t* x;
   uint16_t* out;
   int32_t* dev_status;
+  unsigned long long limit_ns; // of each wait
   // workspace, zero between launches
   uint32_t* ctl;               // barrier arrivals, barrier generation, next tile, CTAs done
   int32_t* tile_count;         // [H / 32] experts done of a row tile
@@ -104,6 +105,7 @@ struct LayerShared {
   Feed<MAX_WARPS - 1> feed;
   int ready;                   // leading entries whose h is ready
   int go;
+  int gave_up;                 // a wait of this CTA ran out
   float block[MAX_WARPS];
   short expert[kMaxEntries];   // E for the shared expert
   short first[kMaxEntries];    // first column in cols
@@ -134,14 +136,14 @@ __device__ __forceinline__ uint32_t barrier_arrive(uint32_t* bar) {
   }
   return gen;
 }
-__device__ __forceinline__ bool barrier_wait(uint32_t* bar, uint32_t gen, int32_t* dev_status) {
+__device__ __forceinline__ bool barrier_wait(uint32_t* bar, uint32_t gen, const Patience& patience) {
   const bool ok = wait_for(
       [&] {
         uint32_t now;
         asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(now) : "l"(bar + 1) : "memory");
         return now != gen;
       },
-      dev_status);
+      patience);
   __threadfence();
   return ok;
 }
@@ -309,9 +311,6 @@ struct LayerSched {
     __syncwarp();
     if (lane == 0) *static_cast<volatile int*>(&s.ready) = ready;
     return true;
-  }
-  __device__ __forceinline__ void give_up(int lane) {
-    if (lane == 0) *static_cast<volatile int*>(&s.ready) = s.n_entries;
   }
   __device__ __forceinline__ void describe(int t, int part, const Cut& c, Unit& u) const {
     const bool d = t >= s.n1;
@@ -573,8 +572,8 @@ __device__ __forceinline__ void do_unit(const LayerArgs& a, LayerShared& s, Laye
   }
   Sums<NT> sums;
   const Acts<false> from{down ? a.h_hi : HALF ? a.x16 : a.x, 0};
-  in.template run<NT, PASSES>(sums, from, off, HALF && down, ex, top);
-  if (!join<NT>(sums, s.join, parts, slots, stride, in.cur, in.cur - part, n, lane, a.dev_status)) return;
+  if (!in.template run<NT, PASSES>(sums, from, off, HALF && down, ex, top)) return;
+  if (!join<NT>(sums, s.join, parts, slots, stride, in.cur, in.cur - part, n, lane, in.patience)) return;
   if (!down) {
     store_h<HALF, NT>(a, s, sums, entry, row, lane);
     __syncwarp();
@@ -605,6 +604,8 @@ __global__ void __launch_bounds__(warps_of<FMT>() * 32, 1) layer_kernel(const __
   float2* scratch = reinterpret_cast<float2*>(rings + WORKERS * 2 * Format<FMT, GROUP>::STAGE);
   static_assert(ROUTE_SCRATCH * 8 <= PARTS_BYTES, "");
   uint32_t gen = 0;
+  const Patience patience{&s.gave_up, a.dev_status, a.limit_ns};
+  if (tid == 0) s.gave_up = 0;
   if (HALF)
     // by the last CTAs, which have the fewest router rows
     for (int t = gridDim.x - 1 - blockIdx.x; t < a.T; t += gridDim.x) token_to_half<WARPS>(a, s, t, tid);
@@ -616,7 +617,7 @@ __global__ void __launch_bounds__(warps_of<FMT>() * 32, 1) layer_kernel(const __
     if (tid == 0) gen = barrier_arrive(a.ctl);
   }
   if (a.w_router) {
-    if (tid == 0) s.go = barrier_wait(a.ctl, gen, a.dev_status);
+    if (tid == 0) s.go = barrier_wait(a.ctl, gen, patience);
     __syncthreads();
   }
   const float* logits = a.w_router ? a.logits : a.logits_in;
@@ -654,7 +655,7 @@ __global__ void __launch_bounds__(warps_of<FMT>() * 32, 1) layer_kernel(const __
   }
   if (tid == 0) {
     if (!sync) s.go = 1;
-    else if (!a.w_router) s.go = barrier_wait(a.ctl, gen, a.dev_status);
+    else if (!a.w_router) s.go = barrier_wait(a.ctl, gen, patience);
   }
   join_init(s.join);
   feed_init(s.feed);
@@ -667,7 +668,7 @@ __global__ void __launch_bounds__(warps_of<FMT>() * 32, 1) layer_kernel(const __
   }
   if (warp == WORKERS) {
     LayerSched<FMT, GROUP> src{a, s, 0, 0, 0, 0, 0};
-    schedule<WORKERS>(s.feed, src, lane, a.dev_status);
+    schedule<WORKERS>(s.feed, src, lane, patience);
   } else {
     constexpr int RING = 2 * Format<FMT, GROUP>::STAGE;
     float4* parts = reinterpret_cast<float4*>(rings + WORKERS * RING);
@@ -677,7 +678,7 @@ __global__ void __launch_bounds__(warps_of<FMT>() * 32, 1) layer_kernel(const __
     in.ring_addr = gg::smem_u32(in.ring);
     in.bars = gg::smem_u32(&s.feed.full[warp][0]);
     in.lane = lane;
-    in.dev_status = a.dev_status;
+    in.patience = patience;
     in.dx = a.tiled ? 0 : 128;
     in.dy = a.tiled ? 128 : 0;
     in.block = FMT == F_W4 ? w4_block(GROUP, a.zeros) : 0;
@@ -689,7 +690,10 @@ __global__ void __launch_bounds__(warps_of<FMT>() * 32, 1) layer_kernel(const __
       const bool down = in.src.unit(in.cur).down;
       const int nc = s.ncols[entry];
       if (down) {
-        if (!warp_wait_for([&] { return *ready > entry; }, a.dev_status)) in.dead = true;
+        if (!warp_wait_for([&] { return *ready > entry; }, patience)) {
+          in.dead = 1;
+          break;
+        }
         __threadfence_block();
         __syncwarp();
       }

@@ -39,6 +39,7 @@ struct LinearArgs {
   void* out;
   int out_f32;
   int32_t* dev_status;
+  unsigned long long limit_ns; // of each wait
   int nsl;                     // items per tile row
   int splits, split_len;       // shares of K, items per share
   Cut cut;                     // of a share
@@ -146,8 +147,8 @@ __device__ __forceinline__ void linear_unit(const LinearArgs& a, LinearStream<GR
 #pragma unroll
   for (int n = 0; n < NT; ++n) off[0][n] = (t0 + n * 8 + g < a.T ? n * 8 + g : 0) * a.pitch;
   Sums<NT> sums;
-  in.template run<NT, 1>(sums, Acts<true>{nullptr, xs}, off);
-  if (!join<NT>(sums, j, parts, a.slots, NT * 64, in.cur, in.cur - un.part, un.parts, lane, a.dev_status)) return;
+  if (!in.template run<NT, 1>(sums, Acts<true>{nullptr, xs}, off)) return;
+  if (!join<NT>(sums, j, parts, a.slots, NT * 64, in.cur, in.cur - un.part, un.parts, lane, in.patience)) return;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -222,6 +223,7 @@ template <int GROUP, int NT>
 __global__ void __launch_bounds__(lin_warps<NT>() * 32, 1) linear_w4_kernel(const __grid_constant__ LinearArgs a) {
   extern __shared__ __align__(1024) uint8_t rings[];
   __shared__ JoinShared j;
+  __shared__ int gave_up;                          // a wait of this CTA ran out
   constexpr int LIN_WARPS = lin_warps<NT>();
   __shared__ uint32_t most[LIN_COLS];              // largest finite |x| of a row, as bits
   __shared__ float unit[LIN_COLS];                 // what 1 in the FP16 row stands for
@@ -238,7 +240,8 @@ __global__ void __launch_bounds__(lin_warps<NT>() * 32, 1) linear_w4_kernel(cons
   in.ring_addr = gg::smem_u32(in.ring);
   in.bars = gg::smem_u32(&full[warp][0]);
   in.lane = lane;
-  in.dev_status = a.dev_status;
+  in.patience = {&gave_up, a.dev_status, a.limit_ns};
+  if (threadIdx.x == 0) gave_up = 0;
   in.block = w4_block(GROUP, a.zeros);
   in.zeros = a.zeros;
   if (lane == 0) {
@@ -489,10 +492,10 @@ extern "C" size_t moe_linear_w4_workspace_bytes(int T, int N, int K) {
   return align256(4 * (size_t)p.tiles) + std::max(sums, p.sum_bytes());
 }
 
-extern "C" moe_status_t moe_linear_w4(const uint16_t* x, int T, int K, long long x_stride, const uint8_t* packed, int N,
-                                      int group, int zeros, const float* bias, void* out, int out_f32,
-                                      long long out_stride, void* ws, size_t ws_bytes, int32_t* dev_status,
-                                      void* stream) {
+static moe_status_t linear_impl(const uint16_t* x, int T, int K, long long x_stride, const uint8_t* packed, int N,
+                                int group, int zeros, const float* bias, void* out, int out_f32, long long out_stride,
+                                void* ws, size_t ws_bytes, int32_t* dev_status, unsigned long long limit_ns,
+                                void* stream) {
   using namespace moe;
   using namespace moe::few;
   if (T < 0 || !w4_shape_ok(0, N, K, group) || (zeros != 0 && zeros != 1) || x_stride < K || x_stride % 8 ||
@@ -529,8 +532,29 @@ extern "C" moe_status_t moe_linear_w4(const uint16_t* x, int T, int K, long long
   a.count = static_cast<int32_t*>(ws);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + (ws_bytes - p.sum_bytes()) / 256 * 256);
   a.dev_status = dev_status;
+  a.limit_ns = limit_ns;
   cudaStream_t st = as_stream(stream);
   return group == 32   ? launch_linear<32>(a, p, st)
          : group == 64 ? launch_linear<64>(a, p, st)
                        : launch_linear<128>(a, p, st);
+}
+
+extern "C" moe_status_t moe_linear_w4(const uint16_t* x, int T, int K, long long x_stride, const uint8_t* packed, int N,
+                                      int group, int zeros, const float* bias, void* out, int out_f32,
+                                      long long out_stride, void* ws, size_t ws_bytes, int32_t* dev_status,
+                                      void* stream) {
+  return linear_impl(x, T, K, x_stride, packed, N, group, zeros, bias, out, out_f32, out_stride, ws, ws_bytes, dev_status,
+                     moe::few::TIMEOUT_NS, stream);
+}
+
+// Test hook, deliberately absent from the public header: moe_linear_w4 with the limit of each wait in
+// nanoseconds instead of the built-in 2 s, so that a test can make a wait run out.
+extern "C" moe_status_t moe_testing_linear_w4_wait_limit(const uint16_t* x, int T, int K, long long x_stride,
+                                                         const uint8_t* packed, int N, int group, int zeros,
+                                                         const float* bias, void* out, int out_f32,
+                                                         long long out_stride, void* ws, size_t ws_bytes,
+                                                         int32_t* dev_status, unsigned long long limit_ns,
+                                                         void* stream) {
+  return linear_impl(x, T, K, x_stride, packed, N, group, zeros, bias, out, out_f32, out_stride, ws, ws_bytes, dev_status,
+                     limit_ns, stream);
 }
