@@ -365,19 +365,19 @@ __global__ void __launch_bounds__(256) pack_w4_kernel(const uint8_t* __restrict_
 struct LinearPlan {
   int nt, slots, splits, split_len, pitch, ctas, smem;
   Cut cut;
-  long long tiles;
+  long long tiles, cost;
   size_t sum_bytes() const { return splits > 1 ? (size_t)tiles * splits * nt * 1024 : 0; }
 };
-inline LinearPlan plan_linear(int T, int N, int K, int group, int sms) {
+inline int linear_cols(int T) { return T < LIN_COLS ? T : LIN_COLS; }
+// With room for this many slots of the joins, which are as many as a tile may have units.
+inline LinearPlan plan_linear(int T, int N, int K, int group, int sms, int slots) {
   LinearPlan p;
-  const int cols = T < LIN_COLS ? T : LIN_COLS;
+  const int cols = linear_cols(T);
   p.nt = (cols + 7) / 8;
+  p.slots = slots;
   const int warps = p.nt == 1 ? lin_warps<1>() : lin_warps<4>();
-  // At least a tile's units.  9 with 24 columns leave room for half of K = 4096: 53 us for 24 x 40960,
-  // against 56 with 12 slots and thirds.
-  p.slots = p.nt == 1 ? 32 : p.nt == 2 ? 16 : p.nt == 3 ? 9 : 12;
   const int stage = 2 * (2048 + 8 * (256 / group) * 6);
-  const int fixed = warps * 2 * stage + p.slots * p.nt * 1024;
+  const int fixed = warps * 2 * stage + slots * p.nt * 1024;
   const int room = (LIN_SMEM - fixed) / 2 / cols - 32;      // elements of a row
   const int nsl = w4_slices(K), fit = room / 256 < 1 ? 1 : room / 256;
   p.splits = (nsl + fit - 1) / fit;
@@ -397,15 +397,25 @@ inline LinearPlan plan_linear(int T, int N, int K, int group, int sms) {
   // and 22.9 us, 7 x 7168 x 2048 7.5 and 8.1, others the same; with a cost of two instead of four 24 x 40960 x
   // 4096 takes 44.5 instead of 42.3.
   const long long mine = (p.tiles + p.ctas / p.splits - 1) / (p.ctas / p.splits);      // tiles of a CTA
-  long long best = 0;
   for (int parts = 1; parts <= p.slots && parts <= p.split_len; ++parts) {
     const int len = (p.split_len + parts - 1) / parts;
     const long long cost = (mine * parts + warps - 1) / warps * (len + UNIT_COST);
-    if (parts > 1 && cost >= best) continue;
-    best = cost;
+    if (parts > 1 && cost >= p.cost) continue;
+    p.cost = cost;
     p.cut.set(p.split_len, parts);
   }
   return p;
+}
+// 32 KB of slots, and one for each warp; with three or four column groups three for each four warps instead where the
+// shares of K that this saves make the rounds cheaper: 32 x 40960 x 4096, groups of 32, 58.7 us instead of 75.9 (four
+// shares, six); 32 x 7168 x 7168 25.0 instead of 33.2.  Where they do not, more slots are better: 25 x 2048 x 4096,
+// groups of 128, 12.3 us with 12, 14.3 with 9 and a share less.
+inline int linear_slots(int T) { return std::max(lin_warps<4>(), 32 / ((linear_cols(T) + 7) / 8)); }
+inline LinearPlan plan_linear(int T, int N, int K, int group, int sms) {
+  const LinearPlan p = plan_linear(T, N, K, group, sms, linear_slots(T));
+  if (p.nt < 3 || p.splits == 1) return p;
+  const LinearPlan q = plan_linear(T, N, K, group, sms, lin_warps<4>() * 3 / 4);
+  return q.cost < p.cost ? q : p;
 }
 
 template <int GROUP, int NT>
@@ -480,15 +490,16 @@ extern "C" moe_status_t moe_pack_w4(const uint8_t* q, const uint16_t* scales, co
 
 // The counters of the tiles at the start, the shares' sums at the end of what the caller has: a workspace
 // made for T serves fewer rows too, whose sums must not lie where more rows have counters.  So the sums get
-// what any T up to this one needs, with the group whose items leave least room for x.
+// what any T up to this one needs, with the group whose items leave least room for x and the most slots.
 extern "C" size_t moe_linear_w4_workspace_bytes(int T, int N, int K) {
   using namespace moe;
   using namespace moe::few;
   if (T < 0 || !w4_shape_ok(0, N, K, 32)) return 0;
   if (T == 0) return 256;
+  auto plan = [&](int t) { return plan_linear(t, N, K, 32, num_sms(), linear_slots(t)); };
   size_t sums = 0;
-  for (int t = 8; t < T && t < LIN_COLS; t += 8) sums = std::max(sums, plan_linear(t, N, K, 32, num_sms()).sum_bytes());
-  const LinearPlan p = plan_linear(T, N, K, 32, num_sms());
+  for (int t = 8; t < T && t < LIN_COLS; t += 8) sums = std::max(sums, plan(t).sum_bytes());
+  const LinearPlan p = plan(T);
   return align256(4 * (size_t)p.tiles) + std::max(sums, p.sum_bytes());
 }
 
