@@ -640,7 +640,7 @@ def moe_linear_w4(x, w, bias=None, out=None, out_dtype=torch.bfloat16, ws=None, 
 
 
 def moe_route_hidden_workspace(T=None, E=None, device="cuda"):
-    """A workspace for moe_route_hidden (zeroed once here)."""
+    """A workspace for moe_route_hidden (zeroed once here); one size serves all, whatever T and E."""
     return _zeroed(lib().moe_route_hidden_workspace_bytes(), device)
 
 

@@ -112,23 +112,19 @@ __device__ __forceinline__ void e4m3x4_to_half(uint32_t v, uint32_t& lo, uint32_
       : "r"(v));
 }
 
-// Eight 4-bit codes of one word minus their zero point -> four pairs (columns 0 1, 2 3, 4 5, 6 7).
+// Eight 4-bit codes of one word minus their zero point -> four FP16 pairs (columns 0 1, 2 3, 4 5, 6 7).
 // Column 2i sits at nibble i and 2i + 1 at nibble i + 4, so a mask leaves a pair of codes in
-// the low mantissa bits of two 16-bit halves.  BF16: 0x4300 | c is exactly 128 + c, and minus
-// (128 + z) is exact (as a multiply-add by one: BF16 has no plain addition).  FP16: 0x6400 | c is 1024 + c, and 0x6400 | 16 c is 1024 + 16 c, a
-// sixteenth of which minus (64 + z) is exact in one multiply-add: two shifts fewer.
-template <bool HALF>
+// the low mantissa bits of two 16-bit halves: 0x6400 | c is 1024 + c, and 0x6400 | 16 c is 1024 + 16 c, a
+// sixteenth of which minus (64 + z) is exact in one multiply-add, for any byte z.  Integers placed under a
+// fixed exponent and brought down by a subtraction are a published way of making floats of codes: Y. J.
+// Kim, R. Henry, R. Fahim, H. H. Awadalla, "Who Says Elephants Can't Run: Bringing Large Scale MoE Models into Cloud
+// Scale Production", 2022.
 struct W4Zero {
-  uint32_t a, b;               // -(128 + z); or 1024 + z and -(64 + z)
+  uint32_t a, b;               // 1024 + z and -(64 + z)
   // z in byte `sel` of the word
   __device__ __forceinline__ W4Zero(uint32_t z, int sel) {
-    if (HALF) {
-      a = __byte_perm(z, 0x64u, 0x4040 | sel * 0x0101);
-      asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(b) : "r"(a), "r"(0xbc00bc00u), "r"(0x63806380u));   // 960 - a
-    } else {
-      a = __byte_perm(z, 0xc3u, 0x4040 | sel * 0x0101);
-      b = 0;
-    }
+    a = __byte_perm(z, 0x64u, 0x4040 | sel * 0x0101);
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(b) : "r"(a), "r"(0xbc00bc00u), "r"(0x63806380u));   // 960 - a
   }
 };
 // (v & mask) | magic in one instruction: the magic number comes in a register, which the compiler
@@ -138,29 +134,19 @@ __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t m
   asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(v), "r"(mask), "r"(magic));
   return r;
 }
-template <bool HALF>
 __device__ __forceinline__ uint32_t w4_magic() {
   uint32_t r;
-  asm volatile("mov.b32 %0, %1;" : "=r"(r) : "n"(HALF ? 0x64006400 : 0x43004300));
+  asm volatile("mov.b32 %0, %1;" : "=r"(r) : "n"(0x64006400));
   return r;
 }
-template <bool HALF>
-__device__ __forceinline__ void w4_pairs(uint32_t v, const W4Zero<HALF>& z, uint32_t magic, uint32_t (&p)[4]) {
-  if (HALF) {
-    const uint32_t w = v >> 8;
-    const uint32_t c0 = and_or(v, 0x000f000fu, magic), c1 = and_or(v, 0x00f000f0u, magic);
-    const uint32_t c2 = and_or(w, 0x000f000fu, magic), c3 = and_or(w, 0x00f000f0u, magic);
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p[0]) : "r"(c0), "r"(z.a));
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p[1]) : "r"(c1), "r"(0x2c002c00u), "r"(z.b));   // 0x2c00 = 1/16
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p[2]) : "r"(c2), "r"(z.a));
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p[3]) : "r"(c3), "r"(0x2c002c00u), "r"(z.b));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t c = and_or(v >> (4 * i), 0x000f000fu, magic);
-      asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(p[i]) : "r"(c), "r"(0x3f803f80u), "r"(z.a));
-    }
-  }
+__device__ __forceinline__ void w4_pairs(uint32_t v, const W4Zero& z, uint32_t magic, uint32_t (&p)[4]) {
+  const uint32_t w = v >> 8;
+  const uint32_t c0 = and_or(v, 0x000f000fu, magic), c1 = and_or(v, 0x00f000f0u, magic);
+  const uint32_t c2 = and_or(w, 0x000f000fu, magic), c3 = and_or(w, 0x00f000f0u, magic);
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p[0]) : "r"(c0), "r"(z.a));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p[1]) : "r"(c1), "r"(0x2c002c00u), "r"(z.b));   // 0x2c00 = 1/16
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p[2]) : "r"(c2), "r"(z.a));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p[3]) : "r"(c3), "r"(0x2c002c00u), "r"(z.b));
 }
 
 // The power of two that brings a positive finite float (bits m) to [2^14, 2^15), as far as float32
@@ -342,7 +328,8 @@ __device__ __forceinline__ void half_item(Sums<NT>& sums, Sums<NT>& acc, const u
     // word j of the lane's 8 holds columns j*32 + t*8 .. + 8
     constexpr int WPG = GROUP / 32;   // words per scale group
     constexpr int HG = F::NG / 2;     // groups of half an item
-    const uint32_t magic = w4_magic<HALF>();
+    static_assert(HALF, "codes become FP16");
+    const uint32_t magic = w4_magic();
     uint32_t scs[2][HG], zps[2][(HG + 1) / 2];     // by half tile: BF16 pairs; bytes, two groups a word
     const uint8_t* par = stage + 2048 + (g * F::NG + J * HG) * 4;
     const uint8_t* zpar = stage + 2048 + F::SC + (g * F::NG + J * HG) * 2;
@@ -365,8 +352,8 @@ __device__ __forceinline__ void half_item(Sums<NT>& sums, Sums<NT>& acc, const u
 #pragma unroll
     for (int i0 = 0; i0 < 4; i0 += WPG) {
       const int gi = i0 / WPG, zb = (gi & 1) * 2;
-      const W4Zero<HALF> z[4] = {{zps[0][gi >> 1], zb}, {zps[0][gi >> 1], zb + 1}, {zps[1][gi >> 1], zb},
-                                 {zps[1][gi >> 1], zb + 1}};
+      const W4Zero z[4] = {{zps[0][gi >> 1], zb}, {zps[0][gi >> 1], zb + 1}, {zps[1][gi >> 1], zb},
+                           {zps[1][gi >> 1], zb + 1}};
       Sums<NT> part;
 #pragma unroll
       for (int i = i0; i < i0 + WPG; ++i) {
@@ -374,7 +361,7 @@ __device__ __forceinline__ void half_item(Sums<NT>& sums, Sums<NT>& acc, const u
         acts(b, i);
         uint32_t a[4][4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) w4_pairs<HALF>(word(q[r], i), z[r], magic, a[r]);
+        for (int r = 0; r < 4; ++r) w4_pairs(word(q[r], i), z[r], magic, a[r]);
 #pragma unroll
         for (int p = 0; p < PASSES; ++p) mma_step<HALF, NT>(part, a, b[p], i == i0 && p == 0);
       }
