@@ -525,11 +525,6 @@ def _need_word(t, what):
         raise ValueError(f"{what} is an int32 on the GPU")
 
 
-def _need_ws(ws):
-    if not (ws.is_cuda and ws.is_contiguous()):
-        raise ValueError("a workspace is a contiguous GPU tensor")
-
-
 class W4Packed:
     """4-bit weights in the kernels' order (moe_pack_w4): `mats` matrices of N rows, K columns,
     scales per `group` columns, zero points or not; data uint8 [mats, bytes].  [i] is one
@@ -617,8 +612,10 @@ def moe_linear_w4(x, w, bias=None, out=None, out_dtype=torch.bfloat16, ws=None, 
     N = w.N
     assert x.is_cuda and x.dtype is torch.bfloat16 and x.stride(1) == 1, "x is BF16 [T, K] on the GPU, rows dense"
     assert w.mats == 1 and w.K == K, "w is one matrix with x's K"
-    _need_tensor(bias, torch.float32, (N,), "bias")
-    _need_word(dev_status, "dev_status")
+    if bias is not None:
+        _need_tensor(bias, torch.float32, (N,), "bias")
+    if dev_status is not None:
+        _need_word(dev_status, "dev_status")
     if out is None:
         out = torch.empty(T, N, dtype=out_dtype, device=x.device)
         os = N
@@ -630,8 +627,8 @@ def moe_linear_w4(x, w, bias=None, out=None, out_dtype=torch.bfloat16, ws=None, 
     assert out_dtype is torch.bfloat16 or out_dtype is torch.float32, "out is BF16 or float32"
     if ws is None:
         ws = moe_linear_w4_workspace(T, N, K, x.device)
-    else:
-        _need_ws(ws)
+    elif not (ws.is_cuda and ws.is_contiguous()):
+        raise ValueError("ws is a contiguous GPU tensor")
     _check("moe_linear_w4", (_lib or lib()).moe_linear_w4(
         x.data_ptr(), T, K, x.stride(0) if T > 1 else K, w.data.data_ptr(), N, w.group, w.zeros,
         None if bias is None else bias.data_ptr(), out.data_ptr(), out_dtype is torch.float32, os, ws.data_ptr(),
@@ -653,10 +650,13 @@ def moe_route_hidden(x, w_router, K, bias=None, num_tokens=None, logits=None, to
     assert x.is_cuda and x.is_contiguous() and w_router.is_contiguous(), "expected contiguous CUDA tensors"
     assert x.dtype is torch.bfloat16 and w_router.dtype is torch.bfloat16
     T, H = x.shape
-    E = w_router.shape[0]
-    _need_tensor(w_router, torch.bfloat16, (E, H), "w_router")
-    _need_tensor(bias, torch.float32, (E,), "bias")
-    _need_word(num_tokens, "num_tokens")
+    E, wide = w_router.shape
+    if wide != H or not w_router.is_cuda:
+        raise ValueError("w_router is [E, H] on the GPU")
+    if bias is not None:
+        _need_tensor(bias, torch.float32, (E,), "bias")
+    if num_tokens is not None:
+        _need_word(num_tokens, "num_tokens")
     if logits is None:
         logits = torch.empty(T, E, dtype=torch.float32, device=x.device)
     else:
@@ -671,8 +671,8 @@ def moe_route_hidden(x, w_router, K, bias=None, num_tokens=None, logits=None, to
         _need_rows(topk_w, torch.float32, T, K, "topk_w")
     if ws is None:
         ws = moe_route_hidden_workspace(device=x.device)
-    else:
-        _need_ws(ws)
+    elif not (ws.is_cuda and ws.is_contiguous()):
+        raise ValueError("ws is a contiguous GPU tensor")
     _check("moe_route_hidden", (_lib or lib()).moe_route_hidden(
         x.data_ptr(), T, H, w_router.data_ptr(), _ptr(bias), E, K, _ptr(num_tokens), logits.data_ptr(),
         topk_idx.data_ptr(), topk_w.data_ptr(), ws.data_ptr(), ws.numel(), _stream(None)))
@@ -740,9 +740,12 @@ class MoeLayerFew:
             out = torch.empty_like(x)
         else:
             _need_rows(out, torch.bfloat16, t, H, "out")
-        _need_rows(logits, torch.float32, t, d.E, "logits")
-        _need_word(num_tokens, "num_tokens")
-        _need_word(dev_status, "dev_status")
+        if logits is not None:
+            _need_rows(logits, torch.float32, t, d.E, "logits")
+        if num_tokens is not None:
+            _need_word(num_tokens, "num_tokens")
+        if dev_status is not None:
+            _need_word(dev_status, "dev_status")
         if (topk_idx is None or topk_w is None) and self.weights.w_router is None and logits is None:
             raise ValueError("topk_idx and topk_w are needed: the layer has no router and no logits")
         if topk_idx is None:
