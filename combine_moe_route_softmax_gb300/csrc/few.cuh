@@ -5,8 +5,9 @@
 // The mathematics: y[n, c] = sum_k W[n, k] x[c, k] for a handful of columns c.  Every weight is
 // used a few times only, so the bound is reading W once; the arithmetic rides along on
 // mma.sync.m16n8k16 (16-bit operands, float32 sums), weights as the 16-row operand and activation
-// rows as the 8 columns -- 2 to 8 tensor instructions per KB of weights, far below any
-// tensor-core limit, which is why these kernels do not use the 128-row tcgen05 tiles.
+// rows as the 8 columns.  Per KB of weights and group of 8 columns these are 2 (BF16), 4 (E4M3) or 8 (4 bits)
+// tensor instructions, twice that with two terms of more than 4 columns: the tensor pipe is 7 to 12 %
+// busy in the layers, 29 % in the 24-row product, and a 128-row tcgen05 tile would have 1 to 32 columns of work.
 //
 // Work is cut into items: 32 weight rows (a row tile) x 128 bytes of K, 4 KB; a few neighbouring
 // items of a tile are a unit.  A CTA (one per SM) takes whole tiles, one after the other.  Its
@@ -19,7 +20,9 @@
 // was last.
 //
 // BF16 and E4M3 items keep up with the copies.  A 4-bit item holds four times the weights of a BF16 one and
-// takes 700 to 900 instructions (with its share of joins and results), so 4-bit layers run at 40 % of the copies' rate.
+// takes 700 to 900 instructions (with its share of joins and results), in one chain from the load of the codes to
+// the scaling of a group's sums; three warps to a scheduler (their 168 registers allow no more) use 37 to 41 % of its
+// issue slots, so 4-bit layers run at 40 % of the copies' rate, by latency before instructions.
 //
 // Measured with the copies alone (15 warps, two 4 KB stages each, two boxes of 16 rows an item):
 // 7.1 TB/s over 1.6 GB and 6.8 over 0.4 GB, row-major or tiled; three stages no faster; per-warp

@@ -23,13 +23,15 @@
 // power of two, so nothing has to wait for the whole of h but the largest exponent.
 //
 // Bound: reading the weights of the experts met once.  Measured (6.68 TB/s is the copy bandwidth):
-//   E4M3, 16 tokens at H = 7168, I = 2048, E = 256, top-8 + shared: 667-681 us, 6.7-6.8 TB/s
-//   E4M3, one token at those sizes: 82 us for 400 MB -- 10 until the experts are known, 60
+//   E4M3, 16 tokens at H = 7168, I = 2048, E = 256, top-8 + shared: 655-710 us with where the weights lie in
+//     memory, 6.4-6.9 TB/s (reads alone may pass the copy bandwidth)
+//   E4M3, one token at those sizes: 84 us for 400 MB -- 10 until the experts are known, 60
 //     streaming at the copy bandwidth, 8 from the average warp's last unit to the last combine, launch
-//   BF16, 5 tokens at H = 2048, I = 1408, E = 64, top-8: 84 us, 5.9 TB/s
-//   4 bits, one token at the E4M3 sizes: 72 us, 2.9 TB/s; 32 tokens at the BF16 sizes, groups of 32 with
-//     zero points: 126 us, 2.6 TB/s -- bound by unpacking (few.cuh)
-//   BF16, one token at H = 256, I = 512, E = 8, top-2: 18 us, latency throughout
+//   BF16, 5 tokens at H = 2048, I = 1408, E = 64, top-8: 85 us, 5.9 TB/s
+//   4 bits, one token at the E4M3 sizes: 75 us, 2.8 TB/s; 32 tokens at the BF16 sizes, groups of 32 with
+//     zero points: 141 us, 2.3 TB/s (126 with one term of h) -- latency of an item (few.cuh)
+//   BF16, one token at H = 256, I = 512, E = 8, top-2: 19 us, latency throughout
+// An expert's weights are read once for each 16 columns: a shared expert of 17 to 32 tokens twice.
 // An L2 prefetch of the shared expert while the routing is found out changed none of these.
 //
 // Roundings of h: one FP16 term keeps 11 bits, an error of 1.4e-4 of the output that moves one BF16
@@ -48,7 +50,8 @@ constexpr int MAX_WARPS = 16;
 // Warps of a CTA, the last of which schedules.  W4's unpacking wants more than the 128 registers a
 // thread has with 16 warps: 144 us with 12 warps, 157 with 14, 168 with 16 on 32 tokens at H = 2048,
 // I = 1408, E = 64, top-8, groups of 32; E4M3's does not: 720 us with 16 against 796 on 16 tokens at H = 7168, I = 2048,
-// E = 256, top-8.
+// E = 256, top-8 (both measured with one term of h).  At these limits 36 to 56 bytes of a thread's registers are
+// kept in local memory (W4, E4M3), around the variants of a unit.
 template <int FMT>
 __host__ __device__ constexpr int warps_of() { return FMT == F_W4 ? 12 : MAX_WARPS; }
 constexpr int PARTS_BYTES = 40 * 1024;      // slots of the joins

@@ -9,10 +9,10 @@
 // weights' bytes.  Where the rows are too long for that, K is shared between CTAs, whose sums the
 // last of them adds up in order.
 //
-// Bound: reading W once; in fact the unpacking and, with 24 columns, the tensor instructions.  Measured
-// (group 128 unless said otherwise): 24 x 40960 x 4096, float32 out 42 us (2.1 TB/s); 1 x 4096 x 7168
-// 7.8 us; 7 x 7168 x 2048, group 64, zero points, bias 7.5 us; 1 x 512 x 256, group 32 4.2 us
-// (launch and latency).
+// Bound: reading W once; in fact the latency of an item's unpacking (few.cuh) and, with 24 columns, the tensor
+// instructions (pipe 29 % busy).  Measured (group 128 unless said otherwise): 24 x 40960 x 4096, float32 out
+// 42.6 us (2.1 TB/s); 1 x 4096 x 7168 7.9 us; 7 x 7168 x 2048, group 64, zero points, bias 7.6 us; 1 x 512 x 256, group 32
+// 4.4 us (launch and latency).
 //
 // Also the one-time preparation of such weights: moe_quantize_weight_w4 and moe_pack_w4.
 #include <algorithm>

@@ -1,8 +1,9 @@
 // moe_route_hidden: router logits from hidden states, top-k and weights in one launch.
 // The warps share out the tasks of route_few.cuh; the CTA that finishes last selects.  Bound:
 // reading the router matrix (2 * E * H bytes) once; at these sizes it is in L2 and the
-// time is latency: 4.5 to 5.4 us for one token at H = 2048, E = 64, top-8; 6.8 at H = 7168, E = 256;
-// 10 to 13 for 32 tokens there, 2 to 3 of them the selection.
+// time is the latency of a few CTAs (at most 16 have work with 64 experts, 64 with 256): 4.5 to 5.5 us for one
+// token at H = 2048, E = 64, top-8; 6.8 to 7.8 at H = 7168, E = 256; 10 to 13 for 32 tokens there, 2 to 3 of them the
+// selection.
 #include <algorithm>
 
 #include "route_few.cuh"

@@ -64,7 +64,8 @@ typedef enum { MOE_EPI_NONE = 0, MOE_EPI_SWIGLU = 1 } moe_epilogue_t;
  * dispatch fake-quant options, 3 the batched expert layout, 4 the NVFP4 combine
  * and dispatch fake-quant (moe_combine_nvfp4, the dispatch_format arguments,
  * moe_layer_desc_t.combine_fq_format / dispatch_fq_format), 5 moe_grouped_gemm_pairs,
- * 6 the tiled weight layout: moe_pack_weights, MOE_W_TILED, moe_layer_desc_t.weight_tiles). */
+ * 6 the tiled weight layout: moe_pack_weights, MOE_W_TILED, moe_layer_desc_t.weight_tiles; the
+ * few-token calls came within 6: they change nothing that was there). */
 int moe_abi_version(void);
 /* Static, human-readable name of a status code. */
 const char* moe_status_string(moe_status_t s);
@@ -509,7 +510,7 @@ moe_status_t moe_layer_forward(const moe_layer_desc_t* d, const moe_layer_weight
  *   symmetric (zeros NULL): s = bf16_rn(amax / 7), code = clamp(rn(w / s), -8, 7) + 8;
  *   zero points: lo = min(0, min w), hi = max(0, max w), s = bf16_rn((hi - lo) / 15),
  *                z = clamp(rn(-lo / s), 0, 15), code = clamp(rn(w / s) + z, 0, 15);
- *   s is 1 where that is not positive; IEEE float32 steps, ties to even; w finite.
+ *   s is 1 where that is not positive; IEEE float32 steps, ties to even; |w| at most 1e38.
  * moe_pack_w4: the same values in the order the kernels read them, once per model: mats *
  *   moe_w4_packed_bytes(N, K, group, zeros given) bytes, 16-byte aligned, of blocks of 16 rows
  *   x 256 columns (codes, then the scales, then the zero points), row block major, whole
