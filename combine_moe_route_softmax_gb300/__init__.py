@@ -98,6 +98,12 @@ _SIGS = {
     "moe_route_hidden_workspace_bytes": ([], _Z),
     "moe_route_hidden": ([_P, _I, _I, _P, _P, _I, _I, _P, _P, _P, _P, _P, _Z, _P], _I),
     "moe_layer_few_workspace_bytes": ([ctypes.POINTER(FewDesc)], _Z),
+    "moe_rmsnorm": ([_P, _I, _I, _L, _P, _I, ctypes.c_float, _P, _I, _P, _P, _P, _P, _P, _P], _I),
+    "moe_linear_e4m3_workspace_bytes": ([_I, _I, _I], _Z),
+    "moe_linear_e4m3": ([_P, _P, _I, _I, _P, _P, _I, _P, _P, _I, _L, _P, _Z, _P, _P], _I),
+    "moe_permute_e4m3": ([_P, _I, _I, _I, _I, _I, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _Z, _P, _P, _P, _P], _I),
+    "moe_layer_forward_e4m3": ([ctypes.POINTER(LayerDesc), ctypes.POINTER(LayerWeights), _P, _P, _P, _P, _P, _P, _P,
+                                _P, _P, _Z, _P, _P], _I),
     "moe_layer_few": ([ctypes.POINTER(FewDesc), ctypes.POINTER(FewWeights), _P, _P, _P, _P, _P, _P, _P, _Z, _P, _P],
                       _I),
 }
@@ -462,10 +468,33 @@ class MoeLayer:
         return self.ws[off:off + n * torch.empty(0, dtype=dtype).element_size()].view(dtype).view(*shape)
 
     def forward(self, x, out, topk_idx, topk_w, logits=None, num_tokens=None, fq_scale=None, dev_status=None,
-                stream=None, dispatch_scale=None):
+                stream=None, dispatch_scale=None, x_scales=None):
+        """x_scales float32 [T, H/128]: x holds E4M3 codes (moe_layer_forward_e4m3; an E4M3 layer)."""
+        if x_scales is not None:
+            return self._forward_e4m3(x, x_scales, out, topk_idx, topk_w, logits, num_tokens, fq_scale, dev_status,
+                                      stream, dispatch_scale)
         _check("moe_layer_forward", lib().moe_layer_forward(
             ctypes.byref(self.desc), ctypes.byref(self.weights), _ptr(logits), _ptr(num_tokens), _ptr(topk_idx),
             _ptr(topk_w), _ptr(x), _ptr(fq_scale), _ptr(dispatch_scale), _ptr(out), _ptr(self.ws), self.ws.numel(),
+            _ptr(dev_status), _stream(stream)))
+        return out
+
+    def _forward_e4m3(self, x, x_scales, out, topk_idx, topk_w, logits, num_tokens, fq_scale, dev_status, stream,
+                      dispatch_scale):
+        d = self.desc
+        _need(d.dtype == MOE_E4M3, "x_scales: E4M3 rows go through an E4M3 layer")
+        _need(dispatch_scale is None, "E4M3 rows take no dispatch fake-quantisation")
+        _need_codes(x, d.T, d.H, "x")
+        _need_tensor(x_scales, torch.float32, (d.T, d.H // 128), "x_scales")
+        _need_tensor(out, torch.bfloat16, (d.T, d.H), "out")
+        _need_tensor(topk_idx, torch.int32, (d.T, d.K), "topk_idx")
+        _need_tensor(topk_w, torch.float32, (d.T, d.K), "topk_w")
+        _need_tensor(logits, torch.float32, (d.T, d.E), "logits")
+        _need_word(num_tokens, "num_tokens")
+        _need_word(dev_status, "dev_status")
+        _check("moe_layer_forward_e4m3", lib().moe_layer_forward_e4m3(
+            ctypes.byref(self.desc), ctypes.byref(self.weights), _ptr(logits), _ptr(num_tokens), _ptr(topk_idx),
+            _ptr(topk_w), _ptr(x), _ptr(x_scales), _ptr(fq_scale), _ptr(out), _ptr(self.ws), self.ws.numel(),
             _ptr(dev_status), _stream(stream)))
         return out
 
@@ -760,3 +789,155 @@ class MoeLayerFew:
             ctypes.byref(d), self._w, x.data_ptr(), _ptr(logits), _ptr(num_tokens), topk_idx.data_ptr(),
             topk_w.data_ptr(), out.data_ptr(), *self._ws, _ptr(dev_status), _stream(None)))
         return out, topk_idx, topk_w
+
+
+# ---------------------------------------------------------------- the 8-bit activation path
+def _need_codes(t, rows, cols, what):
+    """t: E4M3 codes [rows, cols] (uint8 or float8_e4m3fn), contiguous on the GPU, an address, or None."""
+    if t is None or isinstance(t, int):
+        return
+    if not (t.shape == (rows, cols) and (t.dtype is torch.uint8 or t.dtype is torch.float8_e4m3fn) and t.is_cuda and
+            t.is_contiguous()):
+        raise ValueError(f"{what}: expected contiguous E4M3 codes (uint8 or float8_e4m3fn) of shape {(rows, cols)} on the "
+                         f"GPU, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def moe_rmsnorm(x, weight, eps, residual=None, bf16=True, e4m3=False, out=None, q=None, q_scales=None,
+                residual_out=None, num_tokens=None, stream=None):
+    """x BF16 [T, H] (rows may be strided), weight [H] and residual [T, H] (or None) BF16 or float32 ->
+    (out BF16 [T, H], q uint8 [T, H], q_scales float32 [T, H/128], residual_out like residual).
+    Without out, q and q_scales, bf16 and e4m3 say which of them are made; with any of them exactly what is
+    given is written.  What is not asked for is None.  residual_out=residual adds in place.
+    num_tokens: int32 on the GPU; rows from it on are left as they were."""
+    if stream is not None:
+        return _run_on(stream, moe_rmsnorm, x, weight, eps, residual, bf16, e4m3, out, q, q_scales, residual_out,
+                       num_tokens)
+    if not (x.dim() == 2 and x.is_cuda and x.dtype is torch.bfloat16 and x.stride(1) == 1):
+        raise ValueError("x is BF16 [T, H] on the GPU, rows dense")
+    T, H = x.shape
+    w32 = weight.dtype is torch.float32
+    _need_tensor(weight, torch.float32 if w32 else torch.bfloat16, (H,), "weight")
+    _need((q is None) == (q_scales is None), "q and q_scales are given together")
+    if out is None and q is None:
+        _need(bf16 or e4m3, "one of bf16 and e4m3 is wanted")
+        if bf16:
+            out = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
+        if e4m3:
+            q = torch.empty(T, H, dtype=torch.uint8, device=x.device)
+            q_scales = torch.empty(T, H // 128, dtype=torch.float32, device=x.device)
+    else:
+        if out is not None:
+            _need_tensor(out, torch.bfloat16, (T, H), "out")
+        if q is not None:
+            _need_codes(q, T, H, "q")
+            _need_tensor(q_scales, torch.float32, (T, H // 128), "q_scales")
+    r32 = False
+    if residual is not None:
+        r32 = residual.dtype is torch.float32
+        _need_tensor(residual, torch.float32 if r32 else torch.bfloat16, (T, H), "residual")
+        if residual_out is None:
+            residual_out = torch.empty_like(residual)
+        else:
+            _need_tensor(residual_out, residual.dtype, (T, H), "residual_out")
+    else:
+        _need(residual_out is None, "residual_out without a residual")
+    if num_tokens is not None:
+        _need_word(num_tokens, "num_tokens")
+    _check("moe_rmsnorm", (_lib or lib()).moe_rmsnorm(
+        x.data_ptr(), T, H, x.stride(0) if T > 1 else H, weight.data_ptr(), w32, eps, _ptr(residual), r32,
+        _ptr(residual_out), _ptr(out), _ptr(q), _ptr(q_scales), _ptr(num_tokens), _stream(None)))
+    return out, q, q_scales, residual_out
+
+
+def moe_linear_e4m3_workspace(T, N, K, device="cuda"):
+    """A workspace for moe_linear_e4m3 (zeroed once here; each call leaves its counters zero)."""
+    nbytes = lib().moe_linear_e4m3_workspace_bytes(T, N, K)
+    if nbytes == 0:
+        raise MoeError("moe_linear_e4m3_workspace_bytes", 1)
+    return _zeroed(nbytes, device)
+
+
+def moe_linear_e4m3(x, x_scales, w, w_scales, bias=None, out=None, out_dtype=torch.bfloat16, ws=None, dev_status=None,
+                    stream=None):
+    """x E4M3 codes [T, K] with x_scales float32 [T, K/128], w E4M3 codes [N, K] with w_scales float32
+    [ceil(N/128), K/128] -> out [T, N] = x w^T (+ bias float32 [N]) in BF16 or float32 (rows of a given out
+    may be strided).  ws: a workspace kept from moe_linear_e4m3_workspace (made here otherwise); calls that
+    may overlap need one each."""
+    if stream is not None:
+        return _run_on(stream, moe_linear_e4m3, x, x_scales, w, w_scales, bias, out, out_dtype, ws, dev_status)
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x is [T, K] and w [N, K]")
+    (T, K), N = x.shape, w.shape[0]
+    _need_codes(x, T, K, "x")
+    _need_codes(w, N, K, "w")
+    _need_tensor(x_scales, torch.float32, (T, K // 128), "x_scales")
+    _need_tensor(w_scales, torch.float32, (-(-N // 128), K // 128), "w_scales")
+    if bias is not None:
+        _need_tensor(bias, torch.float32, (N,), "bias")
+    if dev_status is not None:
+        _need_word(dev_status, "dev_status")
+    if out is None:
+        out = torch.empty(T, N, dtype=out_dtype, device=x.device)
+        os = N
+    else:
+        _need(out.is_cuda and out.shape == (T, N) and out.stride(1) == 1, "out is [T, N] on the GPU, rows dense")
+        os = out.stride(0) if T > 1 else N
+        out_dtype = out.dtype
+    _need(out_dtype is torch.bfloat16 or out_dtype is torch.float32, "out is BF16 or float32")
+    if ws is None:
+        ws = moe_linear_e4m3_workspace(T, N, K, x.device)
+    elif not (ws.is_cuda and ws.is_contiguous() and ws.dtype is torch.uint8):
+        raise ValueError("ws is a workspace of moe_linear_e4m3_workspace")
+    _check("moe_linear_e4m3", (_lib or lib()).moe_linear_e4m3(
+        x.data_ptr(), x_scales.data_ptr(), T, K, w.data_ptr(), w_scales.data_ptr(), N,
+        None if bias is None else bias.data_ptr(), out.data_ptr(), out_dtype is torch.float32, os, ws.data_ptr(),
+        ws.numel(), None if dev_status is None else dev_status.data_ptr(), _stream(None)))
+    return out
+
+
+def moe_permute_e4m3(topk_idx, E, x, x_scales, with_shared=False, max_tokens=0, xp=None, xp_scales=None, ws=None,
+                     dev_status=None, topk_w=None, stream=None):
+    """moe_permute of rows that are E4M3 already: x codes [T, H], x_scales float32 [T, H/128].  Returns
+    moe_permute's dict, or with max_tokens > 0 moe_permute_batched's (xb, xb_scales, masked_m).
+    xp / xp_scales: buffers to write to ([rows, H], [rows, H/128]; rows past the last one stay as they are)."""
+    if stream is not None:
+        return _run_on(stream, moe_permute_e4m3, topk_idx, E, x, x_scales, with_shared, max_tokens, xp, xp_scales, ws,
+                       dev_status, topk_w)
+    if topk_idx.dim() != 2 or x.dim() != 2:
+        raise ValueError("topk_idx is [T, K] and x [T, H]")
+    (T, K), H = topk_idx.shape, x.shape[1]
+    dev, nseg = x.device, E + int(with_shared)
+    rows = nseg * max_tokens if max_tokens else T * K + (T if with_shared else 0)
+    _need_tensor(topk_idx, torch.int32, (T, K), "topk_idx")
+    _need_codes(x, T, H, "x")
+    _need_tensor(x_scales, torch.float32, (T, H // 128), "x_scales")
+    if xp is None:
+        xp = torch.empty(rows, H, dtype=torch.uint8, device=dev)
+    else:
+        _need_codes(xp, rows, H, "xp")
+    if xp_scales is None:
+        xp_scales = torch.empty(rows, H // 128, dtype=torch.float32, device=dev)
+    else:
+        _need_tensor(xp_scales, torch.float32, (rows, H // 128), "xp_scales")
+    ints = lambda *shape: torch.empty(*shape, dtype=torch.int32, device=dev)  # noqa: E731
+    cu, mm = (None, ints(nseg)) if max_tokens else (ints(nseg + 1), None)
+    src, inv, smap = ints(rows), ints(T, K), ints(T) if with_shared else None
+    roww = None
+    if topk_w is not None:
+        _need_tensor(topk_w, torch.float32, (T, K), "topk_w")
+        roww = torch.empty(rows, dtype=torch.float32, device=dev)
+    if dev_status is not None:
+        _need_word(dev_status, "dev_status")
+    if ws is None:
+        size = moe_permute_batched_workspace_bytes if max_tokens else moe_permute_workspace_bytes
+        ws = torch.empty(size(T, K, E, with_shared), dtype=torch.uint8, device=dev)
+    elif not (ws.is_cuda and ws.is_contiguous()):
+        raise ValueError("ws is a contiguous GPU tensor")
+    _check("moe_permute_e4m3", lib().moe_permute_e4m3(
+        _ptr(topk_idx), T, K, E, int(with_shared), max_tokens, _ptr(x), _ptr(x_scales), H, _ptr(xp), _ptr(xp_scales),
+        _ptr(cu), _ptr(mm), _ptr(src), _ptr(inv), _ptr(smap), _ptr(ws), ws.numel() * ws.element_size(), _ptr(dev_status),
+        _ptr(topk_w), _ptr(roww), _stream(None)))
+    maps = dict(src_row=src, inv_map=inv, shared_map=smap, row_weights=roww)
+    if max_tokens:
+        return dict(xb=xp.view(nseg, max_tokens, H), xb_scales=xp_scales.view(nseg, max_tokens, -1), masked_m=mm, **maps)
+    return dict(xp=xp, xp_scales=xp_scales, cu_seqlens=cu, **maps)

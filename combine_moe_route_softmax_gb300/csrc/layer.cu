@@ -93,12 +93,12 @@ extern "C" moe_status_t moe_layer_views(const moe_layer_desc_t* d, void* ws, moe
   return MOE_OK;
 }
 
-extern "C" moe_status_t moe_layer_forward(const moe_layer_desc_t* d, const moe_layer_weights_t* w,
-                                          const float* logits, const int32_t* num_tokens, int32_t* topk_idx,
-                                          float* topk_w, const uint16_t* x, const float* fq_scale,
-                                          const float* dispatch_scale, uint16_t* out, void* ws, size_t ws_bytes,
-                                          int32_t* dev_status, void* stream) {
-  using namespace moe;
+namespace moe {
+// x_scales non-null: x holds E4M3 codes with these scales (an E4M3 layer copies the rows).
+static moe_status_t layer_impl(const moe_layer_desc_t* d, const moe_layer_weights_t* w, const float* logits,
+                               const int32_t* num_tokens, int32_t* topk_idx, float* topk_w, const uint16_t* x,
+                               const float* x_scales, const float* fq_scale, const float* dispatch_scale, uint16_t* out,
+                               void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
   LayerPlan p;
   if (!plan_layer(d, &p) || !w) return MOE_ERR_ARG;
   if (!ws || ws_bytes < p.total) return MOE_ERR_WORKSPACE;
@@ -136,7 +136,7 @@ extern "C" moe_status_t moe_layer_forward(const moe_layer_desc_t* d, const moe_l
                       v.src_row, v.inv_map, v.shared_map, static_cast<uint8_t*>(ws) + p.off_scratch,
                       p.scratch_bytes, dev_status, dispatch_scale, wd ? topk_w : nullptr,
                       wd ? v.row_weights : nullptr, mt, v.masked_m, stream, v.counters, d->H / 128,
-                      d->dispatch_fq_format);
+                      d->dispatch_fq_format, x_scales);
     if (st != MOE_OK) return st;
     st = moe_grouped_gemm_batched(v.xp, v.xp_scales, v.masked_m, p.nseg, mt, d->H, 2 * d->I, w->w13,
                                   w->w13_scales, d->E, sx13, sx13s, gdt, MOE_EPI_SWIGLU, v.hs, v.hs_scales,
@@ -160,7 +160,7 @@ extern "C" moe_status_t moe_layer_forward(const moe_layer_desc_t* d, const moe_l
   st = permute_impl(topk_idx, d->T, d->K, d->E, d->has_shared, x, d->H, d->dtype, v.xp, v.xp_scales, v.cu_seqlens,
                     v.src_row, v.inv_map, v.shared_map, static_cast<uint8_t*>(ws) + p.off_scratch, p.scratch_bytes,
                     dev_status, dispatch_scale, wd ? topk_w : nullptr, wd ? v.row_weights : nullptr, 0, nullptr,
-                    stream, v.counters, d->H / 128, d->dispatch_fq_format);
+                    stream, v.counters, d->H / 128, d->dispatch_fq_format, x_scales);
   if (st != MOE_OK) return st;
   if (d->gemm_pairs) {
     st = moe_grouped_gemm_pairs(v.xp, v.cu_seqlens, p.nseg, p.cap, d->H, 2 * d->I, w->w13, d->E, sx13, MOE_EPI_SWIGLU,
@@ -194,4 +194,25 @@ extern "C" moe_status_t moe_layer_forward(const moe_layer_desc_t* d, const moe_l
                              d->has_shared ? v.y : nullptr, v.shared_map, fq_scale, out, stream);
   return moe_combine(v.y, v.inv_map, wd ? nullptr : topk_w, d->T, d->K, d->H, d->has_shared ? v.y : nullptr,
                      v.shared_map, fq_scale, out, stream);
+}
+}  // namespace moe
+
+extern "C" moe_status_t moe_layer_forward(const moe_layer_desc_t* d, const moe_layer_weights_t* w,
+                                          const float* logits, const int32_t* num_tokens, int32_t* topk_idx,
+                                          float* topk_w, const uint16_t* x, const float* fq_scale,
+                                          const float* dispatch_scale, uint16_t* out, void* ws, size_t ws_bytes,
+                                          int32_t* dev_status, void* stream) {
+  return moe::layer_impl(d, w, logits, num_tokens, topk_idx, topk_w, x, nullptr, fq_scale, dispatch_scale, out, ws,
+                         ws_bytes, dev_status, stream);
+}
+
+extern "C" moe_status_t moe_layer_forward_e4m3(const moe_layer_desc_t* d, const moe_layer_weights_t* w,
+                                               const float* logits, const int32_t* num_tokens, int32_t* topk_idx,
+                                               float* topk_w, const uint8_t* x, const float* x_scales,
+                                               const float* fq_scale, uint16_t* out, void* ws, size_t ws_bytes,
+                                               int32_t* dev_status, void* stream) {
+  if (!d || d->dtype != MOE_E4M3 || (d->T > 0 && !x_scales) || (reinterpret_cast<uintptr_t>(x_scales) & 3))
+    return MOE_ERR_ARG;
+  return moe::layer_impl(d, w, logits, num_tokens, topk_idx, topk_w, reinterpret_cast<const uint16_t*>(x), x_scales,
+                         fq_scale, nullptr, out, ws, ws_bytes, dev_status, stream);
 }

@@ -1,0 +1,197 @@
+// Root-mean-square norm of a residual stream ahead of a layer, with the residual's addition and
+// E4M3 rows out.  For a row of H columns, all in float32:
+//     h = x (+ residual)                      residual_out = h, rounded once to its type
+//     r = 1 / sqrt(sum(h^2) / H + eps)
+//     y = (h * r) * weight                    out = bf16(y)
+//     per 128 columns: s = amax|y| / 448 (1 if that is not positive), q = e4m3(y / s)
+// y is never rounded to BF16 on its way to the codes, and h is normalised as it was summed, not as
+// the residual keeps it: each output has one rounding.
+//
+// Bound by memory: x and the residual are read once and held in registers between the sum and the
+// outputs.  One block per row; a thread holds VPT vectors of 8 columns, vector j of thread t being
+// columns 8 (t + j * threads).. so that 16 lanes next to each other hold one 128-column block.
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace moe {
+namespace {
+
+struct NormArgs {
+  const uint16_t* x;
+  long long x_stride;
+  int T, H;
+  const void* weight;
+  int weight_f32;
+  float eps;
+  const void* residual;
+  int residual_f32;
+  void* residual_out;
+  uint16_t* out;
+  uint8_t* q;
+  float* q_scales;
+  const int32_t* num_tokens;
+};
+
+__device__ __forceinline__ void unpack8(const uint4 u, float (&f)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = (uint32_t)f32_to_bf16(f[2 * i]) | ((uint32_t)f32_to_bf16(f[2 * i + 1]) << 16);
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// RES: 0 no residual, 1 BF16, 2 float32.
+template <int VPT, int RES>
+__global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a) {
+  __shared__ float part[2][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  const int nvec = a.H / 8;
+  const int rows = a.num_tokens ? min(max(*a.num_tokens, 0), a.T) : a.T;
+  int side = 0;
+  for (int row = blockIdx.x; row < rows; row += gridDim.x, side ^= 1) {
+    float h[VPT][8];
+    float ss = 0.0f;
+    const uint4* xr = reinterpret_cast<const uint4*>(a.x + (size_t)row * a.x_stride);
+    uint4 xv[VPT], rv[RES == 2 ? 2 * VPT : VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = threadIdx.x + j * blockDim.x;
+      const bool ok = v < nvec;
+      xv[j] = ok ? xr[v] : make_uint4(0, 0, 0, 0);
+      if (RES == 1) {
+        const uint4* rr = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.residual) + (size_t)row * a.H);
+        rv[j] = ok ? rr[v] : make_uint4(0, 0, 0, 0);
+      }
+      if (RES == 2) {
+        const uint4* rr = reinterpret_cast<const uint4*>(static_cast<const float*>(a.residual) + (size_t)row * a.H);
+        rv[2 * j] = ok ? rr[2 * v] : make_uint4(0, 0, 0, 0);
+        rv[2 * j + 1] = ok ? rr[2 * v + 1] : make_uint4(0, 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      unpack8(xv[j], h[j]);
+      if (RES == 1) {
+        float r[8];
+        unpack8(rv[j], r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[j][i] = __fadd_rn(h[j][i], r[i]);
+      }
+      if (RES == 2) {
+        const uint32_t r[8] = {rv[2 * j].x, rv[2 * j].y, rv[2 * j].z, rv[2 * j].w,
+                               rv[2 * j + 1].x, rv[2 * j + 1].y, rv[2 * j + 1].z, rv[2 * j + 1].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[j][i] = __fadd_rn(h[j][i], __uint_as_float(r[i]));
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(h[j][i], h[j][i], ss);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+    if (lane == 0) part[side][warp] = ss;
+    __syncthreads();   // the other side was read before the barrier of the row before
+    ss = lane < nw ? part[side][lane] : 0.0f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+    const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)a.H), a.eps)));
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = threadIdx.x + j * blockDim.x;
+      const bool ok = v < nvec;
+      if (RES == 1 && ok)
+        reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.residual_out) + (size_t)row * a.H)[v] = pack8(h[j]);
+      if (RES == 2 && ok) {
+        float4* d = reinterpret_cast<float4*>(static_cast<float*>(a.residual_out) + (size_t)row * a.H) + 2 * v;
+        d[0] = make_float4(h[j][0], h[j][1], h[j][2], h[j][3]);
+        d[1] = make_float4(h[j][4], h[j][5], h[j][6], h[j][7]);
+      }
+      float w[8];
+      if (!ok) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = 0.0f;
+      } else if (a.weight_f32) {
+        const float4* wp = static_cast<const float4*>(a.weight) + 2 * v;
+        const float4 w0 = __ldg(wp), w1 = __ldg(wp + 1);
+        w[0] = w0.x, w[1] = w0.y, w[2] = w0.z, w[3] = w0.w, w[4] = w1.x, w[5] = w1.y, w[6] = w1.z, w[7] = w1.w;
+      } else {
+        unpack8(__ldg(static_cast<const uint4*>(a.weight) + v), w);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[j][i] = __fmul_rn(__fmul_rn(h[j][i], r), w[i]);
+      if (a.out && ok) reinterpret_cast<uint4*>(a.out + (size_t)row * a.H)[v] = pack8(h[j]);
+      if (a.q) {
+        float amax = 0.0f;
+        if (ok) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(h[j][i]));
+        }
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+        const float s = block_scale(amax);
+        uint32_t c[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i >> 2] |= (uint32_t)f32_to_e4m3(__fdiv_rn(h[j][i], s)) << (8 * (i & 3));
+        if (ok) {
+          reinterpret_cast<uint2*>(a.q + (size_t)row * a.H)[v] = make_uint2(c[0], c[1]);
+          if ((lane & 15) == 0) a.q_scales[(size_t)row * (a.H / 128) + v / 16] = s;
+        }
+      }
+    }
+  }
+}
+
+constexpr int kNormMaxH = 65536;   // 1024 threads of 8 vectors
+
+template <int VPT>
+void launch_norm(const NormArgs& a, int threads, cudaStream_t s) {
+  const int blocks = std::min(a.T, num_sms() * std::max(1, 2048 / threads));
+  if (!a.residual)
+    rmsnorm_kernel<VPT, 0><<<blocks, threads, 0, s>>>(a);
+  else if (!a.residual_f32)
+    rmsnorm_kernel<VPT, 1><<<blocks, threads, 0, s>>>(a);
+  else
+    rmsnorm_kernel<VPT, 2><<<blocks, threads, 0, s>>>(a);
+}
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+}  // namespace
+}  // namespace moe
+
+extern "C" moe_status_t moe_rmsnorm(const uint16_t* x, int T, int H, long long x_stride, const void* weight,
+                                    int weight_f32, float eps, const void* residual, int residual_f32,
+                                    void* residual_out, uint16_t* out, uint8_t* q, float* q_scales,
+                                    const int32_t* num_tokens, void* stream) {
+  using namespace moe;
+  if (T < 0 || H <= 0 || H % 8 != 0 || H > kNormMaxH || !(eps >= 0.0f)) return MOE_ERR_ARG;
+  if ((weight_f32 != 0 && weight_f32 != 1) || (residual_f32 != 0 && residual_f32 != 1)) return MOE_ERR_ARG;
+  if (T == 0) return MOE_OK;   // tensors without rows have no addresses
+  if (!out && !q) return MOE_ERR_ARG;
+  if (q && H % 128 != 0) return MOE_ERR_ARG;
+  if ((q != nullptr) != (q_scales != nullptr) || (residual != nullptr) != (residual_out != nullptr)) return MOE_ERR_ARG;
+  if (!x || !weight || x_stride % 8 != 0 || (T > 1 && x_stride < H)) return MOE_ERR_ARG;
+  if (!aligned16(x) || !aligned16(weight) || !aligned16(residual) || !aligned16(residual_out) || !aligned16(out) ||
+      (reinterpret_cast<uintptr_t>(q) & 7) || (reinterpret_cast<uintptr_t>(q_scales) & 3) ||
+      (reinterpret_cast<uintptr_t>(num_tokens) & 3))
+    return MOE_ERR_ARG;
+  NormArgs a{x, x_stride, T, H, weight, weight_f32, eps, residual, residual_f32, residual_out, out, q, q_scales, num_tokens};
+  cudaStream_t s = as_stream(stream);
+  const int nvec = H / 8;
+  auto threads = [&](int vpt) { return ((nvec + vpt - 1) / vpt + 31) / 32 * 32; };
+  if (threads(1) <= 1024 && T <= num_sms())
+    launch_norm<1>(a, threads(1), s);
+  else if (threads(4) <= 1024)
+    launch_norm<4>(a, threads(4), s);
+  else
+    launch_norm<8>(a, threads(8), s);
+  MOE_CHECK_LAUNCH();
+  return MOE_OK;
+}

@@ -258,13 +258,24 @@ __global__ void __launch_bounds__(kPermThreads) permute_scatter_kernel(
   }
 }
 
-// Destination rows of token t: its valid slots' rows (inv_map) and its shared row.  Lane
-// k < K holds the row of slot k, lane K the shared row (or -1).
-__device__ __forceinline__ int token_dest(const int32_t* __restrict__ inv_map, const int32_t* __restrict__ shared_map,
-                                          int t, int K, int lane) {
-  if (lane < K) return inv_map[(size_t)t * K + lane];
-  if (lane == K && shared_map) return shared_map[t];
-  return -1;
+// Destination rows of token t: lane k < K holds the row of slot k (or -1); the token's shared row (or -1) is the
+// same on every lane, since 32 slots leave no lane of its own for it.  A token with a shared row has a
+// slot with a row.
+__device__ __forceinline__ int token_dest(const int32_t* __restrict__ inv_map, int t, int K, int lane) {
+  return lane < K ? inv_map[(size_t)t * K + lane] : -1;
+}
+__device__ __forceinline__ int shared_dest(const int32_t* __restrict__ shared_map, int t) {
+  return shared_map ? shared_map[t] : -1;
+}
+// copy(row, routed) for each of them, by the whole warp.
+template <class F>
+__device__ __forceinline__ void for_each_dest(unsigned live, int my_dst, int shared_row, F&& copy) {
+  while (live) {
+    const int d = __ffs(live) - 1;
+    live &= live - 1;
+    copy(__shfl_sync(0xffffffffu, my_dst, d), true);
+  }
+  if (shared_row >= 0) copy(shared_row, false);
 }
 
 // Dispatch fake-quant of 8 BF16 values: bf16(e4m3(x * s) / s), float32 steps; the division
@@ -326,7 +337,6 @@ __global__ void __launch_bounds__(256) permute_gather_bf16_kernel(const uint16_t
   const int nw = (gridDim.x * blockDim.x) >> 5;
   const int nvec = H / 8;
   const int per_part = ((nvec + 127) / 128 + splits - 1) / splits * 128;   // vectors, whole groups
-  const int ndst = K + 1;
   const float s = DQ ? *dq_scale : 1.0f;
   __shared__ float dq_tbl[DQ == 1 ? 256 : 1];
   __shared__ float inv_tbl[DQ == 2 ? 256 : 1], d_tbl[DQ == 2 ? 256 : 1];
@@ -347,9 +357,10 @@ __global__ void __launch_bounds__(256) permute_gather_bf16_kernel(const uint16_t
     const int t = item / splits;
     const int v_begin = (item - t * splits) * per_part;
     const int v_end = min(nvec, v_begin + per_part);
-    const int my_dst = token_dest(inv_map, shared_map, t, K, lane);
-    const unsigned live = __ballot_sync(0xffffffffu, lane < ndst && my_dst >= 0);
+    const int my_dst = token_dest(inv_map, t, K, lane);
+    const unsigned live = __ballot_sync(0xffffffffu, my_dst >= 0);
     if (!live) continue;                      // padding token: nothing to copy
+    const int shared_row = shared_dest(shared_map, t);
     const uint4* in = reinterpret_cast<const uint4*>(x + (size_t)t * H);
     for (int v0 = v_begin; v0 < v_end; v0 += 128) {
       uint4 r[4], q[4];
@@ -365,24 +376,19 @@ __global__ void __launch_bounds__(256) permute_gather_bf16_kernel(const uint16_t
         // zeros, and so does its partner (parts hold whole 128-vector groups, v_end is even)
         if (DQ == 2) q[j] = qdq8_nvfp4(r[j], s, inv_tbl, d_tbl);
       }
-      unsigned m = live;
-      while (m) {
-        const int d = __ffs(m) - 1;
-        m &= m - 1;
-        const int row = __shfl_sync(0xffffffffu, my_dst, d);
-        const bool routed = d < K;
+      for_each_dest(live, my_dst, shared_row, [&](int row, bool routed) {
         uint4* o = reinterpret_cast<uint4*>(xp + (size_t)row * H);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int v = v0 + lane + 32 * j;
           if (v < v_end) o[v] = (DQ != 0 && routed) ? q[j] : r[j];
         }
-      }
+      });
     }
   }
 }
 
-// ------------------------------------------------------- TMA-staged gather (BF16 rows)
+// ---------------------------------------- TMA-staged gather (BF16 rows, or E4M3 rows with scales)
 // One bulk copy (cp.async.bulk) brings a token's row into shared memory; one bulk store per
 // destination row writes it out as a single contiguous transfer.  Each warp runs a two-deep
 // pipeline (the next token's row loads while the current one is stored); lane 0 issues the
@@ -422,15 +428,20 @@ __device__ __forceinline__ bool bulk_bar_wait(uint32_t bar, uint32_t parity) {
   }
 }
 
-__global__ void __launch_bounds__(256) permute_gather_bf16_bulk_kernel(const uint16_t* __restrict__ x, int T, int K,
-                                                                       int H, const int32_t* __restrict__ inv_map,
-                                                                       const int32_t* __restrict__ shared_map,
-                                                                       uint16_t* __restrict__ xp,
-                                                                       int32_t* dev_status) {
+// SCALES: rows that are E4M3 already (one byte per column), each with its H / 128 scales; the
+// scales of a row (a few hundred bytes, not always whole 16-byte pieces) go through registers.
+template <bool SCALES>
+__global__ void __launch_bounds__(256) permute_gather_bulk_kernel(const uint8_t* __restrict__ x, int T, int K, int H,
+                                                                  const int32_t* __restrict__ inv_map,
+                                                                  const int32_t* __restrict__ shared_map,
+                                                                  uint8_t* __restrict__ xp,
+                                                                  const float* __restrict__ x_scales,
+                                                                  float* __restrict__ xp_scales,
+                                                                  int32_t* dev_status) {
   extern __shared__ __align__(128) uint8_t gsm[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int nwarps = blockDim.x >> 5;
-  const uint32_t row_bytes = static_cast<uint32_t>(H) * 2;
+  const uint32_t row_bytes = static_cast<uint32_t>(H) * (SCALES ? 1 : 2);
   const uint32_t buf_stride = (row_bytes + 127) / 128 * 128;
   uint64_t* bars = reinterpret_cast<uint64_t*>(gsm);                       // [nwarps][2]
   uint8_t* bufs = gsm + 128 + static_cast<size_t>(warp) * 2 * buf_stride;  // this warp's two rows
@@ -442,13 +453,11 @@ __global__ void __launch_bounds__(256) permute_gather_bf16_bulk_kernel(const uin
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncwarp();
-  const int ndst = K + 1;
   const int nw = gridDim.x * nwarps;
   // the next token (stride nw) that has a row to write, or T
   auto next_live = [&](int t) {
     for (; t < T; t += nw) {
-      const int d = token_dest(inv_map, shared_map, t, K, lane);
-      if (__ballot_sync(0xffffffffu, lane < ndst && d >= 0)) return t;
+      if (__ballot_sync(0xffffffffu, token_dest(inv_map, t, K, lane) >= 0)) return t;
     }
     return T;
   };
@@ -456,18 +465,32 @@ __global__ void __launch_bounds__(256) permute_gather_bf16_bulk_kernel(const uin
   int b = 0;
   uint32_t phases = 0;              // bit i: parity of buffer i's next load
   bool loading_next = false;        // a load into buffer b ^ 1 is in flight
-  if (lane == 0 && cur < T) bulk_row_load(buf0, x + (size_t)cur * H, row_bytes, bar0);
+  if (lane == 0 && cur < T) bulk_row_load(buf0, x + (size_t)cur * row_bytes, row_bytes, bar0);
   while (cur < T) {
     const int nxt = next_live(cur + nw);
-    const int my_dst = token_dest(inv_map, shared_map, cur, K, lane);
-    const unsigned live = __ballot_sync(0xffffffffu, lane < ndst && my_dst >= 0);
+    const int my_dst = token_dest(inv_map, cur, K, lane);
+    const int shared_row = shared_dest(shared_map, cur);
+    const unsigned live = __ballot_sync(0xffffffffu, my_dst >= 0);
     const uint32_t nb = static_cast<uint32_t>(b ^ 1);
     if (lane == 0 && nxt < T) {
       // the stores of the token before `cur` read buffer nb: let them finish reading
       asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-      bulk_row_load(buf0 + nb * buf_stride, x + (size_t)nxt * H, row_bytes, bar0 + 8 * nb);
+      bulk_row_load(buf0 + nb * buf_stride, x + (size_t)nxt * row_bytes, row_bytes, bar0 + 8 * nb);
     }
     loading_next = nxt < T;
+    if (SCALES) {
+      const int nblk = H / 128;
+      for (int b0 = 0; b0 < nblk; b0 += 64) {
+        const bool ok0 = b0 + lane < nblk, ok1 = b0 + 32 + lane < nblk;
+        const float s0 = ok0 ? x_scales[(size_t)cur * nblk + b0 + lane] : 0.0f;
+        const float s1 = ok1 ? x_scales[(size_t)cur * nblk + b0 + 32 + lane] : 0.0f;
+        for_each_dest(live, my_dst, shared_row, [&](int row, bool) {
+          float* dst = xp_scales + (size_t)row * nblk + b0 + lane;
+          if (ok0) dst[0] = s0;
+          if (ok1) dst[32] = s1;
+        });
+      }
+    }
     bool ok = true;
     if (lane == 0) ok = bulk_bar_wait(bar0 + 8 * b, (phases >> b) & 1u);
     ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -479,13 +502,9 @@ __global__ void __launch_bounds__(256) permute_gather_bf16_bulk_kernel(const uin
       break;
     }
     phases ^= 1u << b;
-    unsigned m = live;
-    while (m) {
-      const int d = __ffs(m) - 1;
-      m &= m - 1;
-      const int row = __shfl_sync(0xffffffffu, my_dst, d);
-      if (lane == 0) bulk_row_store(xp + (size_t)row * H, buf0 + b * buf_stride, row_bytes);
-    }
+    for_each_dest(live, my_dst, shared_row, [&](int row, bool) {
+      if (lane == 0) bulk_row_store(xp + (size_t)row * row_bytes, buf0 + b * buf_stride, row_bytes);
+    });
     if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     cur = nxt;
     b = static_cast<int>(nb);
@@ -535,14 +554,14 @@ __global__ void __launch_bounds__(256) permute_gather_e4m3_kernel(const uint16_t
   const int nblk = H / 128;
   // parts of whole 32-vector groups (two 1x128 blocks), so each half-warp keeps one block
   const int per_part = ((nvec + 31) / 32 + splits - 1) / splits * 32;
-  const int ndst = K + 1;
   for (int item = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; item < T * splits; item += nw) {
     const int t = item / splits;
     const int v_begin = (item - t * splits) * per_part;
     const int v_end = min(nvec, v_begin + per_part);
-    const int my_dst = token_dest(inv_map, shared_map, t, K, lane);
-    const unsigned live = __ballot_sync(0xffffffffu, lane < ndst && my_dst >= 0);
+    const int my_dst = token_dest(inv_map, t, K, lane);
+    const unsigned live = __ballot_sync(0xffffffffu, my_dst >= 0);
     if (!live) continue;
+    const int shared_row = shared_dest(shared_map, t);
     const uint4* in = reinterpret_cast<const uint4*>(x + (size_t)t * H);
     for (int v0 = v_begin; v0 < v_end; v0 += 32) {
       const int v = v0 + lane;
@@ -550,16 +569,12 @@ __global__ void __launch_bounds__(256) permute_gather_e4m3_kernel(const uint16_t
       const uint4 u = ok ? __ldg(in + v) : make_uint4(0, 0, 0, 0);
       float s;
       const uint2 q = quant8(u, ok, &s);
-      unsigned m = live;
-      while (m) {
-        const int d = __ffs(m) - 1;
-        m &= m - 1;
-        const int row = __shfl_sync(0xffffffffu, my_dst, d);
+      for_each_dest(live, my_dst, shared_row, [&](int row, bool) {
         if (ok) {
           reinterpret_cast<uint2*>(xp + (size_t)row * H)[v] = q;
           if ((lane & 15) == 0) xp_scales[(size_t)row * nblk + v / 16] = s;
         }
-      }
+      });
     }
   }
 }
@@ -583,6 +598,9 @@ __global__ void __launch_bounds__(256) quant_act_kernel(const uint16_t* __restri
     }
   }
 }
+
+// Shared memory of a bulk gather block: barriers, then two rows per warp.
+constexpr int kBulkSmem = 232448;
 
 inline int perm_blocks(int T) { return (T + kChunkTok - 1) / kChunkTok; }
 
@@ -624,7 +642,7 @@ moe_status_t permute_impl(const int32_t* topk_idx, int T, int K, int E, int with
                           int32_t* src_row, int32_t* inv_map, int32_t* shared_map, void* ws, size_t ws_bytes,
                           int32_t* dev_status, const float* dq_scale, const float* topk_w, float* row_w,
                           int max_tokens, int32_t* masked_m, void* stream, int32_t* zero_buf,
-                          int zero_per_token, int dq_format){
+                          int zero_per_token, int dq_format, const float* x_scales) {
   if (T < 0 || K < 1 || K > kMaxTopK || E < 1 || E > kMaxExperts || H <= 0 || H % 128 != 0) return MOE_ERR_ARG;
   if (with_shared != 0 && with_shared != 1) return MOE_ERR_ARG;
   if (out_dtype != MOE_BF16 && out_dtype != MOE_E4M3) return MOE_ERR_ARG;
@@ -646,6 +664,8 @@ moe_status_t permute_impl(const int32_t* topk_idx, int T, int K, int E, int with
   }
   if (!topk_idx || !x || !xp || !src_row || !inv_map || (with_shared && !shared_map)) return MOE_ERR_ARG;
   if (out_dtype == MOE_E4M3 && !xp_scales) return MOE_ERR_ARG;
+  // rows that are E4M3 already: two of them per warp stand in shared memory
+  if (x_scales && (out_dtype != MOE_E4M3 || H > kBulkSmem / 2 - 128)) return MOE_ERR_UNSUPPORTED;
   if (dq_scale && out_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   if (dq_format != 0 && dq_format != 1) return MOE_ERR_ARG;
   if (row_w && !topk_w) return MOE_ERR_ARG;
@@ -684,19 +704,24 @@ moe_status_t permute_impl(const int32_t* topk_idx, int T, int K, int E, int with
   const int32_t* smap = with_shared ? shared_map : nullptr;
   // BF16 rows without dispatch fake-quant: TMA-staged gather, one 8-warp block per SM (two
   // row buffers per warp) when two rows per warp fit in shared memory
-  const size_t row_buf = ((size_t)H * 2 + 127) / 128 * 128;
-  const int bulk_warps = (int)std::min<size_t>(8, (232448 - 128) / (2 * row_buf));
-  if (out_dtype == MOE_BF16 && !dq_scale && bulk_warps >= 1) {
-    const size_t smem = 128 + (size_t)bulk_warps * 2 * row_buf;
+  const size_t row_buf = ((size_t)H * (x_scales ? 1 : 2) + 127) / 128 * 128;
+  int bulk_warps = (int)std::min<size_t>(8, (kBulkSmem - 128) / (2 * row_buf));
+  if (x_scales || (out_dtype == MOE_BF16 && !dq_scale && bulk_warps >= 1)) {
     static std::atomic<unsigned long long> attr_done{0};
     if (!once_per_device(attr_done, [&] {
-          return cudaFuncSetAttribute(permute_gather_bf16_bulk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      232448) == cudaSuccess;
+          return cudaFuncSetAttribute(permute_gather_bulk_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      kBulkSmem) == cudaSuccess &&
+                 cudaFuncSetAttribute(permute_gather_bulk_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      kBulkSmem) == cudaSuccess;
         }))
       return MOE_ERR_CUDA;
+    // rows with scales: few tokens are spread over the SMs before a block takes a second one
+    if (x_scales) bulk_warps = std::min(bulk_warps, (T + num_sms() - 1) / num_sms());
+    const size_t smem = 128 + (size_t)bulk_warps * 2 * row_buf;
     const int blocks = std::max(1, std::min(num_sms(), (T + bulk_warps - 1) / bulk_warps));
-    permute_gather_bf16_bulk_kernel<<<blocks, bulk_warps * 32, smem, s>>>(x, T, K, H, inv_map, smap,
-                                                                          static_cast<uint16_t*>(xp), dev_status);
+    auto kernel = x_scales ? permute_gather_bulk_kernel<true> : permute_gather_bulk_kernel<false>;
+    kernel<<<blocks, bulk_warps * 32, smem, s>>>(reinterpret_cast<const uint8_t*>(x), T, K, H, inv_map, smap,
+                                                 static_cast<uint8_t*>(xp), x_scales, xp_scales, dev_status);
   } else if (out_dtype == MOE_BF16)
     if (dq_scale && dq_format == 1)
       permute_gather_bf16_kernel<2><<<gblocks, 256, 0, s>>>(x, T, K, H, inv_map, smap, dq_scale,
@@ -747,6 +772,17 @@ extern "C" moe_status_t moe_permute_batched(const int32_t* topk_idx, int T, int 
   return moe::permute_impl(topk_idx, T, K, E, with_shared, x, H, out_dtype, xb, xb_scales, nullptr, src_row,
                            inv_map, shared_map, ws, ws_bytes, dev_status, dispatch_scale, topk_w, row_weights,
                            max_tokens, masked_m, stream, nullptr, 0, dispatch_format);
+}
+
+extern "C" moe_status_t moe_permute_e4m3(const int32_t* topk_idx, int T, int K, int E, int with_shared, int max_tokens,
+                                         const uint8_t* x, const float* x_scales, int H, uint8_t* xp, float* xp_scales,
+                                         int32_t* cu_seqlens, int32_t* masked_m, int32_t* src_row, int32_t* inv_map,
+                                         int32_t* shared_map, void* ws, size_t ws_bytes, int32_t* dev_status,
+                                         const float* topk_w, float* row_weights, void* stream) {
+  if (max_tokens < 0 || (T > 0 && !x_scales) || (reinterpret_cast<uintptr_t>(x_scales) & 3)) return MOE_ERR_ARG;
+  return moe::permute_impl(topk_idx, T, K, E, with_shared, reinterpret_cast<const uint16_t*>(x), H, MOE_E4M3, xp,
+                           xp_scales, cu_seqlens, src_row, inv_map, shared_map, ws, ws_bytes, dev_status, nullptr,
+                           topk_w, row_weights, max_tokens, masked_m, stream, nullptr, 0, 0, x_scales);
 }
 
 extern "C" moe_status_t moe_quantize_act_fp8(const uint16_t* x, int rows, int cols, uint8_t* q, float* scales,

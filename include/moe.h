@@ -65,7 +65,7 @@ typedef enum { MOE_EPI_NONE = 0, MOE_EPI_SWIGLU = 1 } moe_epilogue_t;
  * and dispatch fake-quant (moe_combine_nvfp4, the dispatch_format arguments,
  * moe_layer_desc_t.combine_fq_format / dispatch_fq_format), 5 moe_grouped_gemm_pairs,
  * 6 the tiled weight layout: moe_pack_weights, MOE_W_TILED, moe_layer_desc_t.weight_tiles; the
- * few-token calls came within 6: they change nothing that was there). */
+ * few-token calls and the 8-bit activation path came within 6: they change nothing that was there). */
 int moe_abi_version(void);
 /* Static, human-readable name of a status code. */
 const char* moe_status_string(moe_status_t s);
@@ -608,6 +608,72 @@ size_t moe_layer_few_workspace_bytes(const moe_few_desc_t* d);
 moe_status_t moe_layer_few(const moe_few_desc_t* d, const moe_few_weights_t* w, const uint16_t* x,
                            const float* logits, const int32_t* num_tokens, int32_t* topk_idx, float* topk_w,
                            uint16_t* out, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* ======================================================================================
+ * The 8-bit activation path: E4M3 rows with a float32 scale per 1x128 block (the format of
+ * moe_quantize_act_fp8) made by the norm ahead of a layer, moved as they are, and multiplied with E4M3
+ * weights outside the experts.  (The pages have no counterpart: these are additions of this library.
+ * [DeepEP]: the dispatch ships "tokens, and scales".) */
+
+/* Root-mean-square norm with the residual's addition, float32 steps:
+ *     h = x (+ residual);  r = 1 / sqrt(sum_H h^2 / H + eps);  y = (h * r) * weight
+ * residual_out = h rounded once to its type, out = bf16_rn(y), and per 128 columns
+ * s = amax|y| / 448 (1 if that is not positive), q = e4m3_rn_satfinite(y / s): the codes are made from
+ * the float32 y, not from out.
+ *   x          BF16 [T, H], row t at x + t * x_stride (elements, a multiple of 8, >= H).
+ *   weight     BF16 (weight_f32 = 0) or float32 (1) [H].
+ *   residual   nullable BF16 (residual_f32 = 0) or float32 (1) [T, H]; with it residual_out of the same
+ *              type and shape, which may be residual itself.
+ *   out        nullable BF16 [T, H], which may be x itself (x_stride = H).
+ *   q, q_scales  nullable together: E4M3 codes [T, H] and float32 [T, H/128].  At least one of out and q.
+ *   num_tokens nullable device int32 scalar n: rows t >= n are neither read nor written.
+ * H % 8 == 0 (q: H % 128 == 0), H <= 65536, eps >= 0.  x, weight, residual, residual_out and out 16-byte aligned,
+ * q 8-byte.  h whose squares sum past float32's range (|h| near 1e19) gives y = 0.
+ * Errors: MOE_ERR_ARG. */
+moe_status_t moe_rmsnorm(const uint16_t* x, int T, int H, long long x_stride, const void* weight, int weight_f32,
+                         float eps, const void* residual, int residual_f32, void* residual_out, uint16_t* out,
+                         uint8_t* q, float* q_scales, const int32_t* num_tokens, void* stream);
+
+/* out[t, n] = sum over blocks b of 128 columns of x_scales[t, b] * w_scales[n / 128, b] *
+ * (sum_k x[t, k] * w[n, k]) (+ bias[n]): float32 sums, one rounding.
+ *   x, x_scales  E4M3 [T, K], float32 [T, K/128]: rows of moe_rmsnorm, moe_quantize_act_fp8.
+ *   w, w_scales  E4M3 [N, K], float32 [ceil(N/128), K/128]: moe_quantize_weight_fp8's format, where the
+ *              last block of rows may be short.
+ *   bias       nullable float32 [N].
+ *   out        BF16 (out_f32 = 0) or float32 (1) [T, N], row t at out + t * out_stride (>= N).
+ *   ws         moe_linear_e4m3_workspace_bytes(T, N, K) bytes, 256-byte aligned, zero at first use (every
+ *              call leaves its counters zero); it serves any number of rows up to T, of this N and K.
+ *              Two calls that may overlap on the GPU need workspaces of their own.
+ *   dev_status nullable; MOE_DEV_PIPELINE_TIMEOUT if a wait within the kernel gave up (out is invalid; the
+ *              caller zeroes ws).
+ * Any T, any N up to 2^24, K % 128 == 0 and at most 2^22.  x and w 16-byte aligned.  The result does not depend on timing.
+ * Errors: MOE_ERR_ARG, MOE_ERR_WORKSPACE. */
+size_t moe_linear_e4m3_workspace_bytes(int T, int N, int K);
+moe_status_t moe_linear_e4m3(const uint8_t* x, const float* x_scales, int T, int K, const uint8_t* w,
+                             const float* w_scales, int N, const float* bias, void* out, int out_f32,
+                             long long out_stride, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* moe_permute (max_tokens = 0) or moe_permute_batched (max_tokens > 0) of rows that are E4M3 already: x E4M3
+ * [T, H] with x_scales float32 [T, H/128] in place of BF16 x.  Codes and scales are copied; the layouts, maps and
+ * their meaning are those calls'.
+ *   cu_seqlens out int32 [nseg + 1] when max_tokens = 0; masked_m out int32 [nseg] when max_tokens > 0; the
+ *              other one is not used.
+ *   ws         moe_permute_workspace_bytes / moe_permute_batched_workspace_bytes, as for those calls.
+ *   topk_w, row_weights  as moe_permute_ex.
+ * Errors: theirs; MOE_ERR_UNSUPPORTED for H above 116096 (two rows of a warp stand in shared memory). */
+moe_status_t moe_permute_e4m3(const int32_t* topk_idx, int T, int K, int E, int with_shared, int max_tokens,
+                              const uint8_t* x, const float* x_scales, int H, uint8_t* xp, float* xp_scales,
+                              int32_t* cu_seqlens, int32_t* masked_m, int32_t* src_row, int32_t* inv_map,
+                              int32_t* shared_map, void* ws, size_t ws_bytes, int32_t* dev_status,
+                              const float* topk_w, float* row_weights, void* stream);
+
+/* moe_layer_forward of an E4M3 layer (d->dtype MOE_E4M3, else MOE_ERR_ARG) on rows that are E4M3
+ * already: x and x_scales as moe_permute_e4m3.  With the codes and scales that moe_quantize_act_fp8 makes of
+ * BF16 rows the output is that of moe_layer_forward on those rows, bit for bit. */
+moe_status_t moe_layer_forward_e4m3(const moe_layer_desc_t* d, const moe_layer_weights_t* w, const float* logits,
+                                    const int32_t* num_tokens, int32_t* topk_idx, float* topk_w, const uint8_t* x,
+                                    const float* x_scales, const float* fq_scale, uint16_t* out, void* ws,
+                                    size_t ws_bytes, int32_t* dev_status, void* stream);
 
 #ifdef __cplusplus
 }
