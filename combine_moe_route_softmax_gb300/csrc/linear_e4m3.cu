@@ -4,23 +4,11 @@
 // The weights are the 16-row operand of mma.sync and the rows of x its 8 columns.  A 128-column block is four
 // instructions of 32 columns; which column sits where inside a block does not matter as long as both operands agree, so a
 // lane loads 16 consecutive bytes of a row and uses them as the operands of two instructions.
-#include <algorithm>
-
-#include "common.cuh"
+#include "gemm_common.cuh"
+#include "linear_e4m3.cuh"
 
 namespace moe {
 namespace lin8 {
-
-struct Args {
-  const uint8_t* x;
-  const float* x_scales;
-  const uint8_t* w;
-  const float* w_scales;
-  const float* bias;
-  void* out;
-  long long out_stride;
-  int T, N, K, out_f32;
-};
 
 __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -31,78 +19,257 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-constexpr int ROWS = 16, COLS = 32, NT = COLS / 8, WARPS = 8;
+constexpr int FEW_WARPS = 16, FEW_COLS = 16;
+constexpr int ITEM = 4096, RING = 2;               // bytes of an item; items that a warp has in flight
+template <int NT, int MT>
+constexpr int few_smem() { return FEW_WARPS * RING * ITEM + 2 * FEW_WARPS * NT * MT * 512 + FEW_WARPS * RING * 8 + 1024; }
 
-__global__ void __launch_bounds__(WARPS * 32) linear_kernel(const Args a) {
-  __shared__ float part[WARPS][NT][4][32];
+// Up to 8 NT rows of x.  A warp's unit is an item: 16 MT weight rows x 2 / MT K blocks, 4 KB by one TMA copy into the warp's ring,
+// RING items in flight per warp (131 KB an SM), on across tiles, so that the memory never waits for a tile to be finished.
+// A CTA's round is `tiles` row tiles (more than one where K has fewer than eight items): warp w takes item w, and of long
+// rows w + 16, w + 32, ..  The warps' sums of a tile meet in shared memory and are added in their order.
+template <int NT, int MT>
+__global__ void __launch_bounds__(FEW_WARPS * 32, 1)
+    linear_few_kernel(const __grid_constant__ CUtensorMap tm, const Args a, int tiles) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr int ROWS = 16 * MT, CHUNK = 2 / MT, SUMS = NT * MT * 128;         // SUMS: of a warp
+  float* part = reinterpret_cast<float*>(smem + FEW_WARPS * RING * ITEM);     // [2][warp][MT][NT][4][32]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-  const int n0 = blockIdx.x * ROWS, t0 = blockIdx.y * COLS, kblocks = a.K / 128;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  const bool r0 = n0 + g < a.N, r1 = n0 + g + 8 < a.N;
-  float acc[NT][4] = {};
-  for (int kb = warp; kb < kblocks; kb += WARPS) {
-    const uint8_t* w0 = a.w + (size_t)(n0 + g) * a.K + kb * 128 + 16 * c;
-    const uint8_t* w1 = w0 + (size_t)8 * a.K;
-    uint4 p[2], q[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      p[j] = r0 ? __ldg(reinterpret_cast<const uint4*>(w0 + 64 * j)) : zero;
-      q[j] = r1 ? __ldg(reinterpret_cast<const uint4*>(w1 + 64 * j)) : zero;
+  const int kblocks = a.K / 128, chunks = (kblocks + CHUNK - 1) / CHUNK;
+  const int rounds = (a.N + ROWS * tiles - 1) / (ROWS * tiles);
+  uint8_t* ring = smem + warp * RING * ITEM;
+  const uint32_t bars = gg::smem_u32(smem + FEW_WARPS * RING * ITEM + 2 * FEW_WARPS * SUMS * 4) + warp * RING * 8;
+  if (lane < RING) gg::mbar_init(bars + 8 * lane, 1);
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+
+  // this warp's items in order: round, chunk of the row
+  const bool busy = warp < tiles * chunks;
+  const int first = tiles > 1 ? warp % chunks : warp, tile = tiles > 1 ? warp / chunks : 0;
+  int load_round = busy ? (int)blockIdx.x : rounds, load_chunk = first;
+  uint32_t armed = 0;          // stages with a copy that was not waited for
+  auto load = [&](int stage) {
+    if (load_round >= rounds) return;
+    if (lane == 0) {
+      const uint32_t bar = bars + 8 * stage;
+      gg::mbar_expect_tx(bar, ITEM);     // rows past N and blocks past K arrive as zeros
+      asm volatile(
+          "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+              gg::smem_u32(ring + stage * ITEM)),
+          "l"(reinterpret_cast<uint64_t>(&tm)), "r"(0), "r"((load_round * tiles + tile) * ROWS), "r"(load_chunk * CHUNK), "r"(bar)
+          : "memory");
     }
-    const float ws = a.w_scales[(size_t)(n0 / 128) * kblocks + kb];
+    armed |= 1u << stage;
+    load_chunk += FEW_WARPS;
+    if (load_chunk >= chunks) {
+      load_chunk = first;
+      load_round += gridDim.x;
+    }
+  };
+  for (int i = 0; i < RING; ++i) load(i);
+
+  const uint8_t* x[NT];
+  const float* xs[NT][2];      // rows past the last one repeat it; their sums are not stored
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int t = t0 + 8 * i + g;
-      float d[4] = {};
+  for (int i = 0; i < NT; ++i) {
+    x[i] = a.x + (size_t)min(8 * i + g, a.T - 1) * a.K + 16 * c;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint4 b = t < a.T ? __ldg(reinterpret_cast<const uint4*>(a.x + (size_t)t * a.K + kb * 128 + 16 * c + 64 * j)) : zero;
-        mma_e4m3(d, p[j].x, q[j].x, p[j].y, q[j].y, b.x, b.y);
-        mma_e4m3(d, p[j].z, q[j].z, p[j].w, q[j].w, b.z, b.w);
+    for (int h = 0; h < 2; ++h) xs[i][h] = a.x_scales + (size_t)min(8 * i + 2 * c + h, a.T - 1) * kblocks;
+  }
+  int stage = 0, side = 0;
+  uint32_t phase = 0;
+  bool dead = false;           // a wait ran out: nothing more is loaded or added, the rounds are still walked through
+  for (int round = blockIdx.x; round < rounds; round += gridDim.x, side ^= 1) {
+    const int t0 = (round * tiles + tile) * ROWS;
+    float acc[MT][NT][4] = {};
+    if (busy) {
+      const float* ws = a.w_scales + (size_t)(min(t0, a.N - 1) / 128) * kblocks;
+      for (int chunk = first; chunk < chunks; chunk += FEW_WARPS) {
+        const int kb = chunk * CHUNK, n = min(CHUNK, kblocks - kb);
+        uint4 b[CHUNK][NT][2];
+        float sw[CHUNK], sx[CHUNK][NT][2];
+#pragma unroll
+        for (int j = 0; j < CHUNK; ++j) {
+          const int k = kb + min(j, n - 1);
+          sw[j] = __ldg(ws + k);
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              b[j][i][h] = __ldg(reinterpret_cast<const uint4*>(x[i] + (size_t)k * 128 + 64 * h));
+              sx[j][i][h] = __ldg(xs[i][h] + k);
+            }
+        }
+        if (!dead) {
+          const uint32_t bar = bars + 8 * stage;
+          if (!gg::mbar_try_wait(bar, phase)) {
+            const unsigned long long since = gg::globaltimer();
+            bool got = false;
+            while (!(got = gg::mbar_try_wait(bar, phase)) && gg::globaltimer() - since <= a.limit_ns) {
+            }
+            dead = !got;
+          }
+          dead = __any_sync(0xffffffffu, dead);
+        }
+        if (dead) continue;
+        const uint8_t* w0 = ring + stage * ITEM + g * 128;
+#pragma unroll
+        for (int j = 0; j < CHUNK; ++j) {
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            uint4 p[2], q[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              // 16-byte pieces of a row lie where the copy's 128-byte swizzle put them
+              const uint8_t* from = w0 + (j * ROWS + 16 * m) * 128 + (((c + 4 * h) ^ g) << 4);
+              p[h] = *reinterpret_cast<const uint4*>(from);
+              q[h] = *reinterpret_cast<const uint4*>(from + 1024);
+            }
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              float d[4] = {};
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                mma_e4m3(d, p[h].x, q[h].x, p[h].y, q[h].y, b[j][i][h].x, b[j][i][h].y);
+                mma_e4m3(d, p[h].z, q[h].z, p[h].w, q[h].w, b[j][i][h].z, b[j][i][h].w);
+              }
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float s = j < n ? __fmul_rn(sx[j][i][h], sw[j]) : 0.0f;   // past K: zeros
+                acc[m][i][h] = fmaf(d[h], s, acc[m][i][h]);
+                acc[m][i][2 + h] = fmaf(d[2 + h], s, acc[m][i][2 + h]);
+              }
+            }
+          }
+        }
+        __syncwarp();          // every lane has read the item
+        armed &= ~(1u << stage);
+        load(stage);
+        if (++stage == RING) {
+          stage = 0;
+          phase ^= 1;
+        }
       }
+    }
+    float* mine = part + (side * FEW_WARPS + warp) * SUMS + lane;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int col = t0 + 8 * i + 2 * c + h;
-        const float s = col < a.T ? __fmul_rn(a.x_scales[(size_t)col * kblocks + kb], ws) : 0.0f;
-        acc[i][h] = fmaf(d[h], s, acc[i][h]);
-        acc[i][2 + h] = fmaf(d[2 + h], s, acc[i][2 + h]);
-      }
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) mine[((m * NT + i) * 4 + v) * 32] = acc[m][i][v];
+    __syncthreads();           // the other side was read before the barrier of the round before
+    for (int e = threadIdx.x; e < tiles * ROWS * a.T; e += FEW_WARPS * 32) {
+      // element: row r of the round's rows, column t
+      const int t = e / (ROWS * tiles), r = e - t * ROWS * tiles, row = round * tiles * ROWS + r;
+      if (row >= a.N) continue;
+      const int l = (r & 7) * 4 + ((t & 7) >> 1), v = ((r >> 3) & 1) * 2 + (t & 1);
+      const int of = r / ROWS, m = (r / 16) % MT;
+      const int w0 = tiles > 1 ? of * chunks : 0, w1 = tiles > 1 ? w0 + chunks : min(FEW_WARPS, chunks);
+      const float* from = part + side * FEW_WARPS * SUMS + (m * NT + (t >> 3)) * 128 + v * 32 + l;
+      float s = from[w0 * SUMS];
+      for (int w = w0 + 1; w < w1; ++w) s = __fadd_rn(s, from[w * SUMS]);
+      if (a.bias) s = __fadd_rn(s, a.bias[row]);
+      const long long o = (long long)t * a.out_stride + row;
+      if (a.out_f32)
+        static_cast<float*>(a.out)[o] = s;
+      else
+        static_cast<uint16_t*>(a.out)[o] = f32_to_bf16(s);
     }
   }
-#pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) part[warp][i][v][lane] = acc[i][v];
-  __syncthreads();
-  for (int e = threadIdx.x; e < NT * 128; e += WARPS * 32) {
-    // element e: row r of the tile, column t of the block
-    const int r = e & 15, t = e >> 4;
-    const int l = (r & 7) * 4 + ((t & 7) >> 1), v = (r >> 3) * 2 + (t & 1);
-    float s = 0.0f;
-    for (int w = 0; w < WARPS; ++w) s += part[w][t >> 3][v][l];
-    if (n0 + r >= a.N || t0 + t >= a.T) continue;
-    if (a.bias) s += a.bias[n0 + r];
-    const long long o = (long long)(t0 + t) * a.out_stride + n0 + r;
-    if (a.out_f32)
-      static_cast<float*>(a.out)[o] = s;
-    else
-      static_cast<uint16_t*>(a.out)[o] = f32_to_bf16(s);
+  if (dead) {
+    // copies still in flight land before the shared memory goes away
+    if (lane == 0 && a.dev_status) atomicOr(a.dev_status, MOE_DEV_PIPELINE_TIMEOUT);
+    for (int i = 0; i < RING; ++i)
+      if (armed & (1u << i)) gg::mbar_drain(bars + 8 * i, i < stage ? phase ^ 1 : phase);
   }
 }
 
+template <int NT, int MT>
+moe_status_t launch_few(const Args& a, cudaStream_t s) {
+  auto kern = linear_few_kernel<NT, MT>;
+  static std::atomic<unsigned long long> attr_done{0};
+  if (!once_per_device(attr_done, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, few_smem<NT, MT>()) == cudaSuccess;
+      }))
+    return MOE_ERR_CUDA;
+  // as many row tiles to a round as keep the warps busy, as long as every SM has a round
+  constexpr int ROWS = 16 * MT, CHUNK = 2 / MT;
+  const int kblocks = a.K / 128, chunks = (kblocks + CHUNK - 1) / CHUNK, all = (a.N + ROWS - 1) / ROWS;
+  const int tiles = std::max(1, std::min(FEW_WARPS / chunks, all / num_sms()));
+  const int rounds = (all + tiles - 1) / tiles;
+  // the weights as K blocks of 128 bytes x rows
+  const auto encode = gg::encode_fn();
+  if (!encode) return MOE_ERR_CUDA;
+  CUtensorMap tm;
+  const cuuint64_t dims[3] = {128, (cuuint64_t)a.N, (cuuint64_t)kblocks}, strides[2] = {(cuuint64_t)a.K, 128};
+  const cuuint32_t box[3] = {128, ROWS, CHUNK}, unit[3] = {1, 1, 1};
+  if (encode(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(a.w), dims, strides, box, unit,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return MOE_ERR_CUDA;
+  kern<<<std::min(rounds, num_sms()), FEW_WARPS * 32, few_smem<NT, MT>(), s>>>(tm, a, tiles);
+  MOE_CHECK_LAUNCH();
+  return MOE_OK;
+}
+
 inline bool shape_ok(int T, int N, int K) { return T >= 0 && N > 0 && K > 0 && K % 128 == 0 && N <= (1 << 24) && K <= (1 << 22); }
+
+struct Plan {
+  int variant;     // -1: linear_few_kernel
+  Split split;
+};
+
+// The cut of a variant, its K shared by `parts` CTAs to a tile (TC_64; as far as there are SMs and K blocks).
+Split cut(Variant v, int T, int N, int kblocks, int parts) {
+  const int tiles = tc_tiles(v, T, N), most = num_sms();
+  if (v == TC_64) parts = std::min(parts, std::min(most / tiles, kblocks));
+  return v == TC_64 && parts > 1 ? Split{tiles * parts, parts} : Split{std::min(most, tiles), 1};
+}
+
+// Up to 16 rows the kernel for few rows; beyond, the tile width and the parts of K whose time, modelled in microseconds
+// from measured calls, is least:
+//   rounds of the SMs x (K blocks x the time of one + a tile's start and store), where a block takes 0.215 (64 columns) or
+//   0.5 (256), or its weights' share of the memory (8 and 32 KB at 41 GB/s an SM, read once for all row tiles);
+//   parts of K: their join takes 1.6 and 0.35 each.
+// Measured (64 / 256 columns): 512 x 4096 x 7168 27.5 / 32.8 us, 1024 x 4096 x 7168 50.3 / 33.3, 3000 x 576 x 7168 27.7 / 32.6,
+// 128 x 40960 x 4096 45.7 / 51.5; 64 columns, 1 / 2 / 4 / 8 parts: 24 x 576 x 7168 12.9 / 10.1 / 8.4 / 8.6.  Few rows against 64
+// columns: 16 x 4096 x 7168 10.5 / 21.5 (17.0 in two parts), 16 x 7168 x 16384 31 / 30, 24 x 4096 x 7168 with 32 rows of x
+// in the kernel for few 12.8 / 14.7 but 32 x 7168 x 16384 58 / 30.
+Plan plan(int T, int N, int K) {
+  if (T <= FEW_COLS) return Plan{-1, {}};
+  const int kblocks = K / 128, most = num_sms();
+  const double row_tiles = (T + 127) / 128;
+  auto rounds = [&](Variant v) { return (tc_tiles(v, T, N) + most - 1) / most; };
+  const double narrow = kblocks * std::max(0.215, 0.2 / row_tiles);
+  const double t256 = rounds(TC_256) * (kblocks * std::max(0.5, 0.78 / row_tiles) + 2.3);
+  double best = rounds(TC_64) * (narrow + 0.9);
+  int parts = 1;
+  for (int p = 2; p <= std::min(8, most / tc_tiles(TC_64, T, N)); ++p) {
+    const double t = narrow / p + 0.9 + 1.6 + 0.35 * p;
+    if (t < best) {
+      best = t;
+      parts = p;
+    }
+  }
+  const Variant v = t256 < best ? TC_256 : TC_64;
+  return Plan{v, cut(v, T, N, kblocks, parts)};
+}
 
 }  // namespace lin8
 }  // namespace moe
 
 extern "C" size_t moe_linear_e4m3_workspace_bytes(int T, int N, int K) {
-  return moe::lin8::shape_ok(T, N, K) ? 256 : 0;
+  using namespace moe::lin8;
+  return shape_ok(T, N, K) ? count_bytes() + sum_bytes() : 0;
 }
 
-extern "C" moe_status_t moe_linear_e4m3(const uint8_t* x, const float* x_scales, int T, int K, const uint8_t* w,
-                                        const float* w_scales, int N, const float* bias, void* out, int out_f32,
-                                        long long out_stride, void* ws, size_t ws_bytes, int32_t* dev_status,
-                                        void* stream) {
+static moe_status_t linear_e4m3_impl(const uint8_t* x, const float* x_scales, int T, int K, const uint8_t* w,
+                                     const float* w_scales, int N, const float* bias, void* out, int out_f32,
+                                     long long out_stride, void* ws, size_t ws_bytes, int32_t* dev_status,
+                                     const moe::lin8::Plan* forced, unsigned long long limit_ns, void* stream) {
   using namespace moe;
   using namespace moe::lin8;
   auto bits = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
@@ -114,9 +281,34 @@ extern "C" moe_status_t moe_linear_e4m3(const uint8_t* x, const float* x_scales,
   if (((bits(x) | bits(w)) & 15) || ((bits(x_scales) | bits(w_scales) | bits(bias) | bits(dev_status)) & 3) ||
       (bits(out) & (out_f32 ? 3 : 1)))
     return MOE_ERR_ARG;
-  if ((T + COLS - 1) / COLS > 65535) return MOE_ERR_UNSUPPORTED;
-  const Args a{x, x_scales, w, w_scales, bias, out, out_stride, T, N, K, out_f32};
-  linear_kernel<<<dim3((N + ROWS - 1) / ROWS, (T + COLS - 1) / COLS), WARPS * 32, 0, as_stream(stream)>>>(a);
-  MOE_CHECK_LAUNCH();
-  return MOE_OK;
+  const Args a{x, x_scales, w, w_scales, bias, out, out_stride, T, N, K, out_f32, static_cast<int32_t*>(ws),
+               reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + count_bytes()), dev_status, limit_ns};
+  const Plan p = forced ? *forced : plan(T, N, K);
+  if (p.variant >= 0) return launch_tc((Variant)p.variant, a, p.split, as_stream(stream));
+  const bool wide = N / 32 >= moe::num_sms() / 2;
+  if (T <= 8) return wide ? launch_few<1, 2>(a, as_stream(stream)) : launch_few<1, 1>(a, as_stream(stream));
+  return wide ? launch_few<2, 2>(a, as_stream(stream)) : launch_few<2, 1>(a, as_stream(stream));
+}
+
+extern "C" moe_status_t moe_linear_e4m3(const uint8_t* x, const float* x_scales, int T, int K, const uint8_t* w,
+                                        const float* w_scales, int N, const float* bias, void* out, int out_f32,
+                                        long long out_stride, void* ws, size_t ws_bytes, int32_t* dev_status,
+                                        void* stream) {
+  return linear_e4m3_impl(x, x_scales, T, K, w, w_scales, N, bias, out, out_f32, out_stride, ws, ws_bytes, dev_status,
+                          nullptr, moe::lin8::LIMIT_NS, stream);
+}
+
+// Test hook, deliberately absent from the public header: moe_linear_e4m3 by one variant whatever the sizes (-1: the
+// kernel for few rows, 0.. the tensor-core kernel's), with K shared by up to `parts` CTAs (variant 0), and with the limit of each wait
+// in nanoseconds, so that a test can make a wait run out.
+extern "C" moe_status_t moe_testing_linear_e4m3(const uint8_t* x, const float* x_scales, int T, int K, const uint8_t* w,
+                                                const float* w_scales, int N, const float* bias, void* out, int out_f32,
+                                                long long out_stride, void* ws, size_t ws_bytes, int32_t* dev_status,
+                                                int variant, int parts, unsigned long long limit_ns, void* stream) {
+  using namespace moe::lin8;
+  if (!shape_ok(T, N, K) || variant < -1 || variant >= TC_VARIANTS || (variant == -1 && T > FEW_COLS)) return MOE_ERR_ARG;
+  Plan p{variant, {}};
+  if (variant >= 0 && T > 0) p.split = cut((Variant)variant, T, N, K / 128, std::max(1, parts));
+  return linear_e4m3_impl(x, x_scales, T, K, w, w_scales, N, bias, out, out_f32, out_stride, ws, ws_bytes, dev_status,
+                          &p, limit_ns, stream);
 }

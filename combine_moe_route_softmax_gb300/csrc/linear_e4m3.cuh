@@ -1,0 +1,45 @@
+// moe_linear_e4m3's two kernels and how a call is cut.  Internal header.
+#pragma once
+
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace moe {
+namespace lin8 {
+
+struct Args {
+  const uint8_t* x;
+  const float* x_scales;
+  const uint8_t* w;
+  const float* w_scales;
+  const float* bias;
+  void* out;
+  long long out_stride;
+  int T, N, K, out_f32;
+  int32_t* count;          // arrivals at the tiles whose K is shared, zero between launches
+  float* part;             // their sums
+  int32_t* dev_status;
+  unsigned long long limit_ns;   // of each wait
+};
+
+constexpr unsigned long long LIMIT_NS = 2000000000ull;
+
+// A workspace: the counters (eight for each shared tile, of which there are fewer than SMs), then the sums of the parts (of at
+// most 128 x 64 values, no more of them than SMs).
+inline size_t count_bytes() { return ((size_t)num_sms() * 32 + 255) / 256 * 256; }
+inline size_t sum_bytes() { return (size_t)num_sms() * 128 * 64 * 4; }
+
+// Variants of the tensor-core kernel: 128 rows x so many weight rows of a tile.
+enum Variant { TC_64 = 0, TC_256 = 1, TC_VARIANTS = 2 };
+
+// parts = 1: worker w computes the tiles w, w + workers, ..  parts > 1: worker w computes part w % parts of tile w / parts.
+struct Split {
+  int workers, parts;
+};
+
+moe_status_t launch_tc(Variant v, const Args& a, const Split& split, cudaStream_t s);
+int tc_tiles(Variant v, int T, int N);
+
+}  // namespace lin8
+}  // namespace moe
