@@ -792,14 +792,44 @@ class MoeLayerFew:
 
 
 # ---------------------------------------------------------------- the 8-bit activation path
+# A call of a few rows takes less time on the GPU than its checks here, so these look at everything in one
+# expression and name what does not fit only where something does not.  get_device() is -1 off the GPU.
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_here = lambda: torch._C._cuda_getDevice()  # noqa: E731
+
+
 def _need_codes(t, rows, cols, what):
     """t: E4M3 codes [rows, cols] (uint8 or float8_e4m3fn), contiguous on the GPU, an address, or None."""
     if t is None or isinstance(t, int):
         return
-    if not (t.shape == (rows, cols) and (t.dtype is torch.uint8 or t.dtype is torch.float8_e4m3fn) and t.is_cuda and
-            t.is_contiguous()):
+    if not (t.shape == (rows, cols) and t.dtype in _CODES and t.is_cuda and t.is_contiguous()):
         raise ValueError(f"{what}: expected contiguous E4M3 codes (uint8 or float8_e4m3fn) of shape {(rows, cols)} on the "
                          f"GPU, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _refuse(what):
+    """Something did not fit and no check of its own named it: tensors of another device than the current one."""
+    raise ValueError(f"{what}: expected contiguous tensors on the current device")
+
+
+def _opt(t, dtype, count, dev, what):
+    """The address of an optional contiguous tensor of `count` values on the current device."""
+    if t is None:
+        return None
+    if not (t.dtype is dtype and t.numel() == count and t.get_device() == dev and t.is_contiguous()):
+        _need_tensor(t, dtype, (count,), what)
+        _refuse(what)
+    return t.data_ptr()
+
+
+def _word(t, dev, what):
+    if t is None:
+        return None
+    if not (t.dtype is _I32 and t.numel() >= 1 and t.get_device() == dev):
+        _need_word(t, what)
+        _refuse(what)
+    return t.data_ptr()
 
 
 def moe_rmsnorm(x, weight, eps, residual=None, bf16=True, e4m3=False, out=None, q=None, q_scales=None,
@@ -812,40 +842,50 @@ def moe_rmsnorm(x, weight, eps, residual=None, bf16=True, e4m3=False, out=None, 
     if stream is not None:
         return _run_on(stream, moe_rmsnorm, x, weight, eps, residual, bf16, e4m3, out, q, q_scales, residual_out,
                        num_tokens)
-    if not (x.dim() == 2 and x.is_cuda and x.dtype is torch.bfloat16 and x.stride(1) == 1):
-        raise ValueError("x is BF16 [T, H] on the GPU, rows dense")
-    T, H = x.shape
-    w32 = weight.dtype is torch.float32
-    _need_tensor(weight, torch.float32 if w32 else torch.bfloat16, (H,), "weight")
+    T, H = shape = x.shape
+    dev = _here()
+    w32 = weight.dtype is _F32
+    if not (x.dtype is _BF16 and x.get_device() == dev and (T == 0 or x.stride(1) == 1) and (w32 or weight.dtype is _BF16) and
+            weight.numel() == H and weight.get_device() == dev and weight.is_contiguous()):
+        _need(x.is_cuda and x.dtype is _BF16 and x.stride(1) == 1, "x is BF16 [T, H] on the GPU, rows dense")
+        _need_tensor(weight, _F32 if w32 else _BF16, (H,), "weight")
+        _refuse("x, weight")
     _need((q is None) == (q_scales is None), "q and q_scales are given together")
     if out is None and q is None:
         _need(bf16 or e4m3, "one of bf16 and e4m3 is wanted")
         if bf16:
-            out = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
+            out = torch.empty(shape, dtype=_BF16, device=x.device)
         if e4m3:
-            q = torch.empty(T, H, dtype=torch.uint8, device=x.device)
-            q_scales = torch.empty(T, H // 128, dtype=torch.float32, device=x.device)
+            q = torch.empty(shape, dtype=torch.uint8, device=x.device)
+            q_scales = torch.empty((T, H // 128), dtype=_F32, device=x.device)
     else:
-        if out is not None:
-            _need_tensor(out, torch.bfloat16, (T, H), "out")
-        if q is not None:
+        if out is not None and not (out.dtype is _BF16 and out.shape == shape and out.get_device() == dev and out.is_contiguous()):
+            _need_tensor(out, _BF16, shape, "out")
+            _refuse("out")
+        if q is not None and not (q.dtype in _CODES and q.shape == shape and q_scales.dtype is _F32 and
+                                  q_scales.shape == (T, H // 128) and q.get_device() == dev and q_scales.get_device() == dev and
+                                  q.is_contiguous() and q_scales.is_contiguous()):
             _need_codes(q, T, H, "q")
-            _need_tensor(q_scales, torch.float32, (T, H // 128), "q_scales")
+            _need_tensor(q_scales, _F32, (T, H // 128), "q_scales")
+            _refuse("q, q_scales")
     r32 = False
     if residual is not None:
-        r32 = residual.dtype is torch.float32
-        _need_tensor(residual, torch.float32 if r32 else torch.bfloat16, (T, H), "residual")
+        r32 = residual.dtype is _F32
         if residual_out is None:
             residual_out = torch.empty_like(residual)
-        else:
-            _need_tensor(residual_out, residual.dtype, (T, H), "residual_out")
+        if not ((r32 or residual.dtype is _BF16) and residual.shape == shape and residual.get_device() == dev and
+                residual.is_contiguous() and residual_out.dtype is residual.dtype and residual_out.shape == shape and
+                residual_out.get_device() == dev and residual_out.is_contiguous()):
+            _need_tensor(residual, _F32 if r32 else _BF16, shape, "residual")
+            _need_tensor(residual_out, residual.dtype, shape, "residual_out")
+            _refuse("residual")
     else:
         _need(residual_out is None, "residual_out without a residual")
-    if num_tokens is not None:
-        _need_word(num_tokens, "num_tokens")
     _check("moe_rmsnorm", (_lib or lib()).moe_rmsnorm(
-        x.data_ptr(), T, H, x.stride(0) if T > 1 else H, weight.data_ptr(), w32, eps, _ptr(residual), r32,
-        _ptr(residual_out), _ptr(out), _ptr(q), _ptr(q_scales), _ptr(num_tokens), _stream(None)))
+        x.data_ptr(), T, H, x.stride(0) if T > 1 else H, weight.data_ptr(), w32, eps,
+        None if residual is None else residual.data_ptr(), r32, None if residual is None else residual_out.data_ptr(),
+        None if out is None else out.data_ptr(), None if q is None else q.data_ptr(),
+        None if q is None else q_scales.data_ptr(), _word(num_tokens, dev, "num_tokens"), _stream(None)))
     return out, q, q_scales, residual_out
 
 
@@ -865,33 +905,36 @@ def moe_linear_e4m3(x, x_scales, w, w_scales, bias=None, out=None, out_dtype=tor
     may overlap need one each."""
     if stream is not None:
         return _run_on(stream, moe_linear_e4m3, x, x_scales, w, w_scales, bias, out, out_dtype, ws, dev_status)
-    if x.dim() != 2 or w.dim() != 2:
-        raise ValueError("x is [T, K] and w [N, K]")
-    (T, K), N = x.shape, w.shape[0]
-    _need_codes(x, T, K, "x")
-    _need_codes(w, N, K, "w")
-    _need_tensor(x_scales, torch.float32, (T, K // 128), "x_scales")
-    _need_tensor(w_scales, torch.float32, (-(-N // 128), K // 128), "w_scales")
-    if bias is not None:
-        _need_tensor(bias, torch.float32, (N,), "bias")
-    if dev_status is not None:
-        _need_word(dev_status, "dev_status")
+    T, K = x.shape
+    N, k = w.shape
+    dev = _here()
+    if not (k == K and x.dtype in _CODES and w.dtype in _CODES and x_scales.dtype is _F32 and w_scales.dtype is _F32 and
+            x_scales.shape == (T, K // 128) and w_scales.shape == ((N + 127) // 128, K // 128) and
+            x.get_device() == dev and w.get_device() == dev and x_scales.get_device() == dev and
+            w_scales.get_device() == dev and x.is_contiguous() and w.is_contiguous() and x_scales.is_contiguous() and
+            w_scales.is_contiguous()):
+        _need_codes(x, T, K, "x")
+        _need_codes(w, N, K, "w")
+        _need_tensor(x_scales, _F32, (T, K // 128), "x_scales")
+        _need_tensor(w_scales, _F32, ((N + 127) // 128, K // 128), "w_scales")
+        _refuse("x, w")
     if out is None:
-        out = torch.empty(T, N, dtype=out_dtype, device=x.device)
+        out = torch.empty((T, N), dtype=out_dtype, device=x.device)
         os = N
     else:
-        _need(out.is_cuda and out.shape == (T, N) and out.stride(1) == 1, "out is [T, N] on the GPU, rows dense")
+        _need(out.get_device() == dev and out.shape == (T, N) and out.stride(1) == 1,
+              "out is [T, N] on the current device, rows dense")
         os = out.stride(0) if T > 1 else N
         out_dtype = out.dtype
-    _need(out_dtype is torch.bfloat16 or out_dtype is torch.float32, "out is BF16 or float32")
+    f32 = out_dtype is _F32
+    _need(f32 or out_dtype is _BF16, "out is BF16 or float32")
     if ws is None:
         ws = moe_linear_e4m3_workspace(T, N, K, x.device)
-    elif not (ws.is_cuda and ws.is_contiguous() and ws.dtype is torch.uint8):
-        raise ValueError("ws is a workspace of moe_linear_e4m3_workspace")
+    elif not (ws.dtype is torch.uint8 and ws.get_device() == dev and ws.is_contiguous()):
+        raise ValueError("ws is a workspace of moe_linear_e4m3_workspace on the current device")
     _check("moe_linear_e4m3", (_lib or lib()).moe_linear_e4m3(
-        x.data_ptr(), x_scales.data_ptr(), T, K, w.data_ptr(), w_scales.data_ptr(), N,
-        None if bias is None else bias.data_ptr(), out.data_ptr(), out_dtype is torch.float32, os, ws.data_ptr(),
-        ws.numel(), None if dev_status is None else dev_status.data_ptr(), _stream(None)))
+        x.data_ptr(), x_scales.data_ptr(), T, K, w.data_ptr(), w_scales.data_ptr(), N, _opt(bias, _F32, N, dev, "bias"),
+        out.data_ptr(), f32, os, ws.data_ptr(), ws.numel(), _word(dev_status, dev, "dev_status"), _stream(None)))
     return out
 
 
@@ -903,40 +946,47 @@ def moe_permute_e4m3(topk_idx, E, x, x_scales, with_shared=False, max_tokens=0, 
     if stream is not None:
         return _run_on(stream, moe_permute_e4m3, topk_idx, E, x, x_scales, with_shared, max_tokens, xp, xp_scales, ws,
                        dev_status, topk_w)
-    if topk_idx.dim() != 2 or x.dim() != 2:
-        raise ValueError("topk_idx is [T, K] and x [T, H]")
-    (T, K), H = topk_idx.shape, x.shape[1]
-    dev, nseg = x.device, E + int(with_shared)
+    T, K = topk_idx.shape
+    t, H = x.shape
+    dev, nseg = _here(), E + int(with_shared)
     rows = nseg * max_tokens if max_tokens else T * K + (T if with_shared else 0)
-    _need_tensor(topk_idx, torch.int32, (T, K), "topk_idx")
-    _need_codes(x, T, H, "x")
-    _need_tensor(x_scales, torch.float32, (T, H // 128), "x_scales")
+    if not (t == T and topk_idx.dtype is _I32 and x.dtype in _CODES and x_scales.dtype is _F32 and
+            x_scales.shape == (T, H // 128) and topk_idx.get_device() == dev and x.get_device() == dev and
+            x_scales.get_device() == dev and topk_idx.is_contiguous() and x.is_contiguous() and x_scales.is_contiguous()):
+        _need_tensor(topk_idx, _I32, (T, K), "topk_idx")
+        _need_codes(x, T, H, "x")
+        _need_tensor(x_scales, _F32, (T, H // 128), "x_scales")
+        _refuse("topk_idx, x")
     if xp is None:
-        xp = torch.empty(rows, H, dtype=torch.uint8, device=dev)
-    else:
+        xp = torch.empty((rows, H), dtype=torch.uint8, device=x.device)
+    elif not (xp.dtype in _CODES and xp.shape == (rows, H) and xp.get_device() == dev and xp.is_contiguous()):
         _need_codes(xp, rows, H, "xp")
+        _refuse("xp")
     if xp_scales is None:
-        xp_scales = torch.empty(rows, H // 128, dtype=torch.float32, device=dev)
-    else:
-        _need_tensor(xp_scales, torch.float32, (rows, H // 128), "xp_scales")
-    ints = lambda *shape: torch.empty(*shape, dtype=torch.int32, device=dev)  # noqa: E731
-    cu, mm = (None, ints(nseg)) if max_tokens else (ints(nseg + 1), None)
-    src, inv, smap = ints(rows), ints(T, K), ints(T) if with_shared else None
+        xp_scales = torch.empty((rows, H // 128), dtype=_F32, device=x.device)
+    elif not (xp_scales.dtype is _F32 and xp_scales.shape == (rows, H // 128) and xp_scales.get_device() == dev and
+              xp_scales.is_contiguous()):
+        _need_tensor(xp_scales, _F32, (rows, H // 128), "xp_scales")
+        _refuse("xp_scales")
+    on = x.device
+    cu = None if max_tokens else torch.empty(nseg + 1, dtype=_I32, device=on)
+    mm = torch.empty(nseg, dtype=_I32, device=on) if max_tokens else None
+    src, inv = torch.empty(rows, dtype=_I32, device=on), torch.empty_like(topk_idx)
+    smap = torch.empty(T, dtype=_I32, device=on) if with_shared else None
     roww = None
     if topk_w is not None:
-        _need_tensor(topk_w, torch.float32, (T, K), "topk_w")
-        roww = torch.empty(rows, dtype=torch.float32, device=dev)
-    if dev_status is not None:
-        _need_word(dev_status, "dev_status")
+        _need_tensor(topk_w, _F32, (T, K), "topk_w")
+        roww = torch.empty(rows, dtype=_F32, device=on)
     if ws is None:
         size = moe_permute_batched_workspace_bytes if max_tokens else moe_permute_workspace_bytes
-        ws = torch.empty(size(T, K, E, with_shared), dtype=torch.uint8, device=dev)
-    elif not (ws.is_cuda and ws.is_contiguous()):
-        raise ValueError("ws is a contiguous GPU tensor")
-    _check("moe_permute_e4m3", lib().moe_permute_e4m3(
-        _ptr(topk_idx), T, K, E, int(with_shared), max_tokens, _ptr(x), _ptr(x_scales), H, _ptr(xp), _ptr(xp_scales),
-        _ptr(cu), _ptr(mm), _ptr(src), _ptr(inv), _ptr(smap), _ptr(ws), ws.numel() * ws.element_size(), _ptr(dev_status),
-        _ptr(topk_w), _ptr(roww), _stream(None)))
+        ws = torch.empty(size(T, K, E, with_shared), dtype=torch.uint8, device=on)
+    elif not (ws.get_device() == dev and ws.is_contiguous()):
+        raise ValueError("ws is a contiguous tensor on the current device")
+    _check("moe_permute_e4m3", (_lib or lib()).moe_permute_e4m3(
+        topk_idx.data_ptr(), T, K, E, int(with_shared), max_tokens, x.data_ptr(), x_scales.data_ptr(), H, xp.data_ptr(),
+        xp_scales.data_ptr(), _ptr(cu), _ptr(mm), src.data_ptr(), inv.data_ptr(), _ptr(smap), ws.data_ptr(),
+        ws.numel() * ws.element_size(), _word(dev_status, dev, "dev_status"), _opt(topk_w, _F32, T * K, dev, "topk_w"),
+        _ptr(roww), _stream(None)))
     maps = dict(src_row=src, inv_map=inv, shared_map=smap, row_weights=roww)
     if max_tokens:
         return dict(xb=xp.view(nseg, max_tokens, H), xb_scales=xp_scales.view(nseg, max_tokens, -1), masked_m=mm, **maps)

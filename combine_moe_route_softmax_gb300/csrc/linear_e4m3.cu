@@ -261,9 +261,13 @@ Plan plan(int T, int N, int K) {
 }  // namespace lin8
 }  // namespace moe
 
+// Only calls whose K is shared use a workspace: more rows than the kernel for few takes, and so few columns that even one
+// row tile leaves SMs over.  One size for all of them, so that what was made for T rows serves fewer.
 extern "C" size_t moe_linear_e4m3_workspace_bytes(int T, int N, int K) {
   using namespace moe::lin8;
-  return shape_ok(T, N, K) ? count_bytes() + sum_bytes() : 0;
+  if (!shape_ok(T, N, K)) return 0;
+  if (T <= FEW_COLS || 2 * tc_tiles(TC_64, 1, N) > moe::num_sms()) return 256;
+  return count_bytes() + sum_bytes();
 }
 
 static moe_status_t linear_e4m3_impl(const uint8_t* x, const float* x_scales, int T, int K, const uint8_t* w,

@@ -8,8 +8,12 @@
 // the residual keeps it: each output has one rounding.
 //
 // Bound by memory: x and the residual are read once and held in registers between the sum and the
-// outputs.  One block per row; a thread holds VPT vectors of 8 columns, vector j of thread t being
+// outputs.  A row belongs to a block; a thread holds VPT vectors of 8 columns, vector j of thread t being
 // columns 8 (t + j * threads).. so that 16 lanes next to each other hold one 128-column block.
+//   Rows up to the SMs: one vector a thread, the most loads in flight (1 x 7168: 3.0 us, launch and latency).
+//   More: two vectors and 1024 threads an SM, the next row loaded ahead: 12000 x 7168, BF16 residual, all outputs: 120 us,
+//   0.97 of the measured copy bandwidth (without loading ahead 141, four vectors 129, 1536 threads 147); 16384 x 2048 48.6 us.
+//   Rows longer than 8192 columns, whose registers leave no room for the next: four or eight vectors.
 #include <algorithm>
 
 #include "common.cuh"
@@ -48,52 +52,87 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// RES: 0 no residual, 1 BF16, 2 float32.
+// Codes of 8 values with scale s: e4m3(v / s) with the quotients correctly rounded.  The division is Markstein's ("Computation
+// of elementary functions on the IBM RISC System/6000 processor", 1990): with inv the correctly rounded reciprocal,
+// t = v inv is within an ulp, and t + (v - t s) inv rounds to the quotient; three instructions where an IEEE division takes
+// ten.  It asks that nothing on the way under- or overflows: outside [2^-80, 2^80] s is divided by as usual (inside, a v so
+// small that the remainder underflows is below half of the smallest code either way).
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float s) {
+  uint32_t c[2] = {0, 0};
+  if (s > 8e-25f && s < 1e24f) {
+    const float inv = __frcp_rn(s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float t = __fmul_rn(v[i], inv);
+      c[i >> 2] |= (uint32_t)f32_to_e4m3(fmaf(fmaf(-t, s, v[i]), inv, t)) << (8 * (i & 3));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i >> 2] |= (uint32_t)f32_to_e4m3(__fdiv_rn(v[i], s)) << (8 * (i & 3));
+  }
+  return make_uint2(c[0], c[1]);
+}
+
+// What a thread holds of a row as it was loaded.  RES: 0 no residual, 1 BF16, 2 float32.
 template <int VPT, int RES>
+struct Raw {
+  uint4 x[VPT], r[RES == 2 ? 2 * VPT : VPT];
+  __device__ __forceinline__ void load(const NormArgs& a, int row, int nvec) {
+    const uint4* xr = reinterpret_cast<const uint4*>(a.x + (size_t)row * a.x_stride);
+    const uint4* rr = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.residual) + (size_t)row * a.H * (2 * RES));
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = threadIdx.x + j * blockDim.x;
+      const bool ok = v < nvec;
+      x[j] = ok ? xr[v] : make_uint4(0, 0, 0, 0);
+      if (RES == 1) r[j] = ok ? rr[v] : make_uint4(0, 0, 0, 0);
+      if (RES == 2) {
+        r[2 * j] = ok ? rr[2 * v] : make_uint4(0, 0, 0, 0);
+        r[2 * j + 1] = ok ? rr[2 * v + 1] : make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+  __device__ __forceinline__ void sum(float (&h)[VPT][8]) const {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      unpack8(x[j], h[j]);
+      if (RES == 1) {
+        float f[8];
+        unpack8(r[j], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[j][i] = __fadd_rn(h[j][i], f[i]);
+      }
+      if (RES == 2) {
+        const uint32_t f[8] = {r[2 * j].x, r[2 * j].y, r[2 * j].z, r[2 * j].w,
+                               r[2 * j + 1].x, r[2 * j + 1].y, r[2 * j + 1].z, r[2 * j + 1].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[j][i] = __fadd_rn(h[j][i], __uint_as_float(f[i]));
+      }
+    }
+  }
+};
+
+// A block's rows one after the other.  AHEAD: the next row is loaded while this one is summed, scaled and stored (where a
+// block has several rows).
+template <int VPT, int RES, bool AHEAD>
 __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a) {
   __shared__ float part[2][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int nvec = a.H / 8;
   const int rows = a.num_tokens ? min(max(*a.num_tokens, 0), a.T) : a.T;
   int side = 0;
+  Raw<VPT, RES> raw;
+  if (AHEAD && (int)blockIdx.x < rows) raw.load(a, blockIdx.x, nvec);
   for (int row = blockIdx.x; row < rows; row += gridDim.x, side ^= 1) {
     float h[VPT][8];
     float ss = 0.0f;
-    const uint4* xr = reinterpret_cast<const uint4*>(a.x + (size_t)row * a.x_stride);
-    uint4 xv[VPT], rv[RES == 2 ? 2 * VPT : VPT];
+    if (!AHEAD) raw.load(a, row, nvec);
+    raw.sum(h);
+    if (AHEAD && row + (int)gridDim.x < rows) raw.load(a, row + gridDim.x, nvec);
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int v = threadIdx.x + j * blockDim.x;
-      const bool ok = v < nvec;
-      xv[j] = ok ? xr[v] : make_uint4(0, 0, 0, 0);
-      if (RES == 1) {
-        const uint4* rr = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.residual) + (size_t)row * a.H);
-        rv[j] = ok ? rr[v] : make_uint4(0, 0, 0, 0);
-      }
-      if (RES == 2) {
-        const uint4* rr = reinterpret_cast<const uint4*>(static_cast<const float*>(a.residual) + (size_t)row * a.H);
-        rv[2 * j] = ok ? rr[2 * v] : make_uint4(0, 0, 0, 0);
-        rv[2 * j + 1] = ok ? rr[2 * v + 1] : make_uint4(0, 0, 0, 0);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      unpack8(xv[j], h[j]);
-      if (RES == 1) {
-        float r[8];
-        unpack8(rv[j], r);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[j][i] = __fadd_rn(h[j][i], r[i]);
-      }
-      if (RES == 2) {
-        const uint32_t r[8] = {rv[2 * j].x, rv[2 * j].y, rv[2 * j].z, rv[2 * j].w,
-                               rv[2 * j + 1].x, rv[2 * j + 1].y, rv[2 * j + 1].z, rv[2 * j + 1].w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[j][i] = __fadd_rn(h[j][i], __uint_as_float(r[i]));
-      }
+    for (int j = 0; j < VPT; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss = fmaf(h[j][i], h[j][i], ss);
-    }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
     if (lane == 0) part[side][warp] = ss;
@@ -136,11 +175,9 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a) {
 #pragma unroll
         for (int off = 8; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
         const float s = block_scale(amax);
-        uint32_t c[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) c[i >> 2] |= (uint32_t)f32_to_e4m3(__fdiv_rn(h[j][i], s)) << (8 * (i & 3));
+        const uint2 c = codes8(h[j], s);
         if (ok) {
-          reinterpret_cast<uint2*>(a.q + (size_t)row * a.H)[v] = make_uint2(c[0], c[1]);
+          reinterpret_cast<uint2*>(a.q + (size_t)row * a.H)[v] = c;
           if ((lane & 15) == 0) a.q_scales[(size_t)row * (a.H / 128) + v / 16] = s;
         }
       }
@@ -150,15 +187,14 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a) {
 
 constexpr int kNormMaxH = 65536;   // 1024 threads of 8 vectors
 
-template <int VPT>
-void launch_norm(const NormArgs& a, int threads, cudaStream_t s) {
-  const int blocks = std::min(a.T, num_sms() * std::max(1, 2048 / threads));
+template <int VPT, bool AHEAD>
+void launch_norm(const NormArgs& a, int threads, int blocks, cudaStream_t s) {
   if (!a.residual)
-    rmsnorm_kernel<VPT, 0><<<blocks, threads, 0, s>>>(a);
+    rmsnorm_kernel<VPT, 0, AHEAD><<<blocks, threads, 0, s>>>(a);
   else if (!a.residual_f32)
-    rmsnorm_kernel<VPT, 1><<<blocks, threads, 0, s>>>(a);
+    rmsnorm_kernel<VPT, 1, AHEAD><<<blocks, threads, 0, s>>>(a);
   else
-    rmsnorm_kernel<VPT, 2><<<blocks, threads, 0, s>>>(a);
+    rmsnorm_kernel<VPT, 2, AHEAD><<<blocks, threads, 0, s>>>(a);
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -187,11 +223,13 @@ extern "C" moe_status_t moe_rmsnorm(const uint16_t* x, int T, int H, long long x
   const int nvec = H / 8;
   auto threads = [&](int vpt) { return ((nvec + vpt - 1) / vpt + 31) / 32 * 32; };
   if (threads(1) <= 1024 && T <= num_sms())
-    launch_norm<1>(a, threads(1), s);
+    launch_norm<1, false>(a, threads(1), T, s);
+  else if (threads(2) <= 512)
+    launch_norm<2, true>(a, threads(2), std::min(T, num_sms() * (1024 / threads(2))), s);
   else if (threads(4) <= 1024)
-    launch_norm<4>(a, threads(4), s);
+    launch_norm<4, false>(a, threads(4), std::min(T, num_sms() * std::max(1, 1024 / threads(4))), s);
   else
-    launch_norm<8>(a, threads(8), s);
+    launch_norm<8, false>(a, threads(8), std::min(T, num_sms()), s);
   MOE_CHECK_LAUNCH();
   return MOE_OK;
 }
