@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(FEW_WARPS * 32, 1)
   // this warp's items in order: round, chunk of the row
   const bool busy = warp < tiles * chunks;
   const int first = tiles > 1 ? warp % chunks : warp, tile = tiles > 1 ? warp / chunks : 0;
-  int load_round = busy ? (int)blockIdx.x : rounds, load_chunk = first;
+  int load_round = busy && !a.mute ? (int)blockIdx.x : rounds, load_chunk = first;
   uint32_t armed = 0;          // stages with a copy that was not waited for
   auto load = [&](int stage) {
     if (load_round >= rounds) return;
@@ -222,39 +222,54 @@ struct Plan {
   Split split;
 };
 
-// The cut of a variant, its K shared by `parts` CTAs to a tile (TC_64; as far as there are SMs and K blocks).
-Split cut(Variant v, int T, int N, int kblocks, int parts) {
-  const int tiles = tc_tiles(v, T, N), most = num_sms();
-  if (v == TC_64) parts = std::min(parts, std::min(most / tiles, kblocks));
-  return v == TC_64 && parts > 1 ? Split{tiles * parts, parts} : Split{std::min(most, tiles), 1};
+int tiles_of(Variant v, int T, int N) {
+  const long long t = v == SWAP ? (N + 127) / 128
+                                : (((long long)T + 127) / 128) * (((long long)N + (v == TC_64 ? 63 : 255)) / (v == TC_64 ? 64 : 256));
+  return (int)std::min<long long>(t, 0x7fffffff);
 }
 
-// Up to 16 rows the kernel for few rows; beyond, the tile width and the parts of K whose time, modelled in microseconds
-// from measured calls, is least:
-//   rounds of the SMs x (K blocks x the time of one + a tile's start and store), where a block takes 0.215 (64 columns) or
-//   0.5 (256), or its weights' share of the memory (8 and 32 KB at 41 GB/s an SM, read once for all row tiles);
-//   parts of K: their join takes 1.6 and 0.35 each.
-// Measured (64 / 256 columns): 512 x 4096 x 7168 27.5 / 32.8 us, 1024 x 4096 x 7168 50.3 / 33.3, 3000 x 576 x 7168 27.7 / 32.6,
-// 128 x 40960 x 4096 45.7 / 51.5; 64 columns, 1 / 2 / 4 / 8 parts: 24 x 576 x 7168 12.9 / 10.1 / 8.4 / 8.6.  Few rows against 64
-// columns: 16 x 4096 x 7168 10.5 / 21.5 (17.0 in two parts), 16 x 7168 x 16384 31 / 30, 24 x 4096 x 7168 with 32 rows of x
-// in the kernel for few 12.8 / 14.7 but 32 x 7168 x 16384 58 / 30.
+// The cut of a variant, its K shared by `parts` CTAs to a tile as far as there are SMs and K blocks (not the 256-column tiles,
+// which are for many rows).
+Split cut(Variant v, int T, int N, int kblocks, int parts) {
+  const int tiles = tiles_of(v, T, N), most = num_sms();
+  if (v != TC_256) parts = std::min(parts, std::min(most / tiles, kblocks));
+  return v != TC_256 && parts > 1 ? Split{tiles * parts, parts} : Split{std::min(most, tiles), 1};
+}
+
+moe_status_t launch_variant(Variant v, const Args& a, const Split& split, cudaStream_t s) {
+  return v == SWAP ? launch_swap(a, split, s) : launch_tc(v, a, split, s);
+}
+
+// By rows and weights, then the tile width and the parts of K whose time, modelled in microseconds from measured calls, is
+// least:
+//   up to 8 rows, and up to 16 where the weights are below 32 MB: the kernel for few rows
+//     (1 x 40960 x 4096 30.0 us, with weight rows as M 32.5; 16 x 4096 x 7168 10.7 / 10.5; 16 x 40960 x 4096 45.5 / 33.5);
+//   up to 32: weight rows as M (32 x 4096 x 7168 11.1, 128 x 64 tiles 12.2; 32 x 7168 x 2048 7.0 / 9.7);
+//   more: 128 x 64 or 128 x 256 tiles, rounds of the SMs x (K blocks x the time of one + a tile's start and store), where a
+//     block takes 0.215 (64 columns) or 0.5 (256), or its weights' share of the memory (8 and 32 KB at 41 GB/s an SM, read
+//     once for all row tiles).  64 / 256 columns: 512 x 4096 x 7168 27.5 / 32.8, 1024 x 4096 x 7168 50.3 / 33.3, 3000 x 576 x
+//     7168 27.7 / 32.6, 128 x 40960 x 4096 45.7 / 51.5.
+//   Parts of K: their join takes 1.6 and 0.35 each (1.3 and 0.2 with weight rows as M).  1 / 2 / 4 / 8 parts: 64 x 576 x 7168
+//     13.9 / 10.6 / 8.8 / 8.8, 32 x 4096 x 7168 15.3 / 11.9 / 11.1.
 Plan plan(int T, int N, int K) {
-  if (T <= FEW_COLS) return Plan{-1, {}};
+  if (T <= 8 || (T <= FEW_COLS && (long long)N * K < (32 << 20))) return Plan{-1, {}};
   const int kblocks = K / 128, most = num_sms();
+  const bool swap = T <= SWAP_ROWS;
+  const Variant narrow = swap ? SWAP : TC_64;
   const double row_tiles = (T + 127) / 128;
-  auto rounds = [&](Variant v) { return (tc_tiles(v, T, N) + most - 1) / most; };
-  const double narrow = kblocks * std::max(0.215, 0.2 / row_tiles);
-  const double t256 = rounds(TC_256) * (kblocks * std::max(0.5, 0.78 / row_tiles) + 2.3);
-  double best = rounds(TC_64) * (narrow + 0.9);
+  auto rounds = [&](Variant v) { return ((long long)tiles_of(v, T, N) + most - 1) / most; };
+  const double t = kblocks * std::max(0.215, 0.2 / row_tiles);
+  double best = rounds(narrow) * (t + 0.9);
   int parts = 1;
-  for (int p = 2; p <= std::min(8, most / tc_tiles(TC_64, T, N)); ++p) {
-    const double t = narrow / p + 0.9 + 1.6 + 0.35 * p;
-    if (t < best) {
-      best = t;
+  for (int p = 2; p <= std::min(8, most / tiles_of(narrow, T, N)); ++p) {
+    const double shared = t / p + 0.9 + (swap ? 1.3 + 0.2 * p : 1.6 + 0.35 * p);
+    if (shared < best) {
+      best = shared;
       parts = p;
     }
   }
-  const Variant v = t256 < best ? TC_256 : TC_64;
+  const bool wide = !swap && rounds(TC_256) * (kblocks * std::max(0.5, 0.78 / row_tiles) + 2.3) < best;
+  const Variant v = wide ? TC_256 : narrow;
   return Plan{v, cut(v, T, N, kblocks, parts)};
 }
 
@@ -266,14 +281,14 @@ Plan plan(int T, int N, int K) {
 extern "C" size_t moe_linear_e4m3_workspace_bytes(int T, int N, int K) {
   using namespace moe::lin8;
   if (!shape_ok(T, N, K)) return 0;
-  if (T <= FEW_COLS || 2 * tc_tiles(TC_64, 1, N) > moe::num_sms()) return 256;
+  if (T <= 8 || 2 * tiles_of(SWAP, 1, N) > moe::num_sms()) return 256;
   return count_bytes() + sum_bytes();
 }
 
 static moe_status_t linear_e4m3_impl(const uint8_t* x, const float* x_scales, int T, int K, const uint8_t* w,
                                      const float* w_scales, int N, const float* bias, void* out, int out_f32,
                                      long long out_stride, void* ws, size_t ws_bytes, int32_t* dev_status,
-                                     const moe::lin8::Plan* forced, unsigned long long limit_ns, void* stream) {
+                                     const moe::lin8::Plan* forced, unsigned long long limit_ns, int mute, void* stream) {
   using namespace moe;
   using namespace moe::lin8;
   auto bits = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
@@ -286,9 +301,10 @@ static moe_status_t linear_e4m3_impl(const uint8_t* x, const float* x_scales, in
       (bits(out) & (out_f32 ? 3 : 1)))
     return MOE_ERR_ARG;
   const Args a{x, x_scales, w, w_scales, bias, out, out_stride, T, N, K, out_f32, static_cast<int32_t*>(ws),
-               reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + count_bytes()), dev_status, limit_ns};
+               reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + count_bytes()), dev_status, limit_ns,
+               mute};
   const Plan p = forced ? *forced : plan(T, N, K);
-  if (p.variant >= 0) return launch_tc((Variant)p.variant, a, p.split, as_stream(stream));
+  if (p.variant >= 0) return launch_variant((Variant)p.variant, a, p.split, as_stream(stream));
   const bool wide = N / 32 >= moe::num_sms() / 2;
   if (T <= 8) return wide ? launch_few<1, 2>(a, as_stream(stream)) : launch_few<1, 1>(a, as_stream(stream));
   return wide ? launch_few<2, 2>(a, as_stream(stream)) : launch_few<2, 1>(a, as_stream(stream));
@@ -299,20 +315,22 @@ extern "C" moe_status_t moe_linear_e4m3(const uint8_t* x, const float* x_scales,
                                         long long out_stride, void* ws, size_t ws_bytes, int32_t* dev_status,
                                         void* stream) {
   return linear_e4m3_impl(x, x_scales, T, K, w, w_scales, N, bias, out, out_f32, out_stride, ws, ws_bytes, dev_status,
-                          nullptr, moe::lin8::LIMIT_NS, stream);
+                          nullptr, moe::lin8::LIMIT_NS, 0, stream);
 }
 
 // Test hook, deliberately absent from the public header: moe_linear_e4m3 by one variant whatever the sizes (-1: the
-// kernel for few rows, 0.. the tensor-core kernel's), with K shared by up to `parts` CTAs (variant 0), and with the limit of each wait
-// in nanoseconds, so that a test can make a wait run out.
+// kernel for few rows, 0.. the tensor-core kernel's), with K shared by up to `parts` CTAs (not variant 1), and with the limit of each wait
+// in nanoseconds.  mute: copies (few rows) or MMAs are never issued, so that a test can make the waits for them run
+// out.
 extern "C" moe_status_t moe_testing_linear_e4m3(const uint8_t* x, const float* x_scales, int T, int K, const uint8_t* w,
                                                 const float* w_scales, int N, const float* bias, void* out, int out_f32,
                                                 long long out_stride, void* ws, size_t ws_bytes, int32_t* dev_status,
-                                                int variant, int parts, unsigned long long limit_ns, void* stream) {
+                                                int variant, int parts, unsigned long long limit_ns, int mute,
+                                                void* stream) {
   using namespace moe::lin8;
-  if (!shape_ok(T, N, K) || variant < -1 || variant >= TC_VARIANTS || (variant == -1 && T > FEW_COLS)) return MOE_ERR_ARG;
+  if (!shape_ok(T, N, K) || variant < -1 || variant >= VARIANTS || (variant == -1 && T > FEW_COLS) || (variant == SWAP && T > SWAP_ROWS)) return MOE_ERR_ARG;
   Plan p{variant, {}};
   if (variant >= 0 && T > 0) p.split = cut((Variant)variant, T, N, K / 128, std::max(1, parts));
   return linear_e4m3_impl(x, x_scales, T, K, w, w_scales, N, bias, out, out_f32, out_stride, ws, ws_bytes, dev_status,
-                          &p, limit_ns, stream);
+                          &p, limit_ns, mute, stream);
 }

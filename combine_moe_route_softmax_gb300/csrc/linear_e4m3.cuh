@@ -21,6 +21,7 @@ struct Args {
   float* part;             // their sums
   int32_t* dev_status;
   unsigned long long limit_ns;   // of each wait
+  int mute;                // tests only: what the waits are for is never issued, so that they run out
 };
 
 constexpr unsigned long long LIMIT_NS = 2000000000ull;
@@ -30,8 +31,10 @@ constexpr unsigned long long LIMIT_NS = 2000000000ull;
 inline size_t count_bytes() { return ((size_t)num_sms() * 32 + 255) / 256 * 256; }
 inline size_t sum_bytes() { return (size_t)num_sms() * 128 * 64 * 4; }
 
-// Variants of the tensor-core kernel: 128 rows x so many weight rows of a tile.
-enum Variant { TC_64 = 0, TC_256 = 1, TC_VARIANTS = 2 };
+// Variants of the tensor-core kernels: tiles of 128 rows of x by 64 or 256 weight rows (linear_e4m3_tc.cu), or of 128 weight
+// rows by all of up to 32 rows of x (linear_e4m3_swap.cu).
+enum Variant { TC_64 = 0, TC_256 = 1, SWAP = 2, VARIANTS = 3 };
+constexpr int SWAP_ROWS = 32;
 
 // parts = 1: worker w computes the tiles w, w + workers, ..  parts > 1: worker w computes part w % parts of tile w / parts.
 struct Split {
@@ -39,7 +42,7 @@ struct Split {
 };
 
 moe_status_t launch_tc(Variant v, const Args& a, const Split& split, cudaStream_t s);
-int tc_tiles(Variant v, int T, int N);
+moe_status_t launch_swap(const Args& a, const Split& split, cudaStream_t s);
 
 }  // namespace lin8
 }  // namespace moe

@@ -4,19 +4,21 @@
 // blocks of 128, not a format that the MMA applies itself, so every block is an accumulation of its own: the MMAs of a K
 // block write a fresh accumulator in tensor memory, and the epilogue warps add it, times the product of its two
 // scales, to float32 sums in registers ("promotion") while the MMAs of the next blocks run.  A tile's 128 x BN float32
-// sums therefore have to fit into the registers of eight warps (BN <= 256: 128 of a thread's 232).
+// sums therefore have to fit into the registers of eight warps (BN <= 256: 128 of a thread's 224).
 //
-// What bounds it (8192 x 4096 x 7168, 207 us, 2320 TFLOP/s; a K block of a 128 x 256 tile takes 930 cycles where its MMAs need
+// What bounds it (8192 x 4096 x 7168, 200 us, 2400 TFLOP/s; a K block of a 128 x 256 tile takes 900 cycles where its MMAs need
 // 512): the hand-over of an accumulator.  Two of them fill tensor memory, and from a block's first MMA to the one that
 // overwrites it pass the MMAs, 280 cycles until the epilogue warps see them done, 400 until its 128 columns are
 // read (64 at a time: the sums leave no registers for more), and 300 until the issuing thread sees them free.  The same loop
 // without the reading takes 715, and without the MMAs 600 (operand tiles from L2, 48 KB a block, 19 TB/s).
-//   Tried and not kept: pairs of SMs (cta_group::2, M = 256, 32 KB a block): 222 us, each hand-over crosses an SM more;
-//   192 columns, read at once: 265; 128 columns, four accumulators: 236 here and behind 64 or 256 at every other size; two MMAs of 128 columns with barriers of their own: 236; packed fma.f32x2: 228 against
-//   217 (its operands have to be moved into pairs).
+//   Tried and not kept: pairs of SMs (cta_group::2, M = 256, 32 KB a block): 222 us where this took 207, each hand-over crosses
+//   an SM more; 192 columns, read at once: 265; 128 columns, four accumulators: 236 here and behind 64 or 256 at every other
+//   size; two MMAs of 128 columns with barriers of their own: 236; packed fma.f32x2: 228 against 217 (its operands have to be
+//   moved into pairs); sixteen epilogue warps of 64 columns: 208.
 //   Kept: one lane issues behind elect.sync, in a form that the compiler knows to be one thread (128 columns: 326 -> 228 us);
-//   one commit per block, on whose barrier both the producer and the epilogue wait; the accumulator is given back
-//   before its last 64 columns are added (217 -> 207); two issuing threads, even and odd blocks (BN = 64: 345 -> 308).
+//   one commit per block, on whose barrier both the producer and the epilogue wait; the accumulator is given back before
+//   its last 64 columns are added (217 -> 207); two issuing threads, even and odd blocks (64 columns: 345 -> 308); 56 registers
+//   for the first warpgroup, whose threads kept some in local memory with 40 (207 -> 200).
 //
 // Warps (384 threads, one CTA per SM): 0 loads the operands by TMA; 1 and 2 issue the MMAs (1 allocates the tensor
 // memory); 3 is idle; 4..11 epilogue: warp w reads TMEM lanes 32 (w % 4).. and half (w - 4) / 4 of the columns.  The first
@@ -28,17 +30,13 @@
 //
 // Every wait is bounded; on expiry the CTA sets MOE_DEV_PIPELINE_TIMEOUT and every role leaves its loop, as in the
 // grouped GEMM kernels.
-#include "gemm_common.cuh"
-#include "linear_e4m3.cuh"
+#include "linear_e4m3_tc.cuh"
 
 namespace moe {
 namespace lin8 {
 
-using namespace gg;
-
 namespace {
 
-constexpr int TC_THREADS = 384;
 constexpr int EPI = 8;
 constexpr int STAGE_RING = 192 * 1024;
 constexpr int OUT_BYTES = 32 * 128;      // an epilogue warp's transpose: 32 rows of 128 bytes
@@ -58,44 +56,8 @@ struct Cfg {
   static_assert(stage % 1024 == 0, "swizzle atoms");
 };
 
-// tcgen05.wait::ld, with the loaded registers as operands: nothing that uses them is moved ahead of it.
-__device__ __forceinline__ void wait_ld(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
-}
-// One lane of a converged warp, in a form by which the compiler knows that a single thread runs what follows: the
-// operands of tcgen05 and TMA instructions live in the warp's uniform registers, and behind a condition on the lane's
-// number every such instruction is wrapped in a loop over the lanes that might be there.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.b32 %0, 1, 0, q;\n\t}" : "=r"(p));
-  return p != 0;
-}
 constexpr int SHARED_COLS = 64;
 
-// A stretch of one tile's K.
-struct Piece {
-  int tile, k0, k1;
-};
-// The pieces of worker `w`, in order (the same for every role of its CTA): whole tiles, one for each round of the workers,
-// or its part of the one tile that it shares.
-struct Walk {
-  int next, step, tiles, k0, k1;
-  __device__ __forceinline__ Walk(int w, int tiles_, int kblocks, const Split& s)
-      : next(w / s.parts), step(s.workers), tiles(tiles_), k0((int)((long long)kblocks * (w % s.parts) / s.parts)),
-        k1((int)((long long)kblocks * (w % s.parts + 1) / s.parts)) {}
-  __device__ __forceinline__ bool get(Piece& p) {
-    if (next >= tiles) return false;
-    p.tile = next;
-    p.k0 = k0;
-    p.k1 = k1;
-    next += step;      // at least all tiles where K is shared
-    return true;
-  }
-};
 // Tile -> row tile and column tile: groups of 8 row tiles, column tile after column tile inside a group, so that
 // the workers of a round share both operands' tiles in L2.
 constexpr int GROUP_M = 8;
@@ -213,78 +175,20 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   Piece p;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0 && elect_one()) {
-      // -------------------------------------------------------------- TMA producer
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmA)) : "memory");
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmB)) : "memory");
-      int stage = 0;
-      uint32_t phase = 0, armed = 0, last_parity = 0;
-      bool ok = true;
-      while (ok && walk.get(p)) {
-        int m, n;
-        tile_at(p.tile, mt, nt, m, n);
-        const int ra = m * 128, rb = n * BN_;
-        for (int kb = p.k0; kb < p.k1; ++kb) {
-          if (!wait(bar_done(stage), phase ^ 1)) {
-            ok = false;
-            break;
-          }
-          armed |= 1u << stage;
-          last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
-          const uint32_t sa = sbase + stage * C::stage;
-          mbar_expect_tx(bar_full(stage), C::stage);
-          tma_load_2d(sa, &tmA, kb * 128, ra, bar_full(stage));
-          tma_load_2d(sa + A_BYTES, &tmB, kb * 128, rb, bar_full(stage));
-          if (++stage == C::stages) {
-            stage = 0;
-            phase ^= 1;
-          }
-        }
-      }
-      // copies still in flight land before this CTA's shared memory goes away (and with a stage's copies its MMAs)
-      for (int s = 0; s < C::stages; ++s)
-        if (armed & (1u << s)) mbar_drain(ok ? bar_done(s) : bar_full(s), (last_parity >> s) & 1u);
-    } else if ((warp == 1 || warp == 2) && elect_one()) {
-      // -------------------------------------------------------------- MMA issuers: even and odd K blocks of the CTA's
-      // sequence (the stages and accumulators are even in number, so each has its own of them)
-      constexpr uint32_t idesc = (1u << 4) | (uint32_t)(BN_ >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
-      int stage = 0, buf = 0;
-      uint32_t phase = 0, tphase = 0, g = (uint32_t)warp - 1;
-      bool ok = true;
-      while (ok && walk.get(p)) {
-        for (int kb = p.k0; kb < p.k1; ++kb, ++g) {
-          if ((g & 1u) == 0) {
-            if (!wait(bar_full(stage), phase) || !wait(bar_tempty(buf), tphase ^ 1)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t sa = sbase + stage * C::stage, dt = tmem_base + buf * BN_;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc_mma<true>(dt, smem_desc(sa + 32 * k), smem_desc(sa + A_BYTES + 32 * k), idesc, k != 0);
-            tc_commit(bar_done(stage));
-          }
-          if (++stage == C::stages) {
-            stage = 0;
-            phase ^= 1;
-          }
-          if (++buf == C::bufs) {
-            buf = 0;
-            tphase ^= 1;
-          }
-        }
-      }
-      if (!ok) {
-        const uint32_t drain = bar_drain + 8u * ((uint32_t)warp - 1);
-        tc_commit(drain);   // arrives once every MMA that this thread issued has completed
-        mbar_drain(drain, 0);
-      }
+      load_tiles<C::stages, C::stage>(walk, &tmA, &tmB, sbase, bar_full(0), bar_done(0), wait, [&](int tile, int& ra, int& rb) {
+        tile_at(tile, mt, nt, ra, rb);
+        ra *= 128;
+        rb *= BN_;
+      });
+    } else if ((warp == 1 || warp == 2) && !a.mute && elect_one()) {
+      issue_mmas<C::stages, C::stage, C::bufs, BN_>(walk, (uint32_t)warp - 1, sbase, tmem_base, bar_full(0), bar_done(0),
+                                                    bar_tempty(0), bar_drain, wait);
     }
     __syncwarp();
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     // ---------------------------------------------------------------- epilogue
     const int ew = warp - 4, q = warp & 3, half = ew >> 2;
     const uint32_t lane_addr = (uint32_t)(32 * q) << 16;
@@ -430,21 +334,9 @@ moe_status_t launch(const Args& a, const Split& split, cudaStream_t s) {
   return MOE_OK;
 }
 
-constexpr int kCols[TC_VARIANTS] = {64, 256};
-
 }  // namespace
 
-int tc_tiles(Variant v, int T, int N) {
-  const long long t = ((long long)T + 127) / 128 * (((long long)N + kCols[v] - 1) / kCols[v]);
-  return (int)std::min<long long>(t, 0x7fffffff);
-}
-
 moe_status_t launch_tc(Variant v, const Args& a, const Split& split, cudaStream_t s) {
-  if (split.workers < 1 || split.parts < 1 || split.workers > num_sms()) return MOE_ERR_ARG;
-  // a shared tile's parts are one round of the workers, and none is empty
-  if (split.parts > 1 && (kCols[v] != SHARED_COLS || split.parts > a.K / 128 ||
-                          split.workers != tc_tiles(v, a.T, a.N) * split.parts))
-    return MOE_ERR_ARG;
   switch (v) {
     case TC_64: return launch<64>(a, split, s);
     default: return launch<256>(a, split, s);
