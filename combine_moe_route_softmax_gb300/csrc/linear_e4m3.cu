@@ -223,66 +223,72 @@ struct Plan {
 };
 
 int tiles_of(Variant v, int T, int N) {
-  const long long t = v == SWAP ? (N + 127) / 128
-                                : (((long long)T + 127) / 128) * (((long long)N + (v == TC_64 ? 63 : 255)) / (v == TC_64 ? 64 : 256));
+  const int cols = v == TC_64 ? 64 : v == TC_256 ? 256 : 128;
+  const long long t = (v == SWAP ? 1 : ((long long)T + 127) / 128) * (((long long)N + cols - 1) / cols);
   return (int)std::min<long long>(t, 0x7fffffff);
 }
 
-// The cut of a variant, its K shared by `parts` CTAs to a tile as far as there are SMs and K blocks (not the 256-column tiles,
-// which are for many rows).
+// The cut of a variant: whole tiles in full rounds of the SMs, and the rest, each shared by `parts` CTAs as far as there are
+// SMs and K blocks (not the 256-column tiles, which are for many rows).
 Split cut(Variant v, int T, int N, int kblocks, int parts) {
-  const int tiles = tiles_of(v, T, N), most = num_sms();
-  if (v != TC_256) parts = std::min(parts, std::min(most / tiles, kblocks));
-  return v != TC_256 && parts > 1 ? Split{tiles * parts, parts} : Split{std::min(most, tiles), 1};
+  const int tiles = tiles_of(v, T, N), most = num_sms(), rest = tiles % most;
+  parts = v == TC_256 || rest == 0 ? 1 : std::min(parts, std::min(most / rest, kblocks));
+  if (parts <= 1) return Split{std::min(most, tiles), tiles, 1};
+  return Split{tiles > rest ? most : rest * parts, tiles - rest, parts};
 }
 
 moe_status_t launch_variant(Variant v, const Args& a, const Split& split, cudaStream_t s) {
   return v == SWAP ? launch_swap(a, split, s) : launch_tc(v, a, split, s);
 }
 
-// By rows and weights, then the tile width and the parts of K whose time, modelled in microseconds from measured calls, is
-// least:
-//   up to 8 rows, and up to 16 where the weights are below 32 MB: the kernel for few rows
-//     (1 x 40960 x 4096 30.0 us, with weight rows as M 32.5; 16 x 4096 x 7168 10.7 / 10.5; 16 x 40960 x 4096 45.5 / 33.5);
-//   up to 32: weight rows as M (32 x 4096 x 7168 11.1, 128 x 64 tiles 12.2; 32 x 7168 x 2048 7.0 / 9.7);
-//   more: 128 x 64 or 128 x 256 tiles, rounds of the SMs x (K blocks x the time of one + a tile's start and store), where a
-//     block takes 0.215 (64 columns) or 0.5 (256), or its weights' share of the memory (8 and 32 KB at 41 GB/s an SM, read
-//     once for all row tiles).  64 / 256 columns: 512 x 4096 x 7168 27.5 / 32.8, 1024 x 4096 x 7168 50.3 / 33.3, 3000 x 576 x
-//     7168 27.7 / 32.6, 128 x 40960 x 4096 45.7 / 51.5.
-//   Parts of K: their join takes 1.6 and 0.35 each (1.3 and 0.2 with weight rows as M).  1 / 2 / 4 / 8 parts: 64 x 576 x 7168
-//     13.9 / 10.6 / 8.8 / 8.8, 32 x 4096 x 7168 15.3 / 11.9 / 11.1.
+// By rows and weights, then the tile width and the parts of K whose time, modelled from measured calls, is least.
+//   Up to 8 rows, and up to 16 where the weights are below 32 MB: the kernel for few rows (1 x 40960 x 4096 30.0 us, with weight
+//   rows as M 32.5; 16 x 4096 x 7168 10.7 / 10.5; 16 x 40960 x 4096 45.5 / 33.5).
+//   Up to 32: weight rows as M (32 x 4096 x 7168 10.7, with 128 x 64 tiles 12.0; 32 x 7168 x 2048 7.0 / 9.6).
+//   More, 64 / 128 / 256 columns: 64 x 4096 x 7168 12.5 / 14.9 / 31, 512 x 4096 x 7168 26.8 / 21.0 / 31.7, 3000 x 576 x 7168 24.3 /
+//   20.6 / 31.5, 2048 x 2048 x 2048 19.4 / 18.0 / 14.8, 8192 x 4096 x 7168 304 / 239 / 200.
+//   Parts 1 / 2 / 4 / 8: 64 x 576 x 7168 14.0 / 10.7 / 8.8 / 8.8, 700 x 576 x 7168 14.7 / 11.8, 32 x 4096 x 7168 14.3 / 11.7 / 10.7; of a
+//   last round (128 x 40960 x 4096) 43.4 / 42.5 / 42.0 / 41.9.
 Plan plan(int T, int N, int K) {
   if (T <= 8 || (T <= FEW_COLS && (long long)N * K < (32 << 20))) return Plan{-1, {}};
+  // microseconds of a K block, of a tile's start and store, of a join and of each of its parts; a block takes at least its
+  // weights' share of the memory (41 bytes a nanosecond and SM), read once for all row tiles
+  struct Cost {
+    Variant v;
+    double block, bytes, tile, join, part;
+  };
+  static constexpr Cost kCosts[] = {{TC_64, 0.205, 8192, 0.6, 2.2, 0.45},
+                                    {TC_128, 0.30, 16384, 2.0, 4.0, 0.75},
+                                    {TC_256, 0.49, 32768, 2.3, 0.0, 0.0},
+                                    {SWAP, 0.21, 16384, 0.6, 1.7, 0.8}};
   const int kblocks = K / 128, most = num_sms();
-  const bool swap = T <= SWAP_ROWS;
-  const Variant narrow = swap ? SWAP : TC_64;
   const double row_tiles = (T + 127) / 128;
-  auto rounds = [&](Variant v) { return ((long long)tiles_of(v, T, N) + most - 1) / most; };
-  const double t = kblocks * std::max(0.215, 0.2 / row_tiles);
-  double best = rounds(narrow) * (t + 0.9);
-  int parts = 1;
-  for (int p = 2; p <= std::min(8, most / tiles_of(narrow, T, N)); ++p) {
-    const double shared = t / p + 0.9 + (swap ? 1.3 + 0.2 * p : 1.6 + 0.35 * p);
-    if (shared < best) {
-      best = shared;
-      parts = p;
+  Plan best{-1, {}};
+  double least = 0.0;
+  for (const Cost& c : kCosts) {
+    if ((c.v == SWAP) != (T <= SWAP_ROWS)) continue;
+    const double k = kblocks * std::max(c.block, c.bytes / 41e3 / row_tiles);
+    const int tiles = tiles_of(c.v, T, N), rest = tiles % most;
+    for (int p = 1; p <= 8; ++p) {
+      if (p > 1 && (c.v == TC_256 || rest == 0 || p * rest > most || p > kblocks)) break;
+      const double t = tiles / most * (k + c.tile) + (rest ? k / p + c.tile : 0.0) + (p > 1 ? c.join + c.part * p : 0.0);
+      if (best.variant < 0 || t < least) {
+        least = t;
+        best = Plan{c.v, cut(c.v, T, N, kblocks, p)};
+      }
     }
   }
-  const bool wide = !swap && rounds(TC_256) * (kblocks * std::max(0.5, 0.78 / row_tiles) + 2.3) < best;
-  const Variant v = wide ? TC_256 : narrow;
-  return Plan{v, cut(v, T, N, kblocks, parts)};
+  return best;
 }
 
 }  // namespace lin8
 }  // namespace moe
 
-// Only calls whose K is shared use a workspace: more rows than the kernel for few takes, and so few columns that even one
-// row tile leaves SMs over.  One size for all of them, so that what was made for T rows serves fewer.
+// Only calls whose K is shared use a workspace.  One size for all of them, so that what was made for T rows serves fewer.
 extern "C" size_t moe_linear_e4m3_workspace_bytes(int T, int N, int K) {
   using namespace moe::lin8;
   if (!shape_ok(T, N, K)) return 0;
-  if (T <= 8 || 2 * tiles_of(SWAP, 1, N) > moe::num_sms()) return 256;
-  return count_bytes() + sum_bytes();
+  return T <= 8 ? 256 : count_bytes() + sum_bytes();
 }
 
 static moe_status_t linear_e4m3_impl(const uint8_t* x, const float* x_scales, int T, int K, const uint8_t* w,

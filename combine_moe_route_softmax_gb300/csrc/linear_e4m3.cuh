@@ -27,18 +27,19 @@ struct Args {
 constexpr unsigned long long LIMIT_NS = 2000000000ull;
 
 // A workspace: the counters (eight for each shared tile, of which there are fewer than SMs), then the sums of the parts (of at
-// most 128 x 64 values, no more of them than SMs).
+// most 128 x 128 values, no more of them than SMs).
 inline size_t count_bytes() { return ((size_t)num_sms() * 32 + 255) / 256 * 256; }
-inline size_t sum_bytes() { return (size_t)num_sms() * 128 * 64 * 4; }
+inline size_t sum_bytes() { return (size_t)num_sms() * 128 * 128 * 4; }
 
-// Variants of the tensor-core kernels: tiles of 128 rows of x by 64 or 256 weight rows (linear_e4m3_tc.cu), or of 128 weight
-// rows by all of up to 32 rows of x (linear_e4m3_swap.cu).
-enum Variant { TC_64 = 0, TC_256 = 1, SWAP = 2, VARIANTS = 3 };
+// Variants of the tensor-core kernels: tiles of 128 rows of x by 64, 128 or 256 weight rows (linear_e4m3_tc.cu), or of 128
+// weight rows by all of up to 32 rows of x (linear_e4m3_swap.cu).
+enum Variant { TC_64 = 0, TC_128 = 1, TC_256 = 2, SWAP = 3, VARIANTS = 4 };
 constexpr int SWAP_ROWS = 32;
 
-// parts = 1: worker w computes the tiles w, w + workers, ..  parts > 1: worker w computes part w % parts of tile w / parts.
+// Tiles [0, whole): worker w computes the tiles w, w + workers, ..  The others are shared: worker w computes part w % parts
+// of tile whole + w / parts, if there is one.
 struct Split {
-  int workers, parts;
+  int workers, whole, parts;
 };
 
 moe_status_t launch_tc(Variant v, const Args& a, const Split& split, cudaStream_t s);

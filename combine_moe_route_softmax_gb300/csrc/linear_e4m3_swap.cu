@@ -1,9 +1,9 @@
 // moe_linear_e4m3 on the 5th-generation tensor cores for up to 32 rows of x: the weights are the MMA's M operand (128 rows),
 // the rows of x its N (32 columns), so that a K block of 16 KB of weights needs 4 KB of x beside it, where a 128-row tile
-// of x would be mostly padding.  Such a call is a stream of weights, each read once: 32 x 40960 x 4096 34 us (4.9 TB/s; 40
-// with 128 x 64 tiles), 32 x 7168 x 16384 24.6 us in two parts (30), 32 x 4096 x 7168 11.1 us in four (12.2).  With 64 columns
-// (8 KB of x and twice the sums) it only draws level: 64 x 4096 x 7168 13.2 against 12.7, 64 x 40960 x 4096 39 against 42.5;
-// with 128 it falls behind.
+// of x would be mostly padding.  Such a call is a stream of weights, each read once: 32 x 40960 x 4096 32.1 us (5.2 TB/s; 38
+// with 128 x 64 tiles), 32 x 4096 x 7168 10.7 us with each tile's K in four parts (12.0 in two).  The same with 64 or 128 columns
+// was not kept: 64 x 4096 x 7168 13.1 against 12.5, 64 x 40960 x 4096 37.0 against 39.4, 128 x 40960 x 4096 59 against 42 (the
+// scales of each column have to be fetched for each block).
 //
 // As in linear_e4m3_tc.cu every K block is an accumulation of its own, scaled and added to float32 registers.  Here a lane
 // holds a weight row and the columns are rows of x, so the scales differ from column to column: warp 3 multiplies a block's
@@ -12,7 +12,8 @@
 // neighbours in a row of out.
 //
 // Warps: 0 TMA, 1 and 2 MMA issuers (1 allocates the tensor memory), 3 scales, 4..11 epilogue: warp w reads TMEM lanes
-// 32 (w % 4).. and half (w - 4) / 4 of the columns.  Shared K and bounded waits as in linear_e4m3_tc.cu.
+// 32 (w % 4).. of every second K block (warps 4..7 the even ones, 8..11 the odd ones); the sums of the two meet in shared
+// memory at the end of a tile.  Shared K and bounded waits as in linear_e4m3_tc.cu.
 #include "linear_e4m3_tc.cuh"
 
 namespace moe {
@@ -28,14 +29,15 @@ struct C {
   static constexpr int stages = 192 * 1024 / stage < 8 ? 192 * 1024 / stage : 8;
   static constexpr int bufs = 4;
   static constexpr int tmem = bufs * TB;
-  static constexpr int cols = TB / 2;                          // of an epilogue warp
-  static constexpr int scales = stages * stage;                // float [bufs][TB]
+  static constexpr int meet_bytes = 16 * 32 * 4;               // of an epilogue warp
+  static constexpr int meets = stages * stage;
+  static constexpr int scales = meets + EPI * meet_bytes;      // float [bufs][TB]
   static constexpr int bars = scales + bufs * TB * 4;
   static constexpr int n_bars = 2 * stages + 2 * bufs + 2;
   static constexpr int smem = bars + n_bars * 8 + 16 + 1024;   // + align slack
   static_assert(smem <= SMEM_MAX, "shared memory");
   static_assert(stage % 1024 == 0, "swizzle atoms");
-  static_assert(TB == 32 && cols == 16, "a lane of the scale warp to a row, one load of an accumulator");
+  static_assert(TB == 32, "a lane of the scale warp to a row of x, one load of an accumulator");
 };
 
 __global__ void __launch_bounds__(TC_THREADS, 1)
@@ -63,7 +65,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       mbar_init(bar_done(s), 1);
     }
     for (int b = 0; b < C::bufs; ++b) {
-      mbar_init(bar_tempty(b), EPI);
+      mbar_init(bar_tempty(b), EPI / 2);
       mbar_init(bar_sfull(b), 1);
     }
     mbar_init(bar_drain, 1);
@@ -85,84 +87,85 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   Walk walk((int)blockIdx.x, tiles, kblocks, split);
   Piece p;
 
-  if (warp < 3) {
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
       if (elect_one())
         load_tiles<C::stages, C::stage>(walk, &tmW, &tmX, sbase, bar_full(0), bar_done(0), wait, [&](int tile, int& ra, int& rb) {
           ra = tile * 128;
           rb = 0;
         });
-    } else if (!a.mute && elect_one()) {
-      issue_mmas<C::stages, C::stage, C::bufs, TB>(walk, (uint32_t)warp - 1, sbase, tmem_base, bar_full(0), bar_done(0),
-                                                   bar_tempty(0), bar_drain, wait);
-    }
-    __syncwarp();
-  } else if (warp == 3) {
-    // ---------------------------------------------------------------- scales: lane l that of row l
-    int buf = 0;
-    uint32_t tphase = 0;
-    bool ok = true;
-    while (ok && walk.get(p)) {
-      const float* ws = a.w_scales + (long long)p.tile * kblocks;
-      const float* xs = a.x_scales + (long long)min(lane, a.T - 1) * kblocks;
-      float x = __ldg(xs + p.k0), w = __ldg(ws + p.k0);
-      for (int kb = p.k0; kb < p.k1; ++kb) {
-        const float s = __fmul_rn(x, w);
-        if (kb + 1 < p.k1) {
-          w = __ldg(ws + kb + 1);
-          x = __ldg(xs + kb + 1);
-        }
-        if (!__all_sync(0xffffffffu, wait(bar_tempty(buf), tphase ^ 1))) {
-          ok = false;
-          break;
-        }
-        scales[buf * TB + lane] = s;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_sfull(buf));
-        if (++buf == C::bufs) {
-          buf = 0;
-          tphase ^= 1;
+    } else if (warp < 3) {
+      if (!a.mute && elect_one())
+        issue_mmas<C::stages, C::stage, C::bufs, TB>(walk, (uint32_t)warp - 1, sbase, tmem_base, bar_full(0), bar_done(0),
+                                                     bar_tempty(0), bar_drain, wait);
+    } else {
+      // -------------------------------------------------------------- scales: lane l that of row l
+      int buf = 0;
+      uint32_t tphase = 0;
+      bool ok = true;
+      while (ok && walk.get(p)) {
+        const float* ws = a.w_scales + (long long)p.tile * kblocks;
+        const float* xs = a.x_scales + (long long)min(lane, a.T - 1) * kblocks;
+        float x = __ldg(xs + p.k0), w = __ldg(ws + p.k0);
+        for (int kb = p.k0; kb < p.k1; ++kb) {
+          const float s = __fmul_rn(x, w);
+          if (kb + 1 < p.k1) {
+            w = __ldg(ws + kb + 1);
+            x = __ldg(xs + kb + 1);
+          }
+          if (!__all_sync(0xffffffffu, wait(bar_tempty(buf), tphase ^ 1))) {
+            ok = false;
+            break;
+          }
+          scales[buf * TB + lane] = s;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_sfull(buf));
+          if (++buf == C::bufs) {
+            buf = 0;
+            tphase ^= 1;
+          }
         }
       }
     }
+    __syncwarp();
   } else {
-    // ---------------------------------------------------------------- epilogue
-    const int ew = warp - 4, q = warp & 3, half = ew >> 2, t0 = half * C::cols;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    // ---------------------------------------------------------------- epilogue: the warpgroups take K blocks in turns
+    const int ew = warp - 4, q = warp & 3, half = ew >> 2;
     const uint32_t lane_addr = (uint32_t)(32 * q) << 16;
-    const bool live = t0 < a.T;
+    float* mine = reinterpret_cast<float*>(smem + C::meets + ew * C::meet_bytes);
+    const float* other = reinterpret_cast<const float*>(smem + C::meets + (ew ^ 4) * C::meet_bytes);
     int buf = 0, stage = 0;
-    uint32_t phase = 0, bphase = 0;
+    uint32_t phase = 0, bphase = 0, g = (uint32_t)half;
     bool ok = true;
     while (ok && walk.get(p)) {
-      float acc[C::cols];
+      float acc[TB];
 #pragma unroll
-      for (int i = 0; i < C::cols; ++i) acc[i] = 0.0f;
-      for (int kb = p.k0; kb < p.k1; ++kb) {
-        // the warp leaves together: what follows is executed by all of its lanes
-        if (!__all_sync(0xffffffffu, wait(bar_sfull(buf), bphase) && wait(bar_done(stage), phase))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (live) {
-          uint32_t r[C::cols];
-          float4 s[C::cols / 4];
-          const float4* from = reinterpret_cast<const float4*>(scales + buf * TB + t0);
-#pragma unroll
-          for (int i = 0; i < C::cols / 4; ++i) s[i] = from[i];
-          tmem_ld16(tmem_base + lane_addr + buf * TB + t0, r);
-          wait_ld(r);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_tempty(buf));
-#pragma unroll
-          for (int i = 0; i < C::cols / 4; ++i) {
-            acc[4 * i] = fmaf(__uint_as_float(r[4 * i]), s[i].x, acc[4 * i]);
-            acc[4 * i + 1] = fmaf(__uint_as_float(r[4 * i + 1]), s[i].y, acc[4 * i + 1]);
-            acc[4 * i + 2] = fmaf(__uint_as_float(r[4 * i + 2]), s[i].z, acc[4 * i + 2]);
-            acc[4 * i + 3] = fmaf(__uint_as_float(r[4 * i + 3]), s[i].w, acc[4 * i + 3]);
+      for (int i = 0; i < TB; ++i) acc[i] = 0.0f;
+      for (int kb = p.k0; kb < p.k1; ++kb, ++g) {
+        if ((g & 1u) == 0) {
+          // the warp leaves together: what follows is executed by all of its lanes
+          if (!__all_sync(0xffffffffu, wait(bar_sfull(buf), bphase) && wait(bar_done(stage), phase))) {
+            ok = false;
+            break;
           }
-        } else {
+          tc_fence_after();
+          const uint32_t tb = tmem_base + lane_addr + buf * TB;
+          const float4* sc = reinterpret_cast<const float4*>(scales + buf * TB);
+          uint32_t r[32];
+          float4 f[8];
+          tmem_ld32(tb, r);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = sc[i];
+          wait_ld(r);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            acc[4 * i] = fmaf(__uint_as_float(r[4 * i]), f[i].x, acc[4 * i]);
+            acc[4 * i + 1] = fmaf(__uint_as_float(r[4 * i + 1]), f[i].y, acc[4 * i + 1]);
+            acc[4 * i + 2] = fmaf(__uint_as_float(r[4 * i + 2]), f[i].z, acc[4 * i + 2]);
+            acc[4 * i + 3] = fmaf(__uint_as_float(r[4 * i + 3]), f[i].w, acc[4 * i + 3]);
+          }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_tempty(buf));
@@ -176,45 +179,23 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           phase ^= 1;
         }
       }
-      if (!ok) break;
-      const int n = p.tile * 128 + 32 * q + lane;
-      if (!live || p.tile * 128 + 32 * q >= a.N) continue;
-      if (split.parts > 1) {
-        // a part of the tile: the sums go to this worker's slot, and the last of the tile's parts to be counted adds all
-        // of them up in their order
-        const int worker = (int)blockIdx.x, first = worker - worker % split.parts;
-        auto slot = [&](int w) { return a.part + ((size_t)w * EPI + ew) * (C::cols * 32) + lane; };
-        float* own = slot(worker);
-#pragma unroll
-        for (int i = 0; i < C::cols; ++i) __stcg(own + 32 * i, acc[i]);
-        __syncwarp();
-        int before = 0;
-        int32_t* count = a.count + p.tile * EPI + ew;
-        if (lane == 0)
-          asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(count) : "memory");
-        before = __shfl_sync(0xffffffffu, before, 0);
-        if (before != split.parts - 1) continue;
-        if (lane == 0) *count = 0;
-        for (int w = 0; w < split.parts; ++w) {
-          const float* from = slot(first + w);
-          float f[C::cols];
-#pragma unroll
-          for (int i = 0; i < C::cols; ++i) f[i] = __ldcg(from + 32 * i);
-#pragma unroll
-          for (int i = 0; i < C::cols; ++i) acc[i] = w ? __fadd_rn(acc[i], f[i]) : f[i];
-        }
-      }
+      constexpr int KEEP = TB / 2;
+      float v[KEEP];
+      if (!meet<16>(acc, v, mine, other, half, lane, 1 + q, ok)) break;
+      const int n = p.tile * 128 + 32 * q + lane, t0 = half * KEEP;
+      if (p.tile * 128 + 32 * q >= a.N || t0 >= a.T) continue;
+      if (p.tile >= split.whole && !join_parts(a, split, p.tile, (int)blockIdx.x, ew, lane, v)) continue;
       if (n < a.N) {
         const float b = a.bias ? __ldg(a.bias + n) : 0.0f;
 #pragma unroll
-        for (int i = 0; i < C::cols; ++i) {
+        for (int i = 0; i < KEEP; ++i) {
           if (t0 + i < a.T) {
-            const float v = a.bias ? __fadd_rn(acc[i], b) : acc[i];
+            const float o = a.bias ? __fadd_rn(v[i], b) : v[i];
             const long long at = (long long)(t0 + i) * a.out_stride + n;
             if (a.out_f32)
-              static_cast<float*>(a.out)[at] = v;
+              static_cast<float*>(a.out)[at] = o;
             else
-              static_cast<uint16_t*>(a.out)[at] = f32_to_bf16(v);
+              static_cast<uint16_t*>(a.out)[at] = f32_to_bf16(o);
           }
         }
       }

@@ -47,7 +47,10 @@ struct Cfg {
   static constexpr int stages = STAGE_RING / stage < 8 ? STAGE_RING / stage : 8;
   static constexpr int bufs = 512 / BN_ < 4 ? 512 / BN_ : 4;
   static constexpr int tmem = bufs * BN_;
-  static constexpr int cols = BN_ / 2;                         // of an epilogue warp
+  // TURNS: the epilogue's two warpgroups take even and odd K blocks in turns, all columns each; else every block, half of
+  // the columns each
+  static constexpr bool TURNS = BN_ == 128;
+  static constexpr int cols = TURNS ? BN_ : BN_ / 2;           // of an epilogue warp
   static constexpr int out = stages * stage;
   static constexpr int bars = out + EPI * OUT_BYTES;
   static constexpr int n_bars = 2 * stages + bufs + 2;
@@ -55,8 +58,6 @@ struct Cfg {
   static_assert(smem <= SMEM_MAX, "shared memory");
   static_assert(stage % 1024 == 0, "swizzle atoms");
 };
-
-constexpr int SHARED_COLS = 64;
 
 // Tile -> row tile and column tile: groups of 8 row tiles, column tile after column tile inside a group, so that
 // the workers of a round share both operands' tiles in L2.
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       mbar_init(bar_full(s), 1);
       mbar_init(bar_done(s), 1);
     }
-    for (int b = 0; b < C::bufs; ++b) mbar_init(bar_tempty(b), EPI);
+    for (int b = 0; b < C::bufs; ++b) mbar_init(bar_tempty(b), C::TURNS ? EPI / 2 : EPI);
     mbar_init(bar_drain, 1);
     mbar_init(bar_drain + 8, 1);
     *abort_flag = 0;
@@ -195,67 +196,71 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     uint8_t* buf_w = smem + C::out + ew * OUT_BYTES;
     const bool vec = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && a.out_stride % (a.out_f32 ? 4 : 8) == 0;
     int buf = 0, stage = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, g = (uint32_t)half;     // g: K blocks until this warp's next one (TURNS)
     bool ok = true;
     while (ok && walk.get(p)) {
       int m, n;
       tile_at(p.tile, mt, nt, m, n);
       const long long row0 = (long long)m * 128 + 32 * q;
       const int rows = (int)min((long long)32, a.T - row0);     // of this warp that exist (may be negative)
-      const int col0 = n * BN_ + half * C::cols;
+      const int col0 = n * BN_ + (C::TURNS ? 0 : half * C::cols);
       const bool live = rows > 0 && col0 < a.N;
       float acc[C::cols];
 #pragma unroll
       for (int i = 0; i < C::cols; ++i) acc[i] = 0.0f;
       const float* xs = a.x_scales + (row0 + min(lane, max(rows - 1, 0))) * kblocks;
       const float* ws = a.w_scales + (long long)(col0 >> 7) * kblocks;
-      float sx = live ? __ldg(xs + p.k0) : 0.0f, sw = live ? __ldg(ws + p.k0) : 0.0f;
-      for (int kb = p.k0; kb < p.k1; ++kb) {
-        const float s = __fmul_rn(sx, sw);
-        if (live && kb + 1 < p.k1) {
-          sx = __ldg(xs + kb + 1);
-          sw = __ldg(ws + kb + 1);
-        }
-        // the warp leaves together: what follows is executed by all of its lanes
-        if (!__all_sync(0xffffffffu, wait(bar_done(stage), phase))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t tb = tmem_base + lane_addr + buf * BN_ + half * C::cols;
-        auto release = [&] {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_tempty(buf));
-        };
-        constexpr int CH = C::cols / 32;
-        uint32_t r[2][32];
-        auto add = [&](int c) {
+      constexpr int STEP = C::TURNS ? 2 : 1;
+      const int kb0 = p.k0 + (C::TURNS ? (int)(g & 1u) : 0);     // the first that is this warp's
+      float sx = live && kb0 < p.k1 ? __ldg(xs + kb0) : 0.0f, sw = live && kb0 < p.k1 ? __ldg(ws + kb0) : 0.0f;
+      for (int kb = p.k0; kb < p.k1; ++kb, ++g) {
+        if (!C::TURNS || (g & 1u) == 0) {
+          const float s = __fmul_rn(sx, sw);
+          if (live && kb + STEP < p.k1) {
+            sx = __ldg(xs + kb + STEP);
+            sw = __ldg(ws + kb + STEP);
+          }
+          // the warp leaves together: what follows is executed by all of its lanes
+          if (!__all_sync(0xffffffffu, wait(bar_done(stage), phase))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t tb = tmem_base + lane_addr + buf * BN_ + (C::TURNS ? 0 : half * C::cols);
+          auto release = [&] {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_tempty(buf));
+          };
+          constexpr int CH = C::cols / 32;
+          uint32_t r[2][32];
+          auto add = [&](int c) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) acc[32 * c + i] = fmaf(__uint_as_float(r[c & 1][i]), s, acc[32 * c + i]);
-        };
-        if (live) {
-          tmem_ld32(tb, r[0]);
-          if (CH > 1) tmem_ld32(tb + 32, r[1]);
-          wait_ld(r[0]);
-          if (CH > 1) wait_ld(r[1]);
-          if (CH == 4) {
-            add(0);
-            tmem_ld32(tb + 64, r[0]);
-            add(1);
-            tmem_ld32(tb + 96, r[1]);
+            for (int i = 0; i < 32; ++i) acc[32 * c + i] = fmaf(__uint_as_float(r[c & 1][i]), s, acc[32 * c + i]);
+          };
+          if (live) {
+            tmem_ld32(tb, r[0]);
+            if (CH > 1) tmem_ld32(tb + 32, r[1]);
             wait_ld(r[0]);
-            wait_ld(r[1]);
-            release();
-            add(2);
-            add(3);
+            if (CH > 1) wait_ld(r[1]);
+            if (CH == 4) {
+              add(0);
+              tmem_ld32(tb + 64, r[0]);
+              add(1);
+              tmem_ld32(tb + 96, r[1]);
+              wait_ld(r[0]);
+              wait_ld(r[1]);
+              release();
+              add(2);
+              add(3);
+            } else {
+              release();
+              add(0);
+              if (CH > 1) add(1);
+            }
           } else {
             release();
-            add(0);
-            if (CH > 1) add(1);
           }
-        } else {
-          release();
         }
         if (++buf == C::bufs) buf = 0;
         if (++stage == C::stages) {
@@ -263,52 +268,31 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           phase ^= 1;
         }
       }
-      if (!ok) break;
-      if (!live) continue;
-      if (BN_ != SHARED_COLS || split.parts == 1) {
+      auto store = [&](const float* sums, int c, int col) {
+        float u[32];
 #pragma unroll
-        for (int c = 0; c < C::cols / 32; ++c) {
-          float v[32];
+        for (int i = 0; i < 32; ++i) u[i] = sums[c + i];
+        add_bias(a, u, col + c);
+        store_chunk(a, u, buf_w, lane, row0, rows, col + c, vec);
+      };
+      if constexpr (C::TURNS) {
+        constexpr int KEEP = C::cols / 2;
+        float v[KEEP];
+        if (!meet<32>(acc, v, reinterpret_cast<float*>(buf_w), reinterpret_cast<const float*>(smem + C::out + (ew ^ 4) * OUT_BYTES),
+                      half, lane, 1 + q, ok))
+          break;
+        const int col = col0 + KEEP * half;
+        if (!live || col >= a.N) continue;
+        if (p.tile >= split.whole && !join_parts(a, split, p.tile, worker, ew, lane, v)) continue;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = acc[32 * c + i];
-          add_bias(a, v, col0 + 32 * c);
-          store_chunk(a, v, buf_w, lane, row0, rows, col0 + 32 * c, vec);
-        }
-        continue;
-      }
-      if constexpr (BN_ == SHARED_COLS) {
-        // a part of the tile: the sums go to this worker's slot, and the last of the tile's parts to be counted adds all
-        // of them up in their order, one after the other (four loaded at a time: the K loop above went from 12.9 to 20.3
-        // us at 24 x 576 x 7168, by what the registers were given to)
-        static_assert(C::cols == 32, "one chunk");
-        auto slot = [&](int w) { return reinterpret_cast<float4*>(a.part) + ((size_t)w * EPI + ew) * 256 + lane; };
-        float4* mine = slot(worker);
+        for (int c = 0; c < KEEP; c += 32) store(v, c, col);
+      } else {
+        if (!ok) break;
+        if (!live) continue;
+        if constexpr (BN_ == 64)
+          if (p.tile >= split.whole && !join_parts(a, split, p.tile, worker, ew, lane, acc)) continue;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          __stcg(mine + 32 * i, make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]));
-        __syncwarp();
-        int before = 0;
-        int32_t* count = a.count + p.tile * EPI + ew;
-        if (lane == 0)
-          asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(count) : "memory");
-        before = __shfl_sync(0xffffffffu, before, 0);
-        if (before != split.parts - 1) continue;
-        if (lane == 0) *count = 0;
-        const int first = worker - worker % split.parts;
-        float v[32];
-        for (int w = 0; w < split.parts; ++w) {
-          float4 f[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = __ldcg(slot(first + w) + 32 * i);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float g[4] = {f[i].x, f[i].y, f[i].z, f[i].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[4 * i + j] = w ? __fadd_rn(v[4 * i + j], g[j]) : g[j];
-          }
-        }
-        add_bias(a, v, col0);
-        store_chunk(a, v, buf_w, lane, row0, rows, col0, vec);
+        for (int c = 0; c < C::cols; c += 32) store(acc, c, col0);
       }
     }
   }
@@ -339,6 +323,7 @@ moe_status_t launch(const Args& a, const Split& split, cudaStream_t s) {
 moe_status_t launch_tc(Variant v, const Args& a, const Split& split, cudaStream_t s) {
   switch (v) {
     case TC_64: return launch<64>(a, split, s);
+    case TC_128: return launch<128>(a, split, s);
     default: return launch<256>(a, split, s);
   }
 }

@@ -426,3 +426,24 @@ def test_block_of_the_path_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         check(got, live)
+
+
+@pytest.mark.parametrize("weights", ["e4m3", "w4"])
+def test_decode_step_with_norms_and_an_e4m3_head(weights):
+    """The decode step's own path: the router inside the layers and ahead of them give the same bits, and each step of the
+    stack is the sum of its parts."""
+    from combine_moe_route_softmax_gb300 import decode_few
+    size = dict(layers=2, H=256, I=128, E=8, K=2, vocab=512, weights=weights, act8=True)
+    ms, same = decode_few.run(tokens=5, steps=3, **size)
+    assert same and all(t > 0 for t in ms.values())
+    step = decode_few.DecodeStep(5, **size)
+    x = step.table[:5].clone()
+    logits, ids = step(x)
+    d = stream = None
+    for i, layer in enumerate(step.inside):
+        a, _, _, r = moe.moe_rmsnorm(x if i == 0 else d, step.norms[i], EPS, residual=None if i == 0 else stream)
+        stream = x if i == 0 else r
+        d, idx, _ = layer.forward(a)
+        assert torch.equal(idx, ids[i])
+    _, q, s, _ = moe.moe_rmsnorm(d, step.norms[-1], EPS, residual=stream, bf16=False, e4m3=True)
+    check_linear(logits, q, s, *step.head)

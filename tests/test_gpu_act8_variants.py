@@ -11,7 +11,7 @@ from gpu_helpers import need_gpu
 from test_gpu_act8 import check_linear, operands
 
 pytestmark = pytest.mark.gpu
-FEW, TILES_64, TILES_256, SWAP = -1, 0, 1, 2
+FEW, TILES_64, TILES_128, TILES_256, SWAP = -1, 0, 1, 2, 3
 _P, _I, _L, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t
 
 
@@ -37,7 +37,8 @@ def call(o, variant, parts=1, dtype=torch.float32, limit_ns=2_000_000_000, ws=No
 
 
 @pytest.mark.parametrize("variant,T", [(FEW, 1), (FEW, 8), (FEW, 9), (FEW, 16), (SWAP, 1), (SWAP, 16), (SWAP, 32), (TILES_64, 1),
-                                       (TILES_64, 130), (TILES_64, 1500), (TILES_256, 1), (TILES_256, 100), (TILES_256, 385)])
+                                       (TILES_64, 130), (TILES_64, 1500), (TILES_128, 1), (TILES_128, 300),
+                                       (TILES_128, 1100), (TILES_256, 1), (TILES_256, 100), (TILES_256, 385)])
 @pytest.mark.parametrize("N,K", [(1, 128), (127, 256), (300, 640), (1029, 2048), (5000, 384), (20000, 128)])
 def test_variants(variant, T, N, K):
     o = operands(T, N, K, bias=N % 2 == 0)
@@ -46,7 +47,9 @@ def test_variants(variant, T, N, K):
 
 
 @pytest.mark.parametrize("variant,T,N", [(SWAP, 20, 300), (SWAP, 32, 4096), (SWAP, 3, 1), (TILES_64, 20, 300), (TILES_64, 200, 900),
-                                         (TILES_64, 128, 1), (TILES_64, 700, 576)])
+                                         (TILES_64, 128, 1), (TILES_64, 700, 576), (TILES_64, 1100, 1200),
+                                         (TILES_128, 20, 300), (TILES_128, 400, 1000), (TILES_128, 2000, 1300),
+                                         (SWAP, 32, 20000)])
 @pytest.mark.parametrize("K", [128, 384, 2176])
 @pytest.mark.parametrize("parts", [2, 3, 5, 8])
 def test_shared_k(variant, T, N, K, parts):
@@ -60,7 +63,7 @@ def test_shared_k(variant, T, N, K, parts):
     assert not ws[:4096].any()          # the counters are left zero
 
 
-@pytest.mark.parametrize("variant", [FEW, SWAP, TILES_64, TILES_256])
+@pytest.mark.parametrize("variant", [FEW, SWAP, TILES_64, TILES_128, TILES_256])
 def test_strided_unaligned_out(variant):
     """An out that starts on an odd element, rows an odd number of elements apart."""
     o = operands(16, 300, 256, bias=True)
@@ -73,7 +76,8 @@ def test_strided_unaligned_out(variant):
 
 
 @pytest.mark.parametrize("variant,T,parts", [(FEW, 8, 1), (FEW, 16, 1), (SWAP, 32, 1), (SWAP, 32, 4), (TILES_64, 300, 1),
-                                             (TILES_64, 100, 4), (TILES_256, 600, 1)])
+                                             (TILES_64, 100, 4), (TILES_128, 300, 1), (TILES_128, 200, 3),
+                                             (TILES_256, 600, 1)])
 @pytest.mark.parametrize("N,K", [(1000, 7168), (300, 128)])
 def test_wait_that_runs_out(variant, T, parts, N, K):
     """Copies or MMAs that are never issued, and a limit of 20 ms: the call comes back soon with the status set, and the
