@@ -298,7 +298,8 @@ def check_dispatch(p, idx, E, x, xs, shared, max_tokens=0, fill=None):
 
 @pytest.mark.parametrize("T,H,E,K", [(1, 128, 1, 1), (1, 7168, 256, 8), (3, 256, 8, 2), (64, 640, 60, 6), (65, 2048, 64, 8),
                                      (128, 7168, 256, 8), (333, 384, 1024, 3), (700, 8320, 16, 4), (2500, 512, 256, 8),
-                                     (40, 16384, 40, 32)])
+                                     (40, 16384, 40, 32), (512, 128, 16, 8), (513, 128, 16, 8), (1216, 256, 8, 1),
+                                     (1217, 256, 8, 3), (3, 116096, 8, 2), (4097, 128, 4, 1)])
 @pytest.mark.parametrize("shared", [False, True])
 def test_dispatch(T, H, E, K, shared):
     g = gen(T + H + E)
