@@ -215,7 +215,10 @@ moe_status_t launch_few(const Args& a, cudaStream_t s) {
   return MOE_OK;
 }
 
-inline bool shape_ok(int T, int N, int K) { return T >= 0 && N > 0 && K > 0 && K % 128 == 0 && N <= (1 << 24) && K <= (1 << 22); }
+// rows and tiles of rows are counted in 32 bits
+inline bool shape_ok(int T, int N, int K) {
+  return T >= 0 && T <= (1 << 30) && N > 0 && N <= (1 << 24) && K > 0 && K <= (1 << 22) && K % 128 == 0;
+}
 
 struct Plan {
   int variant;     // -1: linear_few_kernel
@@ -325,16 +328,18 @@ extern "C" moe_status_t moe_linear_e4m3(const uint8_t* x, const float* x_scales,
 }
 
 // Test hook, deliberately absent from the public header: moe_linear_e4m3 by one variant whatever the sizes (-1: the
-// kernel for few rows, 0.. the tensor-core kernel's), with K shared by up to `parts` CTAs (not variant 1), and with the limit of each wait
-// in nanoseconds.  mute: copies (few rows) or MMAs are never issued, so that a test can make the waits for them run
-// out.
+// kernel for few rows, 0.. a Variant), with the K of the tiles of a last round shared by up to `parts` CTAs (not
+// the 256-column tiles'), and with the limit of each wait in nanoseconds.  mute: copies (few rows) or MMAs are
+// never issued, so that a test can make the waits for them run out.
 extern "C" moe_status_t moe_testing_linear_e4m3(const uint8_t* x, const float* x_scales, int T, int K, const uint8_t* w,
                                                 const float* w_scales, int N, const float* bias, void* out, int out_f32,
                                                 long long out_stride, void* ws, size_t ws_bytes, int32_t* dev_status,
                                                 int variant, int parts, unsigned long long limit_ns, int mute,
                                                 void* stream) {
   using namespace moe::lin8;
-  if (!shape_ok(T, N, K) || variant < -1 || variant >= VARIANTS || (variant == -1 && T > FEW_COLS) || (variant == SWAP && T > SWAP_ROWS)) return MOE_ERR_ARG;
+  if (!shape_ok(T, N, K) || variant < -1 || variant >= VARIANTS || (variant == -1 && T > FEW_COLS) ||
+      (variant == SWAP && T > SWAP_ROWS))
+    return MOE_ERR_ARG;
   Plan p{variant, {}};
   if (variant >= 0 && T > 0) p.split = cut((Variant)variant, T, N, K / 128, std::max(1, parts));
   return linear_e4m3_impl(x, x_scales, T, K, w, w_scales, N, bias, out, out_f32, out_stride, ws, ws_bytes, dev_status,

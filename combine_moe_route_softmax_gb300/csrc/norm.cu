@@ -186,6 +186,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a) {
 }
 
 constexpr int kNormMaxH = 65536;   // 1024 threads of 8 vectors
+constexpr int kNormMaxT = 1 << 30;  // a row and the grid's step to the next one in 32 bits
 
 template <int VPT, bool AHEAD>
 void launch_norm(const NormArgs& a, int threads, int blocks, cudaStream_t s) {
@@ -207,7 +208,7 @@ extern "C" moe_status_t moe_rmsnorm(const uint16_t* x, int T, int H, long long x
                                     void* residual_out, uint16_t* out, uint8_t* q, float* q_scales,
                                     const int32_t* num_tokens, void* stream) {
   using namespace moe;
-  if (T < 0 || H <= 0 || H % 8 != 0 || H > kNormMaxH || !(eps >= 0.0f)) return MOE_ERR_ARG;
+  if (T < 0 || T > kNormMaxT || H <= 0 || H % 8 != 0 || H > kNormMaxH || !(eps >= 0.0f)) return MOE_ERR_ARG;
   if ((weight_f32 != 0 && weight_f32 != 1) || (residual_f32 != 0 && residual_f32 != 1)) return MOE_ERR_ARG;
   if (T == 0) return MOE_OK;   // tensors without rows have no addresses
   if (!out && !q) return MOE_ERR_ARG;

@@ -49,6 +49,17 @@ def test_linear_refusals(lib):
     assert f(T=0, x=None, xs=None, out=None) == 0
 
 
+def test_rows_past_32_bits_are_refused(lib):
+    """Rows and the steps between them are counted in 32 bits: 2^30 rows are the most."""
+    most = 1 << 30
+    assert lib.moe_rmsnorm(A, most + 1, 8, 8, A, 0, 1e-6, None, 0, None, A, None, None, None, None) == ERR_ARG
+    assert lib.moe_rmsnorm(A, (1 << 31) - 1, 8, 8, A, 0, 1e-6, None, 0, None, A, None, None, None, None) == ERR_ARG
+    assert lib.moe_linear_e4m3_workspace_bytes(most, 1, 128) > 0
+    for T in (most + 1, (1 << 31) - 1):
+        assert lib.moe_linear_e4m3_workspace_bytes(T, 1, 128) == 0
+        assert lib.moe_linear_e4m3(A, A, T, 128, A, A, 1, None, A, 0, 1, A, 1 << 30, None, None) == ERR_ARG
+
+
 @pytest.mark.parametrize("N,K", [(64, 256), (576, 7168), (4096, 7168), (40960, 4096), (7168, 16384), (1, 128)])
 def test_linear_workspace_serves_fewer_rows(lib, N, K):
     """The size never falls with the rows: a workspace made for T rows serves any number up to T."""
