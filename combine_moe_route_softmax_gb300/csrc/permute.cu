@@ -73,7 +73,8 @@ __global__ void __launch_bounds__(kPermThreads) permute_count_kernel(const int32
 }
 
 // Exclusive scan of v over the block's threads; returns this thread's exclusive prefix
-// and (in *total) the block's sum.  blockDim.x == 256.
+// and (in *total) the block's sum.  blockDim.x == 32 WARPS.
+template <int WARPS = 8>
 __device__ __forceinline__ int block_exclusive_scan(int v, int* warp_sums, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int incl = v;
@@ -85,17 +86,17 @@ __device__ __forceinline__ int block_exclusive_scan(int v, int* warp_sums, int* 
   if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
   if (warp == 0) {
-    int ws = lane < 8 ? warp_sums[lane] : 0;
+    int ws = lane < WARPS ? warp_sums[lane] : 0;
 #pragma unroll
-    for (int off = 1; off < 8; off <<= 1) {
+    for (int off = 1; off < WARPS; off <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, ws, off);
       if (lane >= off) ws += u;
     }
-    if (lane < 8) warp_sums[lane] = ws;  // inclusive over warps
+    if (lane < WARPS) warp_sums[lane] = ws;  // inclusive over warps
   }
   __syncthreads();
   const int excl = incl - v + (warp > 0 ? warp_sums[warp - 1] : 0);
-  *total = warp_sums[7];
+  *total = warp_sums[WARPS - 1];
   __syncthreads();
   return excl;
 }
@@ -517,10 +518,16 @@ __global__ void __launch_bounds__(256) permute_gather_bulk_kernel(const uint8_t*
 // ------------------------------------------------- few tokens with E4M3 rows, in one launch
 // Every block counts all the slots by itself (T * K of them, a few to a thread) and so knows the segments' bounds and the
 // rows of its own tokens without another block's help; a warp then moves its token's row, whose load was issued first.
-// Top-8 and a shared expert, H = 7168: 1 token 5.6 us, 128 tokens 6.5, 300 9.1, 512 17.1, where the four launches take
-// 12.7, 13.9, 15.4 and 20.2 (captured in a graph).
-constexpr int kFewSlots = 4096;     // T * K at most: 16 KB of indices read by every block
+// Bound by launch and latency for few tokens, then by the counting, which every SM repeats, beside the rows' stores.  The
+// additions to a count in shared memory are plain ones (lanes of one expert found and added up by __match_any_sync
+// first: 24.4 us where these take 18.1).
+// Top-8 of 256 and a shared expert, H = 7168: 1 token 5.6 us, 128 tokens 6.0, 512 11.5, 1024 18.1, 2048 33.1, 4000 61.1, where
+// the four launches take 13.0, 14.6, 19.6, 25.4, 38.9 and 61.0 (captured in a graph; a call of its own also
+// saves the host three launches).
+constexpr int kFewSlots = 32768;     // T * K at most: 128 KB of indices read by every block
+constexpr int kFewSmall = 4096;      // slots up to which 512 threads (1 token 5.6 us, with 1024 6.2; 2048 tokens 35.4 / 33.1)
 constexpr int kFewSmem = 200 * 1024;
+constexpr int kFewBars = 256;        // bytes: a barrier for each of up to 32 warps
 struct FewPermute {
   const int32_t* idx;
   const uint8_t* x;
@@ -536,16 +543,17 @@ struct FewPermute {
 };
 __host__ __device__ constexpr int few_align(int n) { return (n + 127) / 128 * 128; }
 
-__global__ void __launch_bounds__(kPermThreads) permute_few_kernel(const FewPermute a) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) permute_few_kernel(const FewPermute a) {
   extern __shared__ __align__(128) uint8_t fsm[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nseg = a.E + a.with_shared;
   // barriers | rows of this block's tokens | total[nseg] then bounds[nseg + 1] | before[nseg] | dest[per_block][K + 1]
   uint64_t* bars = reinterpret_cast<uint64_t*>(fsm);
-  uint8_t* row = fsm + 128 + (size_t)warp * few_align(a.H);
-  int* bounds = reinterpret_cast<int*>(fsm + 128 + (size_t)a.per_block * few_align(a.H));
+  uint8_t* row = fsm + kFewBars + (size_t)warp * few_align(a.H);
+  int* bounds = reinterpret_cast<int*>(fsm + kFewBars + (size_t)a.per_block * few_align(a.H));
   int* before = bounds + nseg + 1;
   int* dest = before + nseg;
-  __shared__ int warp_sums[8];
+  __shared__ int warp_sums[THREADS / 32];
   const int t0 = blockIdx.x * a.per_block, t1 = min(a.T, t0 + a.per_block), t = t0 + warp;
   const bool mine = warp < a.per_block && t < t1;
   const uint32_t bar = smem_u32addr(bars + warp);
@@ -555,26 +563,37 @@ __global__ void __launch_bounds__(kPermThreads) permute_few_kernel(const FewPerm
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     bulk_row_load(smem_u32addr(row), a.x + (size_t)t * a.H, a.H, bar);
   }
-  for (int i = threadIdx.x; i < nseg; i += kPermThreads) bounds[i] = before[i] = 0;
+  for (int i = threadIdx.x; i < nseg; i += THREADS) bounds[i] = before[i] = 0;
   __syncthreads();
   bool bad = false;
   const int slots = a.T * a.K, s0 = t0 * a.K;
-  for (int s = threadIdx.x; s < slots; s += kPermThreads) {
-    const int e = a.idx[s];
-    if (valid_id(e, a.E)) {
-      atomicAdd(&bounds[e], 1);
-      if (s < s0) atomicAdd(&before[e], 1);
-    } else if (e != -1) {
-      bad = true;
+  constexpr int AHEAD = 4;
+  for (int base = threadIdx.x - lane; base < slots; base += AHEAD * THREADS) {
+    int e[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int s = base + i * THREADS + lane;
+      e[i] = s < slots ? __ldg(a.idx + s) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int s = base + i * THREADS + lane;
+      const bool ok = valid_id(e[i], a.E);
+      bad |= !ok && e[i] != -1;
+      if (ok) atomicAdd(&bounds[e[i]], 1);
+      if (ok && s < s0) atomicAdd(&before[e[i]], 1);
     }
   }
   if (a.with_shared) {
-    for (int u = threadIdx.x; u < a.T; u += kPermThreads) {
+    for (int base = threadIdx.x - lane; base < a.T; base += THREADS) {
+      const int u = base + lane;
       bool any = false;
-      for (int k = 0; k < a.K; ++k) any |= valid_id(a.idx[u * a.K + k], a.E);
-      if (any) {
-        atomicAdd(&bounds[a.E], 1);
-        if (u < t0) atomicAdd(&before[a.E], 1);
+      if (u < a.T)
+        for (int i = 0; i < a.K; ++i) any |= valid_id(__ldg(a.idx + u * a.K + i), a.E);
+      const unsigned all = __ballot_sync(0xffffffffu, any), early = __ballot_sync(0xffffffffu, any && u < t0);
+      if (lane == 0 && all) {
+        atomicAdd(&bounds[a.E], __popc(all));
+        if (early) atomicAdd(&before[a.E], __popc(early));
       }
     }
   }
@@ -582,11 +601,11 @@ __global__ void __launch_bounds__(kPermThreads) permute_few_kernel(const FewPerm
   __syncthreads();
   // counts -> bounds, in place (bounds[i] = rows of the segments before i)
   int running = 0;
-  for (int base = 0; base < nseg; base += kPermThreads) {
+  for (int base = 0; base < nseg; base += THREADS) {
     const int i = base + threadIdx.x;
     const int v = i < nseg ? bounds[i] : 0;
     int tot;
-    const int ex = block_exclusive_scan(v, warp_sums, &tot);
+    const int ex = block_exclusive_scan<THREADS / 32>(v, warp_sums, &tot);
     if (i < nseg) bounds[i] = running + ex;
     running += tot;
   }
@@ -595,7 +614,7 @@ __global__ void __launch_bounds__(kPermThreads) permute_few_kernel(const FewPerm
   const bool batched = a.max_tokens > 0;
   if (blockIdx.x == 0) {
     bool over = false;
-    for (int i = threadIdx.x; i <= nseg; i += kPermThreads) {
+    for (int i = threadIdx.x; i <= nseg; i += THREADS) {
       if (!batched) {
         a.cu_seqlens[i] = bounds[i];
       } else if (i < nseg) {
@@ -607,12 +626,12 @@ __global__ void __launch_bounds__(kPermThreads) permute_few_kernel(const FewPerm
     if (over && a.dev_status) atomicOr(a.dev_status, MOE_DEV_OVERFLOW);
   }
   // rows that no slot has
-  for (int p = (batched ? 0 : running) + blockIdx.x * kPermThreads + threadIdx.x; p < a.cap; p += gridDim.x * kPermThreads) {
+  for (int p = (batched ? 0 : running) + blockIdx.x * THREADS + threadIdx.x; p < a.cap; p += gridDim.x * THREADS) {
     const int e = batched ? p / a.max_tokens : 0;
     if (!batched || p - e * a.max_tokens >= bounds[e + 1] - bounds[e]) a.src_row[p] = -1;
   }
   if (a.zero_buf)
-    for (int i = threadIdx.x; i < (t1 - t0) * a.zero_per_token; i += kPermThreads)
+    for (int i = threadIdx.x; i < (t1 - t0) * a.zero_per_token; i += THREADS)
       a.zero_buf[(size_t)t0 * a.zero_per_token + i] = 0;
   // this block's slots in order: lanes with the same expert rank themselves (warp 0)
   if (warp == 0) {
@@ -640,7 +659,7 @@ __global__ void __launch_bounds__(kPermThreads) permute_few_kernel(const FewPerm
       if (ok && rank == 0) before[e] += __popc(peers);
       __syncwarp();
     }
-    // shared rows (t1 - t0 <= 8 tokens)
+    // shared rows (t1 - t0 <= 32 tokens)
     bool any = false;
     if (a.with_shared && t0 + lane < t1)
       for (int k = 0; k < a.K; ++k) any |= valid_id(a.idx[(t0 + lane) * a.K + k], a.E);
@@ -845,18 +864,22 @@ moe_status_t permute_impl(const int32_t* topk_idx, int T, int K, int E, int with
   const int cap = batched ? nseg * max_tokens : T * K + (with_shared ? T : 0);
   if (x_scales && (long long)T * K <= kFewSlots) {
     const int per = (T + num_sms() - 1) / num_sms();
-    const size_t smem = 128 + (size_t)per * few_align(H) + 4 * (2 * (size_t)nseg + 1 + (size_t)per * (K + 1));
-    if (per <= kPermWarps && smem <= (size_t)kFewSmem) {
+    const int threads = T * K <= kFewSmall && per <= 16 ? 512 : 1024;      // a warp for each of a block's tokens
+    const size_t smem = kFewBars + (size_t)per * few_align(H) + 4 * (2 * (size_t)nseg + 1 + (size_t)per * (K + 1));
+    if (per <= threads / 32 && smem <= (size_t)kFewSmem) {
       static std::atomic<unsigned long long> few_attr{0};
       if (!once_per_device(few_attr, [&] {
-            return cudaFuncSetAttribute(permute_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem) ==
-                   cudaSuccess;
+            return cudaFuncSetAttribute(permute_few_kernel<512>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem) ==
+                       cudaSuccess &&
+                   cudaFuncSetAttribute(permute_few_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem) ==
+                       cudaSuccess;
           }))
         return MOE_ERR_CUDA;
       const FewPermute f{topk_idx, reinterpret_cast<const uint8_t*>(x), x_scales, topk_w, T, K, E, with_shared, H,
                          batched ? max_tokens : 0, cap, per, static_cast<uint8_t*>(xp), xp_scales, cu_seqlens, masked_m,
                          src_row, inv_map, shared_map, dev_status, row_w, zero_buf, zero_per_token};
-      permute_few_kernel<<<(T + per - 1) / per, kPermThreads, smem, s>>>(f);
+      auto kernel = threads == 512 ? permute_few_kernel<512> : permute_few_kernel<1024>;
+      kernel<<<(T + per - 1) / per, threads, smem, s>>>(f);
       MOE_CHECK_LAUNCH();
       return MOE_OK;
     }

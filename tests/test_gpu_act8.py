@@ -299,7 +299,9 @@ def check_dispatch(p, idx, E, x, xs, shared, max_tokens=0, fill=None):
 @pytest.mark.parametrize("T,H,E,K", [(1, 128, 1, 1), (1, 7168, 256, 8), (3, 256, 8, 2), (64, 640, 60, 6), (65, 2048, 64, 8),
                                      (128, 7168, 256, 8), (333, 384, 1024, 3), (700, 8320, 16, 4), (2500, 512, 256, 8),
                                      (40, 16384, 40, 32), (512, 128, 16, 8), (513, 128, 16, 8), (1216, 256, 8, 1),
-                                     (1217, 256, 8, 3), (3, 116096, 8, 2), (4097, 128, 4, 1)])
+                                     (1217, 256, 8, 3), (3, 116096, 8, 2), (4097, 128, 4, 1), (2432, 128, 8, 1), (2433, 128, 8, 1),
+                                     (1024, 128, 64, 32), (1025, 128, 64, 32), (4864, 128, 8, 6), (4865, 128, 8, 6),
+                                     (3000, 256, 1, 1), (2048, 7168, 256, 8), (4256, 7168, 8, 2), (4300, 7168, 8, 2)])
 @pytest.mark.parametrize("shared", [False, True])
 def test_dispatch(T, H, E, K, shared):
     g = gen(T + H + E)
@@ -321,6 +323,19 @@ def test_dispatch_batched(max_tokens):
     p = moe.moe_permute_e4m3(idx, E, x, xs, with_shared=True, max_tokens=max_tokens, xp=xp, xp_scales=sc, dev_status=status)
     check_dispatch(p, idx, E, x, xs, True, max_tokens, fill=(77, -3.0))
     assert status.item() == (0 if max_tokens == 64 else moe.MOE_DEV_OVERFLOW)
+
+
+@pytest.mark.parametrize("max_tokens", [300, 900])
+def test_dispatch_batched_many(max_tokens):
+    g = gen(max_tokens)
+    T, H, E, K = 2000, 256, 8, 3
+    x, xs, idx = codes(g, T, H), scales(g, T, H // 128, 1.0), ids(g, T, E, K, 0.1)
+    rows = (E + 1) * max_tokens
+    xp, sc = torch.full((rows, H), 77, dtype=U8, device="cuda"), torch.full((rows, H // 128), -3.0, device="cuda")
+    status = torch.zeros(1, dtype=I32, device="cuda")
+    p = moe.moe_permute_e4m3(idx, E, x, xs, with_shared=True, max_tokens=max_tokens, xp=xp, xp_scales=sc, dev_status=status)
+    check_dispatch(p, idx, E, x, xs, True, max_tokens, fill=(77, -3.0))
+    assert status.item() == moe.MOE_DEV_OVERFLOW      # the shared expert's 1998 or so tokens
 
 
 def test_dispatch_all_padding_bad_ids_and_weights():
