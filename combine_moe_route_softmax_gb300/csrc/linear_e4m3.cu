@@ -215,6 +215,17 @@ moe_status_t launch_few(const Args& a, cudaStream_t s) {
   return MOE_OK;
 }
 
+// Units of 32 weight rows (MT = 2) for up to 16 rows of x, or of 16: those fill a last round of the SMs better, but cost more a byte
+// and a round.  Modelled as rounds times (a start, and the rows' bytes); one row, units of 16 / 32: 7168 x 16384 21.1 / 22.3 us,
+// 40960 x 4096 35.4 / 29.8, 4096 x 7168 8.7 / 8.0, 2048 x 2048 3.0 / 3.3, 16384 x 7168 22.7 / 22.9, 5000 x 4096 8.5 / 8.3.
+bool few_wide(int N, int K) {
+  auto us = [&](int rows, double start, double byte) {
+    const int units = (N + rows - 1) / rows, rounds = (units + num_sms() - 1) / num_sms();
+    return rounds * (start + byte * rows * K);
+  };
+  return us(32, 0.07, 1.88e-5) <= us(16, 0.18, 2.30e-5);
+}
+
 // rows and tiles of rows are counted in 32 bits
 inline bool shape_ok(int T, int N, int K) {
   return T >= 0 && T <= (1 << 30) && N > 0 && N <= (1 << 24) && K > 0 && K <= (1 << 22) && K % 128 == 0;
@@ -314,7 +325,7 @@ static moe_status_t linear_e4m3_impl(const uint8_t* x, const float* x_scales, in
                mute};
   const Plan p = forced ? *forced : plan(T, N, K);
   if (p.variant >= 0) return launch_variant((Variant)p.variant, a, p.split, as_stream(stream));
-  const bool wide = N / 32 >= moe::num_sms() / 2;
+  const bool wide = few_wide(N, K);
   if (T <= 8) return wide ? launch_few<1, 2>(a, as_stream(stream)) : launch_few<1, 1>(a, as_stream(stream));
   return wide ? launch_few<2, 2>(a, as_stream(stream)) : launch_few<2, 1>(a, as_stream(stream));
 }
