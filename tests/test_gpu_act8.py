@@ -338,6 +338,38 @@ def test_dispatch_batched_many(max_tokens):
     assert status.item() == moe.MOE_DEV_OVERFLOW      # the shared expert's 1998 or so tokens
 
 
+@pytest.mark.parametrize("T,E,K", [(50, 8, 4), (900, 60, 6), (9000, 60, 6)])
+def test_dispatch_one_expert_in_several_slots(T, E, K):
+    """A token that names an expert twice has two rows there; one expert may take nearly all rows."""
+    g = gen(T)
+    x, xs = codes(g, T, 256), scales(g, T, 2, 1.0)
+    idx = torch.randint(-1, E, (T, K), generator=g, device="cuda").to(I32)
+    idx[torch.rand(T, K, generator=g, device="cuda") < 0.8] = E - 1
+    check_dispatch(moe.moe_permute_e4m3(idx, E, x, xs, with_shared=True), idx, E, x, xs, True)
+
+
+def test_dispatch_no_tokens():
+    x, xs, idx = torch.empty(0, 256, dtype=U8, device="cuda"), torch.empty(0, 2, device="cuda"), torch.empty(0, 2, dtype=I32, device="cuda")
+    p = moe.moe_permute_e4m3(idx, 4, x, xs, with_shared=True)
+    assert p["cu_seqlens"].tolist() == [0] * 6 and p["xp"].shape == (0, 256)
+    p = moe.moe_permute_e4m3(idx, 4, x, xs, max_tokens=3)
+    assert p["masked_m"].tolist() == [0] * 4 and (p["src_row"] == -1).all()
+
+
+def test_dispatch_large_offsets():
+    """Rows past 2^31 bytes."""
+    g = gen(5)
+    T, H, E, K = 34000, 8192, 128, 8
+    x, xs, idx = codes(g, T, H), scales(g, T, H // 128, 1.0), ids(g, T, E, K)
+    p = moe.moe_permute_e4m3(idx, E, x, xs)
+    inv = p["inv_map"].long()
+    assert torch.equal(inv.flatten().sort()[0], torch.arange(T * K, device="cuda"))
+    for k in range(K):
+        assert torch.equal(p["xp_scales"][inv[:, k]], xs)
+        for i in range(0, T, 8500):
+            assert torch.equal(p["xp"][inv[i:i + 8500, k]], x[i:i + 8500])
+
+
 def test_dispatch_all_padding_bad_ids_and_weights():
     g = gen(31)
     T, H, E, K = 70, 256, 8, 4
