@@ -260,8 +260,8 @@ __global__ void __launch_bounds__(kPermThreads) permute_scatter_kernel(
 }
 
 // Destination rows of token t: lane k < K holds the row of slot k (or -1); the token's shared row (or -1) is the
-// same on every lane, since 32 slots leave no lane of its own for it.  A token with a shared row has a
-// slot with a row.
+// same on every lane, since 32 slots leave no lane of its own for it.  Either may be there without the other: in the
+// batched layout a block that overflows drops slots, and the shared expert's block rows, each by its own ranks.
 __device__ __forceinline__ int token_dest(const int32_t* __restrict__ inv_map, int t, int K, int lane) {
   return lane < K ? inv_map[(size_t)t * K + lane] : -1;
 }
@@ -359,9 +359,9 @@ __global__ void __launch_bounds__(256) permute_gather_bf16_kernel(const uint16_t
     const int v_begin = (item - t * splits) * per_part;
     const int v_end = min(nvec, v_begin + per_part);
     const int my_dst = token_dest(inv_map, t, K, lane);
-    const unsigned live = __ballot_sync(0xffffffffu, my_dst >= 0);
-    if (!live) continue;                      // padding token: nothing to copy
     const int shared_row = shared_dest(shared_map, t);
+    const unsigned live = __ballot_sync(0xffffffffu, my_dst >= 0);
+    if (!live && shared_row < 0) continue;    // padding token: nothing to copy
     const uint4* in = reinterpret_cast<const uint4*>(x + (size_t)t * H);
     for (int v0 = v_begin; v0 < v_end; v0 += 128) {
       uint4 r[4], q[4];
@@ -458,7 +458,8 @@ __global__ void __launch_bounds__(256) permute_gather_bulk_kernel(const uint8_t*
   // the next token (stride nw) that has a row to write, or T
   auto next_live = [&](int t) {
     for (; t < T; t += nw) {
-      if (__ballot_sync(0xffffffffu, token_dest(inv_map, t, K, lane) >= 0)) return t;
+      const int shared_row = shared_dest(shared_map, t);
+      if (__ballot_sync(0xffffffffu, token_dest(inv_map, t, K, lane) >= 0) || shared_row >= 0) return t;
     }
     return T;
   };
@@ -739,9 +740,9 @@ __global__ void __launch_bounds__(256) permute_gather_e4m3_kernel(const uint16_t
     const int v_begin = (item - t * splits) * per_part;
     const int v_end = min(nvec, v_begin + per_part);
     const int my_dst = token_dest(inv_map, t, K, lane);
-    const unsigned live = __ballot_sync(0xffffffffu, my_dst >= 0);
-    if (!live) continue;
     const int shared_row = shared_dest(shared_map, t);
+    const unsigned live = __ballot_sync(0xffffffffu, my_dst >= 0);
+    if (!live && shared_row < 0) continue;    // padding token: nothing to copy
     const uint4* in = reinterpret_cast<const uint4*>(x + (size_t)t * H);
     for (int v0 = v_begin; v0 < v_end; v0 += 32) {
       const int v = v0 + lane;
