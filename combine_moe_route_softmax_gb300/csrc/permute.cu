@@ -236,9 +236,9 @@ __global__ void __launch_bounds__(kPermThreads) permute_scatter_kernel(
     }
   }
   if (!batched) {
-    // rows past the last one: -1
+    // rows past the last one: -1 (there may be 2^31 - 1 rows: a step past the last one passes 31 bits)
     const int total = cu_seqlens[nseg];
-    for (int p = total + blockIdx.x * blockDim.x + threadIdx.x; p < cap; p += gridDim.x * blockDim.x)
+    for (unsigned p = total + blockIdx.x * blockDim.x + threadIdx.x; p < (unsigned)cap; p += gridDim.x * blockDim.x)
       src_row[p] = -1;
     return;
   }
@@ -253,9 +253,9 @@ __global__ void __launch_bounds__(kPermThreads) permute_scatter_kernel(
     }
     if (over && dev_status) atomicOr(dev_status, MOE_DEV_OVERFLOW);
   }
-  for (int p = blockIdx.x * blockDim.x + threadIdx.x; p < cap; p += gridDim.x * blockDim.x) {
-    const int e = p / max_tokens;
-    if (p - e * max_tokens >= cu_seqlens[e + 1] - cu_seqlens[e]) src_row[p] = -1;
+  for (unsigned p = blockIdx.x * blockDim.x + threadIdx.x; p < (unsigned)cap; p += gridDim.x * blockDim.x) {
+    const int e = (int)p / max_tokens;
+    if ((int)p - e * max_tokens >= cu_seqlens[e + 1] - cu_seqlens[e]) src_row[p] = -1;
   }
 }
 
@@ -626,10 +626,10 @@ __global__ void __launch_bounds__(THREADS) permute_few_kernel(const FewPermute a
     }
     if (over && a.dev_status) atomicOr(a.dev_status, MOE_DEV_OVERFLOW);
   }
-  // rows that no slot has
-  for (int p = (batched ? 0 : running) + blockIdx.x * THREADS + threadIdx.x; p < a.cap; p += gridDim.x * THREADS) {
-    const int e = batched ? p / a.max_tokens : 0;
-    if (!batched || p - e * a.max_tokens >= bounds[e + 1] - bounds[e]) a.src_row[p] = -1;
+  // rows that no slot has (up to 2^31 - 1 of them: a step past the last one passes 31 bits)
+  for (unsigned p = (batched ? 0 : running) + blockIdx.x * THREADS + threadIdx.x; p < (unsigned)a.cap; p += gridDim.x * THREADS) {
+    const int e = batched ? (int)p / a.max_tokens : 0;
+    if (!batched || (int)p - e * a.max_tokens >= bounds[e + 1] - bounds[e]) a.src_row[p] = -1;
   }
   if (a.zero_buf)
     for (int i = threadIdx.x; i < (t1 - t0) * a.zero_per_token; i += THREADS)
