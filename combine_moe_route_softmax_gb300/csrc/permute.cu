@@ -850,7 +850,11 @@ moe_status_t permute_impl(const int32_t* topk_idx, int T, int K, int E, int with
   if (dq_scale && out_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   if (dq_format != 0 && dq_format != 1) return MOE_ERR_ARG;
   if (row_w && !topk_w) return MOE_ERR_ARG;
-  if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(xp)) & 15) return MOE_ERR_ARG;
+  auto bits = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
+  if ((bits(x) | bits(xp)) & 15) return MOE_ERR_ARG;
+  if ((bits(topk_idx) | bits(x_scales) | bits(xp_scales) | bits(cu_seqlens) | bits(masked_m) | bits(src_row) | bits(inv_map) |
+       bits(shared_map) | bits(ws) | bits(dev_status) | bits(dq_scale) | bits(topk_w) | bits(row_w) | bits(zero_buf)) & 3)
+    return MOE_ERR_ARG;
   if ((size_t)T * K + T > 0x7fffffffull) return MOE_ERR_ARG;
   const size_t need = batched ? moe_permute_batched_workspace_bytes(T, K, E, with_shared)
                               : moe_permute_workspace_bytes(T, K, E, with_shared);

@@ -120,7 +120,8 @@ moe_status_t moe_route_topk(const float* logits, int T, int E, int K, const int3
  *              scratch carries no hidden states), no state kept between calls.
  *   dev_status nullable; MOE_DEV_BAD_EXPERT is ORed in for ids outside [-1, E).
  * Rows of xp at or past N are not written.
- * Errors: MOE_ERR_ARG for bad sizes / null pointers, MOE_ERR_WORKSPACE if ws_bytes is short. */
+ * Errors: MOE_ERR_ARG for bad sizes / null pointers / misaligned pointers (x and xp 16 bytes, the others 4; so
+ * every permute call), MOE_ERR_WORKSPACE if ws_bytes is short. */
 size_t moe_permute_workspace_bytes(int T, int K, int E, int with_shared);
 moe_status_t moe_permute(const int32_t* topk_idx, int T, int K, int E, int with_shared,
                          const uint16_t* x, int H, moe_dtype_t out_dtype, void* xp, float* xp_scales,
