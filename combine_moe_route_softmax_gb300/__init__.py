@@ -492,6 +492,12 @@ class MoeLayer:
         _need_tensor(logits, torch.float32, (d.T, d.E), "logits")
         _need_word(num_tokens, "num_tokens")
         _need_word(dev_status, "dev_status")
+        _need(fq_scale is None or isinstance(fq_scale, int) or (fq_scale.dtype is torch.float32 and fq_scale.numel() >= 1),
+              "fq_scale is a float32 on the GPU")
+        dev = _here()
+        for t in (x, x_scales, out, topk_idx, topk_w, logits, num_tokens, fq_scale, dev_status, self.ws):
+            if isinstance(t, torch.Tensor) and t.get_device() != dev:
+                _refuse("MoeLayer.forward")
         _check("moe_layer_forward_e4m3", lib().moe_layer_forward_e4m3(
             ctypes.byref(self.desc), ctypes.byref(self.weights), _ptr(logits), _ptr(num_tokens), _ptr(topk_idx),
             _ptr(topk_w), _ptr(x), _ptr(x_scales), _ptr(fq_scale), _ptr(out), _ptr(self.ws), self.ws.numel(),
