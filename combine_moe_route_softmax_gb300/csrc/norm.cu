@@ -54,10 +54,11 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 
 // Codes of 8 values with scale s: e4m3(v / s) with the quotients correctly rounded.  The division is Markstein's ("Computation
 // of elementary functions on the IBM RISC System/6000 processor", 1990): with inv the correctly rounded reciprocal,
-// t = v inv is within an ulp, and t + (v - t s) inv rounds to the quotient; three instructions where an IEEE division takes
-// ten.  It asks that nothing on the way under- or overflows: outside [2^-80, 2^80] s is divided by as usual (inside, a v so
-// small that the remainder underflows is below half of the smallest code either way).  The remainder of a zero is +0 and
-// would make +0 of -0: the quotient takes the sign of v, as s is positive.
+// t = v inv is within an ulp, and t - (t s - v) inv rounds to the quotient.  It asks that nothing on the way under- or
+// overflows: outside [2^-80, 2^80] s is divided by as usual (inside, a v so small that the remainder underflows is below
+// half of the smallest code either way).  A quotient of zero keeps the sign of v: of -0 the remainder t s - v is
+// +0, as a sum of zeros of both signs is, and t less +0 stays -0; the other way round, t + (v - t s) inv, it would be +0.
+// Every block by the usual division instead: 12000 x 7168 133 us, this 121.
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], float s) {
   uint32_t c[2] = {0, 0};
   if (s > 8e-25f && s < 1e24f) {
@@ -65,7 +66,7 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], float s) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float t = __fmul_rn(v[i], inv);
-      c[i >> 2] |= (uint32_t)f32_to_e4m3(copysignf(fmaf(fmaf(-t, s, v[i]), inv, t), v[i])) << (8 * (i & 3));
+      c[i >> 2] |= (uint32_t)f32_to_e4m3(fmaf(-fmaf(t, s, -v[i]), inv, t)) << (8 * (i & 3));
     }
   } else {
 #pragma unroll
