@@ -257,7 +257,10 @@ moe_status_t launch_variant(Variant v, const Args& a, const Split& split, cudaSt
 
 // By rows and weights, then the tile width and the parts of K whose time, modelled from measured calls, is least.
 //   Up to 8 rows, and up to 16 where the weights are below 32 MB: the kernel for few rows (1 x 40960 x 4096 30.0 us, with weight
-//   rows as M 32.5; 16 x 4096 x 7168 10.7 / 10.5; 16 x 40960 x 4096 45.5 / 33.5).
+//   rows as M 32.5; 8 x 40960 x 4096 31.0 / 31.3, but 8 x 16384 x 7168 24.5 / 22.2).  9 and 16 rows, weights from memory:
+//   2048 x 2048 4.1, 4.3 / 6.5; 2112 x 7168 7.2, 7.5 / 8.9; 4096 x 4096 7.8, 8.1 / 8.7; 4096 x 7168 10.2, 10.5 / 10.2; from here on
+//   behind: 8192 x 3584 10.9, 11.9 / 9.9; 8191 x 4096 11.6, 12.7 / 10.7; 8192 x 4096 (32 MB) 11.7, 12.8 / 10.7; 40960 x 4096 37.8, 44.3 /
+//   31.4.  So 24 MB would be the better border by up to a tenth; 7168 x 2048 (8.3, 9.2 / 7.6) goes by the shape, not the bytes.
 //   Up to 32: weight rows as M (32 x 4096 x 7168 10.7, with 128 x 64 tiles 12.0; 32 x 7168 x 2048 7.0 / 9.6).
 //   More, 64 / 128 / 256 columns: 64 x 4096 x 7168 12.5 / 14.9 / 31, 512 x 4096 x 7168 26.8 / 21.0 / 31.7, 3000 x 576 x 7168 24.3 /
 //   20.6 / 31.5, 2048 x 2048 x 2048 19.4 / 18.0 / 14.8, 8192 x 4096 x 7168 304 / 239 / 200.

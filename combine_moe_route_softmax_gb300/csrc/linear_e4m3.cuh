@@ -1,4 +1,4 @@
-// moe_linear_e4m3's two kernels and how a call is cut.  Internal header.
+// moe_linear_e4m3's three kernels (few rows, tiles of rows of x, weight rows as M) and how a call is cut.  Internal header.
 #pragma once
 
 #include <algorithm>

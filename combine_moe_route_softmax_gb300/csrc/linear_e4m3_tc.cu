@@ -15,7 +15,7 @@
 //   an SM more; 192 columns, read at once: 265; 128 columns, four accumulators: 236 here and behind 64 or 256 at every other
 //   size; two MMAs of 128 columns with barriers of their own: 236; packed fma.f32x2: 228 against 217 (its operands have to be
 //   moved into pairs); sixteen epilogue warps of 64 columns: 208.
-//   Kept: one lane issues behind elect.sync, in a form that the compiler knows to be one thread (128 columns: 326 -> 228 us);
+//   Kept: one lane issues, named by elect.sync instead of a condition on its number (128 columns: 326 -> 228 us);
 //   one commit per block, on whose barrier both the producer and the epilogue wait; the accumulator is given back before
 //   its last 64 columns are added (217 -> 207); two issuing threads, even and odd blocks (64 columns: 345 -> 308); 56 registers
 //   for the first warpgroup, whose threads kept some in local memory with 40 (207 -> 200).
@@ -24,7 +24,7 @@
 // memory); 3 is idle; 4..11 epilogue: warp w reads TMEM lanes 32 (w % 4).. and half (w - 4) / 4 of the columns.  The first
 // warpgroup gives its registers to the other two.
 //
-// Shared K (few tiles of 64 columns): the K of each tile is cut into equal parts, a CTA each; an epilogue warp leaves its sums
+// Shared K (64 and 128 columns, the tiles of a last, partly filled round): the K of each tile is cut into equal parts, a CTA each; an epilogue warp leaves its sums
 // in the workspace and counts itself in, and the last of a tile's parts to arrive adds all of them up in their order.  No
 // one waits.
 //

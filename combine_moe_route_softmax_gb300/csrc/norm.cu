@@ -11,9 +11,12 @@
 // outputs.  A row belongs to a block; a thread holds VPT vectors of 8 columns, vector j of thread t being
 // columns 8 (t + j * threads).. so that 16 lanes next to each other hold one 128-column block.
 //   Rows up to the SMs: one vector a thread, the most loads in flight (1 x 7168: 3.0 us, launch and latency).
-//   More: two vectors and 1024 threads an SM, the next row loaded ahead: 12000 x 7168, BF16 residual, all outputs: 120 us,
-//   0.97 of the measured copy bandwidth (without loading ahead 141, four vectors 129, 1536 threads 147); 16384 x 2048 48.6 us.
-//   Rows longer than 8192 columns, whose registers leave no room for the next: four or eight vectors.
+//   More: two vectors and 1024 threads an SM, the next row loaded ahead: 12000 x 7168, BF16 residual, all outputs: 121 us,
+//   0.96 of the measured copy bandwidth (without loading ahead 141, four vectors 129, 1536 threads 147); 16384 x 2048 48.6 us.
+//   Rows longer than 8192 columns, whose registers leave no room for the next: four or eight vectors.  Four: 4096 x 12288 with a
+//   BF16 residual and all outputs 85 us, 4096 x 16384 103 (0.80 and 0.88 of the copy bandwidth).  Eight, beyond 32768 columns,
+//   are more than 64 registers hold: 120, 168 and 240 bytes of a thread (no, BF16, float32 residual) stand in local memory;
+//   1024 x 65536 147 us (0.62), 2048 x 32768, still four, 114 (0.80).
 #include <algorithm>
 
 #include "common.cuh"

@@ -629,7 +629,8 @@ moe_status_t moe_layer_few(const moe_few_desc_t* d, const moe_few_weights_t* w, 
  *   q, q_scales  nullable together: E4M3 codes [T, H] and float32 [T, H/128].  At least one of out and q.
  *   num_tokens nullable device int32 scalar n: rows t >= n are neither read nor written.
  * T <= 2^30, H % 8 == 0 (q: H % 128 == 0), H <= 65536, eps >= 0.  x, weight, residual, residual_out and out 16-byte aligned,
- * q 8-byte.  h whose squares sum past float32's range (|h| near 1e19) gives y = 0.
+ * q 8-byte.  h whose squares sum past float32's range (|h| near 1e19) gives y = 0, and with eps = 0 squares below that range
+ * (|h| near 1e-20) are lost to the sum.  NaN has no part in amax; a code of a zero keeps its sign.
  * Errors: MOE_ERR_ARG. */
 moe_status_t moe_rmsnorm(const uint16_t* x, int T, int H, long long x_stride, const void* weight, int weight_f32,
                          float eps, const void* residual, int residual_f32, void* residual_out, uint16_t* out,
@@ -647,7 +648,8 @@ moe_status_t moe_rmsnorm(const uint16_t* x, int T, int H, long long x_stride, co
  *              Two calls that may overlap on the GPU need workspaces of their own.
  *   dev_status nullable; MOE_DEV_PIPELINE_TIMEOUT if a wait within the kernel gave up (out is invalid; the
  *              caller zeroes ws).
- * T up to 2^30, any N up to 2^24, K % 128 == 0 and at most 2^22.  x and w 16-byte aligned.  The result does not depend on
+ * T up to 2^30, any N up to 2^24, K % 128 == 0 and at most 2^22.  x and w 16-byte aligned.  The product of a block's two
+ * scales is formed first, in float32, and has to lie in its range.  The result does not depend on
  * timing; the order of a row's sums, and so their last bits, depends on T, N and K of the call.
  * Errors: MOE_ERR_ARG, MOE_ERR_WORKSPACE. */
 size_t moe_linear_e4m3_workspace_bytes(int T, int N, int K);
