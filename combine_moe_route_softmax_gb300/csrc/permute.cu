@@ -259,24 +259,34 @@ __global__ void __launch_bounds__(kPermThreads) permute_scatter_kernel(
   }
 }
 
-// Destination rows of token t: lane k < K holds the row of slot k (or -1); the token's shared row (or -1) is the
-// same on every lane, since 32 slots leave no lane of its own for it.  Either may be there without the other: in the
-// batched layout a block that overflows drops slots, and the shared expert's block rows, each by its own ranks.
-__device__ __forceinline__ int token_dest(const int32_t* __restrict__ inv_map, int t, int K, int lane) {
-  return lane < K ? inv_map[(size_t)t * K + lane] : -1;
+// Destination rows of token t: lane k < K holds the row of slot k, lane K the shared row (-1: none).  32 slots leave no
+// lane for the shared row: extra_dest holds it then, the same on every lane.  A token may have a shared row and no slot
+// with a row: in the batched layout a block that overflows drops slots, and the shared expert's block rows, each by its
+// own ranks.
+__device__ __forceinline__ int token_dest(const int32_t* __restrict__ inv_map, const int32_t* __restrict__ shared_map, int t,
+                                          int K, int lane) {
+  if (lane < K) return inv_map[(size_t)t * K + lane];
+  return lane == K && shared_map ? shared_map[t] : -1;
 }
-__device__ __forceinline__ int shared_dest(const int32_t* __restrict__ shared_map, int t) {
-  return shared_map ? shared_map[t] : -1;
+__device__ __forceinline__ int extra_dest(const int32_t* __restrict__ shared_map, int t, int K) {
+  return K == 32 && shared_map ? shared_map[t] : -1;
 }
 // copy(row, routed) for each of them, by the whole warp.
 template <class F>
-__device__ __forceinline__ void for_each_dest(unsigned live, int my_dst, int shared_row, F&& copy) {
-  while (live) {
-    const int d = __ffs(live) - 1;
-    live &= live - 1;
-    copy(__shfl_sync(0xffffffffu, my_dst, d), true);
+__device__ __forceinline__ void for_each_dest(unsigned live, int my_dst, int extra, int K, F&& copy) {
+  while (live || extra >= 0) {
+    int row = extra;
+    bool routed = false;
+    if (live) {
+      const int d = __ffs(live) - 1;
+      live &= live - 1;
+      row = __shfl_sync(0xffffffffu, my_dst, d);
+      routed = d < K;
+    } else {
+      extra = -1;
+    }
+    copy(row, routed);
   }
-  if (shared_row >= 0) copy(shared_row, false);
 }
 
 // Dispatch fake-quant of 8 BF16 values: bf16(e4m3(x * s) / s), float32 steps; the division
@@ -358,10 +368,10 @@ __global__ void __launch_bounds__(256) permute_gather_bf16_kernel(const uint16_t
     const int t = item / splits;
     const int v_begin = (item - t * splits) * per_part;
     const int v_end = min(nvec, v_begin + per_part);
-    const int my_dst = token_dest(inv_map, t, K, lane);
-    const int shared_row = shared_dest(shared_map, t);
+    const int my_dst = token_dest(inv_map, shared_map, t, K, lane);
+    const int extra = extra_dest(shared_map, t, K);
     const unsigned live = __ballot_sync(0xffffffffu, my_dst >= 0);
-    if (!live && shared_row < 0) continue;    // padding token: nothing to copy
+    if (!live && extra < 0) continue;         // padding token: nothing to copy
     const uint4* in = reinterpret_cast<const uint4*>(x + (size_t)t * H);
     for (int v0 = v_begin; v0 < v_end; v0 += 128) {
       uint4 r[4], q[4];
@@ -377,7 +387,7 @@ __global__ void __launch_bounds__(256) permute_gather_bf16_kernel(const uint16_t
         // zeros, and so does its partner (parts hold whole 128-vector groups, v_end is even)
         if (DQ == 2) q[j] = qdq8_nvfp4(r[j], s, inv_tbl, d_tbl);
       }
-      for_each_dest(live, my_dst, shared_row, [&](int row, bool routed) {
+      for_each_dest(live, my_dst, extra, K, [&](int row, bool routed) {
         uint4* o = reinterpret_cast<uint4*>(xp + (size_t)row * H);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -458,8 +468,8 @@ __global__ void __launch_bounds__(256) permute_gather_bulk_kernel(const uint8_t*
   // the next token (stride nw) that has a row to write, or T
   auto next_live = [&](int t) {
     for (; t < T; t += nw) {
-      const int shared_row = shared_dest(shared_map, t);
-      if (__ballot_sync(0xffffffffu, token_dest(inv_map, t, K, lane) >= 0) || shared_row >= 0) return t;
+      const int d = token_dest(inv_map, shared_map, t, K, lane);
+      if (__ballot_sync(0xffffffffu, d >= 0) || extra_dest(shared_map, t, K) >= 0) return t;
     }
     return T;
   };
@@ -470,8 +480,8 @@ __global__ void __launch_bounds__(256) permute_gather_bulk_kernel(const uint8_t*
   if (lane == 0 && cur < T) bulk_row_load(buf0, x + (size_t)cur * row_bytes, row_bytes, bar0);
   while (cur < T) {
     const int nxt = next_live(cur + nw);
-    const int my_dst = token_dest(inv_map, cur, K, lane);
-    const int shared_row = shared_dest(shared_map, cur);
+    const int my_dst = token_dest(inv_map, shared_map, cur, K, lane);
+    const int extra = extra_dest(shared_map, cur, K);
     const unsigned live = __ballot_sync(0xffffffffu, my_dst >= 0);
     const uint32_t nb = static_cast<uint32_t>(b ^ 1);
     if (lane == 0 && nxt < T) {
@@ -486,7 +496,7 @@ __global__ void __launch_bounds__(256) permute_gather_bulk_kernel(const uint8_t*
         const bool ok0 = b0 + lane < nblk, ok1 = b0 + 32 + lane < nblk;
         const float s0 = ok0 ? x_scales[(size_t)cur * nblk + b0 + lane] : 0.0f;
         const float s1 = ok1 ? x_scales[(size_t)cur * nblk + b0 + 32 + lane] : 0.0f;
-        for_each_dest(live, my_dst, shared_row, [&](int row, bool) {
+        for_each_dest(live, my_dst, extra, K, [&](int row, bool) {
           float* dst = xp_scales + (size_t)row * nblk + b0 + lane;
           if (ok0) dst[0] = s0;
           if (ok1) dst[32] = s1;
@@ -504,7 +514,7 @@ __global__ void __launch_bounds__(256) permute_gather_bulk_kernel(const uint8_t*
       break;
     }
     phases ^= 1u << b;
-    for_each_dest(live, my_dst, shared_row, [&](int row, bool) {
+    for_each_dest(live, my_dst, extra, K, [&](int row, bool) {
       if (lane == 0) bulk_row_store(xp + (size_t)row * row_bytes, buf0 + b * buf_stride, row_bytes);
     });
     if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
@@ -723,7 +733,10 @@ __device__ __forceinline__ uint2 quant8(const uint4 u, bool live, float* scale) 
 }
 
 // Source-ordered gather with the 1x128 E4M3 quantisation: each token is quantised once and
-// its codes and scales written to every destination row.
+// its codes and scales written to every destination row.  EXTRA: 32 slots and a shared row, the only tokens with an
+// extra destination; its check in the loop over the rows of all others costs 3 to 6 % here (8192 x 7168, top-8 of 256: 145 us,
+// without 141; 2048 x 2048, top-8 of 64: 19.7, 18.5), and nothing that is measurable in the other gathers.
+template <bool EXTRA>
 __global__ void __launch_bounds__(256) permute_gather_e4m3_kernel(const uint16_t* __restrict__ x, int T, int K,
                                                                   int H, const int32_t* __restrict__ inv_map,
                                                                   const int32_t* __restrict__ shared_map,
@@ -739,10 +752,10 @@ __global__ void __launch_bounds__(256) permute_gather_e4m3_kernel(const uint16_t
     const int t = item / splits;
     const int v_begin = (item - t * splits) * per_part;
     const int v_end = min(nvec, v_begin + per_part);
-    const int my_dst = token_dest(inv_map, t, K, lane);
-    const int shared_row = shared_dest(shared_map, t);
+    const int my_dst = token_dest(inv_map, shared_map, t, K, lane);
+    const int extra = EXTRA ? extra_dest(shared_map, t, K) : -1;
     const unsigned live = __ballot_sync(0xffffffffu, my_dst >= 0);
-    if (!live && shared_row < 0) continue;    // padding token: nothing to copy
+    if (!live && extra < 0) continue;         // padding token: nothing to copy
     const uint4* in = reinterpret_cast<const uint4*>(x + (size_t)t * H);
     for (int v0 = v_begin; v0 < v_end; v0 += 32) {
       const int v = v0 + lane;
@@ -750,7 +763,7 @@ __global__ void __launch_bounds__(256) permute_gather_e4m3_kernel(const uint16_t
       const uint4 u = ok ? __ldg(in + v) : make_uint4(0, 0, 0, 0);
       float s;
       const uint2 q = quant8(u, ok, &s);
-      for_each_dest(live, my_dst, shared_row, [&](int row, bool) {
+      for_each_dest(live, my_dst, extra, K, [&](int row, bool) {
         if (ok) {
           reinterpret_cast<uint2*>(xp + (size_t)row * H)[v] = q;
           if ((lane & 15) == 0) xp_scales[(size_t)row * nblk + v / 16] = s;
@@ -940,8 +953,8 @@ moe_status_t permute_impl(const int32_t* topk_idx, int T, int K, int E, int with
       permute_gather_bf16_kernel<0><<<gblocks, 256, 0, s>>>(x, T, K, H, inv_map, smap, nullptr,
                                                             static_cast<uint16_t*>(xp), splits);
   else
-    permute_gather_e4m3_kernel<<<gblocks, 256, 0, s>>>(x, T, K, H, inv_map, smap, static_cast<uint8_t*>(xp),
-                                                       xp_scales, splits);
+    (K == 32 && smap ? permute_gather_e4m3_kernel<true> : permute_gather_e4m3_kernel<false>)<<<gblocks, 256, 0, s>>>(
+        x, T, K, H, inv_map, smap, static_cast<uint8_t*>(xp), xp_scales, splits);
   MOE_CHECK_LAUNCH();
   return MOE_OK;
 }

@@ -69,7 +69,8 @@ FORMS = ["bf16", "e4m3", "fq e4m3", "fq nvfp4", "codes"]
                          [(f, 4, 2, 2, 256, 4) for f in FORMS] +             # the first two tokens fill the expert's block
                          [(f, 300, 8, 4, 384, 200) for f in FORMS] +
                          [(f, 8193, 8, 4, 128, 5000) for f in FORMS] +       # more than 32768 slots: codes in four launches
-                         [("codes", 8192, 8, 4, 128, 5000), ("codes", 4800, 8, 4, 128, 3000), ("codes", 1200, 2, 32, 128, 900), ("bf16", 1200, 2, 32, 128, 900),
+                         [(f, 1200, 2, 32, 128, 900) for f in FORMS] +       # no lane left for the shared row
+                         [("codes", 8192, 8, 4, 128, 5000), ("codes", 4800, 8, 4, 128, 3000),
                           ("bf16", 40, 4, 3, 58240, 25)])                    # BF16 rows too long to stand in shared memory
 def test_shared_rows_of_tokens_that_lost_every_slot(form, T, E, K, H, max_tokens):
     idx = np.zeros((T, K), dtype=np.int32) if T == 4 else repeated_ids(T, E, K, seed=T + K)
